@@ -324,6 +324,75 @@ moe_status_t moe_layer_forward(const moe_config_t* cfg, const void* x, const voi
                                const void* w_shared_down, void* y, float* y_f32, void* ws,
                                size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Routing from scores: softmax or sigmoid scores over all experts, a balance bias that
+ * takes part in the choice only, expert groups, renormalised weights; with its gradient.
+ * The ids feed moe_permute and the weights moe_combine, as those of moe_route do. */
+
+/* moe_route_config_t.score */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+typedef struct {
+  int32_t T;             /* tokens, T*K < 2^31 */
+  int32_t E;             /* experts, 1..1024 */
+  int32_t K;             /* experts per token, 1..16, at most top_groups * (E / groups) */
+  int32_t groups;        /* expert groups of E / groups consecutive experts each, 1..32 */
+  int32_t top_groups;    /* groups a token may choose from, 1..groups */
+  int32_t group_rank;    /* a group's score is the sum of its 1 or 2 best keys */
+  int32_t score;         /* moe_score_t */
+  int32_t renormalise;   /* 1: the kept scores are divided by their sum, 0: used as they are */
+  float scale;           /* factor on the weights, finite and > 0 */
+  int32_t dtype;         /* moe_dtype_t of the logits and of their gradient */
+  int64_t logits_stride; /* elements between the rows of logits and d_logits, 0 = E */
+} moe_route_config_t;
+
+/* For every token, with l its logits:
+ *   s[e]   = softmax over the E experts, or the logistic function, of l[e];
+ *   key[e] = s[e] + expert_bias[e];
+ *   the top_groups groups with the largest sum of their group_rank largest keys stay (all
+ *   of them when top_groups == groups);
+ *   ids    = the K largest keys of those groups, descending;
+ *   w      = scale * s[id] / sum of the K kept s (renormalise), or scale * s[id].
+ * Choices compare keys (and group sums) as 64-bit values, whatever the logits' type; equal
+ * values go to the lower expert (group).  The weights are float, never biased.
+ * An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is not available: it is
+ * never chosen, and a masked logit takes no share of the softmax.  A token with fewer than K
+ * available experts in its groups gets -1 / 0 in its last slots.  A logit of +inf counts as
+ * the largest float.
+ *   logits [T,E] dtype in;  expert_bias [E] float in or NULL;
+ *   topk_ids [T,K] int32 out;  topk_w [T,K] float out.
+ * Pointers need only the alignment of their elements.  One launch. */
+moe_status_t moe_route_scored(const moe_route_config_t* cfg, const void* logits,
+                              const float* expert_bias, int32_t* topk_ids, float* topk_w,
+                              moe_stream_t stream);
+
+/* The gradient of moe_route_scored's weights with respect to the logits (the choice and the
+ * bias have none).  With dw = scale * d_topk_w, S the sum of the kept scores:
+ *   renormalise:  d s[id_k] = (dw_k - sum_j dw_j s[id_j] / S) / S;  else d s[id_k] = dw_k;
+ *   sigmoid:      d_logits[e] = d s[e] s[e] (1 - s[e]);
+ *   softmax:      d_logits[e] = s[e] (d s[e] - sum_j d s[j] s[j]).
+ *   logits as given to moe_route_scored; topk_ids its choice (distinct ids; an entry outside
+ *   0..E-1 is an empty slot); d_topk_w [T,K] float in; d_logits [T,E] dtype out, every element
+ *   written (row stride logits_stride; 0 where the logit is masked).
+ * d_logits may be logits itself.  One launch. */
+moe_status_t moe_route_scored_backward(const moe_route_config_t* cfg, const void* logits,
+                                       const int32_t* topk_ids, const float* d_topk_w,
+                                       void* d_logits, moe_stream_t stream);
+
+/* The gradient of moe_combine: what reaches the route weights and the expert rows.
+ *   d_topk_w[t,k]          = sum_h dy[t,h] * out_perm[inv[t,k],h]   (fp32; 0 where inv < 0)
+ *   d_out_perm[inv[t,k],h] = topk_w[t,k] * dy[t,h], rounded once to `act` (the operand type
+ *                            of the products that take it on); rows that no assignment maps
+ *                            to are untouched
+ * (the gradient of shared_out is dy itself).
+ *   dy [T,H] act in; out_perm [T*K,H] float in; inv [T*K] int32 in (entries outside
+ *   0..T*K-1 count as dropped); topk_w [T*K] float in; d_out_perm [T*K,H] act out or NULL;
+ *   d_topk_w [T*K] float out or NULL.  out_perm may be NULL when d_topk_w is, topk_w when
+ *   d_out_perm is.  One launch. */
+moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* dy, const float* out_perm,
+                                  const int32_t* inv, const float* topk_w, void* d_out_perm,
+                                  float* d_topk_w, moe_stream_t stream);
+
 /* Intermediates of the last moe_layer_forward that used `ws` (views into ws; valid
  * until ws is reused).  Any output pointer may be NULL.  Useful to check every stage.
  * x_perm is not written by decode-sized bf16 layers (T <= 16, E <= 256, K <= 16), whose

@@ -18,6 +18,8 @@ from typing import Optional
 __all__ = [
     "MoEConfig", "MoEError", "F32", "BF16", "FLAG_FUSED_COMBINE", "FLAG_CAPACITY", "FLAG_FP8", "library_path", "load", "workspace_size",
     "route", "permute", "permute_noalloc", "grouped_ffn", "expert_gate_up", "expert_gate_up_gather", "quantize_fp8", "expert_gate_up_fp8", "expert_down_fp8", "layer_forward_fp8", "expert_down", "combine", "layer_forward", "workspace_views",
+    "RouteConfig", "SCORE_SOFTMAX", "SCORE_SIGMOID", "route_scored", "route_scored_backward",
+    "combine_backward",
     "sync_check", "debug_wait_timeout", "status_string", "version",
 ]
 
@@ -28,6 +30,9 @@ BF16 = 1
 FLAG_FUSED_COMBINE = 1
 FLAG_CAPACITY = 2
 FLAG_FP8 = 4
+# moe_route_config_t.score
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 _STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -59,6 +64,31 @@ class MoEConfig(ctypes.Structure):
                 f"I_shared={self.I_shared}, theta={self.gate_threshold}, dtype={self.dtype})")
 
 
+class RouteConfig(ctypes.Structure):
+    """moe_route_config_t: T, E, K, groups, top_groups, group_rank, score, renormalise, scale,
+    dtype, logits_stride (0 = E)."""
+
+    _fields_ = [
+        ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+        ("group_rank", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+        ("logits_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, E, K, groups=1, top_groups=1, group_rank=1, score=SCORE_SOFTMAX,
+             renormalise=True, scale=1.0, dtype=F32, logits_stride=0):
+        return cls(T, E, K, groups, top_groups, group_rank, score, int(renormalise), scale, dtype,
+                   logits_stride)
+
+    def __repr__(self):
+        return (f"RouteConfig(T={self.T}, E={self.E}, K={self.K}, groups={self.groups}, "
+                f"top_groups={self.top_groups}, group_rank={self.group_rank}, "
+                f"score={self.score}, renormalise={self.renormalise}, scale={self.scale}, "
+                f"dtype={self.dtype})")
+
+
 def library_path(debug: bool = False) -> str:
     """The release library, or with ``debug`` the bounds-checking build (-DMOE_DEBUG)."""
     return os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -69,6 +99,7 @@ _LIB: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoEConfig)
+_RCFG = ctypes.POINTER(RouteConfig)
 _SIGS = {
     "moe_workspace_size": [_CFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_route": [_CFG, _P, _P, _P, _P, _P, _P, _P],
@@ -86,6 +117,9 @@ _SIGS = {
     "moe_combine": [_CFG, _P, _P, _P, _P, _P, _P, _P],
     "moe_layer_forward": [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_workspace_views": [_CFG, _P] + [ctypes.POINTER(_P)] * 10,
+    "moe_route_scored": [_RCFG, _P, _P, _P, _P, _P],
+    "moe_route_scored_backward": [_RCFG, _P, _P, _P, _P, _P],
+    "moe_combine_backward": [_CFG, _P, _P, _P, _P, _P, _P, _P],
     "moe_sync_check": [_P],
     "moe_debug_wait_timeout": [ctypes.c_uint, _P, _P],
     "moe_status_string": [ctypes.c_int],
@@ -275,6 +309,27 @@ def layer_forward(cfg, x, w_router, router_bias, w_gate_up, w_down, w_shared_gat
                                     _ptr(w_gate_up), _ptr(w_down), _ptr(w_shared_gate_up),
                                     _ptr(w_shared_down), _ptr(y), _ptr(y_f32), _ptr(ws), nb,
                                     _stream(stream)), "moe_layer_forward")
+
+
+def route_scored(cfg, logits, expert_bias, topk_ids, topk_w, stream=None):
+    """Expert ids and weights from scores (softmax or sigmoid, balance bias, groups)."""
+    _check(load().moe_route_scored(ctypes.byref(cfg), _ptr(logits), _ptr(expert_bias),
+                                   _ptr(topk_ids), _ptr(topk_w), _stream(stream)),
+           "moe_route_scored")
+
+
+def route_scored_backward(cfg, logits, topk_ids, d_topk_w, d_logits, stream=None):
+    """d_logits from the gradient of route_scored's weights."""
+    _check(load().moe_route_scored_backward(ctypes.byref(cfg), _ptr(logits), _ptr(topk_ids),
+                                            _ptr(d_topk_w), _ptr(d_logits), _stream(stream)),
+           "moe_route_scored_backward")
+
+
+def combine_backward(cfg, dy, out_perm, inv, topk_w, d_out_perm, d_topk_w, stream=None):
+    """Gradients of combine: the expert rows' (or None) and the route weights' (or None)."""
+    _check(load().moe_combine_backward(ctypes.byref(cfg), _ptr(dy), _ptr(out_perm), _ptr(inv),
+                                       _ptr(topk_w), _ptr(d_out_perm), _ptr(d_topk_w),
+                                       _stream(stream)), "moe_combine_backward")
 
 
 def workspace_views(cfg, ws) -> dict:

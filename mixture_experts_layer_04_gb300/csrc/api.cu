@@ -464,6 +464,7 @@ const char* const kFaultPoints[] = {
     "moe_expert_gate_up_gather", "moe_expert_down",         "moe_quantize_fp8",
     "moe_expert_gate_up_fp8",  "moe_expert_down_fp8",       "moe_combine",
     "moe_layer_forward",       "moe_layer_forward_fp8",     "moe_sync_check",
+    "moe_route_scored",        "moe_route_scored_backward", "moe_combine_backward",
     "moe_layer_forward.route", "moe_layer_forward.permute", "moe_layer_forward.gate_up",
     "moe_layer_forward.shared", "moe_layer_forward.down",   "moe_layer_forward.combine"};
 
@@ -555,6 +556,11 @@ struct StageRanges {
 moe_status_t check_current_device() {
   const DeviceInfo* d = nullptr;
   return check_device(&d);
+}
+
+int device_num_sms() {
+  const DeviceInfo* d = device_info();
+  return d != nullptr ? d->num_sms : 0;
 }
 
 }  // namespace moe

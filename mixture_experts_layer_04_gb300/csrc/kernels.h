@@ -111,6 +111,8 @@ moe_status_t fault_point(const char* name);
 // every entry point makes), MOE_ERR_UNSUPPORTED when it is not, MOE_ERR_CUDA when the
 // device cannot be queried.
 moe_status_t check_current_device();
+// SMs of the current device, 0 when it cannot be queried.
+int device_num_sms();
 // Maximum number of m-tiles of `bm` rows over all groups of T*K rows and E experts.
 inline int max_mtiles(int T, int K, int E, int bm) {
   return static_cast<int>((static_cast<long long>(T) * K + bm - 1) / bm) + E;

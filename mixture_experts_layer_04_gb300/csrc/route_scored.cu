@@ -1,0 +1,598 @@
+// Routing from scores and its gradient (moe_route_scored, moe_route_scored_backward).
+//
+// One warp per token.  Lane i holds the NJ consecutive experts i*NJ .. i*NJ+NJ-1, so that
+// among equal keys the lowest lane (and in it the lowest register) is the lowest expert, and
+// a group whose size is a multiple of NJ never straddles lanes.
+//
+// The choice.  It is defined on 64-bit keys s[e] + bias[e], and 64-bit arithmetic is slow on
+// this GPU, so it is taken in float first and certified: every float score carries a bound on
+// its error, and the token is chosen again in 64 bits only if two neighbouring choices (the
+// K-th and the first one left out among them), or the last group kept and the best one
+// dropped, lie within the sum of their bounds.  Without a bias the keys are ordered as the
+// logits are, so the logits themselves are compared, exactly.  Two experts of equal logit and
+// equal bias tie in any precision and need no second look.
+//
+// What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
+// written; the work is K+1 warp-wide maxima per token, so at prefill sizes it is bound by
+// instruction issue and the latency of the warp reductions, at one token by the launch.
+#include <cfloat>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "topk.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct RouteParams {
+  const void* logits;
+  const float* bias;  // or null
+  int32_t* ids;
+  float* w;
+  const int32_t* ids_in;  // backward
+  const float* d_w;
+  void* d_logits;
+  long long stride;  // elements between rows
+  int T, E, K, groups, per, top_groups, rank;
+  int renorm;
+  int vec;  // rows allow whole-lane vector loads (and, backward, 16-byte stores)
+  float scale;
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// A logit as the definition reads it: NaN counts as -inf (masked), +inf as the largest float.
+__device__ __forceinline__ float clean_logit(float l) {
+  return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// This lane's NJ logits of one row (masked ones and those past E as -inf).
+template <int NJ, typename TL>
+__device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec, float (&l)[NJ]) {
+  const int e0 = lane * NJ;
+  constexpr int kBytes = NJ * static_cast<int>(sizeof(TL));
+  if constexpr (kBytes >= 4) {
+    if (vec) {
+      constexpr int kVec = kBytes >= 16 ? 16 : kBytes;  // bytes per load
+      constexpr int kPer = kVec / static_cast<int>(sizeof(TL));
+      if (e0 < E) {
+#pragma unroll
+        for (int i = 0; i < NJ / kPer; ++i) {
+          alignas(16) TL v[kPer];
+          if constexpr (kVec == 16)
+            *reinterpret_cast<uint4*>(v) = reinterpret_cast<const uint4*>(row + e0)[i];
+          else if constexpr (kVec == 8)
+            *reinterpret_cast<uint2*>(v) = reinterpret_cast<const uint2*>(row + e0)[i];
+          else
+            *reinterpret_cast<uint32_t*>(v) = reinterpret_cast<const uint32_t*>(row + e0)[i];
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) l[i * kPer + q] = clean_logit(to_float(v[q]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) l[j] = -INFINITY;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    l[j] = e0 + j < E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
+}
+
+// The choice in 64 bits; lane k < K returns the k-th expert or -1.  Only tokens whose float
+// choice could not be certified come here.  m: the row's largest logit (softmax).
+template <int NJ, typename TL, bool kSig>
+__device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float m, int lane) {
+  constexpr double kNone = -INFINITY;
+  double key[NJ];
+  double sum = 0.0;
+  const int e0 = lane * NJ;
+#pragma unroll 1
+  for (int j = 0; j < NJ; ++j) {
+    const float l = e0 + j < p.E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
+    double s = 0.0;
+    if (l > -INFINITY)
+      s = kSig ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
+               : exp(static_cast<double>(l) - static_cast<double>(m));
+    sum += s;
+    key[j] = s;
+  }
+  if (!kSig) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+#pragma unroll 1
+  for (int j = 0; j < NJ; ++j) {
+    const float l = e0 + j < p.E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
+    const float b = e0 + j < p.E && p.bias != nullptr ? p.bias[e0 + j] : 0.f;
+    const double k = (kSig ? key[j] : key[j] / sum) + static_cast<double>(b);
+    key[j] = (l > -INFINITY && b > -INFINITY) ? k : kNone;
+  }
+  // the largest key among the experts that `use` admits, ties to the lower expert, or -1
+  auto best = [&](auto use, double* value) {
+    double kb = kNone;
+    int eb = -1;
+#pragma unroll 1
+    for (int j = 0; j < NJ; ++j)
+      if (use(e0 + j) && key[j] > kb) {
+        kb = key[j];
+        eb = e0 + j;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ko = __shfl_xor_sync(0xffffffffu, kb, o);
+      const int eo = __shfl_xor_sync(0xffffffffu, eb, o);
+      if (eo >= 0 && (eb < 0 || ko > kb || (ko == kb && eo < eb))) {
+        kb = ko;
+        eb = eo;
+      }
+    }
+    *value = kb;
+    return eb;
+  };
+  uint32_t live = 0xffffffffu;
+  if (p.top_groups < p.groups) {
+    double mine = kNone;
+#pragma unroll 1
+    for (int g = 0; g < p.groups; ++g) {
+      const int lo = g * p.per, hi = lo + p.per;
+      double v1, v2 = 0.0;
+      const int a = best([&](int e) { return e >= lo && e < hi; }, &v1);
+      if (a >= 0 && p.rank > 1) {
+        const int b = best([&](int e) { return e >= lo && e < hi && e != a; }, &v2);
+        if (b < 0) v2 = 0.0;
+      }
+      if (lane == g) mine = a >= 0 ? v1 + v2 : kNone;
+    }
+    int better = 0;
+#pragma unroll 1
+    for (int h = 0; h < p.groups; ++h) {
+      const double v = __shfl_sync(0xffffffffu, mine, h);
+      better += (v > mine || (v == mine && h < lane)) ? 1 : 0;
+    }
+    live = __ballot_sync(0xffffffffu, lane < p.groups && better < p.top_groups);
+  }
+  int chosen = -1;
+#pragma unroll 1
+  for (int k = 0; k < p.K; ++k) {
+    double v;
+    const int e = best([&](int c) { return c < p.E && ((live >> (c / p.per)) & 1u); }, &v);
+    if (e < 0) break;
+    if (lane == k) chosen = e;
+    if (e >= e0 && e < e0 + NJ) key[e - e0] = kNone;
+  }
+  return chosen;
+}
+
+// A float score and a bound on its absolute error.  The hardware exponential is off by at
+// most 2 + 1.17 |x| units of 2^-23, the sum of the softmax, the reciprocal and the product by
+// a few more; for the logistic function the error of the exponential shrinks with 1 - s.
+template <bool kSig>
+__device__ __forceinline__ float score_of(float l, float m, float inv_sum, float* err) {
+  if (kSig) {
+    // below -80 the score is under 2e-35, which the bound's floor (see `slack`) covers
+    const float s = l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + __expf(-l));
+    *err = s * 0x1p-20f;
+    return s;
+  }
+  const float x = l - m;
+  const float s = __expf(x) * inv_sum;
+  *err = s * (4.0f - x) * 0x1p-21f;
+  return s;
+}
+constexpr float kErrFloor = 1e-34f;
+
+template <int NJ, typename TL, bool kSig>
+__global__ void __launch_bounds__(32 * kWarps)
+    route_scored_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ float s_key[kWarps][NJ * 32];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= p.T) return;
+  const TL* row = static_cast<const TL*>(p.logits) + static_cast<size_t>(t) * p.stride;
+  const int e0 = lane * NJ;
+  float l[NJ];
+  load_row<NJ, TL>(row, p.E, lane, p.vec, l);
+  const bool has_bias = p.bias != nullptr;
+
+  float m = 0.f, inv_sum = 0.f;
+  if (!kSig) {
+    m = l[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;  // every expert is masked
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) sum += __expf(l[j] - m);
+    inv_sum = 1.0f / warp_sum(sum);
+  }
+
+  // `ord` orders the experts by their keys (0 = not available)
+  const bool grouped = p.top_groups < p.groups;
+  uint32_t ord[NJ];
+  bool unsure = false;
+  if (has_bias || grouped) {
+    float key[NJ];
+    float err_max = kErrFloor;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float b = has_bias && e0 + j < p.E ? __ldg(p.bias + e0 + j) : 0.f;
+      const bool ok = l[j] > -INFINITY && b > -INFINITY;
+      float err;
+      const float k = score_of<kSig>(l[j], m, inv_sum, &err) + b;
+      key[j] = ok ? k : -INFINITY;
+      if (ok) err_max = fmaxf(err_max, err + fabsf(k) * 0x1p-23f);
+      ord[j] = !ok ? 0u : (has_bias ? float_key(k) : float_key(l[j]));
+    }
+    if (grouped) {
+      // the sum of the group's best one or two keys, for group g in lane g
+      float v1 = -INFINITY, v2 = -INFINITY, gs;
+      const int lanes = p.per / NJ;
+      if (p.per % NJ == 0 && (lanes & (lanes - 1)) == 0) {
+        // whole lanes per group: best two of each lane, then of neighbouring lanes
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          v2 = fmaxf(v2, fminf(v1, key[j]));
+          v1 = fmaxf(v1, key[j]);
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+          const float a = __shfl_xor_sync(0xffffffffu, v1, o);
+          const float b = __shfl_xor_sync(0xffffffffu, v2, o);
+          v2 = fmaxf(fmaxf(v2, b), fminf(v1, a));
+          v1 = fmaxf(v1, a);
+        }
+        gs = p.rank > 1 && v2 > -INFINITY ? v1 + v2 : v1;
+        gs = __shfl_sync(0xffffffffu, gs, (lane * lanes) & 31);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s_key[warp][e0 + j] = key[j];
+        __syncwarp();
+        if (lane < p.groups) {
+          for (int i = 0; i < p.per; ++i) {
+            const float k = s_key[warp][lane * p.per + i];
+            v2 = fmaxf(v2, fminf(v1, k));
+            v1 = fmaxf(v1, k);
+          }
+        }
+        gs = p.rank > 1 && v2 > -INFINITY ? v1 + v2 : v1;
+      }
+      if (lane >= p.groups) gs = -INFINITY;
+      int better = 0;
+      for (int h = 0; h < p.groups; ++h) {
+        const float v = __shfl_sync(0xffffffffu, gs, h);
+        better += (v > gs || (v == gs && h < lane)) ? 1 : 0;
+      }
+      const bool in = lane < p.groups && better < p.top_groups;
+      const uint32_t live = __ballot_sync(0xffffffffu, in);
+      const float lowest_in = -warp_max(in ? -gs : -INFINITY);
+      const float best_out = warp_max(in ? -INFINITY : gs);
+      if (best_out > -INFINITY) {
+        // each sum is off by at most two bounds and one rounding
+        const float slack = 4.0f * warp_max(err_max) +
+                            0x1p-23f * (fabsf(lowest_in) + fabsf(best_out));
+        unsure = !(lowest_in - best_out > slack);
+      }
+      int g = e0 / p.per, r = e0 - g * p.per;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
+        if (++r == p.per) {
+          r = 0;
+          ++g;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) ord[j] = l[j] > -INFINITY ? float_key(l[j]) : 0u;
+  }
+
+  // the K best and the one after them; lane k keeps the k-th
+  int mine = -1;
+  for (int k = 0; k <= p.K; ++k) {
+    uint32_t kb = ord[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) kb = max(kb, ord[j]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, kb);
+    if (top == 0u) break;
+    const int win = __ffs(__ballot_sync(0xffffffffu, kb == top)) - 1;
+    int e = 0;
+    if (lane == win) {
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (!found && ord[j] == top) {
+          found = true;
+          ord[j] = 0u;
+          e = e0 + j;
+        }
+      }
+    }
+    e = __shfl_sync(0xffffffffu, e, win);
+    if (lane == k) mine = e;
+  }
+
+  // certify: neighbouring choices must be further apart than their bounds
+  float my_l = -INFINITY, my_s = 0.f, my_err = 0.f, my_b = 0.f;
+  if (mine >= 0) {
+    my_l = clean_logit(to_float(row[mine]));
+    my_b = has_bias ? __ldg(p.bias + mine) : 0.f;
+    my_s = score_of<kSig>(my_l, m, inv_sum, &my_err);
+  }
+  const float my_k = my_s + my_b;
+  const int next = __shfl_down_sync(0xffffffffu, mine, 1);
+  const float next_l = __shfl_down_sync(0xffffffffu, my_l, 1);
+  const float next_b = __shfl_down_sync(0xffffffffu, my_b, 1);
+  const float next_k = __shfl_down_sync(0xffffffffu, my_k, 1);
+  const float next_err = __shfl_down_sync(0xffffffffu, my_err, 1);
+  if (lane < p.K && mine >= 0 && next >= 0 && !(my_l == next_l && my_b == next_b)) {
+    if (has_bias) {
+      const float slack =
+          my_err + next_err + 2.0f * kErrFloor + 0x1p-23f * (fabsf(my_k) + fabsf(next_k));
+      unsure |= !(my_k - next_k > slack);
+    } else if (kSig) {
+      // d s = s (1 - s) d l: below a few 2^-53 of s the 64-bit scores may round together
+      unsure |= my_l > 80.f || next_l < -600.f ||
+                !(__fdividef(my_l - next_l, 1.0f + __expf(my_l)) > 1e-14f);
+    } else {
+      unsure |= !(my_l - next_l > 1e-14f) || next_l - m < -600.f;
+    }
+  }
+  if (__any_sync(0xffffffffu, unsure)) mine = choose64<NJ, TL, kSig>(p, row, m, lane);
+  if (lane >= p.K) mine = -1;
+
+  // weights from the unbiased scores
+  const float kl = mine >= 0 ? clean_logit(to_float(row[mine])) : -INFINITY;
+  float s = 0.f;
+  if (p.renorm) {
+    const float top = warp_max(kl);
+    // far below zero the logistic function is exp(l); the common factor cancels
+    if (mine >= 0) s = (kSig && top > -60.f) ? 1.0f / (1.0f + expf(-kl)) : expf(kl - top);
+    const float total = warp_sum(s);
+    s = mine >= 0 ? s / total : 0.f;
+  } else if (mine >= 0) {
+    s = kSig ? 1.0f / (1.0f + expf(-kl)) : expf(kl - m) * inv_sum;
+  }
+  if (lane < p.K) {
+    const size_t at = static_cast<size_t>(t) * p.K + lane;
+    p.ids[at] = mine;
+    p.w[at] = s * p.scale;
+  }
+}
+
+// The gradient, one warp per token.  Only a softmax without renormalisation reaches every
+// expert; in the other cases the gradient is zero off the K chosen experts (with
+// renormalisation the softmax's own sum cancels), so K logits are gathered, the row is put
+// together in shared memory and written once.  Bound by the write of T*E elements.
+template <int NJ, typename TL, bool kSig>
+__global__ void __launch_bounds__(32 * kWarps)
+    route_scored_grad_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ __align__(16) float s_row[kWarps][NJ * 32];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= p.T) return;
+  const TL* row = static_cast<const TL*>(p.logits) + static_cast<size_t>(t) * p.stride;
+  TL* out = static_cast<TL*>(p.d_logits) + static_cast<size_t>(t) * p.stride;
+  float* sr = s_row[warp];
+
+  int id = -1;
+  float dw = 0.f, kl = -INFINITY;
+  if (lane < p.K) {
+    const size_t at = static_cast<size_t>(t) * p.K + lane;
+    id = p.ids_in[at];
+    if (id < 0 || id >= p.E) id = -1;
+    if (id >= 0) kl = clean_logit(to_float(row[id]));
+    if (kl == -INFINITY) id = -1;
+    if (id >= 0) dw = p.scale * p.d_w[at];
+  }
+  if (!kSig && !p.renorm) {
+    const int e0 = lane * NJ;
+    float l[NJ];
+    load_row<NJ, TL>(row, p.E, lane, p.vec, l);
+    float m = l[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      l[j] = expf(l[j] - m);
+      sum += l[j];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const float sk = id >= 0 ? expf(kl - m) * inv : 0.f;
+    const float dot = warp_sum(dw * sk);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) sr[e0 + j] = -l[j] * inv * dot;
+    __syncwarp();
+    if (id >= 0) sr[id] = sk * (dw - dot);
+  } else {
+    float d = 0.f;
+    if (p.renorm) {
+      const float top = warp_max(kl);
+      float s = 0.f;
+      if (id >= 0) s = (kSig && top > -60.f) ? 1.0f / (1.0f + expf(-kl)) : expf(kl - top);
+      const float total = warp_sum(s);
+      const float rho = id >= 0 ? s / total : 0.f;
+      const float dot = warp_sum(dw * rho);
+      d = (dw - dot) * rho;
+    } else if (id >= 0) {
+      d = dw / (1.0f + expf(-kl));
+    }
+    if (kSig) d /= 1.0f + expf(kl);  // 1 - s
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) sr[lane + 32 * j] = 0.f;
+    __syncwarp();
+    if (id >= 0) sr[id] = d;
+  }
+  __syncwarp();
+  if (p.vec) {
+    constexpr int kPer = 16 / static_cast<int>(sizeof(TL));
+    for (int c = lane * kPer; c < p.E; c += 32 * kPer) {
+      alignas(16) TL v[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; q += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(sr + c + q);
+        v[q] = from_float<TL>(f.x);
+        v[q + 1] = from_float<TL>(f.y);
+        v[q + 2] = from_float<TL>(f.z);
+        v[q + 3] = from_float<TL>(f.w);
+      }
+      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(v);
+    }
+  } else {
+    for (int c = lane; c < p.E; c += 32) out[c] = from_float<TL>(sr[c]);
+  }
+}
+
+template <int NJ, typename TL, bool kGrad>
+cudaError_t launch_typed(bool sigmoid, const RouteParams& p, cudaStream_t s) {
+  const dim3 grid((static_cast<unsigned>(p.T) + kWarps - 1) / kWarps), block(32 * kWarps);
+  if constexpr (kGrad)
+    return sigmoid ? launch_pdl(route_scored_grad_kernel<NJ, TL, true>, grid, block, 0, s, p)
+                   : launch_pdl(route_scored_grad_kernel<NJ, TL, false>, grid, block, 0, s, p);
+  else
+    return sigmoid ? launch_pdl(route_scored_kernel<NJ, TL, true>, grid, block, 0, s, p)
+                   : launch_pdl(route_scored_kernel<NJ, TL, false>, grid, block, 0, s, p);
+}
+
+template <bool kGrad>
+cudaError_t launch_route(const moe_route_config_t& c, RouteParams p, cudaStream_t s) {
+  const int nj = (c.E + 31) / 32;
+  const int NJ = nj <= 1 ? 1 : nj <= 2 ? 2 : nj <= 4 ? 4 : nj <= 8 ? 8 : nj <= 16 ? 16 : 32;
+  // whole-lane vector loads (and the gradient's 16-byte stores): rows on 16-byte boundaries,
+  // no lane or vector half inside the row
+  const int eb = static_cast<int>(act_bytes(c.dtype));
+  const int q = kGrad && 16 / eb > NJ ? 16 / eb : NJ;
+  p.vec = c.E % q == 0 && (p.stride * eb) % 16 == 0 &&
+          (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 &&
+          (reinterpret_cast<uintptr_t>(p.d_logits) & 15u) == 0;
+  const bool sig = c.score == MOE_SCORE_SIGMOID;
+  auto go = [&](auto nj_c) {
+    constexpr int N = decltype(nj_c)::value;
+    return c.dtype == MOE_BF16 ? launch_typed<N, __nv_bfloat16, kGrad>(sig, p, s)
+                               : launch_typed<N, float, kGrad>(sig, p, s);
+  };
+  switch (NJ) {
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 8: return go(std::integral_constant<int, 8>{});
+    case 16: return go(std::integral_constant<int, 16>{});
+    default: return go(std::integral_constant<int, 32>{});
+  }
+}
+
+moe_status_t check_route_config(const moe_route_config_t* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (c->renormalise != 0 && c->renormalise != 1) return MOE_ERR_INVALID_ARG;
+  if (c->T < 0 || c->E <= 0 || c->E > 1024 || c->K <= 0 || c->K > 16) return MOE_ERR_INVALID_ARG;
+  if (c->groups <= 0 || c->groups > 32 || c->E % c->groups != 0) return MOE_ERR_INVALID_ARG;
+  if (c->top_groups <= 0 || c->top_groups > c->groups) return MOE_ERR_INVALID_ARG;
+  if (c->group_rank != 1 && c->group_rank != 2) return MOE_ERR_INVALID_ARG;
+  if (c->K > c->top_groups * (c->E / c->groups)) return MOE_ERR_INVALID_ARG;
+  if (!(c->scale > 0.0f && c->scale <= FLT_MAX)) return MOE_ERR_INVALID_ARG;
+  if (c->logits_stride != 0 && (c->logits_stride < c->E || c->logits_stride > (1ll << 31)))
+    return MOE_ERR_INVALID_ARG;
+  if (static_cast<long long>(c->T) * c->K >= (1ll << 31)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+inline bool unaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+RouteParams base_params(const moe_route_config_t* c, const void* logits) {
+  RouteParams p{};
+  p.logits = logits;
+  p.stride = c->logits_stride != 0 ? c->logits_stride : c->E;
+  p.T = c->T;
+  p.E = c->E;
+  p.K = c->K;
+  p.groups = c->groups;
+  p.per = c->E / c->groups;
+  p.top_groups = c->top_groups;
+  p.rank = c->group_rank;
+  p.renorm = c->renormalise;
+  p.scale = c->scale;
+  return p;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_route_scored(const moe_route_config_t* cfg, const void* logits,
+                                         const float* expert_bias, int32_t* topk_ids,
+                                         float* topk_w, moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_route_scored");
+  if (st != MOE_OK) return st;
+  st = check_route_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
+  if (unaligned(logits, act_bytes(cfg->dtype)) || unaligned(expert_bias, 4) ||
+      unaligned(topk_ids, 4) || unaligned(topk_w, 4))
+    return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  RouteParams p = base_params(cfg, logits);
+  p.bias = expert_bias;
+  p.ids = topk_ids;
+  p.w = topk_w;
+  const cudaError_t e = launch_route<false>(*cfg, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status_t moe_route_scored_backward(const moe_route_config_t* cfg,
+                                                  const void* logits, const int32_t* topk_ids,
+                                                  const float* d_topk_w, void* d_logits,
+                                                  moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_route_scored_backward");
+  if (st != MOE_OK) return st;
+  st = check_route_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (logits == nullptr || topk_ids == nullptr || d_topk_w == nullptr || d_logits == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (unaligned(logits, act_bytes(cfg->dtype)) || unaligned(topk_ids, 4) ||
+      unaligned(d_topk_w, 4) || unaligned(d_logits, act_bytes(cfg->dtype)))
+    return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  RouteParams p = base_params(cfg, logits);
+  p.ids_in = topk_ids;
+  p.d_w = d_topk_w;
+  p.d_logits = d_logits;
+  const cudaError_t e = launch_route<true>(*cfg, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
