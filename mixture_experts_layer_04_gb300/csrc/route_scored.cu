@@ -5,12 +5,14 @@
 // a group whose size is a multiple of NJ never straddles lanes.
 //
 // The choice.  It is defined on 64-bit keys s[e] + bias[e], and 64-bit arithmetic is slow on
-// this GPU, so it is taken in float first and certified: every float score carries a bound on
-// its error, and the token is chosen again in 64 bits only if two neighbouring choices (the
-// K-th and the first one left out among them), or the last group kept and the best one
-// dropped, lie within the sum of their bounds.  Without a bias the keys are ordered as the
-// logits are, so the logits themselves are compared, exactly.  Two experts of equal logit and
-// equal bias tie in any precision and need no second look.
+// this GPU (16 clocks per warp instruction), so it is taken in float first and certified:
+// every float score carries a bound on its error.  Neighbouring choices (the K-th and the
+// first one left out among them) closer than the sum of their bounds are put in order by
+// their 64-bit keys, K+1 lanes at once; the groups are chosen again in 64 bits if the last
+// one kept and the best one dropped are that close; and only if the first two experts left
+// out are close to the last one kept is the whole token chosen again.  Without a bias the
+// keys are ordered as the logits are, so the logits themselves are compared, exactly.  Two
+// experts of equal logit and equal bias tie in any precision and need no second look.
 //
 // What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
 // written; the work is K+1 warp-wide maxima per token, so at prefill sizes it is bound by
@@ -100,34 +102,43 @@ __device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec
     l[j] = e0 + j < E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
 }
 
-// The choice in 64 bits; lane k < K returns the k-th expert or -1.  Only tokens whose float
-// choice could not be certified come here.  m: the row's largest logit (softmax).
-template <int NJ, typename TL, bool kSig>
-__device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float m, int lane) {
-  constexpr double kNone = -INFINITY;
-  double key[NJ];
+// The 64-bit score of a logit, and what it needs of its row: the softmax's sum.
+template <bool kSig>
+__device__ __forceinline__ double score64(float l, float m, double sum) {
+  if (!(l > -INFINITY)) return 0.0;
+  return kSig ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
+              : exp(static_cast<double>(l) - static_cast<double>(m)) / sum;
+}
+template <int NJ, typename TL>
+__device__ __forceinline__ double softmax_sum64(const TL* row, int E, float m, int lane) {
   double sum = 0.0;
-  const int e0 = lane * NJ;
 #pragma unroll 1
   for (int j = 0; j < NJ; ++j) {
-    const float l = e0 + j < p.E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
-    double s = 0.0;
-    if (l > -INFINITY)
-      s = kSig ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
-               : exp(static_cast<double>(l) - static_cast<double>(m));
-    sum += s;
-    key[j] = s;
+    const int e = lane * NJ + j;
+    const float l = e < E ? clean_logit(to_float(row[e])) : -INFINITY;
+    if (l > -INFINITY) sum += exp(static_cast<double>(l) - static_cast<double>(m));
   }
-  if (!kSig) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The groups (`live` == nullptr: returns their mask) or, with the groups given, the choice
+// (lane k < K returns the k-th expert or -1) from 64-bit keys throughout.  Few tokens come
+// here.  m: the row's largest logit (softmax).
+template <int NJ, typename TL, bool kSig>
+__device__ __noinline__ uint32_t choose64(const RouteParams& p, const TL* row, float m, int lane,
+                                          const uint32_t* live) {
+  constexpr double kNone = -INFINITY;
+  double key[NJ];
+  const int e0 = lane * NJ;
+  const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
 #pragma unroll 1
   for (int j = 0; j < NJ; ++j) {
     const float l = e0 + j < p.E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
     const float b = e0 + j < p.E && p.bias != nullptr ? p.bias[e0 + j] : 0.f;
-    const double k = (kSig ? key[j] : key[j] / sum) + static_cast<double>(b);
-    key[j] = (l > -INFINITY && b > -INFINITY) ? k : kNone;
+    key[j] = (l > -INFINITY && b > -INFINITY) ? score64<kSig>(l, m, sum) + static_cast<double>(b)
+                                              : kNone;
   }
   // the largest key among the experts that `use` admits, ties to the lower expert, or -1
   auto best = [&](auto use, double* value) {
@@ -151,8 +162,7 @@ __device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float 
     *value = kb;
     return eb;
   };
-  uint32_t live = 0xffffffffu;
-  if (p.top_groups < p.groups) {
+  if (live == nullptr) {
     double mine = kNone;
 #pragma unroll 1
     for (int g = 0; g < p.groups; ++g) {
@@ -171,37 +181,81 @@ __device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float 
       const double v = __shfl_sync(0xffffffffu, mine, h);
       better += (v > mine || (v == mine && h < lane)) ? 1 : 0;
     }
-    live = __ballot_sync(0xffffffffu, lane < p.groups && better < p.top_groups);
+    return __ballot_sync(0xffffffffu, lane < p.groups && better < p.top_groups);
   }
   int chosen = -1;
 #pragma unroll 1
   for (int k = 0; k < p.K; ++k) {
     double v;
-    const int e = best([&](int c) { return c < p.E && ((live >> (c / p.per)) & 1u); }, &v);
+    const int e = best([&](int c) { return c < p.E && ((*live >> (c / p.per)) & 1u); }, &v);
     if (e < 0) break;
     if (lane == k) chosen = e;
     if (e >= e0 && e < e0 + NJ) key[e - e0] = kNone;
   }
-  return chosen;
+  return static_cast<uint32_t>(chosen);
 }
 
-// A float score and a bound on its absolute error.  The hardware exponential is off by at
-// most 2 + 1.17 |x| units of 2^-23, the sum of the softmax, the reciprocal and the product by
-// a few more; for the logistic function the error of the exponential shrinks with 1 - s.
+// Puts the experts in lanes 0..K (-1 from the first empty lane on) in the order of their
+// 64-bit keys, ties to the lower expert.
+template <int NJ, typename TL, bool kSig>
+__device__ __noinline__ int order64(const RouteParams& p, const TL* row, float m, int lane,
+                                    int mine, float l, float b) {
+  const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
+  const double key = score64<kSig>(l, m, sum) + static_cast<double>(b);
+  const int n = __popc(__ballot_sync(0xffffffffu, mine >= 0));
+  int rank = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const double kj = __shfl_sync(0xffffffffu, key, j);
+    const int ej = __shfl_sync(0xffffffffu, mine, j);
+    rank += (kj > key || (kj == key && ej < mine)) ? 1 : 0;
+  }
+  int out = -1;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int rj = __shfl_sync(0xffffffffu, rank, j);
+    const int ej = __shfl_sync(0xffffffffu, mine, j);
+    if (lane == rj) out = ej;
+  }
+  return out;
+}
+
+// A float score and a bound on its absolute error.  expf is off by at most 2 units in the last
+// place (2^-22 relative) on top of the rounding of its argument (|x| 2^-24), the sum of the
+// softmax, the reciprocal and the product by a few more; for the logistic function the error
+// of the exponential shrinks with 1 - s.
 template <bool kSig>
 __device__ __forceinline__ float score_of(float l, float m, float inv_sum, float* err) {
   if (kSig) {
-    // below -80 the score is under 2e-35, which the bound's floor (see `slack`) covers
-    const float s = l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + __expf(-l));
-    *err = s * 0x1p-20f;
+    // below -80 the score is under 2e-35, which the bound's floor covers
+    const float s = l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + expf(-l));
+    *err = s * 0x1p-21f;
     return s;
   }
   const float x = l - m;
-  const float s = __expf(x) * inv_sum;
-  *err = s * (4.0f - x) * 0x1p-21f;
+  const float s = expf(x) * inv_sum;
+  *err = s * (8.0f - x) * 0x1p-23f;
   return s;
 }
 constexpr float kErrFloor = 1e-34f;
+
+// One chosen (or next best) expert as a lane holds it.
+struct Pick {
+  float l, b, key, err;
+};
+
+// Whether the order of two picks, a before b, is open to doubt in float.
+template <bool kSig>
+__device__ __forceinline__ bool in_doubt(const Pick& a, const Pick& b, bool has_bias, float m) {
+  if (a.l == b.l && a.b == b.b) return false;  // a tie in any precision
+  if (has_bias)
+    return !(a.key - b.key >
+             a.err + b.err + 2.0f * kErrFloor + 0x1p-23f * (fabsf(a.key) + fabsf(b.key)));
+  // no bias: a.l > b.l, but a few 2^-53 of the score apart the 64-bit scores may round together
+  if (kSig)
+    return a.l > 80.f || b.l < -600.f || !(__fdividef(a.l - b.l, 1.0f + __expf(a.l)) > 1e-14f);
+  return !(a.l - b.l > 1e-14f) || b.l - m < -600.f;
+}
 
 template <int NJ, typename TL, bool kSig>
 __global__ void __launch_bounds__(32 * kWarps)
@@ -227,14 +281,14 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (m == -INFINITY) m = 0.f;  // every expert is masked
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) sum += __expf(l[j] - m);
+    for (int j = 0; j < NJ; ++j) sum += expf(l[j] - m);
     inv_sum = 1.0f / warp_sum(sum);
   }
 
   // `ord` orders the experts by their keys (0 = not available)
   const bool grouped = p.top_groups < p.groups;
   uint32_t ord[NJ];
-  bool unsure = false;
+  uint32_t live = 0xffffffffu;  // groups in play
   if (has_bias || grouped) {
     float key[NJ];
     float err_max = kErrFloor;
@@ -287,14 +341,15 @@ __global__ void __launch_bounds__(32 * kWarps)
         better += (v > gs || (v == gs && h < lane)) ? 1 : 0;
       }
       const bool in = lane < p.groups && better < p.top_groups;
-      const uint32_t live = __ballot_sync(0xffffffffu, in);
+      live = __ballot_sync(0xffffffffu, in);
       const float lowest_in = -warp_max(in ? -gs : -INFINITY);
       const float best_out = warp_max(in ? -INFINITY : gs);
       if (best_out > -INFINITY) {
         // each sum is off by at most two bounds and one rounding
         const float slack = 4.0f * warp_max(err_max) +
                             0x1p-23f * (fabsf(lowest_in) + fabsf(best_out));
-        unsure = !(lowest_in - best_out > slack);
+        if (!(lowest_in - best_out > slack))
+          live = choose64<NJ, TL, kSig>(p, row, m, lane, nullptr);
       }
       int g = e0 / p.per, r = e0 - g * p.per;
 #pragma unroll
@@ -311,14 +366,13 @@ __global__ void __launch_bounds__(32 * kWarps)
     for (int j = 0; j < NJ; ++j) ord[j] = l[j] > -INFINITY ? float_key(l[j]) : 0u;
   }
 
-  // the K best and the one after them; lane k keeps the k-th
-  int mine = -1;
-  for (int k = 0; k <= p.K; ++k) {
+  // takes the best expert still in play (uniform over the warp), or -1
+  auto take_best = [&]() {
     uint32_t kb = ord[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) kb = max(kb, ord[j]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, kb);
-    if (top == 0u) break;
+    if (top == 0u) return -1;
     const int win = __ffs(__ballot_sync(0xffffffffu, kb == top)) - 1;
     int e = 0;
     if (lane == win) {
@@ -332,37 +386,44 @@ __global__ void __launch_bounds__(32 * kWarps)
         }
       }
     }
-    e = __shfl_sync(0xffffffffu, e, win);
+    return __shfl_sync(0xffffffffu, e, win);
+  };
+  auto pick_of = [&](int e) {
+    Pick q{-INFINITY, 0.f, 0.f, 0.f};
+    if (e >= 0) {
+      q.l = clean_logit(to_float(row[e]));
+      q.b = has_bias ? __ldg(p.bias + e) : 0.f;
+      q.key = score_of<kSig>(q.l, m, inv_sum, &q.err) + q.b;
+    }
+    return q;
+  };
+
+  // the K best and the one after them; lane k keeps the k-th
+  int mine = -1;
+  for (int k = 0; k <= p.K; ++k) {
+    const int e = take_best();
+    if (e < 0) break;
     if (lane == k) mine = e;
   }
 
-  // certify: neighbouring choices must be further apart than their bounds
-  float my_l = -INFINITY, my_s = 0.f, my_err = 0.f, my_b = 0.f;
-  if (mine >= 0) {
-    my_l = clean_logit(to_float(row[mine]));
-    my_b = has_bias ? __ldg(p.bias + mine) : 0.f;
-    my_s = score_of<kSig>(my_l, m, inv_sum, &my_err);
-  }
-  const float my_k = my_s + my_b;
-  const int next = __shfl_down_sync(0xffffffffu, mine, 1);
-  const float next_l = __shfl_down_sync(0xffffffffu, my_l, 1);
-  const float next_b = __shfl_down_sync(0xffffffffu, my_b, 1);
-  const float next_k = __shfl_down_sync(0xffffffffu, my_k, 1);
-  const float next_err = __shfl_down_sync(0xffffffffu, my_err, 1);
-  if (lane < p.K && mine >= 0 && next >= 0 && !(my_l == next_l && my_b == next_b)) {
-    if (has_bias) {
-      const float slack =
-          my_err + next_err + 2.0f * kErrFloor + 0x1p-23f * (fabsf(my_k) + fabsf(next_k));
-      unsure |= !(my_k - next_k > slack);
-    } else if (kSig) {
-      // d s = s (1 - s) d l: below a few 2^-53 of s the 64-bit scores may round together
-      unsure |= my_l > 80.f || next_l < -600.f ||
-                !(__fdividef(my_l - next_l, 1.0f + __expf(my_l)) > 1e-14f);
-    } else {
-      unsure |= !(my_l - next_l > 1e-14f) || next_l - m < -600.f;
+  // certify the order of neighbours
+  const Pick me = pick_of(mine);
+  const Pick next{__shfl_down_sync(0xffffffffu, me.l, 1), __shfl_down_sync(0xffffffffu, me.b, 1),
+                  __shfl_down_sync(0xffffffffu, me.key, 1),
+                  __shfl_down_sync(0xffffffffu, me.err, 1)};
+  const int next_e = __shfl_down_sync(0xffffffffu, mine, 1);
+  const uint32_t doubts = __ballot_sync(
+      0xffffffffu, lane < p.K && next_e >= 0 && in_doubt<kSig>(me, next, has_bias, m));
+  if (doubts != 0u) {
+    bool whole = false;
+    if ((doubts >> (p.K - 1)) & 1u) {  // the last one kept and the first one left out
+      const int second = take_best();
+      const Pick q = pick_of(second);
+      whole = __shfl_sync(0xffffffffu, second >= 0 && in_doubt<kSig>(me, q, has_bias, m), p.K);
     }
+    mine = whole ? static_cast<int>(choose64<NJ, TL, kSig>(p, row, m, lane, &live))
+                 : order64<NJ, TL, kSig>(p, row, m, lane, mine, me.l, me.b);
   }
-  if (__any_sync(0xffffffffu, unsure)) mine = choose64<NJ, TL, kSig>(p, row, m, lane);
   if (lane >= p.K) mine = -1;
 
   // weights from the unbiased scores
