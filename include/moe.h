@@ -393,6 +393,64 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* dy, const
                                   const int32_t* inv, const float* topk_w, void* d_out_perm,
                                   float* d_topk_w, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Linear layers that stand next to an MoE layer (router logits, an attention output
+ * projection with its residual, dense feed-forward layers): the matrix product with bias,
+ * activation and residual in its epilogue, and its gradients. */
+
+/* moe_linear_config_t.activation.  GELU: z Phi(z) with the error function; GELU_TANH: its
+ * tanh form z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; SILU: z / (1 + exp(-z)). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_GELU_TANH = 3,
+  MOE_ACT_SILU = 4
+} moe_activation_t;
+
+typedef struct {
+  int32_t rows;            /* tokens, 0..2^30 */
+  int32_t in_features;     /* 1..2^20 */
+  int32_t out_features;    /* 1..2^20 */
+  int32_t dtype;           /* moe_dtype_t of x, w, residual, z, dx and dw ("act") */
+  int32_t out_dtype;       /* moe_dtype_t of y and dy: dtype, or MOE_F32 */
+  int32_t activation;      /* moe_activation_t */
+  /* elements between rows, 0 = contiguous */
+  int64_t x_stride, w_stride, residual_stride, y_stride, z_stride, dx_stride, dw_stride;
+} moe_linear_config_t;
+
+/* Bytes of device workspace that moe_linear and moe_linear_backward need for `cfg` (the
+ * larger of the two; 0 is possible).  Scratch, as moe_workspace_size's. */
+moe_status_t moe_linear_workspace_size(const moe_linear_config_t* cfg, size_t* bytes);
+
+/* y = act(x w^T + bias) + residual, accumulated in fp32, each output rounded once.
+ *   x [rows,in] act; w [out,in] act; bias [out] float or NULL; residual [rows,out] act or
+ *   NULL; y [rows,out] out_dtype out; z [rows,out] act out or NULL: the value before the
+ *   activation, which the backward needs (y is computed from the unrounded value).
+ *   ws: moe_linear_workspace_size() bytes, 16-byte aligned (NULL when that is 0).
+ * y may be residual itself (same type and stride).  Pointers need the alignment of their
+ * elements; x and w, whose row stride is a multiple of 16 bytes, must start on a 16-byte
+ * boundary (MOE_ERR_MISALIGNED; other strides are copied into the workspace first).
+ * Float32 products run on the tensor cores as three bf16 parts per value, with the partial
+ * sums added in fp32 registers every 128 values; where an input is infinite or NaN
+ * the outputs that it reaches are not finite.  More rows than 8 run on the tensor cores, up
+ * to 8 on the CUDA cores, where the weights' read is what counts. */
+moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x, const void* w,
+                        const float* bias, const void* residual, void* y, void* z, void* ws,
+                        size_t ws_bytes, moe_stream_t stream);
+
+/* The gradients of moe_linear: with dz = dy * act'(z),
+ *   dx = dz w;  dw = dz^T x;  dbias = the column sums of dz;  (d residual is dy).
+ *   dy [rows,out] out_dtype (row stride y_stride); x, w as given to moe_linear; z as it
+ *   returned it (NULL without an activation); dx [rows,in] act out or NULL; dw [out,in] act
+ *   out or NULL; dbias [out] float out or NULL; ws as for moe_linear.
+ * dz is rounded to act before the products (the operand type of the tensor cores); dbias
+ * sums it unrounded.  x may be NULL when dw is, w when dx is.  dy keeps to the rule on 16
+ * bytes that x and w have.  With rows == 0, dw and dbias are zeroed. */
+moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, const void* dy, const void* x,
+                                 const void* w, const void* z, void* dx, void* dw, float* dbias,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Intermediates of the last moe_layer_forward that used `ws` (views into ws; valid
  * until ws is reused).  Any output pointer may be NULL.  Useful to check every stage.
  * x_perm is not written by decode-sized bf16 layers (T <= 16, E <= 256, K <= 16), whose

@@ -19,7 +19,8 @@ __all__ = [
     "MoEConfig", "MoEError", "F32", "BF16", "FLAG_FUSED_COMBINE", "FLAG_CAPACITY", "FLAG_FP8", "library_path", "load", "workspace_size",
     "route", "permute", "permute_noalloc", "grouped_ffn", "expert_gate_up", "expert_gate_up_gather", "quantize_fp8", "expert_gate_up_fp8", "expert_down_fp8", "layer_forward_fp8", "expert_down", "combine", "layer_forward", "workspace_views",
     "RouteConfig", "SCORE_SOFTMAX", "SCORE_SIGMOID", "route_scored", "route_scored_backward",
-    "combine_backward",
+    "combine_backward", "LinearConfig", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH",
+    "ACT_SILU", "linear_workspace_size", "linear", "linear_backward",
     "sync_check", "debug_wait_timeout", "status_string", "version",
 ]
 
@@ -33,6 +34,12 @@ FLAG_FP8 = 4
 # moe_route_config_t.score
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
+# moe_linear_config_t.activation
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
 
 _STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -89,6 +96,34 @@ class RouteConfig(ctypes.Structure):
                 f"dtype={self.dtype})")
 
 
+class LinearConfig(ctypes.Structure):
+    """moe_linear_config_t: rows, in_features, out_features, dtype, out_dtype, activation and
+    the row strides in elements (0 = contiguous)."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("dw_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, rows, in_features, out_features, dtype=BF16, out_dtype=None,
+             activation=ACT_NONE, x_stride=0, w_stride=0, residual_stride=0, y_stride=0,
+             z_stride=0, dx_stride=0, dw_stride=0):
+        return cls(rows, in_features, out_features, dtype,
+                   dtype if out_dtype is None else out_dtype, activation, x_stride, w_stride,
+                   residual_stride, y_stride, z_stride, dx_stride, dw_stride)
+
+    def __repr__(self):
+        return (f"LinearConfig(rows={self.rows}, in_features={self.in_features}, "
+                f"out_features={self.out_features}, dtype={self.dtype}, "
+                f"out_dtype={self.out_dtype}, activation={self.activation})")
+
+
 def library_path(debug: bool = False) -> str:
     """The release library, or with ``debug`` the bounds-checking build (-DMOE_DEBUG)."""
     return os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -100,6 +135,7 @@ _LIB: Optional[ctypes.CDLL] = None
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoEConfig)
 _RCFG = ctypes.POINTER(RouteConfig)
+_LCFG = ctypes.POINTER(LinearConfig)
 _SIGS = {
     "moe_workspace_size": [_CFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_route": [_CFG, _P, _P, _P, _P, _P, _P, _P],
@@ -120,6 +156,9 @@ _SIGS = {
     "moe_route_scored": [_RCFG, _P, _P, _P, _P, _P],
     "moe_route_scored_backward": [_RCFG, _P, _P, _P, _P, _P],
     "moe_combine_backward": [_CFG, _P, _P, _P, _P, _P, _P, _P],
+    "moe_linear_workspace_size": [_LCFG, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_linear": [_LCFG, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_linear_backward": [_LCFG, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_sync_check": [_P],
     "moe_debug_wait_timeout": [ctypes.c_uint, _P, _P],
     "moe_status_string": [ctypes.c_int],
@@ -330,6 +369,34 @@ def combine_backward(cfg, dy, out_perm, inv, topk_w, d_out_perm, d_topk_w, strea
     _check(load().moe_combine_backward(ctypes.byref(cfg), _ptr(dy), _ptr(out_perm), _ptr(inv),
                                        _ptr(topk_w), _ptr(d_out_perm), _ptr(d_topk_w),
                                        _stream(stream)), "moe_combine_backward")
+
+
+def linear_workspace_size(cfg: LinearConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_linear_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_linear_workspace_size")
+    return n.value
+
+
+def _ws(ws, ws_bytes):
+    if ws_bytes is not None:
+        return ws_bytes
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def linear(cfg, x, w, bias, residual, y, z=None, ws=None, ws_bytes=None, stream=None):
+    """y = act(x w^T + bias) + residual; z (optional) receives the value before act."""
+    _check(load().moe_linear(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                             _ptr(y), _ptr(z), _ptr(ws), _ws(ws, ws_bytes), _stream(stream)),
+           "moe_linear")
+
+
+def linear_backward(cfg, dy, x, w, z, dx, dw, dbias, ws=None, ws_bytes=None, stream=None):
+    """dx, dw and dbias (each may be None) of linear; z is what linear stored."""
+    _check(load().moe_linear_backward(ctypes.byref(cfg), _ptr(dy), _ptr(x), _ptr(w), _ptr(z),
+                                      _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws),
+                                      _ws(ws, ws_bytes), _stream(stream)),
+           "moe_linear_backward")
 
 
 def workspace_views(cfg, ws) -> dict:

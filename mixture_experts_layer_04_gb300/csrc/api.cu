@@ -465,6 +465,7 @@ const char* const kFaultPoints[] = {
     "moe_expert_gate_up_fp8",  "moe_expert_down_fp8",       "moe_combine",
     "moe_layer_forward",       "moe_layer_forward_fp8",     "moe_sync_check",
     "moe_route_scored",        "moe_route_scored_backward", "moe_combine_backward",
+    "moe_linear",              "moe_linear_backward",       "moe_linear_workspace_size",
     "moe_layer_forward.route", "moe_layer_forward.permute", "moe_layer_forward.gate_up",
     "moe_layer_forward.shared", "moe_layer_forward.down",   "moe_layer_forward.combine"};
 

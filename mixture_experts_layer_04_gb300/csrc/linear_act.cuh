@@ -1,0 +1,97 @@
+// Activations of the linear layers and their derivatives, in fp32.
+//
+// kFast forms serve results that are rounded to bf16 (2^-8): the hardware exponential, the
+// approximate division and, for the normal distribution function, the rational approximation
+// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions (absolute error under
+// 7e-8 here), whose exponential the derivative shares.
+#pragma once
+
+#include "../../include/moe.h"
+#include "common.cuh"
+
+namespace moe {
+
+// Phi(z) for kFast; *e = exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf_fast(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  float poly = fmaf(t, 1.061405429f, -1.453152027f);
+  poly = fmaf(t, poly, 1.421413741f);
+  poly = fmaf(t, poly, -0.284496736f);
+  poly = fmaf(t, poly, 0.254829592f);
+  *e = __expf(-0.5f * z * z);
+  const float tail = 0.5f * t * poly * *e;  // Phi(-|z|)
+  return z < 0.f ? tail : 1.0f - tail;
+}
+
+// y = act(z).
+template <bool kFast>
+__device__ __forceinline__ float act_value(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU:
+      return z > 0.f ? z : (z != z ? z : 0.f);
+    case MOE_ACT_GELU: {
+      if (kFast) {
+        float e;
+        return z * normal_cdf_fast(z, &e);
+      }
+      return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    }
+    case MOE_ACT_GELU_TANH: {
+      // (1 + tanh u) / 2 is the logistic function of 2u
+      const float u2 = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
+      return kFast ? __fdividef(z, 1.0f + __expf(-u2)) : z / (1.0f + expf(-u2));
+    }
+    case MOE_ACT_SILU:
+      return kFast ? silu_bf16out(z) : silu_f(z);
+    default:
+      return z;
+  }
+}
+
+// d act / d z (ReLU: 0 at 0).
+template <bool kFast>
+__device__ __forceinline__ float act_slope(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU:
+      return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_GELU: {
+      if (kFast) {
+        float e;
+        const float cdf = normal_cdf_fast(z, &e);
+        return fmaf(z * 0.39894228f, e, cdf);
+      }
+      return 0.5f * erfcf(-0.70710678118654752f * z) +
+             z * 0.3989422804014327f * expf(-0.5f * z * z);
+    }
+    case MOE_ACT_GELU_TANH: {
+      constexpr float c = 1.5957691216057308f;
+      const float z2 = z * z;
+      const float u2 = c * fmaf(0.044715f * z2, z, z);
+      const float p = kFast ? __fdividef(1.0f, 1.0f + __expf(-u2)) : 1.0f / (1.0f + expf(-u2));
+      const float q = p * (1.0f - p);
+      return q > 0.f ? fmaf(z * q, c * fmaf(0.134145f, z2, 1.0f), p) : p;
+    }
+    case MOE_ACT_SILU: {
+      if (z > 0.f) {
+        const float p = kFast ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+        return p * fmaf(z, 1.0f - p, 1.0f);
+      }
+      // p (1 + z q) = p q (1 + z + e^z) with q = 1 - p; the bracket vanishes at z0 and is there
+      // d + e^z0 (e^d - 1) with d = z - z0, whose terms have one sign: nothing cancels
+      const float d = (z + 1.2784645557403564f) - 1.2979282759673083e-08f;
+      if (kFast) {  // a column's sum is float32, so near z0 the slope keeps its accuracy too
+        const float ez = __expf(z), q = __fdividef(1.0f, 1.0f + ez);
+        const float series =  // e^d - 1 to 2e-6 of itself for |d| < 1/4
+            d * fmaf(d, fmaf(d, fmaf(d, fmaf(d, 1.0f / 120.f, 1.0f / 24.f), 1.0f / 6.f), 0.5f), 1.0f);
+        return ez * q * q * (fabsf(d) < 0.25f ? fmaf(0.27846454f, series, d) : 1.0f + z + ez);
+      }
+      return 1.0f / (1.0f + expf(-z)) * (1.0f / (1.0f + expf(z))) *
+             fmaf(0.2784645427610737f, expm1f(d), d);
+    }
+    default:
+      return 1.f;
+  }
+}
+
+}  // namespace moe

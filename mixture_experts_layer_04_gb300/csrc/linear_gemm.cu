@@ -1,0 +1,817 @@
+// The matrix product of the linear layers on the 5th-generation tensor cores: tcgen05.mma fed
+// by TMA, accumulators in TMEM, bias / activation / residual in the epilogue.
+//
+// The forward and both gradients are one product with differently laid out operands: y = x w^T
+// has both reduction-contiguous, dx = dz w has w row-contiguous, dw = dz^T x both.  TMA loads
+// either layout in 128-byte swizzled boxes, and the matrix descriptors and the instruction
+// descriptor name the layout, so nothing is transposed in memory:
+//   k-contiguous: a box of 64 k x R rows; 8-row atoms of 1024 bytes follow one another along
+//                 the rows; a step of 16 k advances 32 bytes inside the atom;
+//   row-contiguous: boxes of 64 rows x 64 k (8 KB); atoms of 8 k follow one another, the next
+//                 64 rows are one box on; a step of 16 k advances two atoms (2 KB).
+//
+// Two kernels:
+//  - linear_pair_kernel: persistent CTA pairs (cta_group::2), 256 x 256 tiles, for products
+//    with tiles enough to fill the GPU;
+//  - linear_tile_kernel: one 128 x BN tile per CTA or per cluster, whose CTAs take slices of
+//    the reduction and exchange partial tiles through distributed shared memory, summed in
+//    rank order (deterministic).  For few output rows the operands are swapped, so that the
+//    weights are on the 128-row side and the tokens on a side of 16, 32 or 64.  Its epilogue
+//    warps add the accumulator into registers every `chunk` k-blocks (float32 results): the tensor core truncates
+//    each addition (over 7168 products the mean error is 8e-6 of the result's size, against
+//    2e-7 for rounded additions), which float32 results have to avoid.
+#include <cstring>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "linear.h"
+#include "linear_act.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 64;        // bf16 elements per k-block: one 128-byte swizzle row
+constexpr int kThreads = 192; // TMA warp, MMA warp, four epilogue warps
+
+struct Epilogue {
+  void* c;
+  const float* bias;
+  const void* res;
+  void* z;
+  long long ldc, ldr, ldz;
+  int rows, cols;
+  int act;
+  int c_f32;
+  int vec_c, vec_r, vec_z;  // 16-byte accesses allowed
+};
+
+struct GemmParams {
+  CUtensorMap tm_a, tm_b;
+  Epilogue epi;
+  unsigned* err;
+  int a_mn, b_mn;
+  int num_kb;
+  int chunk;    // k-blocks between register additions (tile kernel)
+  int tiles_a;  // tiles along the side of operand A
+  int tiles_b;
+  int swap;     // operand A carries the output columns (tile kernel)
+};
+
+// ------------------------------------------------------------------ epilogue ----
+
+__device__ __forceinline__ void unpack_bf16(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// n <= 8 values at p[0..], with 16-byte accesses when `vec` and n == 8.
+__device__ __forceinline__ void load_n(const float* p, int n, bool vec, float (&v)[8]) {
+  if (vec && n == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = q < n ? p[q] : 0.f;
+}
+__device__ __forceinline__ void load_n(const __nv_bfloat16* p, int n, bool vec, float (&v)[8]) {
+  if (vec && n == 8) {
+    unpack_bf16(*reinterpret_cast<const uint4*>(p), v);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = q < n ? __bfloat162float(p[q]) : 0.f;
+}
+__device__ __forceinline__ void store_n(float* p, int n, bool vec, const float (&v)[8]) {
+  if (vec && n == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < n) p[q] = v[q];
+}
+__device__ __forceinline__ void store_n(__nv_bfloat16* p, int n, bool vec, const float (&v)[8]) {
+  if (vec && n == 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < n) p[q] = __float2bfloat16_rn(v[q]);
+}
+
+// Eight neighbouring outputs of row `row` from column `col` on (row < rows, col < cols).  The
+// residual is read by the thread that then stores y, so the two may be one buffer.
+template <typename TA>
+__device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, float (&v)[8]) {
+  const int n = min(8, e.cols - col);
+  if (e.bias != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) v[q] += __ldg(e.bias + col + q);
+  }
+  if (e.z != nullptr)
+    store_n(static_cast<TA*>(e.z) + static_cast<size_t>(row) * e.ldz + col, n, e.vec_z, v);
+  if (e.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = act_value<sizeof(TA) == 2>(e.act, v[q]);
+  }
+  if (e.res != nullptr) {
+    float r[8];
+    load_n(static_cast<const TA*>(e.res) + static_cast<size_t>(row) * e.ldr + col, n, e.vec_r, r);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += r[q];
+  }
+  const size_t at = static_cast<size_t>(row) * e.ldc + col;
+  if (e.c_f32)
+    store_n(static_cast<float*>(e.c) + at, n, e.vec_c, v);
+  else
+    store_n(static_cast<__nv_bfloat16*>(e.c) + at, n, e.vec_c, v);
+}
+
+// --------------------------------------------------------- operands in smem ----
+
+// Descriptor of a 128-byte-swizzled operand tile (see the layouts above): k-contiguous tiles
+// have 1024 bytes between 8-row atoms (the other offset is not used), row-contiguous ones
+// 1024 bytes between atoms of 8 k and 8192 between chunks of 64 rows.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
+  uint64_t d = smem_desc_sw128(saddr);
+  if (mn) d = (d & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(8192u >> 4) << 16);
+  return d;
+}
+
+// One k-block of `rows` (a multiple of 64 when row-contiguous) operand rows from r0 on.
+__device__ __forceinline__ void load_operand(uint32_t dst, const void* map, uint32_t bar, int mn,
+                                             int r0, int rows, int kb, int plane) {
+  if (!mn) {
+    tma_load_3d(dst, map, bar, kb * BK, r0, plane);
+  } else {
+    for (int c = 0; c < rows; c += 64)
+      tma_load_3d(dst + c * 128u, map, bar, r0 + c, kb * BK, plane);
+  }
+}
+__device__ __forceinline__ void load_operand_pair(uint32_t dst, const void* map, uint32_t bar,
+                                                  int mn, int r0, int kb) {
+  if (!mn) {
+    tma_load_3d_pair(dst, map, bar, kb * BK, r0, 0);
+  } else {
+    tma_load_3d_pair(dst, map, bar, r0, kb * BK, 0);
+    tma_load_3d_pair(dst + 8192u, map, bar, r0 + 64, kb * BK, 0);
+  }
+}
+
+// ---------------------------------------------------------- one tile per CTA ----
+
+template <int BN, int PL>
+struct TileCfg {
+  static constexpr int kABytes = 128 * BK * 2, kBBytes = BN * BK * 2;
+  static constexpr int kStageBytes = PL * (kABytes + kBBytes);
+  static constexpr int kBarBytes = 256;
+  static constexpr int kStagesRaw = (232448 - 1024 - kBarBytes) / kStageBytes;
+  static constexpr int kStages = kStagesRaw > 12 ? 12 : kStagesRaw;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes;
+  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  // the exchanged partial tiles reuse the stages: 128 x (BN + 4) floats, or BN rows of
+  // 128 + 4 floats per CTA of the cluster when the operands are swapped
+  static_assert(128 * (BN + 4) * 4 <= kStages * kStageBytes, "partial tile");
+  static_assert(BN * (128 + 4 * 8) * 4 <= kStages * kStageBytes, "swapped partial tile");
+  static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier region");
+};
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+               "f"(c), "f"(d)
+               : "memory");
+}
+
+template <int BN, int PL, typename TA>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_tile_kernel(const __grid_constant__ GemmParams p) {
+  using Cfg = TileCfg<BN, PL>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Cfg::kStageBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t mma_done_bar = bar0 + 8u * (2 * S + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t nranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nranks));
+  const int split = static_cast<int>(nranks), rank = static_cast<int>(cluster_ctarank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_trigger();
+
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int a0 = (tile % p.tiles_a) * 128, b0 = (tile / p.tiles_a) * BN;
+  // this CTA's slice of the reduction (never empty: split <= num_kb)
+  const int kb0 = static_cast<int>(static_cast<long long>(p.num_kb) * rank / split);
+  const int nkb = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / split) - kb0;
+  const int R = 128 / split;  // rows of the A side that each CTA finishes
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer ----
+    if (elect_one_sync()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) break;
+        const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
+        mbar_arrive_expect_tx(full_bar(stage), Cfg::kStageBytes);
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+          load_operand(dst + pl * Cfg::kABytes, &p.tm_a, full_bar(stage), p.a_mn, a0, 128, kb0 + i, pl);
+          load_operand(dst + PL * Cfg::kABytes + pl * Cfg::kBBytes, &p.tm_b, full_bar(stage), p.b_mn,
+                       b0, BN, kb0 + i, pl);
+        }
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // drain: no load may still be in flight when the CTA gives up its shared memory
+      const int n = issued < S ? issued : S;
+      volatile int no_abort = 0;
+      for (int j = 0; j < n; ++j) {
+        if (--stage < 0) {
+          stage = S - 1;
+          phase ^= 1u;
+        }
+        mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // every CTA's stages are free
+    cluster_sync_all();  // the partial tiles have arrived
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA ----
+    if (elect_one_sync()) {
+      const uint32_t idesc = idesc_bf16_f32(128, BN) | (static_cast<uint32_t>(p.a_mn) << 15) |
+                             (static_cast<uint32_t>(p.b_mn) << 16);
+      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0, c = 0; ok && i < nkb; ++c) {
+        const int acc = c & 1;
+        if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(c >> 1) & 1u) ^ 1u, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+        const int end = min(nkb, i + p.chunk);
+        uint32_t accumulate = 0;
+        for (; i < end; ++i) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
+          const uint32_t b_base = a_base + PL * Cfg::kABytes;
+          // smallest products first
+          constexpr int kTerms = PL == 3 ? 6 : 1;
+          constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+          for (int q = 0; q < kTerms; ++q) {
+            const int qa = PL == 3 ? pa[q] : 0, qb = PL == 3 ? pb[q] : 0;
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              tc_mma_bf16(d, operand_desc(a_base + qa * Cfg::kABytes + kk * a_step, p.a_mn),
+                          operand_desc(b_base + qb * Cfg::kBBytes + kk * b_step, p.b_mn), idesc,
+                          accumulate);
+              accumulate = 1u;
+            }
+          }
+          tc_commit(empty_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit(tfull_bar(acc));
+      }
+      if (!ok || *abort_flag) {
+        tc_commit(mma_done_bar);
+        volatile int no_abort = 0;
+        mbar_wait(mma_done_bar, 0, &no_abort, p.err);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    cluster_sync_all();
+  } else {
+    // ------------------------------------------------------------ epilogue ----
+    const int quad = warp & 3;
+    float acc[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) acc[j] = 0.f;
+    const int chunks = (nkb + p.chunk - 1) / p.chunk;
+    for (int c = 0; c < chunks; ++c) {
+      const int buf = c & 1;
+      const bool ready =
+          mbar_wait(tfull_bar(buf), static_cast<uint32_t>(c >> 1) & 1u, abort_flag, p.err);
+      if (__any_sync(0xffffffffu, !ready)) break;
+      tc_fence_after();
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                         static_cast<uint32_t>(buf * BN);
+      if constexpr (BN >= 32) {
+#pragma unroll
+        for (int j = 0; j < BN; j += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t + j, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) acc[j + q] += __uint_as_float(r[q]);
+        }
+      } else {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(t, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[q] += __uint_as_float(r[q]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(buf));
+    }
+    __syncwarp();
+    cluster_sync_all();
+    // this CTA's partial tile, row by row to the CTA that finishes the row
+    const int row = quad * 32 + lane;
+    const int owner = row / R, local = row - owner * R;
+    const uint32_t base = mapa_shared(smem_u32(smem), static_cast<uint32_t>(owner));
+    if (!p.swap) {
+      const uint32_t at = base + static_cast<uint32_t>(((rank * R + local) * (BN + 4)) * 4);
+#pragma unroll
+      for (int j = 0; j < BN; j += 4)
+        st_cluster_v4(at + j * 4u, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    } else {
+      const uint32_t at = base + static_cast<uint32_t>((rank * BN * (R + 4) + local) * 4);
+#pragma unroll
+      for (int j = 0; j < BN; ++j)
+        st_shared_cluster(at + static_cast<uint32_t>(j * (R + 4) * 4), __float_as_int(acc[j]));
+    }
+    cluster_sync_all();
+  }
+
+  // sum the slices in rank order and finish eight neighbouring columns per thread and step
+  if (*abort_flag == 0) {
+    const float* part = reinterpret_cast<const float*>(smem);
+    const int out_rows = p.swap ? BN : R, out_cols = p.swap ? R : BN;
+    const int stride = out_cols + 4, slice = out_rows * stride;
+    const int row0 = p.swap ? b0 : a0 + rank * R, col0 = p.swap ? a0 + rank * R : b0;
+    const int per_row = out_cols / 8;
+    for (int it = threadIdx.x; it < out_rows * per_row; it += kThreads) {
+      const int r = it / per_row, c = (it - r * per_row) * 8;
+      if (row0 + r >= p.epi.rows || col0 + c >= p.epi.cols) continue;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = 0.f;
+      for (int s = 0; s < split; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(part + s * slice + r * stride + c);
+        const float4 x = src[0], y = src[1];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      }
+      finish8<TA>(p.epi, row0 + r, col0 + c, v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, Cfg::kTmemCols);
+}
+
+// ------------------------------------------------------ persistent CTA pairs ----
+
+struct PairCfg {
+  static constexpr int kABytes = 128 * BK * 2;  // this CTA's 128 rows of A
+  static constexpr int kBBytes = 128 * BK * 2;  // this CTA's half of the 256 rows of B
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 6;
+  static constexpr int kBN = 256;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kStgRow = 36;  // floats per staged row: 32 and a pad against conflicts
+  static constexpr int kStgBytes = 4 * 32 * kStgRow * 4;
+  static constexpr int kBarBytes = 256;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+// Tiles in chunks of 8 rows of tiles, so that the pairs at work share operand tiles in L2.
+__device__ __forceinline__ void pair_tile(const GemmParams& p, int idx, int* ta, int* tb) {
+  constexpr int kSwz = 8;
+  const int per = kSwz * p.tiles_b;
+  const int c = idx / per, in = idx - c * per;
+  const int h = min(kSwz, p.tiles_a - c * kSwz);
+  *tb = in / h;
+  *ta = c * kSwz + in - *tb * h;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ GemmParams p) {
+  using Cfg = PairCfg;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* stg_all = reinterpret_cast<float*>(smem + S * Cfg::kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Cfg::kStageBytes + Cfg::kStgBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t mma_done_bar = bar0 + 8u * (2 * S + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 8);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_trigger();
+
+  const int total = p.tiles_a * p.tiles_b;
+  const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer ----
+    if (elect_one_sync()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int idx = pair; ok && idx < total; idx += npairs) {
+        int ta, tb;
+        pair_tile(p, idx, &ta, &tb);
+        const int a_row = ta * 256 + static_cast<int>(rank) * 128;
+        const int b_row = tb * 256 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * Cfg::kStageBytes);
+          load_operand_pair(dst, &p.tm_a, fb, p.a_mn, a_row, kb);
+          load_operand_pair(dst + Cfg::kABytes, &p.tm_b, fb, p.b_mn, b_row, kb);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (rank == 0) {
+        // drain: both CTAs' loads complete on the even CTA's barriers
+        const int n = issued < S ? static_cast<int>(issued) : S;
+        volatile int no_abort = 0;
+        for (int j = 0; j < n; ++j) {
+          if (--stage < 0) {
+            stage = S - 1;
+            phase ^= 1u;
+          }
+          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA ----
+    if (rank == 0 && elect_one_sync()) {
+      const uint32_t idesc = idesc_bf16_f32(256, Cfg::kBN) | (static_cast<uint32_t>(p.a_mn) << 15) |
+                             (static_cast<uint32_t>(p.b_mn) << 16);
+      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      for (int idx = pair; ok && idx < total; idx += npairs, ++local) {
+        const int acc = local & 1;
+        if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
+                       p.err))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::kBN);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
+          const uint32_t b_base = a_base + Cfg::kABytes;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, p.a_mn),
+                             operand_desc(b_base + kk * b_step, p.b_mn), idesc,
+                             (kb | kk) != 0 ? 1u : 0u);
+          tc_commit_pair(empty_bar(stage), 0x3);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
+      }
+      if (!ok || *abort_flag) {
+        tc_commit_pair(mma_done_bar, 0x1);
+        volatile int no_abort = 0;
+        mbar_wait(mma_done_bar, 0, &no_abort, p.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue ----
+    const int quad = warp & 3;
+    float* stg = stg_all + (warp - 2) * 32 * Cfg::kStgRow;
+    int local = 0;
+    for (int idx = pair; idx < total; idx += npairs, ++local) {
+      int ta, tb;
+      pair_tile(p, idx, &ta, &tb);
+      const int acc = local & 1;
+      const bool ready =
+          mbar_wait(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err);
+      if (__any_sync(0xffffffffu, !ready)) break;
+      tc_fence_after();
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                         static_cast<uint32_t>(acc * Cfg::kBN);
+      const int row0 = ta * 256 + static_cast<int>(rank) * 128 + quad * 32;
+#pragma unroll 1
+      for (int c = 0; c < Cfg::kBN; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t + c, r);
+        tmem_ld_wait();
+        if (c + 32 == Cfg::kBN) {  // the accumulator is free for the tile after next
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        }
+#pragma unroll
+        for (int q = 0; q < 32; q += 4)
+          *reinterpret_cast<float4*>(stg + lane * Cfg::kStgRow + q) =
+              make_float4(__uint_as_float(r[q]), __uint_as_float(r[q + 1]),
+                          __uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), cc = (lane & 3) * 8;
+          const int row = row0 + rr, col = tb * 256 + c + cc;
+          if (row < p.epi.rows && col < p.epi.cols) {
+            const float4* src = reinterpret_cast<const float4*>(stg + rr * Cfg::kStgRow + cc);
+            const float4 x = src[0], y = src[1];
+            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            finish8<__nv_bfloat16>(p.epi, row, col, v);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no peer still reads this CTA's shared memory or arrives on it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+}
+
+// ---------------------------------------------------------------------- host ----
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// The operand's planes as [planes][outer][inner] with boxes of 64 inner elements x box_rows.
+// What lies past an edge reads as zero.
+bool operand_map(CUtensorMap* m, const void* base, int rows, int depth, int mn, long long ld,
+                 int planes, long long plane, int tile_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t inner = static_cast<cuuint64_t>(mn ? rows : depth);
+  const cuuint64_t outer = static_cast<cuuint64_t>(mn ? depth : rows);
+  cuuint64_t dims[3] = {inner, outer, static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                           static_cast<cuuint64_t>(planes > 1 ? plane : ld * static_cast<long long>(outer)) * 2};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(BK),
+                       static_cast<cuuint32_t>(mn ? BK : tile_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int BN, int PL, typename TA>
+cudaError_t launch_tile(const GemmParams& p, int split, cudaStream_t s) {
+  auto kernel = linear_tile_kernel<BN, PL, TA>;
+  cudaError_t e = allow_smem(kernel, TileCfg<BN, PL>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc;
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = dim3(static_cast<unsigned>(p.tiles_a) * static_cast<unsigned>(p.tiles_b) *
+                    static_cast<unsigned>(split));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = TileCfg<BN, PL>::kSmem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  return count_launch(cudaLaunchKernelEx(&lc, kernel, p));
+}
+
+inline int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
+
+inline bool vec_ok(const void* p, long long ld, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * bytes) % 16 == 0;
+}
+
+// CTA pairs or single tiles.  A pair's 256 x 256 tile is two 128 x 128 tiles of work per SM; a
+// pair is preferred unless the coarser tiles leave more of the GPU idle than its better reuse
+// of shared memory gains.
+bool prefer_pairs(const LinearGemm& g, int num_sms) {
+  if (g.planes != 1 || g.c_f32) return false;
+  const long long tp = static_cast<long long>(ceil_div(g.rows, 256)) * ceil_div(g.cols, 256);
+  const long long tt = static_cast<long long>(ceil_div(g.rows, 128)) * ceil_div(g.cols, 128);
+  const int pairs = num_sms / 2;
+  const long long waves_p = (tp + pairs - 1) / pairs, waves_t = (tt + num_sms - 1) / num_sms;
+  return 16 * waves_p <= 10 * waves_t && tt > num_sms;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_gemm(const LinearGemm& g, unsigned* err, int num_sms, cudaStream_t s) {
+  if (g.rows == 0 || g.cols == 0) return cudaSuccess;
+  GemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int ab = g.act_f32 ? 4 : 2;
+  p.epi.c = g.c;
+  p.epi.bias = g.bias;
+  p.epi.res = g.res;
+  p.epi.z = g.z;
+  p.epi.ldc = g.ldc;
+  p.epi.ldr = g.ldr;
+  p.epi.ldz = g.ldz;
+  p.epi.rows = g.rows;
+  p.epi.cols = g.cols;
+  p.epi.act = g.act;
+  p.epi.c_f32 = g.c_f32;
+  p.epi.vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2);
+  p.epi.vec_r = vec_ok(g.res, g.ldr, ab);
+  p.epi.vec_z = vec_ok(g.z, g.ldz, ab);
+  p.err = err;
+  p.num_kb = ceil_div(g.depth, BK);
+
+  if (prefer_pairs(g, num_sms)) {
+    if (!operand_map(&p.tm_a, g.a, g.rows, g.depth, g.a_mn, g.lda, 1, 0, 128) ||
+        !operand_map(&p.tm_b, g.b, g.cols, g.depth, g.b_mn, g.ldb, 1, 0, 128))
+      return cudaErrorInvalidValue;
+    p.a_mn = g.a_mn;
+    p.b_mn = g.b_mn;
+    p.tiles_a = ceil_div(g.rows, 256);
+    p.tiles_b = ceil_div(g.cols, 256);
+    cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem);
+    if (e != cudaSuccess) return e;
+    const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
+    const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    return launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(kThreads), PairCfg::kSmem, s, p);
+  }
+
+  // few output rows: the other operand on the 128-row side
+  const bool swap = g.rows <= 64 && g.cols > g.rows;
+  const int narrow = swap ? g.rows : g.cols;
+  const int narrow_mn = swap ? g.a_mn : g.b_mn;
+  int bn = narrow <= 16 ? 16 : narrow <= 32 ? 32 : narrow <= 64 ? 64 : 128;
+  if (narrow_mn && bn < 64) bn = 64;  // row-contiguous boxes are 64 rows wide
+  const void* wa = swap ? g.b : g.a;
+  const void* wb = swap ? g.a : g.b;
+  p.a_mn = swap ? g.b_mn : g.a_mn;
+  p.b_mn = narrow_mn;
+  const int a_rows = swap ? g.cols : g.rows;
+  if (!operand_map(&p.tm_a, wa, a_rows, g.depth, p.a_mn, swap ? g.ldb : g.lda, g.planes,
+                   swap ? g.b_plane : g.a_plane, 128) ||
+      !operand_map(&p.tm_b, wb, narrow, g.depth, p.b_mn, swap ? g.lda : g.ldb, g.planes,
+                   swap ? g.a_plane : g.b_plane, bn))
+    return cudaErrorInvalidValue;
+  p.swap = swap ? 1 : 0;
+  p.tiles_a = ceil_div(a_rows, 128);
+  p.tiles_b = ceil_div(narrow, bn);
+  // bf16 results are rounded far above the tensor core's own error: one chunk.  Float32 ones
+  // leave it after 128 (six products per value, so the drain still hides behind the MMAs) or
+  // 256 values
+  p.chunk = g.planes == 3 ? 2 : g.c_f32 ? 4 : 1 << 30;
+  // a cluster of up to 8 CTAs shares a tile's reduction while SMs would idle otherwise, each
+  // with at least four k-blocks
+  const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= num_sms && p.num_kb >= split * 2 * 4) split *= 2;
+  if (g.planes == 3) {
+    switch (bn) {
+      case 16: return launch_tile<16, 3, float>(p, split, s);
+      case 32: return launch_tile<32, 3, float>(p, split, s);
+      case 64: return launch_tile<64, 3, float>(p, split, s);
+      default: return launch_tile<128, 3, float>(p, split, s);
+    }
+  }
+  switch (bn) {
+    case 16: return launch_tile<16, 1, __nv_bfloat16>(p, split, s);
+    case 32: return launch_tile<32, 1, __nv_bfloat16>(p, split, s);
+    case 64: return launch_tile<64, 1, __nv_bfloat16>(p, split, s);
+    default: return launch_tile<128, 1, __nv_bfloat16>(p, split, s);
+  }
+}
+
+}  // namespace moe

@@ -2,7 +2,7 @@
 
 Tolerances: a dot of H float32 products summed in float32 by 32 to 256 partial sums of at most
 H / 256 + 8 steps each is off by at most (H / 256 + 16) 2^-24 of the sum of the absolute
-products; the rows are one product (2^-24) and one rounding (bf16 2^-9, 2^-8 allowed).
+products; the rows are one product (2^-24) and one rounding (bf16 2^-8).
 """
 
 import ctypes

@@ -7,7 +7,7 @@ Tolerances of the floats (u = 2^-24, the rounding of a float32 operation):
    experts uses the hardware exponential, whose bound (2 + 1.17 |x|) 2^-23 averages to at most
    11 * 2^-21 with |x| under the entropy's ln 1024 = 7;
  - gradients: the same relative errors on each factor, on top of a difference of terms of the
-   size of scale * max |dw|; bf16 gradients are rounded once more (2^-9 relative, 2^-8 allowed).
+   size of scale * max |dw|; bf16 gradients are rounded once more (2^-8).
 """
 
 import ctypes
