@@ -8,15 +8,19 @@
 // this GPU (16 clocks per warp instruction), so it is taken in float first and certified:
 // every float score carries a bound on its error.  Neighbouring choices (the K-th and the
 // first one left out among them) closer than the sum of their bounds are put in order by
-// their 64-bit keys, K+1 lanes at once; the groups are chosen again in 64 bits if the last
-// one kept and the best one dropped are that close; and only if the first two experts left
-// out are close to the last one kept is the whole token chosen again.  Without a bias the
-// keys are ordered as the logits are, so the logits themselves are compared, exactly.  Two
-// experts of equal logit and equal bias tie in any precision and need no second look.
+// their 64-bit keys, K+1 lanes at once; groups whose sums cannot be told apart at the border
+// between kept and dropped are compared by 64-bit sums; and only if the first two experts
+// left out are close to the last one kept is the whole token chosen again.  Without a bias
+// the keys are ordered as the logits are, so the logits themselves are compared, exactly.
+// Two experts of equal logit and equal bias tie in any precision and need no second look.
+//
+// The K+1 best come from the lanes' own two best, kept in order in registers: a step is one
+// warp-wide maximum, a ballot and a shuffle, and a lane that has given both away looks for its
+// next two.  (Searching all registers in every step took three times the instructions.)
 //
 // What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
-// written; the work is K+1 warp-wide maxima per token, so at prefill sizes it is bound by
-// instruction issue and the latency of the warp reductions, at one token by the launch.
+// written, but the instructions come first: about 600 per token.  At one token the launch is
+// all there is.
 #include <cfloat>
 #include <type_traits>
 
@@ -41,6 +45,7 @@ struct RouteParams {
   int T, E, K, groups, per, top_groups, rank;
   int renorm;
   int vec;  // rows allow whole-lane vector loads (and, backward, 16-byte stores)
+  int vec_bias;  // whole-lane vector loads of the bias
   float scale;
 };
 
@@ -62,10 +67,11 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
 }
 
+// The warp's largest value (no NaN among them).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // This lane's NJ logits of one row (masked ones and those past E as -inf).
@@ -102,6 +108,29 @@ __device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec
     l[j] = e0 + j < E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
 }
 
+// This lane's NJ biases (those past E as 0).
+template <int NJ>
+__device__ __forceinline__ void load_bias(const RouteParams& p, int lane, float (&b)[NJ]) {
+  const int e0 = lane * NJ;
+  if constexpr (NJ >= 4) {
+    if (p.vec_bias) {
+      if (e0 < p.E) {
+#pragma unroll
+        for (int i = 0; i < NJ; i += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p.bias + e0 + i));
+          b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) b[j] = 0.f;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) b[j] = e0 + j < p.E ? __ldg(p.bias + e0 + j) : 0.f;
+}
+
 // The 64-bit score of a logit, and what it needs of its row: the softmax's sum.
 template <bool kSig>
 __device__ __forceinline__ double score64(float l, float m, double sum) {
@@ -123,76 +152,98 @@ __device__ __forceinline__ double softmax_sum64(const TL* row, int E, float m, i
   return sum;
 }
 
-// The groups (`live` == nullptr: returns their mask) or, with the groups given, the choice
-// (lane k < K returns the k-th expert or -1) from 64-bit keys throughout.  Few tokens come
-// here.  m: the row's largest logit (softmax).
+// The largest key of a warp's candidates (kNone: no candidate) with its expert, ties to the
+// lower expert, -1 if there is none.
+__device__ __forceinline__ int warp_best64(double* key, int e) {
+  double k = *key;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double ko = __shfl_xor_sync(0xffffffffu, k, o);
+    const int eo = __shfl_xor_sync(0xffffffffu, e, o);
+    if (eo >= 0 && (e < 0 || ko > k || (ko == k && eo < e))) {
+      k = ko;
+      e = eo;
+    }
+  }
+  *key = k;
+  return e;
+}
+
+template <bool kSig, typename TL>
+__device__ __forceinline__ double key64(const RouteParams& p, const TL* row, int e, float m,
+                                        double sum) {
+  const float l = e < p.E ? clean_logit(to_float(row[e])) : -INFINITY;
+  const float b = e < p.E && p.bias != nullptr ? p.bias[e] : 0.f;
+  if (!(l > -INFINITY && b > -INFINITY)) return -INFINITY;
+  return score64<kSig>(l, m, sum) + static_cast<double>(b);
+}
+
+// The sums of the groups in `contested` by 64-bit keys, lane g returns group g's.
 template <int NJ, typename TL, bool kSig>
-__device__ __noinline__ uint32_t choose64(const RouteParams& p, const TL* row, float m, int lane,
-                                          const uint32_t* live) {
-  constexpr double kNone = -INFINITY;
+__device__ __noinline__ double group_sums64(const RouteParams& p, const TL* row, float m, int lane,
+                                            uint32_t contested) {
+  const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
+  double mine = -INFINITY;
+  while (contested != 0u) {
+    const int g = __ffs(contested) - 1;
+    contested &= contested - 1u;
+    // this lane's two best of the group, then the warp's
+    double v1 = -INFINITY, v2 = -INFINITY;
+    int e1 = -1;
+#pragma unroll 1
+    for (int i = lane; i < p.per; i += 32) {
+      const double k = key64<kSig>(p, row, g * p.per + i, m, sum);
+      if (k > v1) {
+        v2 = v1;
+        v1 = k;
+        e1 = g * p.per + i;
+      } else if (k > v2) {
+        v2 = k;
+      }
+    }
+    double best = v1;
+    const int e = warp_best64(&best, e1);
+    double total = best;
+    if (p.rank > 1) {
+      double second = e1 == e ? v2 : v1;
+      warp_best64(&second, second > -INFINITY ? lane : -1);
+      if (second > -INFINITY) total += second;
+    }
+    if (lane == g) mine = total;
+  }
+  return mine;
+}
+
+// The choice from 64-bit keys throughout, among the groups in `live`; lane k < K returns the
+// k-th expert or -1.  m: the row's largest logit (softmax).
+template <int NJ, typename TL, bool kSig>
+__device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float m, int lane,
+                                     uint32_t live) {
   double key[NJ];
   const int e0 = lane * NJ;
   const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
 #pragma unroll 1
   for (int j = 0; j < NJ; ++j) {
-    const float l = e0 + j < p.E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
-    const float b = e0 + j < p.E && p.bias != nullptr ? p.bias[e0 + j] : 0.f;
-    key[j] = (l > -INFINITY && b > -INFINITY) ? score64<kSig>(l, m, sum) + static_cast<double>(b)
-                                              : kNone;
-  }
-  // the largest key among the experts that `use` admits, ties to the lower expert, or -1
-  auto best = [&](auto use, double* value) {
-    double kb = kNone;
-    int eb = -1;
-#pragma unroll 1
-    for (int j = 0; j < NJ; ++j)
-      if (use(e0 + j) && key[j] > kb) {
-        kb = key[j];
-        eb = e0 + j;
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double ko = __shfl_xor_sync(0xffffffffu, kb, o);
-      const int eo = __shfl_xor_sync(0xffffffffu, eb, o);
-      if (eo >= 0 && (eb < 0 || ko > kb || (ko == kb && eo < eb))) {
-        kb = ko;
-        eb = eo;
-      }
-    }
-    *value = kb;
-    return eb;
-  };
-  if (live == nullptr) {
-    double mine = kNone;
-#pragma unroll 1
-    for (int g = 0; g < p.groups; ++g) {
-      const int lo = g * p.per, hi = lo + p.per;
-      double v1, v2 = 0.0;
-      const int a = best([&](int e) { return e >= lo && e < hi; }, &v1);
-      if (a >= 0 && p.rank > 1) {
-        const int b = best([&](int e) { return e >= lo && e < hi && e != a; }, &v2);
-        if (b < 0) v2 = 0.0;
-      }
-      if (lane == g) mine = a >= 0 ? v1 + v2 : kNone;
-    }
-    int better = 0;
-#pragma unroll 1
-    for (int h = 0; h < p.groups; ++h) {
-      const double v = __shfl_sync(0xffffffffu, mine, h);
-      better += (v > mine || (v == mine && h < lane)) ? 1 : 0;
-    }
-    return __ballot_sync(0xffffffffu, lane < p.groups && better < p.top_groups);
+    const bool in = e0 + j < p.E && ((live >> ((e0 + j) / p.per)) & 1u);
+    key[j] = in ? key64<kSig>(p, row, e0 + j, m, sum) : -INFINITY;
   }
   int chosen = -1;
 #pragma unroll 1
   for (int k = 0; k < p.K; ++k) {
-    double v;
-    const int e = best([&](int c) { return c < p.E && ((*live >> (c / p.per)) & 1u); }, &v);
+    double v = -INFINITY;
+    int mine = -1;
+#pragma unroll 1
+    for (int j = 0; j < NJ; ++j)
+      if (key[j] > v) {
+        v = key[j];
+        mine = e0 + j;
+      }
+    const int e = warp_best64(&v, mine);
     if (e < 0) break;
     if (lane == k) chosen = e;
-    if (e >= e0 && e < e0 + NJ) key[e - e0] = kNone;
+    if (e >= e0 && e < e0 + NJ) key[e - e0] = -INFINITY;
   }
-  return static_cast<uint32_t>(chosen);
+  return chosen;
 }
 
 // Puts the experts in lanes 0..K (-1 from the first empty lane on) in the order of their
@@ -220,22 +271,21 @@ __device__ __noinline__ int order64(const RouteParams& p, const TL* row, float m
   return out;
 }
 
-// A float score and a bound on its absolute error.  expf is off by at most 2 units in the last
-// place (2^-22 relative) on top of the rounding of its argument (|x| 2^-24), the sum of the
-// softmax, the reciprocal and the product by a few more; for the logistic function the error
-// of the exponential shrinks with 1 - s.
+// A float score and a bound on its absolute error, in units of 2^-23 of the score: the
+// hardware exponential is off by at most 2 + 1.17 |x| of them.  Logistic function: for l > 0
+// that is damped by 1 - s to 1.1, the sum and the division add under 3.  Softmax: the sum adds
+// its terms' mean error (|x| averages at most ln 1024) and its additions' roundings, 17 in all,
+// the products 2.
 template <bool kSig>
-__device__ __forceinline__ float score_of(float l, float m, float inv_sum, float* err) {
-  if (kSig) {
-    // below -80 the score is under 2e-35, which the bound's floor covers
-    const float s = l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + expf(-l));
-    *err = s * 0x1p-21f;
-    return s;
-  }
-  const float x = l - m;
-  const float s = expf(x) * inv_sum;
-  *err = s * (8.0f - x) * 0x1p-23f;
-  return s;
+__device__ __forceinline__ float score_of(float l, float m, float inv_sum) {
+  // below -80 the score is under 2e-35, which the bound's floor covers
+  if (kSig) return l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + __expf(-l));
+  return __expf(l - m) * inv_sum;
+}
+template <bool kSig>
+__device__ __forceinline__ float score_error(float s, float l, float m) {
+  const float units = kSig ? 5.0f + 1.2f * fmaxf(-l, 0.f) : 21.0f + 1.2f * (m - l);
+  return s * units * 0x1p-23f;
 }
 constexpr float kErrFloor = 1e-34f;
 
@@ -281,7 +331,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (m == -INFINITY) m = 0.f;  // every expert is masked
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) sum += expf(l[j] - m);
+    for (int j = 0; j < NJ; ++j) sum += __expf(l[j] - m);
     inv_sum = 1.0f / warp_sum(sum);
   }
 
@@ -290,21 +340,23 @@ __global__ void __launch_bounds__(32 * kWarps)
   uint32_t ord[NJ];
   uint32_t live = 0xffffffffu;  // groups in play
   if (has_bias || grouped) {
-    float key[NJ];
-    float err_max = kErrFloor;
+    float key[NJ], b[NJ];
+    if (has_bias) {
+      load_bias<NJ>(p, lane, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) b[j] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const float b = has_bias && e0 + j < p.E ? __ldg(p.bias + e0 + j) : 0.f;
-      const bool ok = l[j] > -INFINITY && b > -INFINITY;
-      float err;
-      const float k = score_of<kSig>(l[j], m, inv_sum, &err) + b;
+      const float k = score_of<kSig>(l[j], m, inv_sum) + b[j];
+      const bool ok = l[j] > -INFINITY && b[j] > -INFINITY;
       key[j] = ok ? k : -INFINITY;
-      if (ok) err_max = fmaxf(err_max, err + fabsf(k) * 0x1p-23f);
-      ord[j] = !ok ? 0u : (has_bias ? float_key(k) : float_key(l[j]));
+      ord[j] = !ok ? 0u : float_key(has_bias ? k : l[j]);
     }
     if (grouped) {
-      // the sum of the group's best one or two keys, for group g in lane g
-      float v1 = -INFINITY, v2 = -INFINITY, gs;
+      // the group's best one or two keys, for group g in lane g
+      float v1 = -INFINITY, v2 = -INFINITY;
       const int lanes = p.per / NJ;
       if (p.per % NJ == 0 && (lanes & (lanes - 1)) == 0) {
         // whole lanes per group: best two of each lane, then of neighbouring lanes
@@ -314,13 +366,13 @@ __global__ void __launch_bounds__(32 * kWarps)
           v1 = fmaxf(v1, key[j]);
         }
         for (int o = 1; o < lanes; o <<= 1) {
-          const float a = __shfl_xor_sync(0xffffffffu, v1, o);
-          const float b = __shfl_xor_sync(0xffffffffu, v2, o);
-          v2 = fmaxf(fmaxf(v2, b), fminf(v1, a));
-          v1 = fmaxf(v1, a);
+          const float x1 = __shfl_xor_sync(0xffffffffu, v1, o);
+          const float x2 = __shfl_xor_sync(0xffffffffu, v2, o);
+          v2 = fmaxf(fmaxf(v2, x2), fminf(v1, x1));
+          v1 = fmaxf(v1, x1);
         }
-        gs = p.rank > 1 && v2 > -INFINITY ? v1 + v2 : v1;
-        gs = __shfl_sync(0xffffffffu, gs, (lane * lanes) & 31);
+        v1 = __shfl_sync(0xffffffffu, v1, (lane * lanes) & 31);
+        v2 = __shfl_sync(0xffffffffu, v2, (lane * lanes) & 31);
       } else {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) s_key[warp][e0 + j] = key[j];
@@ -332,9 +384,10 @@ __global__ void __launch_bounds__(32 * kWarps)
             v1 = fmaxf(v1, k);
           }
         }
-        gs = p.rank > 1 && v2 > -INFINITY ? v1 + v2 : v1;
       }
-      if (lane >= p.groups) gs = -INFINITY;
+      const bool two = p.rank > 1 && v2 > -INFINITY;
+      const bool there = lane < p.groups && v1 > -INFINITY;
+      float gs = there ? (two ? v1 + v2 : v1) : -INFINITY;
       int better = 0;
       for (int h = 0; h < p.groups; ++h) {
         const float v = __shfl_sync(0xffffffffu, gs, h);
@@ -345,11 +398,25 @@ __global__ void __launch_bounds__(32 * kWarps)
       const float lowest_in = -warp_max(in ? -gs : -INFINITY);
       const float best_out = warp_max(in ? -INFINITY : gs);
       if (best_out > -INFINITY) {
-        // each sum is off by at most two bounds and one rounding
-        const float slack = 4.0f * warp_max(err_max) +
-                            0x1p-23f * (fabsf(lowest_in) + fabsf(best_out));
-        if (!(lowest_in - best_out > slack))
-          live = choose64<NJ, TL, kSig>(p, row, m, lane, nullptr);
+        // A sum is off by its keys' errors (a score's is largest at the largest score, 1 for
+        // the logistic function and inv_sum for the softmax) and three roundings.
+        const float mag = warp_max(there ? fabsf(v1) + (two ? fabsf(v2) : 0.f) : 0.f);
+        const float slack = 2.0f * (2.0f * score_error<kSig>(kSig ? 1.0f : inv_sum, m, m) +
+                                    2.0f * kErrFloor + mag * 0x1p-22f);
+        if (!(lowest_in - best_out > slack)) {
+          // the groups at the border, by 64-bit sums, for the places that the clear ones leave
+          const bool clear_in = in && gs > best_out + slack;
+          const bool contested = there && !clear_in && !(gs < lowest_in - slack);
+          const uint32_t open = __ballot_sync(0xffffffffu, contested);
+          const uint32_t sure = __ballot_sync(0xffffffffu, clear_in);
+          const double g64 = group_sums64<NJ, TL, kSig>(p, row, m, lane, open);
+          int before = 0;
+          for (int h = 0; h < p.groups; ++h) {
+            const double v = __shfl_sync(0xffffffffu, g64, h);
+            before += ((open >> h) & 1u) && (v > g64 || (v == g64 && h < lane)) ? 1 : 0;
+          }
+          live = sure | __ballot_sync(0xffffffffu, contested && before < p.top_groups - __popc(sure));
+        }
       }
       int g = e0 / p.per, r = e0 - g * p.per;
 #pragma unroll
@@ -366,34 +433,52 @@ __global__ void __launch_bounds__(32 * kWarps)
     for (int j = 0; j < NJ; ++j) ord[j] = l[j] > -INFINITY ? float_key(l[j]) : 0u;
   }
 
+  // this lane's two best still in play, in order (ties: the lower register first)
+  uint32_t o1 = 0u, o2 = 0u;
+  int j1 = 0, j2 = 0, held = 2;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool first = ord[j] > o1, second = ord[j] > o2;
+    o2 = first ? o1 : second ? ord[j] : o2;
+    j2 = first ? j1 : second ? j : j2;
+    o1 = first ? ord[j] : o1;
+    j1 = first ? j : j1;
+  }
   // takes the best expert still in play (uniform over the warp), or -1
   auto take_best = [&]() {
-    uint32_t kb = ord[0];
-#pragma unroll
-    for (int j = 1; j < NJ; ++j) kb = max(kb, ord[j]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, kb);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, o1);
     if (top == 0u) return -1;
-    const int win = __ffs(__ballot_sync(0xffffffffu, kb == top)) - 1;
-    int e = 0;
+    const int win = __ffs(__ballot_sync(0xffffffffu, o1 == top)) - 1;
+    const int e = __shfl_sync(0xffffffffu, e0 + j1, win);
     if (lane == win) {
-      bool found = false;
+      const int last = j1;
+      o1 = o2;
+      j1 = j2;
+      o2 = 0u;
+      if (NJ > 2 && --held == 0) {  // the next two after (top, last)
+        held = 2;
+        o1 = 0u;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if (!found && ord[j] == top) {
-          found = true;
-          ord[j] = 0u;
-          e = e0 + j;
+        for (int j = 0; j < NJ; ++j) {
+          const uint32_t v = ord[j] < top || (ord[j] == top && j > last) ? ord[j] : 0u;
+          const bool first = v > o1, second = v > o2;
+          o2 = first ? o1 : second ? v : o2;
+          j2 = first ? j1 : second ? j : j2;
+          o1 = first ? v : o1;
+          j1 = first ? j : j1;
         }
       }
     }
-    return __shfl_sync(0xffffffffu, e, win);
+    return e;
   };
   auto pick_of = [&](int e) {
     Pick q{-INFINITY, 0.f, 0.f, 0.f};
     if (e >= 0) {
       q.l = clean_logit(to_float(row[e]));
       q.b = has_bias ? __ldg(p.bias + e) : 0.f;
-      q.key = score_of<kSig>(q.l, m, inv_sum, &q.err) + q.b;
+      const float s = score_of<kSig>(q.l, m, inv_sum);
+      q.key = s + q.b;
+      q.err = score_error<kSig>(s, q.l, m);
     }
     return q;
   };
@@ -421,7 +506,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       const Pick q = pick_of(second);
       whole = __shfl_sync(0xffffffffu, second >= 0 && in_doubt<kSig>(me, q, has_bias, m), p.K);
     }
-    mine = whole ? static_cast<int>(choose64<NJ, TL, kSig>(p, row, m, lane, &live))
+    mine = whole ? choose64<NJ, TL, kSig>(p, row, m, lane, live)
                  : order64<NJ, TL, kSig>(p, row, m, lane, mine, me.l, me.b);
   }
   if (lane >= p.K) mine = -1;
@@ -556,6 +641,7 @@ cudaError_t launch_route(const moe_route_config_t& c, RouteParams p, cudaStream_
   p.vec = c.E % q == 0 && (p.stride * eb) % 16 == 0 &&
           (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 &&
           (reinterpret_cast<uintptr_t>(p.d_logits) & 15u) == 0;
+  p.vec_bias = c.E % NJ == 0 && (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0;
   const bool sig = c.score == MOE_SCORE_SIGMOID;
   auto go = [&](auto nj_c) {
     constexpr int N = decltype(nj_c)::value;
