@@ -6,6 +6,8 @@
 // 7e-8 here), whose exponential the derivative shares.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/moe.h"
 #include "common.cuh"
 
@@ -46,6 +48,22 @@ __device__ __forceinline__ float act_value(int act, float z) {
       return kFast ? silu_bf16out(z) : silu_f(z);
     default:
       return z;
+  }
+}
+
+// Eight values at once: one switch for all of them.
+template <bool kFast>
+__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+  auto each = [&](auto a) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = act_value<kFast>(decltype(a)::value, v[q]);
+  };
+  switch (act) {
+    case MOE_ACT_RELU: each(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+    case MOE_ACT_GELU: each(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+    case MOE_ACT_GELU_TANH: each(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+    case MOE_ACT_SILU: each(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+    default: break;
   }
 }
 

@@ -44,7 +44,7 @@ struct Epilogue {
   int rows, cols;
   int act;
   int c_f32;
-  int vec_c, vec_r, vec_z;  // 16-byte accesses allowed
+  int vec_c, vec_r, vec_z, vec_bias;  // 16-byte accesses allowed
 };
 
 struct GemmParams {
@@ -126,10 +126,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, flo
   }
   if (e.z != nullptr)
     store_n(static_cast<TA*>(e.z) + static_cast<size_t>(row) * e.ldz + col, n, e.vec_z, v);
-  if (e.act != MOE_ACT_NONE) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = act_value<sizeof(TA) == 2>(e.act, v[q]);
-  }
+  act_values<sizeof(TA) == 2>(e.act, v);
   if (e.res != nullptr) {
     float r[8];
     load_n(static_cast<const TA*>(e.res) + static_cast<size_t>(row) * e.ldr + col, n, e.vec_r, r);
@@ -141,6 +138,38 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, flo
     store_n(static_cast<float*>(e.c) + at, n, e.vec_c, v);
   else
     store_n(static_cast<__nv_bfloat16*>(e.c) + at, n, e.vec_c, v);
+}
+
+// The same for two rows (row, row + step) of a bf16 tile that lies wholly inside the output,
+// with 16-byte accesses throughout: the residuals are on their way before anything is computed.
+// b: the eight columns' biases.
+__device__ __forceinline__ void finish8_inside(const Epilogue& e, int row, int step, int col,
+                                               const float (&b)[8], float (&v)[2][8]) {
+  using TA = __nv_bfloat16;
+  uint4 r[2];
+  if (e.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r[i] = *reinterpret_cast<const uint4*>(static_cast<const TA*>(e.res) +
+                                             static_cast<size_t>(row + i * step) * e.ldr + col);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[i][q] += b[q];
+    if (e.z != nullptr)
+      store_n(static_cast<TA*>(e.z) + static_cast<size_t>(row + i * step) * e.ldz + col, 8, true,
+              v[i]);
+    act_values<true>(e.act, v[i]);
+    if (e.res != nullptr) {
+      float x[8];
+      unpack_bf16(r[i], x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[i][q] += x[q];
+    }
+    store_n(static_cast<TA*>(e.c) + static_cast<size_t>(row + i * step) * e.ldc + col, 8, true,
+            v[i]);
+  }
 }
 
 // --------------------------------------------------------- operands in smem ----
@@ -433,15 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------ persistent CTA pairs ----
 
+// Eight epilogue warps, two per TMEM lane quarter with half the columns each: with four, the
+// epilogue of a tile took longer than its MMAs (4096 x 4096 -> 14336 with tanh-GELU and the
+// kept pre-activation: 503 us).
 struct PairCfg {
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kABytes = 128 * BK * 2;  // this CTA's 128 rows of A
   static constexpr int kBBytes = 128 * BK * 2;  // this CTA's half of the 256 rows of B
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 6;
   static constexpr int kBN = 256;
   static constexpr int kTmemCols = 512;
-  static constexpr int kStgRow = 36;  // floats per staged row: 32 and a pad against conflicts
-  static constexpr int kStgBytes = 4 * 32 * kStgRow * 4;
+  static constexpr int kChunk = 16;   // columns staged at a time
+  static constexpr int kStgRow = 20;  // floats per staged row: 16 and a pad against conflicts
+  static constexpr int kStgBytes = kEpiWarps * 32 * kStgRow * 4;
   static constexpr int kBarBytes = 256;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -457,7 +492,7 @@ __device__ __forceinline__ void pair_tile(const GemmParams& p, int idx, int* ta,
   *ta = c * kSwz + in - *tb * h;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ GemmParams p) {
   using Cfg = PairCfg;
   constexpr int S = Cfg::kStages;
@@ -484,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);
+      mbar_init(tempty_bar(a), 2 * Cfg::kEpiWarps);
     }
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
@@ -597,48 +632,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue ----
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     float* stg = stg_all + (warp - 2) * 32 * Cfg::kStgRow;
+    const bool wide = p.epi.vec_c && (p.epi.res == nullptr || p.epi.vec_r) &&
+                      (p.epi.z == nullptr || p.epi.vec_z) && p.epi.vec_bias;
     int local = 0;
     for (int idx = pair; idx < total; idx += npairs, ++local) {
       int ta, tb;
       pair_tile(p, idx, &ta, &tb);
       const int acc = local & 1;
+      const int row0 = ta * 256 + static_cast<int>(rank) * 128 + quad * 32;
+      const int col0 = tb * 256 + half * 128;
+      const bool inside = wide && row0 + 32 <= p.epi.rows && col0 + 128 <= p.epi.cols;
       const bool ready =
           mbar_wait(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err);
       if (__any_sync(0xffffffffu, !ready)) break;
       tc_fence_after();
       const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                         static_cast<uint32_t>(acc * Cfg::kBN);
-      const int row0 = ta * 256 + static_cast<int>(rank) * 128 + quad * 32;
+                         static_cast<uint32_t>(acc * Cfg::kBN + half * 128);
+      // lane l reads back columns (l & 1) * 8 of rows l / 2 and l / 2 + 16
+      const int rr = lane >> 1, cc = (lane & 1) * 8;
 #pragma unroll 1
-      for (int c = 0; c < Cfg::kBN; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t + c, r);
+      for (int c = 0; c < 128; c += Cfg::kChunk) {
+        const int row = row0 + rr, col = col0 + c + cc;
+        float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (inside && p.epi.bias != nullptr) load_n(p.epi.bias + col, 8, true, bias);
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(t + c, r);
         tmem_ld_wait();
-        if (c + 32 == Cfg::kBN) {  // the accumulator is free for the tile after next
+        if (c + Cfg::kChunk == 128) {  // the accumulator is free for the tile after next
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
         }
 #pragma unroll
-        for (int q = 0; q < 32; q += 4)
+        for (int q = 0; q < 16; q += 4)
           *reinterpret_cast<float4*>(stg + lane * Cfg::kStgRow + q) =
               make_float4(__uint_as_float(r[q]), __uint_as_float(r[q + 1]),
                           __uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]));
         __syncwarp();
+        float v[2][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2), cc = (lane & 3) * 8;
-          const int row = row0 + rr, col = tb * 256 + c + cc;
-          if (row < p.epi.rows && col < p.epi.cols) {
-            const float4* src = reinterpret_cast<const float4*>(stg + rr * Cfg::kStgRow + cc);
-            const float4 x = src[0], y = src[1];
-            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            finish8<__nv_bfloat16>(p.epi, row, col, v);
+        for (int i = 0; i < 2; ++i)
+          load_n(stg + (rr + 16 * i) * Cfg::kStgRow + cc, 8, true, v[i]);
+        __syncwarp();
+        if (inside) {
+          finish8_inside(p.epi, row, 16, col, bias, v);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            if (row + 16 * i < p.epi.rows && col < p.epi.cols) {
+              float u[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) u[q] = i == 0 ? v[0][q] : v[1][q];
+              finish8<__nv_bfloat16>(p.epi, row + 16 * i, col, u);
+            }
           }
         }
-        __syncwarp();
       }
     }
   }
@@ -752,6 +802,7 @@ cudaError_t launch_linear_gemm(const LinearGemm& g, unsigned* err, int num_sms, 
   p.epi.vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2);
   p.epi.vec_r = vec_ok(g.res, g.ldr, ab);
   p.epi.vec_z = vec_ok(g.z, g.ldz, ab);
+  p.epi.vec_bias = vec_ok(g.bias, 0, 4);
   p.err = err;
   p.num_kb = ceil_div(g.depth, BK);
 
@@ -767,7 +818,7 @@ cudaError_t launch_linear_gemm(const LinearGemm& g, unsigned* err, int num_sms, 
     if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
     const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(kThreads), PairCfg::kSmem, s, p);
+    return launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(PairCfg::kThreads), PairCfg::kSmem, s, p);
   }
 
   // few output rows: the other operand on the 128-row side
