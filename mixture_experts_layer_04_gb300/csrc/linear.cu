@@ -10,7 +10,8 @@
 //    rows whose stride is not a multiple of 16 bytes are copied to one that is.
 //  - dz_kernel: dz = dy * act'(z) in the product's operand form (rounded to bf16, or three
 //    parts) and, in the same pass, the column sums of the unrounded dz over a slice of rows;
-//    column_sum_kernel adds the slices in order.  Bound by reading dy and z and writing dz.
+//    the dw product adds the slices in order along the way (column_sum_kernel where there is
+//    none, or where it runs on CTA pairs).  Bound by reading dy and z and writing dz.
 #include "common.cuh"
 #include "kernels.h"
 #include "linear.h"
@@ -82,22 +83,37 @@ __device__ __forceinline__ void store_parts(__nv_bfloat16* dst, long long plane,
 
 // ------------------------------------------------------------------ packing ----
 
+struct PackTask {
+  const void* src;
+  long long ld;
+  __nv_bfloat16* dst;
+  long long dst_ld, plane;
+  int rows, cols, vec;
+  int blocks;  // of 256 threads, 0: nothing to pack
+};
+
+// One task by `blocks` blocks, of which this is number `block`.
 template <typename T, int PL>
-__global__ void __launch_bounds__(256)
-    pack_kernel(const T* __restrict__ src, long long ld, int rows, int cols, int vec,
-                __nv_bfloat16* __restrict__ dst, long long dst_ld, long long plane) {
-  grid_dep_wait();
-  grid_dep_trigger();
-  const int per_row = static_cast<int>(dst_ld / 8);
-  const long long items = static_cast<long long>(rows) * per_row;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < items;
-       i += static_cast<long long>(gridDim.x) * 256) {
+__device__ __forceinline__ void pack_task(const PackTask& t, int block) {
+  const int per_row = static_cast<int>(t.dst_ld / 8);
+  const long long items = static_cast<long long>(t.rows) * per_row;
+  for (long long i = block * 256ll + threadIdx.x; i < items; i += t.blocks * 256ll) {
     const long long r = i / per_row;
     const int c = static_cast<int>(i - r * per_row) * 8;
     float v[8];
-    load_n(src + r * ld + c, cols - c, vec != 0, v);
-    store_parts<PL>(dst + r * dst_ld + c, plane, v);
+    load_n(static_cast<const T*>(t.src) + r * t.ld + c, t.cols - c, t.vec != 0, v);
+    store_parts<PL>(t.dst + r * t.dst_ld + c, t.plane, v);
   }
+}
+
+template <typename T, int PL>
+__global__ void __launch_bounds__(256)
+    pack_kernel(const __grid_constant__ PackTask x, const __grid_constant__ PackTask w) {
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int b = static_cast<int>(blockIdx.x);
+  if (b < x.blocks) pack_task<T, PL>(x, b);
+  else pack_task<T, PL>(w, b - x.blocks);
 }
 
 // ----------------------------------------------------------------------- dz ----
@@ -111,36 +127,94 @@ struct DzParams {
   float* sums;  // [slices][cols], or null
   int rows, cols, rows_per_slice;
   int act;
-  int vec_y, vec_z;
+  int vec_y, vec_z;  // 16-byte loads allowed
+  int col_blocks, blocks;  // blocks of dz: col_blocks x slices; then x's and w's packing
+  PackTask x, w;
 };
 
-template <typename TY, typename TA, int PL>
-__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams p) {
+// Eight values as they lie in memory, to be on their way before any is used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(u, v); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+// A block takes 256 columns of a slice of rows, a warp every eighth row of it.
+template <typename TY, typename TA, int PL, int ACT>
+__global__ void __launch_bounds__(256, PL == 1 ? 4 : 2)
+    dz_kernel(const __grid_constant__ DzParams p) {
+  constexpr int U = PL == 1 ? 4 : 2;  // rows a thread has in flight
   __shared__ float s_sum[8][256];
   grid_dep_wait();
   grid_dep_trigger();
+  const int block = static_cast<int>(blockIdx.x) - p.blocks;
+  if (block >= 0) {
+    if (block < p.x.blocks) pack_task<TA, PL>(p.x, block);
+    else pack_task<TA, PL>(p.w, block - p.x.blocks);
+    return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
-  const int r0 = blockIdx.y * p.rows_per_slice;
+  const int slice = static_cast<int>(blockIdx.x) / p.col_blocks;
+  const int col_block = static_cast<int>(blockIdx.x) - slice * p.col_blocks;
+  const int c = col_block * 256 + lane * 8;
+  const int r0 = slice * p.rows_per_slice;
   const int r1 = min(p.rows, r0 + p.rows_per_slice);
+  const TY* dy = static_cast<const TY*>(p.dy);
+  const TA* z = static_cast<const TA*>(p.z);
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (c < p.cols) {
-#pragma unroll 2
-    for (int r = r0 + warp; r < r1; r += 8) {
-      float v[8];
-      load_n(static_cast<const TY*>(p.dy) + static_cast<size_t>(r) * p.ldy + c, p.cols - c,
-             p.vec_y != 0, v);
-      if (p.z != nullptr) {
-        float z[8];
-        load_n(static_cast<const TA*>(p.z) + static_cast<size_t>(r) * p.ldz + c, p.cols - c,
-               p.vec_z != 0, z);
+  auto take = [&](int r, float (&v)[8], float (&zv)[8]) {
+    if constexpr (ACT != MOE_ACT_NONE) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] *= act_slope<sizeof(TA) == 2>(p.act, z[q]);
+      for (int q = 0; q < 8; ++q) v[q] *= act_slope<sizeof(TA) == 2>(ACT, zv[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] += v[q];
+    if (p.dz != nullptr)
+      store_parts<PL>(p.dz + static_cast<size_t>(r) * p.dz_ld + c, p.plane, v);
+  };
+  if (c + 8 <= p.cols && p.vec_y && (ACT == MOE_ACT_NONE || p.vec_z)) {
+    for (int rb = r0 + warp; rb < r1; rb += 8 * U) {
+      Raw8<TY> ry[U];
+      Raw8<TA> rz[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = min(rb + 8 * u, r1 - 1);
+        ry[u].load(dy + static_cast<size_t>(r) * p.ldy + c);
+        if constexpr (ACT != MOE_ACT_NONE) rz[u].load(z + static_cast<size_t>(r) * p.ldz + c);
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] += v[q];
-      if (p.dz != nullptr)
-        store_parts<PL>(p.dz + static_cast<size_t>(r) * p.dz_ld + c, p.plane, v);
+      for (int u = 0; u < U; ++u) {
+        if (rb + 8 * u < r1) {
+          float v[8], zv[8];
+          ry[u].get(v);
+          if constexpr (ACT != MOE_ACT_NONE) rz[u].get(zv);
+          take(rb + 8 * u, v, zv);
+        }
+      }
+    }
+  } else if (c < p.cols) {
+    for (int r = r0 + warp; r < r1; r += 8) {
+      float v[8], zv[8];
+      load_n(dy + static_cast<size_t>(r) * p.ldy + c, p.cols - c, p.vec_y != 0, v);
+      if constexpr (ACT != MOE_ACT_NONE)
+        load_n(z + static_cast<size_t>(r) * p.ldz + c, p.cols - c, p.vec_z != 0, zv);
+      take(r, v, zv);
     }
   }
   if (p.sums == nullptr) return;
@@ -152,21 +226,50 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParam
   float total = 0.f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) total += s_sum[w][at];
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < p.cols) p.sums[static_cast<size_t>(blockIdx.y) * p.cols + col] = total;
+  const int col = col_block * 256 + threadIdx.x;
+  if (col < p.cols) p.sums[static_cast<size_t>(slice) * p.cols + col] = total;
 }
 
-__global__ void __launch_bounds__(128)
+// The slices' column sums: 32 columns per block, each warp adds every eighth slice, then the
+// eight partial sums in warp order.
+__global__ void __launch_bounds__(256)
     column_sum_kernel(const float* __restrict__ parts, int slices, int cols,
                       float* __restrict__ out) {
+  __shared__ float s_sum[8][32];
   grid_dep_wait();
   grid_dep_trigger();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= cols) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float total = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < slices; ++s) total += parts[static_cast<size_t>(s) * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int s = warp; s < slices; s += 8) total += parts[static_cast<size_t>(s) * cols + c];
+  }
+  s_sum[warp][lane] = total;
+  __syncthreads();
+  if (warp != 0 || c >= cols) return;
+  total = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) total += s_sum[w][lane];
   out[c] = total;
+}
+
+template <typename TY, typename TA, int PL>
+cudaError_t launch_dz(const DzParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.blocks) + static_cast<unsigned>(p.x.blocks) +
+                  static_cast<unsigned>(p.w.blocks));
+  switch (p.act) {
+    case MOE_ACT_RELU:
+      return launch_pdl(dz_kernel<TY, TA, PL, MOE_ACT_RELU>, grid, dim3(256), 0, s, p);
+    case MOE_ACT_GELU:
+      return launch_pdl(dz_kernel<TY, TA, PL, MOE_ACT_GELU>, grid, dim3(256), 0, s, p);
+    case MOE_ACT_GELU_TANH:
+      return launch_pdl(dz_kernel<TY, TA, PL, MOE_ACT_GELU_TANH>, grid, dim3(256), 0, s, p);
+    case MOE_ACT_SILU:
+      return launch_pdl(dz_kernel<TY, TA, PL, MOE_ACT_SILU>, grid, dim3(256), 0, s, p);
+    default:
+      return launch_pdl(dz_kernel<TY, TA, PL, MOE_ACT_NONE>, grid, dim3(256), 0, s, p);
+  }
 }
 
 // ----------------------------------------------------------------- few rows ----
@@ -307,11 +410,11 @@ inline long long pad8(long long n) { return (n + 7) / 8 * 8; }
 inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 // Slices of rows whose column sums are taken separately: enough blocks for the GPU, at least
-// 32 rows each.
+// 8 rows (one per warp) each.
 int dz_slices(int rows, int out) {
   const int col_blocks = (out + 255) / 256;
   const int want = (1216 + col_blocks - 1) / col_blocks;
-  const int most = (rows + 31) / 32;
+  const int most = (rows + 7) / 8;
   const int n = want < most ? want : most;
   return n < 1 ? 1 : n;
 }
@@ -358,25 +461,23 @@ struct Operand {
   long long ld, plane;
 };
 
-// The operand in place, or packed into `dst`.
-cudaError_t operand(const void* src, long long ld, int rows, int cols, int dtype, bool pack,
-                    void* dst, int num_sms, cudaStream_t s, Operand* out) {
-  if (!pack) {
-    *out = Operand{src, ld, 0};
-    return cudaSuccess;
-  }
-  const long long dst_ld = pad8(cols);
-  const long long plane = dst_ld * rows;
-  *out = Operand{dst, dst_ld, plane};
-  const long long blocks = (plane / 8 + 255) / 256, most = 16ll * num_sms;
-  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
-  const int vec = vec_ok(src, ld, dtype) ? 1 : 0;
-  __nv_bfloat16* d = static_cast<__nv_bfloat16*>(dst);
-  if (dtype == MOE_F32)
-    return launch_pdl(pack_kernel<float, 3>, grid, dim3(256), 0, s,
-                      static_cast<const float*>(src), ld, rows, cols, vec, d, dst_ld, plane);
-  return launch_pdl(pack_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s,
-                    static_cast<const __nv_bfloat16*>(src), ld, rows, cols, vec, d, dst_ld, plane);
+// The operand in place, or packed into `dst` by the task it fills in.
+Operand operand(const void* src, long long ld, int rows, int cols, int dtype, bool pack, void* dst,
+                int num_sms, PackTask* task) {
+  if (!pack) return Operand{src, ld, 0};
+  PackTask t;
+  t.src = src;
+  t.ld = ld;
+  t.dst = static_cast<__nv_bfloat16*>(dst);
+  t.dst_ld = pad8(cols);
+  t.plane = t.dst_ld * rows;
+  t.rows = rows;
+  t.cols = cols;
+  t.vec = vec_ok(src, ld, dtype) ? 1 : 0;
+  const long long blocks = (t.plane / 8 + 255) / 256, most = 16ll * num_sms;
+  t.blocks = static_cast<int>(blocks < most ? blocks : most);
+  *task = t;
+  return Operand{dst, t.dst_ld, t.plane};
 }
 
 // An operand's pointer: the alignment of an element, and a 16-byte boundary when its stride
@@ -451,13 +552,19 @@ extern "C" moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x
   }
 
   const int sms = device_num_sms();
-  Operand ox, ow;
-  cudaError_t e = operand(x, ld.x, cfg->rows, cfg->in_features, cfg->dtype, plan.pack_x,
-                          at<void>(ws, plan.x), sms, s, &ox);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
-  e = operand(w, ld.w, cfg->out_features, cfg->in_features, cfg->dtype, plan.pack_w,
-              at<void>(ws, plan.w), sms, s, &ow);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  PackTask tx{}, tw{};
+  const Operand ox = operand(x, ld.x, cfg->rows, cfg->in_features, cfg->dtype, plan.pack_x,
+                             at<void>(ws, plan.x), sms, &tx);
+  const Operand ow = operand(w, ld.w, cfg->out_features, cfg->in_features, cfg->dtype,
+                             plan.pack_w, at<void>(ws, plan.w), sms, &tw);
+  if (tx.blocks + tw.blocks > 0) {
+    const dim3 grid(static_cast<unsigned>(tx.blocks + tw.blocks));
+    const cudaError_t e =
+        cfg->dtype == MOE_F32
+            ? launch_pdl(pack_kernel<float, 3>, grid, dim3(256), 0, s, tx, tw)
+            : launch_pdl(pack_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s, tx, tw);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
   LinearGemm g{};
   g.rows = cfg->rows;
   g.cols = cfg->out_features;
@@ -479,7 +586,7 @@ extern "C" moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x
   g.ldr = ld.r;
   g.z = z;
   g.ldz = ld.z;
-  return status_of(launch_linear_gemm(g, device_error_word(), sms, s));
+  return status_of(launch_linear_gemms(&g, 1, device_error_word(), sms, s));
 }
 
 extern "C" moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, const void* dy,
@@ -526,11 +633,16 @@ extern "C" moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, cons
   const bool f32 = cfg->dtype == MOE_F32;
   const int rows = cfg->rows, in = cfg->in_features, out = cfg->out_features;
 
-  // dz and the column sums
-  Operand odz{dy, ld.y, 0};
+  // One pass: dz, the slices of the column sums, and x and w where they have to be packed.
+  DzParams p{};
+  Operand odz{dy, ld.y, 0}, ox{}, ow{};
   const bool products = dx != nullptr || dw != nullptr;
+  if (dx != nullptr)
+    ow = operand(w, ld.w, out, in, cfg->dtype, plan.pack_w, at<void>(ws, plan.w), sms, &p.w);
+  if (dw != nullptr)
+    ox = operand(x, ld.x, rows, in, cfg->dtype, plan.pack_x, at<void>(ws, plan.x), sms, &p.x);
+  int slices = 0;
   if ((plan.make_dz && products) || dbias != nullptr) {
-    DzParams p{};
     p.dy = dy;
     p.ldy = ld.y;
     p.z = has_act ? z : nullptr;
@@ -548,24 +660,18 @@ extern "C" moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, cons
     }
     const int want = dz_slices(rows, out);
     p.rows_per_slice = ((rows + want - 1) / want + 7) / 8 * 8;
-    const int slices = (rows + p.rows_per_slice - 1) / p.rows_per_slice;
+    slices = (rows + p.rows_per_slice - 1) / p.rows_per_slice;
     if (dbias != nullptr) p.sums = slices == 1 ? dbias : at<float>(ws, plan.sums);
-    const dim3 grid((static_cast<unsigned>(out) + 255) / 256, static_cast<unsigned>(slices));
-    cudaError_t e;
-    if (f32)
-      e = launch_pdl(dz_kernel<float, float, 3>, grid, dim3(256), 0, s, p);
-    else if (cfg->out_dtype == MOE_F32)
-      e = launch_pdl(dz_kernel<float, __nv_bfloat16, 1>, grid, dim3(256), 0, s, p);
-    else
-      e = launch_pdl(dz_kernel<__nv_bfloat16, __nv_bfloat16, 1>, grid, dim3(256), 0, s, p);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    if (dbias != nullptr && slices > 1) {
-      e = launch_pdl(column_sum_kernel, dim3((static_cast<unsigned>(out) + 127) / 128), dim3(128),
-                     0, s, static_cast<const float*>(p.sums), slices, out, dbias);
-      if (e != cudaSuccess) return MOE_ERR_CUDA;
-    }
+    p.col_blocks = (out + 255) / 256;
+    p.blocks = p.col_blocks * slices;
   }
-
+  if (p.blocks + p.x.blocks + p.w.blocks > 0) {
+    const cudaError_t e = f32 ? launch_dz<float, float, 3>(p, s)
+                          : cfg->out_dtype == MOE_F32
+                              ? launch_dz<float, __nv_bfloat16, 1>(p, s)
+                              : launch_dz<__nv_bfloat16, __nv_bfloat16, 1>(p, s);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
   LinearGemm g{};
   g.planes = f32 ? 3 : 1;
   g.c_f32 = f32;
@@ -573,40 +679,44 @@ extern "C" moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, cons
   g.a = odz.p;
   g.lda = odz.ld;
   g.a_plane = odz.plane;
-  unsigned* err = device_error_word();
+  g.cols = in;
+  g.b_mn = 1;
+  LinearGemm jobs[2];
+  int n = 0;
+  bool sums_left = dbias != nullptr && slices > 1;
   if (dx != nullptr) {
-    Operand ow;
-    cudaError_t e = operand(w, ld.w, out, in, cfg->dtype, plan.pack_w, at<void>(ws, plan.w), sms,
-                            s, &ow);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    g.rows = rows;
-    g.cols = in;
-    g.depth = out;
-    g.a_mn = 0;
-    g.b = ow.p;
-    g.ldb = ow.ld;
-    g.b_plane = ow.plane;
-    g.b_mn = 1;
-    g.c = dx;
-    g.ldc = ld.dx;
-    if (launch_linear_gemm(g, err, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+    LinearGemm& q = jobs[n++] = g;
+    q.rows = rows;
+    q.depth = out;
+    q.b = ow.p;
+    q.ldb = ow.ld;
+    q.b_plane = ow.plane;
+    q.c = dx;
+    q.ldc = ld.dx;
   }
   if (dw != nullptr) {
-    Operand ox;
-    cudaError_t e = operand(x, ld.x, rows, in, cfg->dtype, plan.pack_x, at<void>(ws, plan.x), sms,
-                            s, &ox);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    g.rows = out;
-    g.cols = in;
-    g.depth = rows;
-    g.a_mn = 1;
-    g.b = ox.p;
-    g.ldb = ox.ld;
-    g.b_plane = ox.plane;
-    g.b_mn = 1;
-    g.c = dw;
-    g.ldc = ld.dw;
-    if (launch_linear_gemm(g, err, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+    LinearGemm& q = jobs[n++] = g;
+    q.rows = out;
+    q.depth = rows;
+    q.a_mn = 1;
+    q.b = ox.p;
+    q.ldb = ox.ld;
+    q.b_plane = ox.plane;
+    q.c = dw;
+    q.ldc = ld.dw;
+    if (sums_left && !linear_gemm_on_pairs(q, sms)) {
+      q.sum_parts = p.sums;
+      q.sum_out = dbias;
+      q.sum_slices = slices;
+      sums_left = false;
+    }
   }
-  return MOE_OK;
+  if (sums_left) {
+    const cudaError_t e =
+        launch_pdl(column_sum_kernel, dim3((static_cast<unsigned>(out) + 31) / 32), dim3(256), 0,
+                   s, static_cast<const float*>(p.sums), slices, out, dbias);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (n == 0) return MOE_OK;
+  return status_of(launch_linear_gemms(jobs, n, device_error_word(), sms, s));
 }

@@ -29,8 +29,19 @@ struct LinearGemm {
   long long ldr;
   void* z;
   long long ldz;
+  // tile kernel only: column sums of an earlier pass to finish along the way, or null:
+  // sum_out[i] = sum over s of sum_parts[s][i], i < rows
+  const float* sum_parts;
+  float* sum_out;
+  int sum_slices;
 };
 
-cudaError_t launch_linear_gemm(const LinearGemm& g, unsigned* err, int num_sms, cudaStream_t s);
+// Whether the product runs on CTA pairs (and not in the tile kernel).
+bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms);
+
+// One product, or two with operands and results of the same types and no dependence on each
+// other (in one launch where both suit the tile kernel).
+cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
+                                cudaStream_t s);
 
 }  // namespace moe

@@ -12,16 +12,24 @@
 //
 // Two kernels:
 //  - linear_pair_kernel: persistent CTA pairs (cta_group::2), 256 x 256 tiles, for products
-//    with tiles enough to fill the GPU;
-//  - linear_tile_kernel: one 128 x BN tile per CTA or per cluster, whose CTAs take slices of
+//    with tiles enough to fill the GPU.  It is launched in stream order without overlap with
+//    its neighbours' prologue or tail, and a CTA leaves only after every commit that it asked
+//    for has arrived and its peer has given back its TMEM, so nothing of one launch can reach
+//    into the next;
+//  - linear_tile_kernel: one BA x BN tile per CTA or per cluster, whose CTAs take slices of
 //    the reduction and exchange partial tiles through distributed shared memory, summed in
 //    rank order (deterministic).  For few output rows the operands are swapped, so that the
-//    weights are on the 128-row side and the tokens on a side of 16, 32 or 64.  Its epilogue
-//    warps add the accumulator into registers every `chunk` k-blocks (float32 results): the tensor core truncates
-//    each addition (over 7168 products the mean error is 8e-6 of the result's size, against
-//    2e-7 for rounded additions), which float32 results have to avoid.
+//    weights are on the BA side and the tokens on a side of 16, 32 or 64.  BA = 64 runs the
+//    same 128-row MMA with only the first 64 rows loaded (a row of the result depends on its
+//    own row of A alone): a product bound by streaming one operand then has twice the CTAs to
+//    stream it.  It takes two independent products (the two gradients of a layer) in one
+//    launch, so that the second fills the SMs that the first leaves idle.  Its epilogue warps add the accumulator into registers every `chunk` k-blocks
+//    (float32 results): the tensor core truncates each addition (over 7168 products the mean
+//    error is 8e-6 of the result's size, against 2e-7 for rounded additions).
+#include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -47,17 +55,46 @@ struct Epilogue {
   int vec_c, vec_r, vec_z, vec_bias;  // 16-byte accesses allowed
 };
 
-struct GemmParams {
+struct Job {
   CUtensorMap tm_a, tm_b;
   Epilogue epi;
-  unsigned* err;
   int a_mn, b_mn;
   int num_kb;
-  int chunk;    // k-blocks between register additions (tile kernel)
   int tiles_a;  // tiles along the side of operand A
   int tiles_b;
   int swap;     // operand A carries the output columns (tile kernel)
+  // Column sums to finish (a bias gradient): sum_out[i] = sum_s sum_parts[s][i] over the
+  // output rows i, taken by the tiles of the first column of tiles; or null
+  const float* sum_parts;
+  float* sum_out;
+  int sum_slices;
 };
+
+struct GemmParams {
+  Job job[2];
+  unsigned* err;
+  int first;  // tiles of job[0]; the rest are job[1]'s
+  int total;
+  int chunk;  // k-blocks between register additions (tile kernel)
+};
+
+// The slices of row i's sum, in column_sum_kernel's order: every eighth slice, then the eight
+// partial sums.
+__device__ __forceinline__ void finish_sum(const Job& job, int i) {
+  if (i >= job.epi.rows) return;
+  float part[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int s = 0; s < job.sum_slices; s += 8) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      if (s + w < job.sum_slices)
+        part[w] += __ldg(job.sum_parts + static_cast<size_t>(s + w) * job.epi.rows + i);
+  }
+  float total = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) total += part[w];
+  job.sum_out[i] = total;
+}
 
 // ------------------------------------------------------------------ epilogue ----
 
@@ -205,19 +242,22 @@ __device__ __forceinline__ void load_operand_pair(uint32_t dst, const void* map,
 
 // ---------------------------------------------------------- one tile per CTA ----
 
-template <int BN, int PL>
+template <int BA, int BN, int PL>
 struct TileCfg {
-  static constexpr int kABytes = 128 * BK * 2, kBBytes = BN * BK * 2;
+  static constexpr int kABytes = BA * BK * 2, kBBytes = BN * BK * 2;
   static constexpr int kStageBytes = PL * (kABytes + kBBytes);
   static constexpr int kBarBytes = 256;
-  static constexpr int kStagesRaw = (232448 - 1024 - kBarBytes) / kStageBytes;
+  // The MMA reads 128 rows from an A tile's start: with BA = 64 the second half runs on into
+  // whatever follows (8 KB past the last stage at most).
+  static constexpr int kSlack = BA < 128 ? 8192 : 0;
+  static constexpr int kStagesRaw = (232448 - 1024 - kBarBytes - kSlack) / kStageBytes;
   static constexpr int kStages = kStagesRaw > 12 ? 12 : kStagesRaw;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kSlack;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-  // the exchanged partial tiles reuse the stages: 128 x (BN + 4) floats, or BN rows of
-  // 128 + 4 floats per CTA of the cluster when the operands are swapped
-  static_assert(128 * (BN + 4) * 4 <= kStages * kStageBytes, "partial tile");
-  static_assert(BN * (128 + 4 * 8) * 4 <= kStages * kStageBytes, "swapped partial tile");
+  // the exchanged partial tiles reuse the stages: BA x (BN + 4) floats, or BN rows of
+  // BA + 4 floats per CTA of the cluster when the operands are swapped
+  static_assert(BA * (BN + 4) * 4 <= kStages * kStageBytes, "partial tile");
+  static_assert(BN * (BA + 4 * 8) * 4 <= kStages * kStageBytes, "swapped partial tile");
   static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier region");
 };
 
@@ -227,10 +267,11 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
                : "memory");
 }
 
-template <int BN, int PL, typename TA>
+template <int BA, int BN, int PL>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tile_kernel(const __grid_constant__ GemmParams p) {
-  using Cfg = TileCfg<BN, PL>;
+  using TA = std::conditional_t<PL == 3, float, __nv_bfloat16>;
+  using Cfg = TileCfg<BA, BN, PL>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -249,6 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t nranks;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nranks));
   const int split = static_cast<int>(nranks), rank = static_cast<int>(cluster_ctarank());
+  int tile = static_cast<int>(blockIdx.x) / split;
+  const Job& job = p.job[tile < p.first ? 0 : 1];
+  if (tile >= p.first) tile -= p.first;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -262,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_b);
+    tma_prefetch_desc(&job.tm_a);
+    tma_prefetch_desc(&job.tm_b);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
@@ -276,12 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_trigger();
 
-  const int tile = static_cast<int>(blockIdx.x) / split;
-  const int a0 = (tile % p.tiles_a) * 128, b0 = (tile / p.tiles_a) * BN;
-  // this CTA's slice of the reduction (never empty: split <= num_kb)
-  const int kb0 = static_cast<int>(static_cast<long long>(p.num_kb) * rank / split);
-  const int nkb = static_cast<int>(static_cast<long long>(p.num_kb) * (rank + 1) / split) - kb0;
-  const int R = 128 / split;  // rows of the A side that each CTA finishes
+  const int a0 = (tile % job.tiles_a) * BA, b0 = (tile / job.tiles_a) * BN;
+  // this CTA's slice of the reduction (empty if there are fewer k-blocks than CTAs)
+  const int kb0 = static_cast<int>(static_cast<long long>(job.num_kb) * rank / split);
+  const int nkb = static_cast<int>(static_cast<long long>(job.num_kb) * (rank + 1) / split) - kb0;
+  const int R = BA / split;  // rows of the A side that each CTA finishes
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer ----
@@ -295,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(full_bar(stage), Cfg::kStageBytes);
 #pragma unroll
         for (int pl = 0; pl < PL; ++pl) {
-          load_operand(dst + pl * Cfg::kABytes, &p.tm_a, full_bar(stage), p.a_mn, a0, 128, kb0 + i, pl);
-          load_operand(dst + PL * Cfg::kABytes + pl * Cfg::kBBytes, &p.tm_b, full_bar(stage), p.b_mn,
+          load_operand(dst + pl * Cfg::kABytes, &job.tm_a, full_bar(stage), job.a_mn, a0, BA, kb0 + i, pl);
+          load_operand(dst + PL * Cfg::kABytes + pl * Cfg::kBBytes, &job.tm_b, full_bar(stage), job.b_mn,
                        b0, BN, kb0 + i, pl);
         }
         ++issued;
@@ -305,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       }
-      // drain: no load may still be in flight when the CTA gives up its shared memory
+      // drain: no load or commit may still be in flight when the CTA gives up its shared memory
       const int n = issued < S ? issued : S;
       volatile int no_abort = 0;
       for (int j = 0; j < n; ++j) {
@@ -313,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage = S - 1;
           phase ^= 1u;
         }
-        mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+        if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err))
+          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
       }
     }
     __syncwarp();
@@ -322,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
     if (elect_one_sync()) {
-      const uint32_t idesc = idesc_bf16_f32(128, BN) | (static_cast<uint32_t>(p.a_mn) << 15) |
-                             (static_cast<uint32_t>(p.b_mn) << 16);
-      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+      const uint32_t idesc = idesc_bf16_f32(128, BN) | (static_cast<uint32_t>(job.a_mn) << 15) |
+                             (static_cast<uint32_t>(job.b_mn) << 16);
+      const uint32_t a_step = job.a_mn ? 2048u : 32u, b_step = job.b_mn ? 2048u : 32u;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -354,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qa = PL == 3 ? pa[q] : 0, qb = PL == 3 ? pb[q] : 0;
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk) {
-              tc_mma_bf16(d, operand_desc(a_base + qa * Cfg::kABytes + kk * a_step, p.a_mn),
-                          operand_desc(b_base + qb * Cfg::kBBytes + kk * b_step, p.b_mn), idesc,
+              tc_mma_bf16(d, operand_desc(a_base + qa * Cfg::kABytes + kk * a_step, job.a_mn),
+                          operand_desc(b_base + qb * Cfg::kBBytes + kk * b_step, job.b_mn), idesc,
                           accumulate);
               accumulate = 1u;
             }
@@ -380,6 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue ----
     const int quad = warp & 3;
+    if (job.sum_parts != nullptr && rank == 0 && (job.swap ? a0 : b0) == 0 &&
+        quad * 32 + lane < (job.swap ? BN : BA))
+      finish_sum(job, (job.swap ? b0 : a0) + quad * 32 + lane);
+    __syncwarp();
     float acc[BN];
 #pragma unroll
     for (int j = 0; j < BN; ++j) acc[j] = 0.f;
@@ -416,9 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     // this CTA's partial tile, row by row to the CTA that finishes the row
     const int row = quad * 32 + lane;
-    const int owner = row / R, local = row - owner * R;
+    const int owner = min(row / R, split - 1), local = row - owner * R;
     const uint32_t base = mapa_shared(smem_u32(smem), static_cast<uint32_t>(owner));
-    if (!p.swap) {
+    if (row >= BA) {
+      // rows that were not loaded
+    } else if (!job.swap) {
       const uint32_t at = base + static_cast<uint32_t>(((rank * R + local) * (BN + 4)) * 4);
 #pragma unroll
       for (int j = 0; j < BN; j += 4)
@@ -435,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // sum the slices in rank order and finish eight neighbouring columns per thread and step
   if (*abort_flag == 0) {
     const float* part = reinterpret_cast<const float*>(smem);
-    const int out_rows = p.swap ? BN : R, out_cols = p.swap ? R : BN;
+    const int out_rows = job.swap ? BN : R, out_cols = job.swap ? R : BN;
     const int stride = out_cols + 4, slice = out_rows * stride;
-    const int row0 = p.swap ? b0 : a0 + rank * R, col0 = p.swap ? a0 + rank * R : b0;
+    const int row0 = job.swap ? b0 : a0 + rank * R, col0 = job.swap ? a0 + rank * R : b0;
     const int per_row = out_cols / 8;
     for (int it = threadIdx.x; it < out_rows * per_row; it += kThreads) {
       const int r = it / per_row, c = (it - r * per_row) * 8;
-      if (row0 + r >= p.epi.rows || col0 + c >= p.epi.cols) continue;
+      if (row0 + r >= job.epi.rows || col0 + c >= job.epi.cols) continue;
       float v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = 0.f;
@@ -451,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
         v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
       }
-      finish8<TA>(p.epi, row0 + r, col0 + c, v);
+      finish8<TA>(job.epi, row0 + r, col0 + c, v);
     }
   }
   tc_fence_before();
@@ -483,7 +533,7 @@ struct PairCfg {
 };
 
 // Tiles in chunks of 8 rows of tiles, so that the pairs at work share operand tiles in L2.
-__device__ __forceinline__ void pair_tile(const GemmParams& p, int idx, int* ta, int* tb) {
+__device__ __forceinline__ void pair_tile(const Job& p, int idx, int* ta, int* tb) {
   constexpr int kSwz = 8;
   const int per = kSwz * p.tiles_b;
   const int c = idx / per, in = idx - c * per;
@@ -492,8 +542,13 @@ __device__ __forceinline__ void pair_tile(const GemmParams& p, int idx, int* ta,
   *ta = c * kSwz + in - *tb * h;
 }
 
+struct PairParams {
+  Job job;
+  unsigned* err;
+};
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
-    linear_pair_kernel(const __grid_constant__ GemmParams p) {
+    linear_pair_kernel(const __grid_constant__ PairParams p) {
   using Cfg = PairCfg;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -524,8 +579,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_b);
+    tma_prefetch_desc(&p.job.tm_a);
+    tma_prefetch_desc(&p.job.tm_b);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
@@ -536,10 +591,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   cluster_sync_all();  // the peer's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dep_wait();
-  grid_dep_trigger();
 
-  const int total = p.tiles_a * p.tiles_b;
+  const Job& job = p.job;
+  const int total = job.tiles_a * job.tiles_b;
   const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
 
   if (warp == 0) {
@@ -551,10 +605,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       bool ok = true;
       for (int idx = pair; ok && idx < total; idx += npairs) {
         int ta, tb;
-        pair_tile(p, idx, &ta, &tb);
+        pair_tile(job, idx, &ta, &tb);
         const int a_row = ta * 256 + static_cast<int>(rank) * 128;
         const int b_row = tb * 256 + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = 0; kb < job.num_kb; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
@@ -562,8 +616,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           const uint32_t fb = mapa_shared(full_bar(stage), 0);
           const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * Cfg::kStageBytes);
-          load_operand_pair(dst, &p.tm_a, fb, p.a_mn, a_row, kb);
-          load_operand_pair(dst + Cfg::kABytes, &p.tm_b, fb, p.b_mn, b_row, kb);
+          load_operand_pair(dst, &job.tm_a, fb, job.a_mn, a_row, kb);
+          load_operand_pair(dst + Cfg::kABytes, &job.tm_b, fb, job.b_mn, b_row, kb);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -571,26 +625,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           }
         }
       }
-      if (rank == 0) {
-        // drain: both CTAs' loads complete on the even CTA's barriers
-        const int n = issued < S ? static_cast<int>(issued) : S;
-        volatile int no_abort = 0;
-        for (int j = 0; j < n; ++j) {
-          if (--stage < 0) {
-            stage = S - 1;
-            phase ^= 1u;
-          }
-          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+      // drain: wait until the last commits have arrived here (they follow the loads and the
+      // MMAs); if the pipeline gave up, at least for the loads, both CTAs' of which complete on
+      // the even CTA's barriers
+      const int n = issued < S ? static_cast<int>(issued) : S;
+      volatile int no_abort = 0;
+      for (int j = 0; j < n; ++j) {
+        if (--stage < 0) {
+          stage = S - 1;
+          phase ^= 1u;
         }
+        if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err) && rank == 0)
+          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
     if (rank == 0 && elect_one_sync()) {
-      const uint32_t idesc = idesc_bf16_f32(256, Cfg::kBN) | (static_cast<uint32_t>(p.a_mn) << 15) |
-                             (static_cast<uint32_t>(p.b_mn) << 16);
-      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+      const uint32_t idesc = idesc_bf16_f32(256, Cfg::kBN) |
+                             (static_cast<uint32_t>(job.a_mn) << 15) |
+                             (static_cast<uint32_t>(job.b_mn) << 16);
+      const uint32_t a_step = job.a_mn ? 2048u : 32u, b_step = job.b_mn ? 2048u : 32u;
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
@@ -602,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::kBN);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = 0; kb < job.num_kb; ++kb) {
           if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
             ok = false;
             break;
@@ -612,8 +668,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           const uint32_t b_base = a_base + Cfg::kABytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, p.a_mn),
-                             operand_desc(b_base + kk * b_step, p.b_mn), idesc,
+            tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, job.a_mn),
+                             operand_desc(b_base + kk * b_step, job.b_mn), idesc,
                              (kb | kk) != 0 ? 1u : 0u);
           tc_commit_pair(empty_bar(stage), 0x3);
           if (++stage == S) {
@@ -634,16 +690,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     // ------------------------------------------------------------ epilogue ----
     const int quad = warp & 3, half = (warp - 2) >> 2;
     float* stg = stg_all + (warp - 2) * 32 * Cfg::kStgRow;
-    const bool wide = p.epi.vec_c && (p.epi.res == nullptr || p.epi.vec_r) &&
-                      (p.epi.z == nullptr || p.epi.vec_z) && p.epi.vec_bias;
+    const bool wide = job.epi.vec_c && (job.epi.res == nullptr || job.epi.vec_r) &&
+                      (job.epi.z == nullptr || job.epi.vec_z) && job.epi.vec_bias;
     int local = 0;
     for (int idx = pair; idx < total; idx += npairs, ++local) {
       int ta, tb;
-      pair_tile(p, idx, &ta, &tb);
+      pair_tile(job, idx, &ta, &tb);
       const int acc = local & 1;
       const int row0 = ta * 256 + static_cast<int>(rank) * 128 + quad * 32;
       const int col0 = tb * 256 + half * 128;
-      const bool inside = wide && row0 + 32 <= p.epi.rows && col0 + 128 <= p.epi.cols;
+      const bool inside = wide && row0 + 32 <= job.epi.rows && col0 + 128 <= job.epi.cols;
       const bool ready =
           mbar_wait(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err);
       if (__any_sync(0xffffffffu, !ready)) break;
@@ -656,7 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       for (int c = 0; c < 128; c += Cfg::kChunk) {
         const int row = row0 + rr, col = col0 + c + cc;
         float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (inside && p.epi.bias != nullptr) load_n(p.epi.bias + col, 8, true, bias);
+        if (inside && job.epi.bias != nullptr) load_n(job.epi.bias + col, 8, true, bias);
         uint32_t r[16];
         tmem_ld_32x32b_x16(t + c, r);
         tmem_ld_wait();
@@ -677,15 +733,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           load_n(stg + (rr + 16 * i) * Cfg::kStgRow + cc, 8, true, v[i]);
         __syncwarp();
         if (inside) {
-          finish8_inside(p.epi, row, 16, col, bias, v);
+          finish8_inside(job.epi, row, 16, col, bias, v);
         } else {
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
-            if (row + 16 * i < p.epi.rows && col < p.epi.cols) {
+            if (row + 16 * i < job.epi.rows && col < job.epi.cols) {
               float u[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) u[q] = i == 0 ? v[0][q] : v[1][q];
-              finish8<__nv_bfloat16>(p.epi, row + 16 * i, col, u);
+              finish8<__nv_bfloat16>(job.epi, row + 16 * i, col, u);
             }
           }
         }
@@ -697,6 +753,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
   cluster_sync_all();  // no peer still reads this CTA's shared memory or arrives on it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+  __syncwarp();
+  cluster_sync_all();  // the pair gives its TMEM back before either CTA leaves
 }
 
 // ---------------------------------------------------------------------- host ----
@@ -739,28 +797,63 @@ cudaError_t allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int BN, int PL, typename TA>
-cudaError_t launch_tile(const GemmParams& p, int split, cudaStream_t s) {
-  auto kernel = linear_tile_kernel<BN, PL, TA>;
-  cudaError_t e = allow_smem(kernel, TileCfg<BN, PL>::kSmem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t lc;
-  std::memset(&lc, 0, sizeof(lc));
-  lc.gridDim = dim3(static_cast<unsigned>(p.tiles_a) * static_cast<unsigned>(p.tiles_b) *
-                    static_cast<unsigned>(split));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = TileCfg<BN, PL>::kSmem;
-  lc.stream = s;
-  cudaLaunchAttribute attr[2];
+// A cluster launch of `split` CTAs per tile.
+template <int BA, int BN, int PL>
+void tile_launch(int tiles, int split, cudaStream_t s, cudaLaunchConfig_t* lc,
+                 cudaLaunchAttribute (&attr)[2]) {
+  std::memset(lc, 0, sizeof(*lc));
+  lc->gridDim = dim3(static_cast<unsigned>(tiles) * static_cast<unsigned>(split));
+  lc->blockDim = dim3(kThreads);
+  lc->dynamicSmemBytes = TileCfg<BA, BN, PL>::kSmem;
+  lc->stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = static_cast<unsigned>(split);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 2;
+  lc->attrs = attr;
+  lc->numAttrs = 2;
+}
+
+template <int BA, int BN, int PL>
+cudaError_t launch_tile(const GemmParams& p, int split, cudaStream_t s) {
+  auto kernel = linear_tile_kernel<BA, BN, PL>;
+  cudaError_t e = allow_smem(kernel, TileCfg<BA, BN, PL>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc;
+  cudaLaunchAttribute attr[2];
+  tile_launch<BA, BN, PL>(p.total, split, s, &lc, attr);
   return count_launch(cudaLaunchKernelEx(&lc, kernel, p));
+}
+
+// Clusters of 1, 2, 4 and 8 CTAs (one CTA per SM) that the device holds at a time: fewer than
+// SMs / size, as a cluster stays within one group of SMs (GB300: 152, 76, 36, 15).
+struct ClusterRoom {
+  int room[4];
+};
+const ClusterRoom& cluster_room(int num_sms) {
+  static ClusterRoom rooms[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  dev &= 63;
+  std::call_once(once[dev], [&] {
+    for (int i = 0; i < 4; ++i) {
+      rooms[dev].room[i] = num_sms >> i;
+      if (i == 0) continue;
+      cudaLaunchConfig_t lc;
+      cudaLaunchAttribute attr[2];
+      auto kernel = linear_tile_kernel<128, 128, 1>;
+      int n = 0;
+      if (allow_smem(kernel, TileCfg<128, 128, 1>::kSmem) != cudaSuccess) continue;
+      tile_launch<128, 128, 1>(1, 1 << i, nullptr, &lc, attr);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc) == cudaSuccess && n > 0)
+        rooms[dev].room[i] = n;
+    }
+    cudaGetLastError();  // leave no sticky error behind
+  });
+  return rooms[dev];
 }
 
 inline int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
@@ -781,88 +874,182 @@ bool prefer_pairs(const LinearGemm& g, int num_sms) {
   return 16 * waves_p <= 10 * waves_t && tt > num_sms;
 }
 
-}  // namespace
+// How an output and its operands lie on the tile kernel's sides.
+struct Sides {
+  bool swap;
+  int a, b;        // rows of the A and of the B side
+  int a_mn, b_mn;
+};
+Sides sides_of(const LinearGemm& g) {
+  // few output rows: the other operand on the side of 128 (or 64) rows
+  const bool swap = g.rows <= 64 && g.cols > g.rows;
+  return swap ? Sides{true, g.cols, g.rows, g.b_mn, g.a_mn}
+              : Sides{false, g.rows, g.cols, g.a_mn, g.b_mn};
+}
 
-cudaError_t launch_linear_gemm(const LinearGemm& g, unsigned* err, int num_sms, cudaStream_t s) {
-  if (g.rows == 0 || g.cols == 0) return cudaSuccess;
+struct TileChoice {
+  int ba, bn, split;
+};
+
+// The tile and the split of the reduction, by an estimate in SM clocks: waves of clusters times
+// (a CTA's k-blocks at the slower of 60 bytes per clock into shared memory and the MMA rate of
+// BN / 2 clocks per 16 products, plus the pipeline's fill, the exchange and the epilogue).
+TileChoice choose_tile(const LinearGemm* jobs, int n, int num_sms) {
+  const ClusterRoom& room = cluster_room(num_sms);
+  const int planes = jobs[0].planes;
+  TileChoice best{128, 128, 1};
+  double best_cost = 1e30;
+  for (int ba = 64; ba <= 128; ba *= 2)
+    for (int bn = 16; bn <= 128; bn *= 2) {
+      if (ba == 64 && bn == 128) continue;
+      bool fits = true;
+      long long tiles = 0;
+      int num_kb = 0;
+      for (int i = 0; i < n; ++i) {
+        const Sides sd = sides_of(jobs[i]);
+        // row-contiguous boxes are 64 rows wide
+        if (sd.b_mn && bn < 64) fits = false;
+        tiles += static_cast<long long>(ceil_div(sd.a, ba)) * ceil_div(sd.b, bn);
+        num_kb = std::max(num_kb, ceil_div(jobs[i].depth, BK));
+      }
+      if (!fits) continue;
+      const int terms = planes == 3 ? 6 : 1;
+      const double load = planes * (ba + bn) * 128.0 / 60.0, mma = 4.0 * terms * bn * 0.52;
+      for (int i = 0; i < 4; ++i) {
+        const int split = 1 << i;
+        if (split > num_kb) continue;
+        const long long waves = (tiles + room.room[i] - 1) / room.room[i];
+        const double per_tile = ceil_div(num_kb, split) * (load > mma ? load : mma) + 4000.0 +
+                                (split > 1 ? 1000.0 : 0.0) + 0.25 * ba * bn / split;
+        const double cost = waves * per_tile;
+        if (cost < best_cost) {
+          best_cost = cost;
+          best = TileChoice{ba, bn, split};
+        }
+      }
+    }
+  return best;
+}
+
+Epilogue epilogue_of(const LinearGemm& g) {
+  const int ab = g.act_f32 ? 4 : 2;
+  Epilogue e;
+  e.c = g.c;
+  e.bias = g.bias;
+  e.res = g.res;
+  e.z = g.z;
+  e.ldc = g.ldc;
+  e.ldr = g.ldr;
+  e.ldz = g.ldz;
+  e.rows = g.rows;
+  e.cols = g.cols;
+  e.act = g.act;
+  e.c_f32 = g.c_f32;
+  e.vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2);
+  e.vec_r = vec_ok(g.res, g.ldr, ab);
+  e.vec_z = vec_ok(g.z, g.ldz, ab);
+  e.vec_bias = vec_ok(g.bias, 0, 4);
+  return e;
+}
+
+cudaError_t launch_pairs(const LinearGemm& g, unsigned* err, int num_sms, cudaStream_t s) {
+  PairParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.err = err;
+  Job& j = p.job;
+  if (!operand_map(&j.tm_a, g.a, g.rows, g.depth, g.a_mn, g.lda, 1, 0, 128) ||
+      !operand_map(&j.tm_b, g.b, g.cols, g.depth, g.b_mn, g.ldb, 1, 0, 128))
+    return cudaErrorInvalidValue;
+  j.epi = epilogue_of(g);
+  j.a_mn = g.a_mn;
+  j.b_mn = g.b_mn;
+  j.num_kb = ceil_div(g.depth, BK);
+  j.tiles_a = ceil_div(g.rows, 256);
+  j.tiles_b = ceil_div(g.cols, 256);
+  const long long tiles = static_cast<long long>(j.tiles_a) * j.tiles_b;
+  if (tiles >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  // a plain launch: see the top of the file
+  linear_pair_kernel<<<dim3(2 * pairs), dim3(PairCfg::kThreads), PairCfg::kSmem, s>>>(p);
+  return count_launch(cudaGetLastError());
+}
+
+cudaError_t launch_tiles(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
+                         cudaStream_t s) {
   GemmParams p;
   std::memset(&p, 0, sizeof(p));
-  const int ab = g.act_f32 ? 4 : 2;
-  p.epi.c = g.c;
-  p.epi.bias = g.bias;
-  p.epi.res = g.res;
-  p.epi.z = g.z;
-  p.epi.ldc = g.ldc;
-  p.epi.ldr = g.ldr;
-  p.epi.ldz = g.ldz;
-  p.epi.rows = g.rows;
-  p.epi.cols = g.cols;
-  p.epi.act = g.act;
-  p.epi.c_f32 = g.c_f32;
-  p.epi.vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2);
-  p.epi.vec_r = vec_ok(g.res, g.ldr, ab);
-  p.epi.vec_z = vec_ok(g.z, g.ldz, ab);
-  p.epi.vec_bias = vec_ok(g.bias, 0, 4);
   p.err = err;
-  p.num_kb = ceil_div(g.depth, BK);
-
-  if (prefer_pairs(g, num_sms)) {
-    if (!operand_map(&p.tm_a, g.a, g.rows, g.depth, g.a_mn, g.lda, 1, 0, 128) ||
-        !operand_map(&p.tm_b, g.b, g.cols, g.depth, g.b_mn, g.ldb, 1, 0, 128))
+  const TileChoice t = choose_tile(jobs, n, num_sms);
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    const LinearGemm& g = jobs[i];
+    Job& j = p.job[i];
+    const Sides sd = sides_of(g);
+    if (!operand_map(&j.tm_a, sd.swap ? g.b : g.a, sd.a, g.depth, sd.a_mn, sd.swap ? g.ldb : g.lda,
+                     g.planes, sd.swap ? g.b_plane : g.a_plane, t.ba) ||
+        !operand_map(&j.tm_b, sd.swap ? g.a : g.b, sd.b, g.depth, sd.b_mn, sd.swap ? g.lda : g.ldb,
+                     g.planes, sd.swap ? g.a_plane : g.b_plane, t.bn))
       return cudaErrorInvalidValue;
-    p.a_mn = g.a_mn;
-    p.b_mn = g.b_mn;
-    p.tiles_a = ceil_div(g.rows, 256);
-    p.tiles_b = ceil_div(g.cols, 256);
-    cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem);
-    if (e != cudaSuccess) return e;
-    const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
-    const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_pdl(linear_pair_kernel, dim3(2 * pairs), dim3(PairCfg::kThreads), PairCfg::kSmem, s, p);
+    j.epi = epilogue_of(g);
+    j.swap = sd.swap ? 1 : 0;
+    j.a_mn = sd.a_mn;
+    j.b_mn = sd.b_mn;
+    j.num_kb = ceil_div(g.depth, BK);
+    j.tiles_a = ceil_div(sd.a, t.ba);
+    j.tiles_b = ceil_div(sd.b, t.bn);
+    j.sum_parts = g.sum_parts;
+    j.sum_out = g.sum_out;
+    j.sum_slices = g.sum_slices;
+    total += static_cast<long long>(j.tiles_a) * j.tiles_b;
+    if (i == 0) p.first = static_cast<int>(total);
   }
-
-  // few output rows: the other operand on the 128-row side
-  const bool swap = g.rows <= 64 && g.cols > g.rows;
-  const int narrow = swap ? g.rows : g.cols;
-  const int narrow_mn = swap ? g.a_mn : g.b_mn;
-  int bn = narrow <= 16 ? 16 : narrow <= 32 ? 32 : narrow <= 64 ? 64 : 128;
-  if (narrow_mn && bn < 64) bn = 64;  // row-contiguous boxes are 64 rows wide
-  const void* wa = swap ? g.b : g.a;
-  const void* wb = swap ? g.a : g.b;
-  p.a_mn = swap ? g.b_mn : g.a_mn;
-  p.b_mn = narrow_mn;
-  const int a_rows = swap ? g.cols : g.rows;
-  if (!operand_map(&p.tm_a, wa, a_rows, g.depth, p.a_mn, swap ? g.ldb : g.lda, g.planes,
-                   swap ? g.b_plane : g.a_plane, 128) ||
-      !operand_map(&p.tm_b, wb, narrow, g.depth, p.b_mn, swap ? g.lda : g.ldb, g.planes,
-                   swap ? g.a_plane : g.b_plane, bn))
-    return cudaErrorInvalidValue;
-  p.swap = swap ? 1 : 0;
-  p.tiles_a = ceil_div(a_rows, 128);
-  p.tiles_b = ceil_div(narrow, bn);
+  if (total * t.split >= (1ll << 31)) return cudaErrorInvalidValue;
+  p.total = static_cast<int>(total);
   // bf16 results are rounded far above the tensor core's own error: one chunk.  Float32 ones
   // leave it after 128 (six products per value, so the drain still hides behind the MMAs) or
   // 256 values
-  p.chunk = g.planes == 3 ? 2 : g.c_f32 ? 4 : 1 << 30;
-  // a cluster of up to 8 CTAs shares a tile's reduction while SMs would idle otherwise, each
-  // with at least four k-blocks
-  const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= num_sms && p.num_kb >= split * 2 * 4) split *= 2;
-  if (g.planes == 3) {
-    switch (bn) {
-      case 16: return launch_tile<16, 3, float>(p, split, s);
-      case 32: return launch_tile<32, 3, float>(p, split, s);
-      case 64: return launch_tile<64, 3, float>(p, split, s);
-      default: return launch_tile<128, 3, float>(p, split, s);
+  p.chunk = jobs[0].planes == 3 ? 2 : jobs[0].c_f32 ? 4 : 1 << 30;
+  auto go = [&](auto pl) {
+    constexpr int PL = decltype(pl)::value;
+    if (t.ba == 64) {
+      switch (t.bn) {
+        case 16: return launch_tile<64, 16, PL>(p, t.split, s);
+        case 32: return launch_tile<64, 32, PL>(p, t.split, s);
+        default: return launch_tile<64, 64, PL>(p, t.split, s);
+      }
     }
+    switch (t.bn) {
+      case 16: return launch_tile<128, 16, PL>(p, t.split, s);
+      case 32: return launch_tile<128, 32, PL>(p, t.split, s);
+      case 64: return launch_tile<128, 64, PL>(p, t.split, s);
+      default: return launch_tile<128, 128, PL>(p, t.split, s);
+    }
+  };
+  return jobs[0].planes == 3 ? go(std::integral_constant<int, 3>{})
+                             : go(std::integral_constant<int, 1>{});
+}
+
+}  // namespace
+
+bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms) { return prefer_pairs(g, num_sms); }
+
+cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
+                                cudaStream_t s) {
+  if (n == 2 && !prefer_pairs(jobs[0], num_sms) && !prefer_pairs(jobs[1], num_sms)) {
+    // the longer tiles first: the shorter ones fill the last wave better
+    const int longer = jobs[0].depth >= jobs[1].depth ? 0 : 1;
+    const LinearGemm by_depth[2] = {jobs[longer], jobs[1 - longer]};
+    return launch_tiles(by_depth, 2, err, num_sms, s);
   }
-  switch (bn) {
-    case 16: return launch_tile<16, 1, __nv_bfloat16>(p, split, s);
-    case 32: return launch_tile<32, 1, __nv_bfloat16>(p, split, s);
-    case 64: return launch_tile<64, 1, __nv_bfloat16>(p, split, s);
-    default: return launch_tile<128, 1, __nv_bfloat16>(p, split, s);
+  for (int i = 0; i < n; ++i) {
+    const cudaError_t e = prefer_pairs(jobs[i], num_sms)
+                              ? launch_pairs(jobs[i], err, num_sms, s)
+                              : launch_tiles(jobs + i, 1, err, num_sms, s);
+    if (e != cudaSuccess) return e;
   }
+  return cudaSuccess;
 }
 
 }  // namespace moe
