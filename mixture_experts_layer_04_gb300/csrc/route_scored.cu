@@ -6,21 +6,22 @@
 //
 // The choice.  It is defined on 64-bit keys s[e] + bias[e], and 64-bit arithmetic is slow on
 // this GPU (16 clocks per warp instruction), so it is taken in float first and certified:
-// every float score carries a bound on its error.  Neighbouring choices (the K-th and the
-// first one left out among them) closer than the sum of their bounds are put in order by
-// their 64-bit keys, K+1 lanes at once; groups whose sums cannot be told apart at the border
-// between kept and dropped are compared by 64-bit sums; and only if the first two experts
-// left out are close to the last one kept is the whole token chosen again.  Without a bias
-// the keys are ordered as the logits are, so the logits themselves are compared, exactly.
-// Two experts of equal logit and equal bias tie in any precision and need no second look.
+// every float score carries a bound on its error.  Where two neighbouring choices (the K-th
+// and the first one left out among them) are closer than the sum of their bounds, the K+1
+// best are put in order by their 64-bit keys, one per lane; groups whose sums cannot be told
+// apart at the border between kept and dropped are compared by 64-bit sums; and only if in
+// such a case the first two experts left out are close to each other too is the whole token
+// chosen again.  Without a bias the keys are ordered as the logits are, so the logits
+// themselves are compared.  Two experts of equal logit and equal bias tie in any precision.
 //
-// The K+1 best come from the lanes' own two best, kept in order in registers: a step is one
-// warp-wide maximum, a ballot and a shuffle, and a lane that has given both away looks for its
-// next two.  (Searching all registers in every step took three times the instructions.)
+// The K+1 best come from each lane's own four best, kept in order in registers as integers:
+// the float's bits made monotone, the last log2(NJ) of them replaced by the register's number
+// (the bounds count that rounding).  Keeping them in order is then minima and maxima alone,
+// and a step is one warp-wide maximum, a ballot and a shuffle.
 //
 // What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
-// written, but the instructions come first: about 600 per token.  At one token the launch is
-// all there is.
+// written, but the instructions come first, most of them on the half-rate integer and compare
+// pipe (ncu: 70% busy).  At one token the launch is all there is.
 #include <cfloat>
 #include <type_traits>
 
@@ -141,7 +142,7 @@ __device__ __forceinline__ double score64(float l, float m, double sum) {
 template <int NJ, typename TL>
 __device__ __forceinline__ double softmax_sum64(const TL* row, int E, float m, int lane) {
   double sum = 0.0;
-#pragma unroll 1
+#pragma unroll 4
   for (int j = 0; j < NJ; ++j) {
     const int e = lane * NJ + j;
     const float l = e < E ? clean_logit(to_float(row[e])) : -INFINITY;
@@ -247,12 +248,15 @@ __device__ __noinline__ int choose64(const RouteParams& p, const TL* row, float 
 }
 
 // Puts the experts in lanes 0..K (-1 from the first empty lane on) in the order of their
-// 64-bit keys, ties to the lower expert.
+// 64-bit keys, or of their logits where those decide, ties to the lower expert.
 template <int NJ, typename TL, bool kSig>
 __device__ __noinline__ int order64(const RouteParams& p, const TL* row, float m, int lane,
-                                    int mine, float l, float b) {
-  const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
-  const double key = score64<kSig>(l, m, sum) + static_cast<double>(b);
+                                    int mine, float l, float b, bool by_logit) {
+  double key = l;
+  if (!by_logit) {
+    const double sum = kSig ? 0.0 : softmax_sum64<NJ, TL>(row, p.E, m, lane);
+    key = score64<kSig>(l, m, sum) + static_cast<double>(b);
+  }
   const int n = __popc(__ballot_sync(0xffffffffu, mine >= 0));
   int rank = 0;
 #pragma unroll 1
@@ -271,15 +275,21 @@ __device__ __noinline__ int order64(const RouteParams& p, const TL* row, float m
   return out;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // A float score and a bound on its absolute error, in units of 2^-23 of the score: the
 // hardware exponential is off by at most 2 + 1.17 |x| of them.  Logistic function: for l > 0
-// that is damped by 1 - s to 1.1, the sum and the division add under 3.  Softmax: the sum adds
-// its terms' mean error (|x| averages at most ln 1024) and its additions' roundings, 17 in all,
-// the products 2.
+// that is damped by 1 - s to 1.1, the sum and the reciprocal add under 3.  Softmax: the sum
+// adds its terms' mean error (|x| averages at most ln 1024) and its additions' roundings, 17
+// in all, the products 2.  Scores under 2^-126 may come out as 0, which the bounds' floor
+// covers.
 template <bool kSig>
 __device__ __forceinline__ float score_of(float l, float m, float inv_sum) {
-  // below -80 the score is under 2e-35, which the bound's floor covers
-  if (kSig) return l < -80.f ? 0.f : __fdividef(1.0f, 1.0f + __expf(-l));
+  if (kSig) return rcp_approx(1.0f + __expf(-l));
   return __expf(l - m) * inv_sum;
 }
 template <bool kSig>
@@ -294,17 +304,61 @@ struct Pick {
   float l, b, key, err;
 };
 
-// Whether the order of two picks, a before b, is open to doubt in float.
+// Without a bias the order of the scores is the order of the logits, but scores a few 2^-53 of
+// their size apart may round together in 64 bits.  a.l >= b.l here.
 template <bool kSig>
-__device__ __forceinline__ bool in_doubt(const Pick& a, const Pick& b, bool has_bias, float m) {
-  if (a.l == b.l && a.b == b.b) return false;  // a tie in any precision
+__device__ __forceinline__ bool scores_merge(const Pick& a, const Pick& b, float m) {
+  const float gap = a.l - b.l;
+  if (kSig) return a.l > 80.f || b.l < -600.f || !(__fdividef(gap, 1.0f + __expf(a.l)) > 1e-14f);
+  return !(gap > 1e-14f) || b.l - m < -600.f;
+}
+
+// Whether a and b, a before b, are too close for their order as ordered keys (rounded to
+// `unit`) to be relied on.
+template <bool kSig>
+__device__ __forceinline__ bool close(const Pick& a, const Pick& b, bool has_bias, float m,
+                                      float unit) {
   if (has_bias)
     return !(a.key - b.key >
-             a.err + b.err + 2.0f * kErrFloor + 0x1p-23f * (fabsf(a.key) + fabsf(b.key)));
-  // no bias: a.l > b.l, but a few 2^-53 of the score apart the 64-bit scores may round together
-  if (kSig)
-    return a.l > 80.f || b.l < -600.f || !(__fdividef(a.l - b.l, 1.0f + __expf(a.l)) > 1e-14f);
-  return !(a.l - b.l > 1e-14f) || b.l - m < -600.f;
+             a.err + b.err + 2.0f * kErrFloor + unit * (fabsf(a.key) + fabsf(b.key)));
+  return !(a.l - b.l > unit * (fabsf(a.l) + fabsf(b.l)) + 1e-30f) || scores_merge<kSig>(a, b, m);
+}
+
+// Descending order of two, and of four.
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void order4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  order2(a, b);
+  order2(c, d);
+  order2(a, c);
+  order2(b, d);
+  order2(b, c);
+}
+
+// The four largest of v[0..NJ-1] (zeros after them), descending.
+template <int NJ>
+__device__ __forceinline__ void four_best(const uint32_t (&v)[NJ], uint32_t (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = i < NJ ? v[i < NJ ? i : 0] : 0u;
+  if constexpr (NJ == 2) order2(o[0], o[1]);
+  if constexpr (NJ >= 4) order4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+  for (int j = 4; j < NJ; j += 4) {
+    uint32_t q0 = v[j], q1 = v[j + 1], q2 = v[j + 2], q3 = v[j + 3];
+    order4(q0, q1, q2, q3);
+    // the larger of opposite ends: the four best of the eight, as a bitonic sequence
+    o[0] = max(o[0], q3);
+    o[1] = max(o[1], q2);
+    o[2] = max(o[2], q1);
+    o[3] = max(o[3], q0);
+    order2(o[0], o[2]);
+    order2(o[1], o[3]);
+    order2(o[0], o[1]);
+    order2(o[2], o[3]);
+  }
 }
 
 template <int NJ, typename TL, bool kSig>
@@ -335,9 +389,15 @@ __global__ void __launch_bounds__(32 * kWarps)
     inv_sum = 1.0f / warp_sum(sum);
   }
 
-  // `ord` orders the experts by their keys (0 = not available)
+  // `ord` orders the experts by their keys; those at kNone or below are not available
+  constexpr uint32_t kLow = NJ - 1, kNone = 0x007fffffu;  // kNone: -inf's
+  auto order_key = [](float v, int j) {
+    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 counts as +0
+    const uint32_t mono = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+    return (mono & ~kLow) | (kLow - static_cast<uint32_t>(j));
+  };
   const bool grouped = p.top_groups < p.groups;
-  uint32_t ord[NJ];
+  uint32_t ord[NJ], best[4];
   uint32_t live = 0xffffffffu;  // groups in play
   if (has_bias || grouped) {
     float key[NJ], b[NJ];
@@ -350,16 +410,17 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const float k = score_of<kSig>(l[j], m, inv_sum) + b[j];
-      const bool ok = l[j] > -INFINITY && b[j] > -INFINITY;
-      key[j] = ok ? k : -INFINITY;
-      ord[j] = !ok ? 0u : float_key(has_bias ? k : l[j]);
+      key[j] = l[j] > -INFINITY && k > -INFINITY ? k : -INFINITY;
+      ord[j] = order_key(has_bias ? key[j] : l[j], j);
     }
+    four_best<NJ>(ord, best);
     if (grouped) {
       // the group's best one or two keys, for group g in lane g
       float v1 = -INFINITY, v2 = -INFINITY;
       const int lanes = p.per / NJ;
-      if (p.per % NJ == 0 && (lanes & (lanes - 1)) == 0) {
-        // whole lanes per group: best two of each lane, then of neighbouring lanes
+      const bool whole_lanes = p.per % NJ == 0;
+      if (whole_lanes && (lanes & (lanes - 1)) == 0) {
+        // a power of two of lanes per group: best two of each lane, then of neighbouring lanes
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           v2 = fmaxf(v2, fminf(v1, key[j]));
@@ -418,58 +479,60 @@ __global__ void __launch_bounds__(32 * kWarps)
           live = sure | __ballot_sync(0xffffffffu, contested && before < p.top_groups - __popc(sure));
         }
       }
-      int g = e0 / p.per, r = e0 - g * p.per;
+      int g = e0 / p.per;
+      if (whole_lanes) {  // a lane's experts are of one group
+        if (!((live >> (g & 31)) & 1u)) best[0] = best[1] = best[2] = best[3] = 0u;
+      } else {
+        int r = e0 - g * p.per;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
-        if (++r == p.per) {
-          r = 0;
-          ++g;
+        for (int j = 0; j < NJ; ++j) {
+          if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
+          if (++r == p.per) {
+            r = 0;
+            ++g;
+          }
         }
+        four_best<NJ>(ord, best);
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) ord[j] = l[j] > -INFINITY ? float_key(l[j]) : 0u;
+    for (int j = 0; j < NJ; ++j) ord[j] = order_key(l[j], j);
+    four_best<NJ>(ord, best);
   }
 
-  // this lane's two best still in play, in order (ties: the lower register first)
-  uint32_t o1 = 0u, o2 = 0u;
-  int j1 = 0, j2 = 0, held = 2;
+  // Takes the best expert still in play: its lane and ordered key (uniform over the warp), or
+  // lane -1.  The register numbers do not count between lanes: among equal keys the lower lane.
+  int held = 4;
+  auto take_best = [&](uint32_t* taken) {
+    const uint32_t first = best[0] & ~kLow;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, first);
+    if (top <= kNone) return -1;
+    const int win = __ffs(__ballot_sync(0xffffffffu, first == top)) - 1;
+    *taken = __shfl_sync(0xffffffffu, best[0], win);
+    const bool mine = lane == win;
+    best[0] = mine ? best[1] : best[0];
+    best[1] = mine ? best[2] : best[1];
+    best[2] = mine ? best[3] : best[2];
+    best[3] = mine ? 0u : best[3];
+    if constexpr (NJ > 4) {
+      held -= mine ? 1 : 0;
+      if (__any_sync(0xffffffffu, held == 0)) {  // the lane's next four
+        uint32_t left[NJ], four[4];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const bool first = ord[j] > o1, second = ord[j] > o2;
-    o2 = first ? o1 : second ? ord[j] : o2;
-    j2 = first ? j1 : second ? j : j2;
-    o1 = first ? ord[j] : o1;
-    j1 = first ? j : j1;
-  }
-  // takes the best expert still in play (uniform over the warp), or -1
-  auto take_best = [&]() {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, o1);
-    if (top == 0u) return -1;
-    const int win = __ffs(__ballot_sync(0xffffffffu, o1 == top)) - 1;
-    const int e = __shfl_sync(0xffffffffu, e0 + j1, win);
-    if (lane == win) {
-      const int last = j1;
-      o1 = o2;
-      j1 = j2;
-      o2 = 0u;
-      if (NJ > 2 && --held == 0) {  // the next two after (top, last)
-        held = 2;
-        o1 = 0u;
+        for (int j = 0; j < NJ; ++j) left[j] = ord[j] < *taken ? ord[j] : 0u;
+        four_best<NJ>(left, four);
+        if (held == 0) {
+          held = 4;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint32_t v = ord[j] < top || (ord[j] == top && j > last) ? ord[j] : 0u;
-          const bool first = v > o1, second = v > o2;
-          o2 = first ? o1 : second ? v : o2;
-          j2 = first ? j1 : second ? j : j2;
-          o1 = first ? v : o1;
-          j1 = first ? j : j1;
+          for (int i = 0; i < 4; ++i) best[i] = four[i];
         }
       }
     }
-    return e;
+    return win;
+  };
+  auto expert_of = [&](int win, uint32_t taken) {
+    return win * NJ + static_cast<int>(kLow - (taken & kLow));
   };
   auto pick_of = [&](int e) {
     Pick q{-INFINITY, 0.f, 0.f, 0.f};
@@ -484,12 +547,16 @@ __global__ void __launch_bounds__(32 * kWarps)
   };
 
   // the K best and the one after them; lane k keeps the k-th
-  int mine = -1;
+  int my_win = -1;
+  uint32_t my_key = 0u;
   for (int k = 0; k <= p.K; ++k) {
-    const int e = take_best();
-    if (e < 0) break;
-    if (lane == k) mine = e;
+    uint32_t taken;
+    const int win = take_best(&taken);
+    if (win < 0) break;
+    my_win = lane == k ? win : my_win;
+    my_key = lane == k ? taken : my_key;
   }
+  int mine = my_win < 0 ? -1 : expert_of(my_win, my_key);
 
   // certify the order of neighbours
   const Pick me = pick_of(mine);
@@ -497,17 +564,27 @@ __global__ void __launch_bounds__(32 * kWarps)
                   __shfl_down_sync(0xffffffffu, me.key, 1),
                   __shfl_down_sync(0xffffffffu, me.err, 1)};
   const int next_e = __shfl_down_sync(0xffffffffu, mine, 1);
-  const uint32_t doubts = __ballot_sync(
-      0xffffffffu, lane < p.K && next_e >= 0 && in_doubt<kSig>(me, next, has_bias, m));
-  if (doubts != 0u) {
-    bool whole = false;
-    if ((doubts >> (p.K - 1)) & 1u) {  // the last one kept and the first one left out
-      const int second = take_best();
-      const Pick q = pick_of(second);
-      whole = __shfl_sync(0xffffffffu, second >= 0 && in_doubt<kSig>(me, q, has_bias, m), p.K);
+  constexpr float kUnit = (1 + NJ) * 0x1p-23f;
+  const bool tie = me.l == next.l && me.b == next.b;  // in any precision
+  if (__any_sync(0xffffffffu, lane < p.K && next_e >= 0 && !tie &&
+                                  close<kSig>(me, next, has_bias, m, kUnit))) {
+    // what comes after the first one left out must be clear of it (a tie is not)
+    uint32_t taken = 0u;
+    const int win = take_best(&taken);
+    const int second = win < 0 ? -1 : expert_of(win, taken);
+    const Pick q = pick_of(second);
+    const bool whole = __shfl_sync(
+        0xffffffffu, second >= 0 && close<kSig>(me, q, has_bias, m, kUnit), p.K);
+    if (whole) {
+      mine = choose64<NJ, TL, kSig>(p, row, m, lane, live);
+    } else {
+      // the logits decide unless some neighbours' scores may round together
+      Pick hi = me, lo = next;
+      if (me.l < next.l) hi = next, lo = me;
+      const bool merge = lane < p.K && next_e >= 0 && !tie && scores_merge<kSig>(hi, lo, m);
+      const bool by_logit = !has_bias && !__any_sync(0xffffffffu, merge);
+      mine = order64<NJ, TL, kSig>(p, row, m, lane, mine, me.l, me.b, by_logit);
     }
-    mine = whole ? choose64<NJ, TL, kSig>(p, row, m, lane, live)
-                 : order64<NJ, TL, kSig>(p, row, m, lane, mine, me.l, me.b);
   }
   if (lane >= p.K) mine = -1;
 

@@ -266,6 +266,27 @@ def test_near_ties_are_decided_in_64_bits(score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+def test_exact_ties_behind_a_near_tie(score):
+    # many experts of equal logit and bias, and some just below them in 64 bits that float
+    # keys cannot tell from them, at lower ids: the equal ones fill all places
+    T, E = 40, 96
+    logits = torch.zeros(T, E, device="cuda")
+    bias = torch.full((E,), 0.25, device="cuda")
+    below = torch.randperm(E, generator=torch.Generator().manual_seed(3))[:20]
+    logits[:, below] = 1.0
+    for t in range(T):  # a different number of experts out of the way in each row
+        logits[t, 96 - t:] = -30.0
+    s = np.array([scores(row, score)[0] for row in logits.double().cpu().numpy()])
+    one, zero = int(below[0]), int([e for e in range(40) if e not in below.tolist()][0])
+    gap = s[0, zero] + 0.25 - s[0, one]
+    bias[below] = torch.tensor(np.nextafter(np.float32(gap), np.float32(-9.0)), device="cuda")
+    for K in (1, 3, 8, 16):
+        check(moe.RouteConfig.make(T, E, K, 1, 1, 1, score), logits, bias)
+        check(moe.RouteConfig.make(T, E, K, 4, 3, 2, score), logits, bias)
+
+
+@pytest.mark.gpu
 def test_exact_ties_go_to_the_lower_id():
     for score in (moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID):
         for G, TG in ((1, 1), (8, 3)):
