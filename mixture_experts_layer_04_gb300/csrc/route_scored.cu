@@ -75,9 +75,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// This lane's NJ logits of one row (masked ones and those past E as -inf).
+// This lane's NJ logits of one row as they are in memory (those past E as -inf).
 template <int NJ, typename TL>
-__device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec, float (&l)[NJ]) {
+__device__ __forceinline__ void load_raw(const TL* row, int E, int lane, int vec, float (&l)[NJ]) {
   const int e0 = lane * NJ;
   constexpr int kBytes = NJ * static_cast<int>(sizeof(TL));
   if constexpr (kBytes >= 4) {
@@ -95,7 +95,7 @@ __device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec
           else
             *reinterpret_cast<uint32_t*>(v) = reinterpret_cast<const uint32_t*>(row + e0)[i];
 #pragma unroll
-          for (int q = 0; q < kPer; ++q) l[i * kPer + q] = clean_logit(to_float(v[q]));
+          for (int q = 0; q < kPer; ++q) l[i * kPer + q] = to_float(v[q]);
         }
       } else {
 #pragma unroll
@@ -105,8 +105,21 @@ __device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec
     }
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    l[j] = e0 + j < E ? clean_logit(to_float(row[e0 + j])) : -INFINITY;
+  for (int j = 0; j < NJ; ++j) l[j] = e0 + j < E ? to_float(row[e0 + j]) : -INFINITY;
+}
+
+// The same as the definition reads them (clean_logit).  A sum finds out whether any needs it:
+// it is NaN if one of them is (or if +inf meets -inf), +inf if one of them is.
+template <int NJ, typename TL>
+__device__ __forceinline__ void load_row(const TL* row, int E, int lane, int vec, float (&l)[NJ]) {
+  load_raw<NJ, TL>(row, E, lane, vec, l);
+  float sum = l[0];
+#pragma unroll
+  for (int j = 1; j < NJ; ++j) sum += l[j];
+  if (!(sum < INFINITY)) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) l[j] = clean_logit(l[j]);
+  }
 }
 
 // This lane's NJ biases (those past E as 0).
@@ -397,108 +410,124 @@ __global__ void __launch_bounds__(32 * kWarps)
     return (mono & ~kLow) | (kLow - static_cast<uint32_t>(j));
   };
   const bool grouped = p.top_groups < p.groups;
-  uint32_t ord[NJ], best[4];
+  uint32_t ord[NJ], best[4];  // all keys; the lane's four best still in play, descending
   uint32_t live = 0xffffffffu;  // groups in play
-  if (has_bias || grouped) {
-    float key[NJ], b[NJ];
-    if (has_bias) {
-      load_bias<NJ>(p, lane, b);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = 0.f;
-    }
+  auto value_of = [](uint32_t o) {  // the float of an ordered key, its low bits cleared
+    const uint32_t u = o & ~kLow;
+    return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+  };
+  if (has_bias) {
+    float b[NJ];
+    load_bias<NJ>(p, lane, b);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const float k = score_of<kSig>(l[j], m, inv_sum) + b[j];
-      key[j] = l[j] > -INFINITY && k > -INFINITY ? k : -INFINITY;
-      ord[j] = order_key(has_bias ? key[j] : l[j], j);
-    }
-    four_best<NJ>(ord, best);
-    if (grouped) {
-      // the group's best one or two keys, for group g in lane g
-      float v1 = -INFINITY, v2 = -INFINITY;
-      const int lanes = p.per / NJ;
-      const bool whole_lanes = p.per % NJ == 0;
-      if (whole_lanes && (lanes & (lanes - 1)) == 0) {
-        // a power of two of lanes per group: best two of each lane, then of neighbouring lanes
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          v2 = fmaxf(v2, fminf(v1, key[j]));
-          v1 = fmaxf(v1, key[j]);
-        }
-        for (int o = 1; o < lanes; o <<= 1) {
-          const float x1 = __shfl_xor_sync(0xffffffffu, v1, o);
-          const float x2 = __shfl_xor_sync(0xffffffffu, v2, o);
-          v2 = fmaxf(fmaxf(v2, x2), fminf(v1, x1));
-          v1 = fmaxf(v1, x1);
-        }
-        v1 = __shfl_sync(0xffffffffu, v1, (lane * lanes) & 31);
-        v2 = __shfl_sync(0xffffffffu, v2, (lane * lanes) & 31);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) s_key[warp][e0 + j] = key[j];
-        __syncwarp();
-        if (lane < p.groups) {
-          for (int i = 0; i < p.per; ++i) {
-            const float k = s_key[warp][lane * p.per + i];
-            v2 = fmaxf(v2, fminf(v1, k));
-            v1 = fmaxf(v1, k);
-          }
-        }
-      }
-      const bool two = p.rank > 1 && v2 > -INFINITY;
-      const bool there = lane < p.groups && v1 > -INFINITY;
-      float gs = there ? (two ? v1 + v2 : v1) : -INFINITY;
-      int better = 0;
-      for (int h = 0; h < p.groups; ++h) {
-        const float v = __shfl_sync(0xffffffffu, gs, h);
-        better += (v > gs || (v == gs && h < lane)) ? 1 : 0;
-      }
-      const bool in = lane < p.groups && better < p.top_groups;
-      live = __ballot_sync(0xffffffffu, in);
-      const float lowest_in = -warp_max(in ? -gs : -INFINITY);
-      const float best_out = warp_max(in ? -INFINITY : gs);
-      if (best_out > -INFINITY) {
-        // A sum is off by its keys' errors (a score's is largest at the largest score, 1 for
-        // the logistic function and inv_sum for the softmax) and three roundings.
-        const float mag = warp_max(there ? fabsf(v1) + (two ? fabsf(v2) : 0.f) : 0.f);
-        const float slack = 2.0f * (2.0f * score_error<kSig>(kSig ? 1.0f : inv_sum, m, m) +
-                                    2.0f * kErrFloor + mag * 0x1p-22f);
-        if (!(lowest_in - best_out > slack)) {
-          // the groups at the border, by 64-bit sums, for the places that the clear ones leave
-          const bool clear_in = in && gs > best_out + slack;
-          const bool contested = there && !clear_in && !(gs < lowest_in - slack);
-          const uint32_t open = __ballot_sync(0xffffffffu, contested);
-          const uint32_t sure = __ballot_sync(0xffffffffu, clear_in);
-          const double g64 = group_sums64<NJ, TL, kSig>(p, row, m, lane, open);
-          int before = 0;
-          for (int h = 0; h < p.groups; ++h) {
-            const double v = __shfl_sync(0xffffffffu, g64, h);
-            before += ((open >> h) & 1u) && (v > g64 || (v == g64 && h < lane)) ? 1 : 0;
-          }
-          live = sure | __ballot_sync(0xffffffffu, contested && before < p.top_groups - __popc(sure));
-        }
-      }
-      int g = e0 / p.per;
-      if (whole_lanes) {  // a lane's experts are of one group
-        if (!((live >> (g & 31)) & 1u)) best[0] = best[1] = best[2] = best[3] = 0u;
-      } else {
-        int r = e0 - g * p.per;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
-          if (++r == p.per) {
-            r = 0;
-            ++g;
-          }
-        }
-        four_best<NJ>(ord, best);
-      }
+      ord[j] = order_key(l[j] > -INFINITY && k > -INFINITY ? k : -INFINITY, j);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) ord[j] = order_key(l[j], j);
-    four_best<NJ>(ord, best);
+  }
+  four_best<NJ>(ord, best);
+
+  if (grouped) {
+    // The sum of a group's best one or two keys, for group g in lane g.  Keys come from the
+    // ordered integers (without a bias those hold logits).
+    auto key_of = [&](uint32_t o) {
+      if (o <= (kNone | kLow)) return -INFINITY;
+      const float v = value_of(o);
+      return has_bias ? v : score_of<kSig>(v, m, inv_sum);
+    };
+    float v1 = -INFINITY, v2 = -INFINITY;
+    const int lanes = p.per / NJ;
+    const bool whole_lanes = p.per % NJ == 0;
+    if (whole_lanes && (lanes & (lanes - 1)) == 0) {
+      // a power of two of lanes per group: this lane's best two, then those of its neighbours
+      v1 = key_of(best[0]);
+      v2 = NJ > 1 ? key_of(best[1]) : -INFINITY;
+      for (int o = 1; o < lanes; o <<= 1) {
+        const float x1 = __shfl_xor_sync(0xffffffffu, v1, o);
+        const float x2 = __shfl_xor_sync(0xffffffffu, v2, o);
+        v2 = fmaxf(fmaxf(v2, x2), fminf(v1, x1));
+        v1 = fmaxf(v1, x1);
+      }
+      v1 = __shfl_sync(0xffffffffu, v1, (lane * lanes) & 31);
+      v2 = __shfl_sync(0xffffffffu, v2, (lane * lanes) & 31);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) s_key[warp][e0 + j] = key_of(ord[j]);
+      __syncwarp();
+      if (lane < p.groups) {
+        for (int i = 0; i < p.per; ++i) {
+          const float k = s_key[warp][lane * p.per + i];
+          v2 = fmaxf(v2, fminf(v1, k));
+          v1 = fmaxf(v1, k);
+        }
+      }
+    }
+    const bool two = p.rank > 1 && v2 > -INFINITY;
+    const bool there = lane < p.groups && v1 > -INFINITY;
+    const float gs = there ? (two ? v1 + v2 : v1) : -INFINITY;
+    // the top_groups best sums, ties to the lower group; the last one in and the first one out
+    uint32_t left = there ? float_key(gs) : 0u, last = 0u;
+    live = 0u;
+    for (int r = 0; r < p.top_groups; ++r) {
+      last = __reduce_max_sync(0xffffffffu, left);
+      if (last == 0u) break;  // the groups left have nothing available
+      const uint32_t who = __ballot_sync(0xffffffffu, left == last);
+      const uint32_t first = who & (~who + 1u);
+      live |= first;
+      left = (first >> lane) & 1u ? 0u : left;
+    }
+    const uint32_t out = __reduce_max_sync(0xffffffffu, left);
+    if (last != 0u && out != 0u) {
+      auto sum_of = [](uint32_t k) {
+        return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+      };
+      const float lowest_in = sum_of(last), best_out = sum_of(out);
+      // A sum is off by its keys' errors, a score's being largest at the largest score (1 for
+      // the logistic function, inv_sum for the softmax), by two additions, and by the rounding
+      // of the ordered values: of the keys, or without a bias of the logits, which moves a
+      // logistic score by |l| s (1 - s) < 0.3 and a softmax score by |l| s <= |m| s + |x| s with
+      // |x| s < 0.4 inv_sum.
+      const float mag = warp_max(there ? fabsf(v1) + (two ? fabsf(v2) : 0.f) : 0.f);
+      const float top = kSig ? 1.0f : inv_sum;
+      const float unit = NJ * 0x1p-23f;
+      float rounding = mag * unit;
+      if (!has_bias) rounding = unit * (kSig ? 0.6f : mag * fabsf(m) + 0.8f * top);
+      const float slack = 2.0f * (2.0f * score_error<kSig>(top, m, m) + 2.0f * kErrFloor +
+                                  mag * 0x1p-22f + rounding);
+      if (!(lowest_in - best_out > slack)) {
+        // the groups at the border, by 64-bit sums, for the places that the clear ones leave
+        const bool in = (live >> lane) & 1u;
+        const bool clear_in = in && gs > best_out + slack;
+        const bool contested = there && !clear_in && !(gs < lowest_in - slack);
+        const uint32_t open = __ballot_sync(0xffffffffu, contested);
+        const uint32_t sure = __ballot_sync(0xffffffffu, clear_in);
+        const double g64 = group_sums64<NJ, TL, kSig>(p, row, m, lane, open);
+        int before = 0;
+        for (int h = 0; h < p.groups; ++h) {
+          const double v = __shfl_sync(0xffffffffu, g64, h);
+          before += ((open >> h) & 1u) && (v > g64 || (v == g64 && h < lane)) ? 1 : 0;
+        }
+        live = sure | __ballot_sync(0xffffffffu, contested && before < p.top_groups - __popc(sure));
+      }
+    }
+    int g = e0 / p.per;
+    if (whole_lanes) {  // a lane's experts are of one group
+      if (!((live >> (g & 31)) & 1u)) best[0] = best[1] = best[2] = best[3] = 0u;
+    } else {
+      int r = e0 - g * p.per;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
+        if (++r == p.per) {
+          r = 0;
+          ++g;
+        }
+      }
+      four_best<NJ>(ord, best);
+    }
   }
 
   // Takes the best expert still in play: its lane and ordered key (uniform over the warp), or
@@ -566,8 +595,9 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int next_e = __shfl_down_sync(0xffffffffu, mine, 1);
   constexpr float kUnit = (1 + NJ) * 0x1p-23f;
   const bool tie = me.l == next.l && me.b == next.b;  // in any precision
-  if (__any_sync(0xffffffffu, lane < p.K && next_e >= 0 && !tie &&
-                                  close<kSig>(me, next, has_bias, m, kUnit))) {
+  const bool doubt = __any_sync(0xffffffffu, lane < p.K && next_e >= 0 && !tie &&
+                                                 close<kSig>(me, next, has_bias, m, kUnit));
+  if (doubt) {
     // what comes after the first one left out must be clear of it (a tie is not)
     uint32_t taken = 0u;
     const int win = take_best(&taken);
@@ -589,7 +619,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (lane >= p.K) mine = -1;
 
   // weights from the unbiased scores
-  const float kl = mine >= 0 ? clean_logit(to_float(row[mine])) : -INFINITY;
+  float kl = mine >= 0 ? me.l : -INFINITY;
+  if (doubt && mine >= 0) kl = clean_logit(to_float(row[mine]));
   float s = 0.f;
   if (p.renorm) {
     const float top = warp_max(kl);
