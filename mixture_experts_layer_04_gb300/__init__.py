@@ -201,11 +201,7 @@ def load_debug() -> ctypes.CDLL:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:

@@ -1,8 +1,8 @@
 // moe_linear and moe_linear_backward: argument checks, the workspace, the passes around the
 // tensor-core product (linear_gemm.cu) and the product for a few rows.
 //
-//  - linear_rows_kernel (up to 8 rows): every weight is used `rows` times at most, so the call
-//    is bound by reading the weights once.  A block takes four output features, its eight
+//  - linear_rows_kernel (a few rows): every weight is used `rows` times only, so the call is
+//    bound by reading the weights once.  A block takes four output features, its eight
 //    warps split the input features, so each weight row is in flight as a whole; fp32 FMAs,
 //    partial sums joined in shared memory in warp order.  Any alignment and either type.
 //  - pack_kernel: an operand the tensor cores cannot read in place.  Float32 values become
@@ -21,8 +21,17 @@
 namespace moe {
 namespace {
 
-// Rows up to which moe_linear runs on the CUDA cores.
-constexpr int kFewRows = 8;
+// Whether moe_linear runs on the CUDA cores.  One FMA per weight and row: bf16 weights that the
+// tensor cores read in place are faster there from 3 rows on (4096 x 4096: 2 rows 7.6 us here
+// and 9.5 there, 3 rows 10.7 and 9.5), or from 5 where the weights are few and the launch is
+// what counts (512 x 2048: 4 rows 5.8 and 7.5 us, 8 rows 8.1 and 6.7).  Operands that would
+// have to be packed first, all of float32, gain more from being read once (float32 4096 x 4096,
+// 8 rows: 25 and 45 us).
+constexpr int kMaxFewRows = 8;
+bool few_rows(const moe_linear_config_t* c, bool packed) {
+  if (c->rows <= 2 || (packed && c->rows <= kMaxFewRows)) return true;
+  return c->rows <= 4 && static_cast<long long>(c->in_features) * c->out_features <= 1ll << 22;
+}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -528,7 +537,7 @@ extern "C" moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  if (cfg->rows <= kFewRows) {
+  if (few_rows(cfg, plan.pack_x || plan.pack_w)) {
     RowsParams p{};
     p.x = x;
     p.w = w;

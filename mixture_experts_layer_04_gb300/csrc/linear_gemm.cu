@@ -27,6 +27,7 @@
 //    (float32 results): the tensor core truncates each addition (over 7168 products the mean
 //    error is 8e-6 of the result's size, against 2e-7 for rounded additions).
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -792,9 +793,17 @@ bool operand_map(CUtensorMap* m, const void* base, int rows, int depth, int mn, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Raises a kernel's dynamic shared memory limit, once per device (`done` belongs to the kernel).
 template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // A cluster launch of `split` CTAs per tile.
@@ -819,7 +828,8 @@ void tile_launch(int tiles, int split, cudaStream_t s, cudaLaunchConfig_t* lc,
 template <int BA, int BN, int PL>
 cudaError_t launch_tile(const GemmParams& p, int split, cudaStream_t s) {
   auto kernel = linear_tile_kernel<BA, BN, PL>;
-  cudaError_t e = allow_smem(kernel, TileCfg<BA, BN, PL>::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kernel, TileCfg<BA, BN, PL>::kSmem, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc;
   cudaLaunchAttribute attr[2];
@@ -846,7 +856,9 @@ const ClusterRoom& cluster_room(int num_sms) {
       cudaLaunchAttribute attr[2];
       auto kernel = linear_tile_kernel<128, 128, 1>;
       int n = 0;
-      if (allow_smem(kernel, TileCfg<128, 128, 1>::kSmem) != cudaSuccess) continue;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               TileCfg<128, 128, 1>::kSmem) != cudaSuccess)
+        continue;
       tile_launch<128, 128, 1>(1, 1 << i, nullptr, &lc, attr);
       if (cudaOccupancyMaxActiveClusters(&n, kernel, &lc) == cudaSuccess && n > 0)
         rooms[dev].room[i] = n;
@@ -968,7 +980,8 @@ cudaError_t launch_pairs(const LinearGemm& g, unsigned* err, int num_sms, cudaSt
   j.tiles_b = ceil_div(g.cols, 256);
   const long long tiles = static_cast<long long>(j.tiles_a) * j.tiles_b;
   if (tiles >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem, &done);
   if (e != cudaSuccess) return e;
   const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
   // a plain launch: see the top of the file
