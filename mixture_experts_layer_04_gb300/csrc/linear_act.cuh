@@ -13,16 +13,27 @@
 
 namespace moe {
 
+// The hardware's reciprocal (1 ulp) and power of two (2 ulp), results under 2^-126 as 0.
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Phi(z) for kFast; *e = exp(-z^2 / 2).
 __device__ __forceinline__ float normal_cdf_fast(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  const float t = rcp_ftz(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
   float poly = fmaf(t, 1.061405429f, -1.453152027f);
   poly = fmaf(t, poly, 1.421413741f);
   poly = fmaf(t, poly, -0.284496736f);
   poly = fmaf(t, poly, 0.254829592f);
-  *e = __expf(-0.5f * z * z);
-  const float tail = 0.5f * t * poly * *e;  // Phi(-|z|)
+  *e = exp2_ftz(-0.72134752f * z * z);
+  const float tail = (0.5f * t) * (poly * *e);  // Phi(-|z|)
   return z < 0.f ? tail : 1.0f - tail;
 }
 
@@ -86,7 +97,7 @@ __device__ __forceinline__ float act_slope(int act, float z) {
       constexpr float c = 1.5957691216057308f;
       const float z2 = z * z;
       const float u2 = c * fmaf(0.044715f * z2, z, z);
-      const float p = kFast ? __fdividef(1.0f, 1.0f + __expf(-u2)) : 1.0f / (1.0f + expf(-u2));
+      const float p = kFast ? rcp_ftz(1.0f + __expf(-u2)) : 1.0f / (1.0f + expf(-u2));
       const float q = p * (1.0f - p);
       return q > 0.f ? fmaf(z * q, c * fmaf(0.134145f, z2, 1.0f), p) : p;
     }
@@ -96,7 +107,7 @@ __device__ __forceinline__ float act_slope(int act, float z) {
       // cancels
       const float d = (z + 1.2784645557403564f) - 1.2979282759673083e-08f;
       const float t = kFast ? __expf(-fabsf(z)) : expf(-fabsf(z));
-      const float r = kFast ? __fdividef(1.0f, 1.0f + t) : 1.0f / (1.0f + t);
+      const float r = kFast ? rcp_ftz(1.0f + t) : 1.0f / (1.0f + t);
       const float p = z > 0.f ? r : t * r, q = z > 0.f ? t * r : r;
       float bracket = fmaf(z, q, 1.0f);
       if (kFast) {  // a column's sum is float32, so near z0 the slope keeps its accuracy too

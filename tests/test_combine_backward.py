@@ -169,3 +169,24 @@ def test_graph_capture_and_repeatability():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o2, d_o) and torch.equal(w2, d_w)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # more than 2^31 values in the expert rows; the last tokens equal a small call on them
+    T, H, K, tail = 38_000, 7168, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dy = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    o = torch.zeros(T * K, H, device="cuda")
+    o[-tail * K:] = torch.randn(tail * K, H, generator=g, device="cuda")
+    w = torch.rand(T, K, generator=g, device="cuda")
+    inv = torch.arange(T * K, dtype=torch.int32, device="cuda").view(T, K)
+    d_o = torch.empty(T * K, H, dtype=torch.bfloat16, device="cuda")
+    d_w = torch.empty(T, K, device="cuda")
+    moe.combine_backward(config(T, H, 16, K), dy, o, inv, w, d_o, d_w)
+    local = torch.arange(tail * K, dtype=torch.int32, device="cuda").view(tail, K)
+    so, sw = check(dy[-tail:].contiguous(), o[-tail * K:].contiguous(), local,
+                   w[-tail:].contiguous(), config(tail, H, 16, K))
+    assert torch.equal(d_o[-tail * K:], so)
+    assert (d_w[:-tail] == 0).all()
+    assert torch.allclose(d_w[-tail:], sw, rtol=1e-4, atol=1e-2)

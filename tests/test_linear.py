@@ -401,3 +401,31 @@ def test_calls_repeat_bit_for_bit_and_in_a_graph():
     assert torch.equal(y, y0) and torch.equal(z, z0)
     assert all(torch.equal(p, q) for p, q in zip(grads, grads0))
     moe.sync_check()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # more than 2^31 elements in y, z and dy; the last rows are compared
+    rows, fin, fout, tail = 270_000, 64, 8192, 300
+    x, w, b, _, g = make(rows, fin, fout, torch.bfloat16, 5)
+    x = x.contiguous()
+    c = config(rows, fin, fout, activation=moe.ACT_SILU)
+    y = torch.empty(rows, fout, dtype=torch.bfloat16, device="cuda")
+    z = torch.empty_like(y)
+    ws = torch.empty(moe.linear_workspace_size(c), dtype=torch.uint8, device="cuda")
+    moe.linear(c, x, w, b, None, y, z, ws)
+    zr = x[-tail:].double() @ w.double().t() + b.double()
+    assert ((z[-tail:].double() - zr).abs() <= 2.0 ** -8 * zr.abs() * 1.01 + 1e-4).all()
+    assert ((y[-tail:].double() - act(moe.ACT_SILU, zr)).abs()
+            <= 2.0 ** -8 * zr.abs() * 1.01 + 1e-4).all()
+    # dy is zero but for the last rows, so every gradient is theirs
+    y.zero_()
+    y[-tail:] = torch.randn(tail, fout, generator=g, device="cuda").bfloat16()
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    moe.linear_backward(c, y, x, w, z, dx, dw, db, ws)
+    moe.sync_check()
+    dz = y[-tail:].double() * slope(moe.ACT_SILU, z[-tail:].double())
+    assert (dx[:-tail] == 0).all()
+    for got, want in ((dx[-tail:], dz @ w.double()), (dw, dz.t() @ x[-tail:].double())):
+        assert (got.double() - want).norm() <= 2.0 ** -8 * want.norm()
+    assert (db.double() - dz.sum(0)).norm() <= 2.0 ** -18 * dz.abs().sum(0).norm()

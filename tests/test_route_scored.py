@@ -433,3 +433,23 @@ def test_side_stream_and_graph_capture():
     torch.cuda.synchronize()
     assert torch.equal(ids, ids0) and torch.equal(w, w0) and torch.equal(dl, dl0)
     moe.sync_check()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # more than 2^31 logits; the last rows equal a small call on them
+    T, E, K, tail = 8_500_000, 256, 2, 64
+    logits = torch.zeros(T, E, device="cuda")
+    logits[-tail:] = torch.randn(tail, E, generator=gen(15), device="cuda")
+    ids = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, K, device="cuda")
+    c = moe.RouteConfig.make(T, E, K, score=moe.SCORE_SIGMOID)
+    moe.route_scored(c, logits, None, ids, w)
+    small = moe.RouteConfig.make(tail, E, K, score=moe.SCORE_SIGMOID)
+    sid, sw = check(small, logits[-tail:])
+    assert torch.equal(ids[-tail:], sid) and torch.equal(w[-tail:], sw)
+    dw = torch.randn(T, K, generator=gen(16), device="cuda")
+    moe.route_scored_backward(c, logits, ids, dw, logits)
+    want = grad(small, torch.randn(tail, E, generator=gen(15), device="cuda"), sid,
+                dw[-tail:].contiguous())
+    assert torch.equal(logits[-tail:], want)
