@@ -178,7 +178,77 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int row, int col, flo
     store_n(static_cast<__nv_bfloat16*>(e.c) + at, n, e.vec_c, v);
 }
 
-// The same for two rows (row, row + step) of a bf16 tile that lies wholly inside the output,
+// The outputs that a CTA of the tile kernel finishes: rows x cols (a power of two), eight
+// neighbours of a row per thread at a time.  Rows that do not allow 16-byte accesses are read
+// and written value by value all the same: spreading neighbouring columns over the lanes
+// coalesces those, but needs an address per value, and the few warps at hand are bound by their
+// instructions (float32 333 x 1001 -> 777: 26 us, against 22).
+struct OutTile {
+  int row0, col0, rows, cols, shift;  // cols = 8 << shift
+  __device__ __forceinline__ int items() const { return rows << shift; }
+  __device__ __forceinline__ int row(int item) const { return item >> shift; }
+  __device__ __forceinline__ int col(int item) const { return (item & ((1 << shift) - 1)) * 8; }
+};
+template <typename TA>
+__device__ __forceinline__ void load_addends(const Epilogue& e, const OutTile& o, int item,
+                                             float (&bias)[8], float (&res)[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) bias[u] = res[u] = 0.f;
+  const int row = o.row0 + o.row(item), col = o.col0 + o.col(item);
+  if (item >= o.items() || row >= e.rows || col >= e.cols) return;
+  const int n = min(8, e.cols - col);
+  if (e.bias != nullptr) load_n(e.bias + col, n, e.vec_bias, bias);
+  if (e.res != nullptr)
+    load_n(static_cast<const TA*>(e.res) + static_cast<size_t>(row) * e.ldr + col, n, e.vec_r, res);
+}
+// part: `split` partial tiles of o.rows x (o.cols + 4) floats, summed in order.
+template <typename TA>
+__device__ __forceinline__ void finish_outputs(const Epilogue& e, const OutTile& o, int item,
+                                               const float* part, int split,
+                                               const float (&bias)[8], const float (&res)[8]) {
+  const int row = o.row0 + o.row(item), col = o.col0 + o.col(item);
+  if (row >= e.rows || col >= e.cols) return;
+  const float* src = part + o.row(item) * (o.cols + 4) + o.col(item);
+  float v[8];
+  load_n(src, 8, true, v);
+  for (int s = 1; s < split; ++s) {
+    float x[8];
+    load_n(src + s * o.rows * (o.cols + 4), 8, true, x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] += x[u];
+  }
+  const int n = min(8, e.cols - col);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] += bias[u];
+  if (e.z != nullptr)
+    store_n(static_cast<TA*>(e.z) + static_cast<size_t>(row) * e.ldz + col, n, e.vec_z, v);
+  act_values<sizeof(TA) == 2>(e.act, v);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] += res[u];
+  const size_t at = static_cast<size_t>(row) * e.ldc + col;
+  if (e.c_f32) store_n(static_cast<float*>(e.c) + at, n, e.vec_c, v);
+  else store_n(static_cast<__nv_bfloat16*>(e.c) + at, n, e.vec_c, v);
+}
+
+// Asks L2 for the residual (and the bias) of a tile's rows, long before they are used.
+template <typename TA>
+__device__ __forceinline__ void prefetch_residual(const Epilogue& e, int row0, int rows, int col0,
+                                                  int cols, int t, int threads) {
+  const int row_end = min(row0 + rows, e.rows), col_end = min(col0 + cols, e.cols);
+  if (col0 >= col_end) return;
+  if (e.bias != nullptr && col0 + t * 32 < col_end)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(e.bias + col0 + t * 32));
+  if (e.res == nullptr) return;
+  constexpr int kLine = 128 / static_cast<int>(sizeof(TA));
+  const int lines = (col_end - col0 + kLine - 1) / kLine + 1;  // one more: rows start anywhere
+  for (int i = t; i < (row_end - row0) * lines; i += threads) {
+    const int r = i / lines, c = min((i - r * lines) * kLine, col_end - col0 - 1);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const TA*>(e.res) +
+                                                  static_cast<size_t>(row0 + r) * e.ldr + col0 + c));
+  }
+}
+
+// finish8 for two rows (row, row + step) of a bf16 tile that lies wholly inside the output,
 // with 16-byte accesses throughout: the residuals are on their way before anything is computed.
 // b: the eight columns' biases.
 __device__ __forceinline__ void finish8_inside(const Epilogue& e, int row, int step, int col,
@@ -326,6 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb0 = static_cast<int>(static_cast<long long>(job.num_kb) * rank / split);
   const int nkb = static_cast<int>(static_cast<long long>(job.num_kb) * (rank + 1) / split) - kb0;
   const int R = BA / split;  // rows of the A side that each CTA finishes
+  // the outputs that this CTA finishes; the first ones' biases and residuals are read while the
+  // partial tiles are on their way
+  OutTile out;
+  out.row0 = job.swap ? b0 : a0 + rank * R;
+  out.col0 = job.swap ? a0 + rank * R : b0;
+  out.rows = job.swap ? BN : R;
+  out.cols = job.swap ? R : BN;
+  out.shift = __ffs(out.cols >> 3) - 1;
+  float bias[8], res[8];
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer ----
@@ -349,20 +428,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       }
-      // drain: no load or commit may still be in flight when the CTA gives up its shared memory
+      // drain: no load or commit may still be in flight when the CTA gives up its shared memory.
+      // Oldest stage first, so that only the last one is waited for after the last MMA.
       const int n = issued < S ? issued : S;
       volatile int no_abort = 0;
+      if ((stage -= n) < 0) {
+        stage += S;
+        phase ^= 1u;
+      }
       for (int j = 0; j < n; ++j) {
-        if (--stage < 0) {
-          stage = S - 1;
-          phase ^= 1u;
-        }
         if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err))
           mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     __syncwarp();
     cluster_sync_all();  // every CTA's stages are free
+    load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
+    __syncwarp();
     cluster_sync_all();  // the partial tiles have arrived
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
@@ -421,6 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_sync_all();
+    load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
+    __syncwarp();
     cluster_sync_all();
   } else {
     // ------------------------------------------------------------ epilogue ----
@@ -428,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (job.sum_parts != nullptr && rank == 0 && (job.swap ? a0 : b0) == 0 &&
         quad * 32 + lane < (job.swap ? BN : BA))
       finish_sum(job, (job.swap ? b0 : a0) + quad * 32 + lane);
+    prefetch_residual<TA>(job.epi, out.row0, out.rows, out.col0, out.cols,
+                          static_cast<int>(threadIdx.x) - 64, kThreads - 64);
     __syncwarp();
     float acc[BN];
 #pragma unroll
@@ -480,29 +570,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < BN; ++j)
         st_shared_cluster(at + static_cast<uint32_t>(j * (R + 4) * 4), __float_as_int(acc[j]));
     }
+    load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
+    __syncwarp();
     cluster_sync_all();
   }
 
-  // sum the slices in rank order and finish eight neighbouring columns per thread and step
+  // sum the slices in rank order and finish the outputs, the next ones' addends on their way
   if (*abort_flag == 0) {
     const float* part = reinterpret_cast<const float*>(smem);
-    const int out_rows = job.swap ? BN : R, out_cols = job.swap ? R : BN;
-    const int stride = out_cols + 4, slice = out_rows * stride;
-    const int row0 = job.swap ? b0 : a0 + rank * R, col0 = job.swap ? a0 + rank * R : b0;
-    const int per_row = out_cols / 8;
-    for (int it = threadIdx.x; it < out_rows * per_row; it += kThreads) {
-      const int r = it / per_row, c = (it - r * per_row) * 8;
-      if (row0 + r >= job.epi.rows || col0 + c >= job.epi.cols) continue;
-      float v[8];
+    for (int it = threadIdx.x; it < out.items(); it += kThreads) {
+      float next_bias[8], next_res[8];
+      load_addends<TA>(job.epi, out, it + kThreads, next_bias, next_res);
+      finish_outputs<TA>(job.epi, out, it, part, split, bias, res);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = 0.f;
-      for (int s = 0; s < split; ++s) {
-        const float4* src = reinterpret_cast<const float4*>(part + s * slice + r * stride + c);
-        const float4 x = src[0], y = src[1];
-        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      for (int u = 0; u < 8; ++u) {
+        bias[u] = next_bias[u];
+        res[u] = next_res[u];
       }
-      finish8<TA>(job.epi, row0 + r, col0 + c, v);
     }
   }
   tc_fence_before();
@@ -631,13 +715,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       // the even CTA's barriers
       const int n = issued < S ? static_cast<int>(issued) : S;
       volatile int no_abort = 0;
+      if ((stage -= n) < 0) {
+        stage += S;
+        phase ^= 1u;
+      }
       for (int j = 0; j < n; ++j) {
-        if (--stage < 0) {
-          stage = S - 1;
-          phase ^= 1u;
-        }
         if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err) && rank == 0)
           mbar_wait(full_bar(stage), phase, &no_abort, p.err);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     __syncwarp();
