@@ -311,6 +311,34 @@ __device__ __forceinline__ void load_operand_pair(uint32_t dst, const void* map,
   }
 }
 
+// The producer warp's last act: no load or commit may still be in flight when the CTA gives up
+// its shared memory.  The commits of the last min(issued, S) stages arrive after their loads and
+// MMAs; each lane waits for one of them (one after the other they cost 0.1 us each).  If the
+// pipeline gave up, the loads alone are waited for, where they complete on this CTA's barriers.
+// stage, phase, issued: the issuing lane's (`leader`) state after its last load.
+template <int S, typename Empty, typename Full>
+__device__ __forceinline__ void drain_stages(bool leader, int lane, int stage, uint32_t phase,
+                                             int issued, Empty empty_bar, Full full_bar,
+                                             bool own_loads, volatile int* abort_flag,
+                                             unsigned* err) {
+  const int src = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
+  stage = __shfl_sync(0xffffffffu, stage, src);
+  phase = __shfl_sync(0xffffffffu, phase, src);
+  const int n = min(__shfl_sync(0xffffffffu, issued, src), S);
+  static_assert(S <= 32, "one lane per stage");
+  if (lane < n) {
+    int s = stage - n + lane;
+    if (s < 0) {
+      s += S;
+      phase ^= 1u;
+    }
+    volatile int no_abort = 0;
+    if (!mbar_wait(empty_bar(s), phase, abort_flag, err) && own_loads)
+      mbar_wait(full_bar(s), phase, &no_abort, err);
+  }
+  __syncwarp();
+}
+
 // ---------------------------------------------------------- one tile per CTA ----
 
 template <int BA, int BN, int PL>
@@ -329,13 +357,32 @@ struct TileCfg {
   // BA + 4 floats per CTA of the cluster when the operands are swapped
   static_assert(BA * (BN + 4) * 4 <= kStages * kStageBytes, "partial tile");
   static_assert(BN * (BA + 4 * 8) * 4 <= kStages * kStageBytes, "swapped partial tile");
-  static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier region");
+  static_assert(8 * (2 * kStages + 6) + 8 <= kBarBytes, "barrier region");
 };
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
-               "f"(c), "f"(d)
-               : "memory");
+// Stores into the shared memory of a CTA of the cluster that count as transaction bytes on a
+// barrier there (both shared::cluster addresses): the receiver waits for the bytes, so neither
+// side needs a fence.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, float a, float b, float c,
+                                            float d) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::
+          "r"(addr),
+      "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+      : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t bar, float a) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %2, [%1];" ::"r"(addr),
+      "r"(bar), "f"(a)
+      : "memory");
+}
+// Cluster barrier for control flow alone (no memory is published by it).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <int BA, int BN, int PL>
@@ -354,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
   const uint32_t mma_done_bar = bar0 + 8u * (2 * S + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  const uint32_t xchg_bar = bar0 + 8u * (2 * S + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -375,8 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(a), 4);
     }
     mbar_init(mma_done_bar, 1);
+    mbar_init(xchg_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // the slices of this CTA's rows, from every CTA of the cluster
+    mbar_arrive_expect_tx(xchg_bar, BA * BN * 4);
     tma_prefetch_desc(&job.tm_a);
     tma_prefetch_desc(&job.tm_b);
   }
@@ -408,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer ----
-    if (elect_one_sync()) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
+    const bool leader = elect_one_sync();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    if (leader) {
       for (int i = 0; i < nkb; ++i) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) break;
         const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
@@ -428,28 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u;
         }
       }
-      // drain: no load or commit may still be in flight when the CTA gives up its shared memory.
-      // Oldest stage first, so that only the last one is waited for after the last MMA.
-      const int n = issued < S ? issued : S;
-      volatile int no_abort = 0;
-      if ((stage -= n) < 0) {
-        stage += S;
-        phase ^= 1u;
-      }
-      for (int j = 0; j < n; ++j) {
-        if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err))
-          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
     }
     __syncwarp();
-    cluster_sync_all();  // every CTA's stages are free
+    drain_stages<S>(leader, lane, stage, phase, issued, empty_bar, full_bar, true, abort_flag, p.err);
+    cluster_arrive_relaxed();  // every CTA's stages are free, its exchange barrier is set up
     load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
     __syncwarp();
-    cluster_sync_all();  // the partial tiles have arrived
+    cluster_wait();
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
     if (elect_one_sync()) {
@@ -506,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    cluster_sync_all();
+    cluster_arrive_relaxed();
     load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
     __syncwarp();
-    cluster_sync_all();
+    cluster_wait();
   } else {
     // ------------------------------------------------------------ epilogue ----
     const int quad = warp & 3;
@@ -552,31 +588,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(tempty_bar(buf));
     }
     __syncwarp();
-    cluster_sync_all();
-    // this CTA's partial tile, row by row to the CTA that finishes the row
+    cluster_arrive_relaxed();
+    cluster_wait();
+    // this CTA's partial tile, row by row to the CTA that finishes the row (itself without a
+    // split: plain stores, which are faster than asynchronous ones)
     const int row = quad * 32 + lane;
     const int owner = min(row / R, split - 1), local = row - owner * R;
     const uint32_t base = mapa_shared(smem_u32(smem), static_cast<uint32_t>(owner));
+    const uint32_t bar = mapa_shared(xchg_bar, static_cast<uint32_t>(owner));
     if (row >= BA) {
       // rows that were not loaded
+    } else if (split == 1) {
+      float* mine = reinterpret_cast<float*>(smem);
+      if (!job.swap) {
+#pragma unroll
+        for (int j = 0; j < BN; j += 4)
+          *reinterpret_cast<float4*>(mine + row * (BN + 4) + j) =
+              make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) mine[j * (BA + 4) + row] = acc[j];
+      }
     } else if (!job.swap) {
       const uint32_t at = base + static_cast<uint32_t>(((rank * R + local) * (BN + 4)) * 4);
 #pragma unroll
       for (int j = 0; j < BN; j += 4)
-        st_cluster_v4(at + j * 4u, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        st_async_v4(at + j * 4u, bar, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     } else {
       const uint32_t at = base + static_cast<uint32_t>((rank * BN * (R + 4) + local) * 4);
 #pragma unroll
       for (int j = 0; j < BN; ++j)
-        st_shared_cluster(at + static_cast<uint32_t>(j * (R + 4) * 4), __float_as_int(acc[j]));
+        st_async(at + static_cast<uint32_t>(j * (R + 4) * 4), bar, acc[j]);
     }
     load_addends<TA>(job.epi, out, threadIdx.x, bias, res);
-    __syncwarp();
-    cluster_sync_all();
   }
+  __syncwarp();
+  cluster_arrive_relaxed();  // this CTA's stores are on their way
+  volatile int no_abort = 0;
+  bool received = true;
+  if (split == 1) __syncthreads();
+  else received = mbar_wait<true>(xchg_bar, 0, &no_abort, p.err);
 
   // sum the slices in rank order and finish the outputs, the next ones' addends on their way
-  if (*abort_flag == 0) {
+  if (received && *abort_flag == 0) {
     const float* part = reinterpret_cast<const float*>(smem);
     for (int it = threadIdx.x; it < out.items(); it += kThreads) {
       float next_bias[8], next_res[8];
@@ -589,6 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  __syncwarp();
+  cluster_wait();  // no peer is still to store into this CTA's shared memory
+  if (!received) mbar_wait<true>(xchg_bar, 0, &no_abort, p.err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -683,10 +740,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer ----
-    if (elect_one_sync()) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
+    const bool leader = elect_one_sync();
+    int stage = 0, issued = 0;  // (issued stops counting at S)
+    uint32_t phase = 0;
+    if (leader) {
       bool ok = true;
       for (int idx = pair; ok && idx < total; idx += npairs) {
         int ta, tb;
@@ -703,32 +760,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * Cfg::kStageBytes);
           load_operand_pair(dst, &job.tm_a, fb, job.a_mn, a_row, kb);
           load_operand_pair(dst + Cfg::kABytes, &job.tm_b, fb, job.b_mn, b_row, kb);
-          ++issued;
+          issued = min(issued + 1, S);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // drain: wait until the last commits have arrived here (they follow the loads and the
-      // MMAs); if the pipeline gave up, at least for the loads, both CTAs' of which complete on
-      // the even CTA's barriers
-      const int n = issued < S ? static_cast<int>(issued) : S;
-      volatile int no_abort = 0;
-      if ((stage -= n) < 0) {
-        stage += S;
-        phase ^= 1u;
-      }
-      for (int j = 0; j < n; ++j) {
-        if (!mbar_wait(empty_bar(stage), phase, abort_flag, p.err) && rank == 0)
-          mbar_wait(full_bar(stage), phase, &no_abort, p.err);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
     }
     __syncwarp();
+    // (both CTAs' loads complete on the even CTA's barriers)
+    drain_stages<S>(leader, lane, stage, phase, issued, empty_bar, full_bar, rank == 0, abort_flag,
+                    p.err);
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
     if (rank == 0 && elect_one_sync()) {
