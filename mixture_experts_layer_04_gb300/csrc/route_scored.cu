@@ -20,8 +20,9 @@
 // and a step is one warp-wide maximum, a ballot and a shuffle.
 //
 // What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
-// written, but the instructions come first, most of them on the half-rate integer and compare
-// pipe (ncu: 70% busy).  At one token the launch is all there is.
+// written, but the instructions come first: 985 per token at 256 experts in 8 groups and K = 8,
+// most of them on the half-rate integer and compare pipe (64% busy).  16384 such tokens take
+// 19.7 us (2.6 us of memory traffic), one token 4.4 us, which is its launch.
 #include <cfloat>
 #include <type_traits>
 
@@ -641,7 +642,8 @@ __global__ void __launch_bounds__(32 * kWarps)
 // The gradient, one warp per token.  Only a softmax without renormalisation reaches every
 // expert; in the other cases the gradient is zero off the K chosen experts (with
 // renormalisation the softmax's own sum cancels), so K logits are gathered, the row is put
-// together in shared memory and written once.  Bound by the write of T*E elements.
+// together in shared memory and written once.  Bound by the write of T*E elements: 16384 tokens
+// of 256 experts take 6.7 us, 2.7 us of them at the copy rate.
 template <int NJ, typename TL, bool kSig>
 __global__ void __launch_bounds__(32 * kWarps)
     route_scored_grad_kernel(const __grid_constant__ RouteParams p) {
