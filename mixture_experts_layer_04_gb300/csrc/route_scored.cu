@@ -48,6 +48,8 @@ struct RouteParams {
   int renorm;
   int vec;  // rows allow whole-lane vector loads (and, backward, 16-byte stores)
   int vec_bias;  // whole-lane vector loads of the bias
+  int group_lanes;  // lanes per group where groups do not share lanes, else 0
+  int lane_shift;   // their logarithm where that is whole, else -1
   float scale;
 };
 
@@ -422,8 +424,9 @@ __global__ void __launch_bounds__(32 * kWarps)
     load_bias<NJ>(p, lane, b);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const float k = score_of<kSig>(l[j], m, inv_sum) + b[j];
-      ord[j] = order_key(l[j] > -INFINITY && k > -INFINITY ? k : -INFINITY, j);
+      // a masked logit makes this NaN (0 * -inf), as a NaN bias does, and the maximum -inf
+      const float k = fmaf(0.0f, l[j], score_of<kSig>(l[j], m, inv_sum) + b[j]);
+      ord[j] = order_key(fmaxf(k, -INFINITY), j);
     }
   } else {
 #pragma unroll
@@ -440,20 +443,18 @@ __global__ void __launch_bounds__(32 * kWarps)
       return has_bias ? v : score_of<kSig>(v, m, inv_sum);
     };
     float v1 = -INFINITY, v2 = -INFINITY;
-    const int lanes = p.per / NJ;
-    const bool whole_lanes = p.per % NJ == 0;
-    if (whole_lanes && (lanes & (lanes - 1)) == 0) {
+    if (p.lane_shift >= 0) {
       // a power of two of lanes per group: this lane's best two, then those of its neighbours
       v1 = key_of(best[0]);
       v2 = NJ > 1 ? key_of(best[1]) : -INFINITY;
-      for (int o = 1; o < lanes; o <<= 1) {
+      for (int o = 1; o < p.group_lanes; o <<= 1) {
         const float x1 = __shfl_xor_sync(0xffffffffu, v1, o);
         const float x2 = __shfl_xor_sync(0xffffffffu, v2, o);
         v2 = fmaxf(fmaxf(v2, x2), fminf(v1, x1));
         v1 = fmaxf(v1, x1);
       }
-      v1 = __shfl_sync(0xffffffffu, v1, (lane * lanes) & 31);
-      v2 = __shfl_sync(0xffffffffu, v2, (lane * lanes) & 31);
+      v1 = __shfl_sync(0xffffffffu, v1, (lane << p.lane_shift) & 31);
+      v2 = __shfl_sync(0xffffffffu, v2, (lane << p.lane_shift) & 31);
     } else {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) s_key[warp][e0 + j] = key_of(ord[j]);
@@ -514,11 +515,11 @@ __global__ void __launch_bounds__(32 * kWarps)
         live = sure | __ballot_sync(0xffffffffu, contested && before < p.top_groups - __popc(sure));
       }
     }
-    int g = e0 / p.per;
-    if (whole_lanes) {  // a lane's experts are of one group
+    if (p.group_lanes > 0) {  // a lane's experts are of one group
+      const int g = p.lane_shift >= 0 ? lane >> p.lane_shift : lane / p.group_lanes;
       if (!((live >> (g & 31)) & 1u)) best[0] = best[1] = best[2] = best[3] = 0u;
     } else {
-      int r = e0 - g * p.per;
+      int g = e0 / p.per, r = e0 - g * p.per;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         if (!((live >> (g & 31)) & 1u)) ord[j] = 0u;
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   // Takes the best expert still in play: its lane and ordered key (uniform over the warp), or
   // lane -1.  The register numbers do not count between lanes: among equal keys the lower lane.
   int held = 4;
-  auto take_best = [&](uint32_t* taken) {
+  auto take_best = [&](int k, uint32_t* taken) {
     const uint32_t first = best[0] & ~kLow;
     const uint32_t top = __reduce_max_sync(0xffffffffu, first);
     if (top <= kNone) return -1;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     best[3] = mine ? 0u : best[3];
     if constexpr (NJ > 4) {
       held -= mine ? 1 : 0;
-      if (__any_sync(0xffffffffu, held == 0)) {  // the lane's next four
+      if (k >= 3 && __any_sync(0xffffffffu, held == 0)) {  // the lane's next four
         uint32_t left[NJ], four[4];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) left[j] = ord[j] < *taken ? ord[j] : 0u;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   uint32_t my_key = 0u;
   for (int k = 0; k <= p.K; ++k) {
     uint32_t taken;
-    const int win = take_best(&taken);
+    const int win = take_best(k, &taken);
     if (win < 0) break;
     my_win = lane == k ? win : my_win;
     my_key = lane == k ? taken : my_key;
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (doubt) {
     // what comes after the first one left out must be clear of it (a tie is not)
     uint32_t taken = 0u;
-    const int win = take_best(&taken);
+    const int win = take_best(p.K + 1, &taken);
     const int second = win < 0 ? -1 : expert_of(win, taken);
     const Pick q = pick_of(second);
     const bool whole = __shfl_sync(
@@ -626,9 +627,9 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (p.renorm) {
     const float top = warp_max(kl);
     // far below zero the logistic function is exp(l); the common factor cancels
-    if (mine >= 0) s = (kSig && top > -60.f) ? 1.0f / (1.0f + expf(-kl)) : expf(kl - top);
+    if (mine >= 0) s = (kSig && top > -60.f) ? __fdividef(1.0f, 1.0f + expf(-kl)) : expf(kl - top);
     const float total = warp_sum(s);
-    s = mine >= 0 ? s / total : 0.f;
+    s = mine >= 0 ? __fdividef(s, total) : 0.f;
   } else if (mine >= 0) {
     s = kSig ? 1.0f / (1.0f + expf(-kl)) : expf(kl - m) * inv_sum;
   }
@@ -751,6 +752,10 @@ cudaError_t launch_route(const moe_route_config_t& c, RouteParams p, cudaStream_
   p.vec = c.E % q == 0 && (p.stride * eb) % 16 == 0 &&
           (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 &&
           (reinterpret_cast<uintptr_t>(p.d_logits) & 15u) == 0;
+  p.group_lanes = p.per % NJ == 0 ? p.per / NJ : 0;
+  p.lane_shift = -1;
+  for (int i = 0; i <= 5; ++i)
+    if (p.group_lanes == 1 << i) p.lane_shift = i;
   p.vec_bias = c.E % NJ == 0 && (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0;
   const bool sig = c.score == MOE_SCORE_SIGMOID;
   auto go = [&](auto nj_c) {
