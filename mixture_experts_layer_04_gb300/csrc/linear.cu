@@ -2,7 +2,7 @@
 // tensor-core product (linear_gemm.cu) and the product for a few rows.
 //
 //  - linear_rows_kernel (a few rows): every weight is used `rows` times only, so the call is
-//    bound by reading the weights once.  A block takes four output features, its eight
+//    bound by reading the weights once.  A block takes two or four output features, its eight
 //    warps split the input features, so each weight row is in flight as a whole; fp32 FMAs,
 //    partial sums joined in shared memory in warp order.  Any alignment and either type.  One
 //    row through 4096 x 4096 bf16 weights: 7.5 us, 4.5 TB/s.
@@ -23,16 +23,17 @@
 namespace moe {
 namespace {
 
-// Whether moe_linear runs on the CUDA cores.  One FMA per weight and row: bf16 weights that the
-// tensor cores read in place are faster there from 3 rows on (4096 x 4096: 2 rows 7.6 us here
-// and 9.5 there, 3 rows 10.7 and 9.5), or from 5 where the weights are few and the launch is
-// what counts (512 x 2048: 4 rows 5.8 and 7.5 us, 8 rows 8.1 and 6.7).  Operands that would
-// have to be packed first, all of float32, gain more from being read once (float32 4096 x 4096,
-// 8 rows: 25 and 45 us).
+// Whether moe_linear runs on the CUDA cores.  One FMA per weight and row: with two rows through
+// 4096 x 4096 bf16 weights the tensor cores are ahead (9.2 us against 10.3; one row 7.5 here),
+// with few weights, where the launch is what counts, the CUDA cores (4 rows through 2048 x 256:
+// 2.8 us against 4.2; through 512 x 2048: 4.7 against 4.2).  Operands that would have to be
+// packed first, all of float32, gain more from being read once (float32 4096 x 4096, 8 rows: 28
+// and 45 us).
 constexpr int kMaxFewRows = 8;
 bool few_rows(const moe_linear_config_t* c, bool packed) {
-  if (c->rows <= 2 || (packed && c->rows <= kMaxFewRows)) return true;
-  return c->rows <= 4 && static_cast<long long>(c->in_features) * c->out_features <= 1ll << 22;
+  if (c->rows == 1 || (packed && c->rows <= kMaxFewRows)) return true;
+  return c->rows <= 4 &&
+         static_cast<long long>(c->rows) * c->in_features * c->out_features <= 1ll << 21;
 }
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -296,10 +297,15 @@ struct RowsParams {
   int rows, in, out, act, y_f32, vec;
 };
 
-constexpr int kFeatures = 4;  // output features per block
+// Output features per block, and blocks per SM to compile for: with one row two features in all
+// the blocks that an SM can hold keep the most bytes in flight (4096 x 4096 bf16, weights from
+// HBM: 7.5 us, four features 9.4 us, eight 10.8 us).
+constexpr int rows_features(int mt) { return mt <= 2 ? 2 : 4; }
+constexpr int rows_blocks(int mt) { return mt == 1 ? 8 : 1; }
 
 template <typename TA, int MT>
-__global__ void __launch_bounds__(256) linear_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(256, rows_blocks(MT)) linear_rows_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int kFeatures = rows_features(MT);
   __shared__ float part[8][kFeatures * MT];
   grid_dep_wait();
   grid_dep_trigger();
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const __grid_constant_
   if (p.vec) {
     const int vecs = p.in / 8;
     done = vecs * 8;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = threadIdx.x; i < vecs; i += 256) {
       float wv[kFeatures][8];
 #pragma unroll
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const __grid_constant_
 
 template <typename TA>
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t s) {
-  const dim3 grid((static_cast<unsigned>(p.out) + kFeatures - 1) / kFeatures), block(256);
+  const int features = rows_features(p.rows);
+  const dim3 grid((static_cast<unsigned>(p.out) + features - 1) / features), block(256);
   if (p.rows == 1) return launch_pdl(linear_rows_kernel<TA, 1>, grid, block, 0, s, p);
   if (p.rows == 2) return launch_pdl(linear_rows_kernel<TA, 2>, grid, block, 0, s, p);
   if (p.rows <= 4) return launch_pdl(linear_rows_kernel<TA, 4>, grid, block, 0, s, p);
