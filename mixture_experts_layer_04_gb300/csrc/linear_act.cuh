@@ -62,12 +62,12 @@ __device__ __forceinline__ float act_value(int act, float z) {
   }
 }
 
-// Eight values at once: one switch for all of them.
-template <bool kFast>
-__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+// Several values at once: one switch for all of them.
+template <bool kFast, int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
   auto each = [&](auto a) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = act_value<kFast>(decltype(a)::value, v[q]);
+    for (int q = 0; q < N; ++q) v[q] = act_value<kFast>(decltype(a)::value, v[q]);
   };
   switch (act) {
     case MOE_ACT_RELU: each(std::integral_constant<int, MOE_ACT_RELU>{}); break;

@@ -57,6 +57,7 @@ struct Epilogue {
   int act;
   int c_f32;
   int vec_c, vec_r, vec_z, vec_bias;  // 16-byte accesses allowed
+  int wide16;  // bf16 results: c and z allow 32-byte accesses, res and bias 16-byte ones
 };
 
 struct Job {
@@ -249,6 +250,56 @@ __device__ __forceinline__ void prefetch_residual(const Epilogue& e, int row0, i
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const TA*>(e.res) +
                                                   static_cast<size_t>(row0 + r) * e.ldr + col0 + c));
   }
+}
+
+// Sixteen neighbouring bf16 values of a row, 32-byte aligned: one whole sector.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Sixteen neighbouring outputs of a bf16 tile that lies wholly inside the output, whose arrays
+// allow 32-byte accesses: a thread writes its own row in whole sectors, straight from the
+// accumulator. Against staging through shared memory, 4096 x 128 -> 14336 with its
+// result alone takes 61 us instead of 66 and the weight gradient of 64 rows at 4096 x 4096
+// 18.7 instead of 24.9. Rows that are not 32-byte aligned stay staged, where neighbouring lanes
+// share a row's sectors: 3999 x 1000 -> 2050 takes 113 us that way and 154 us a row per thread.
+__device__ __forceinline__ void finish16_inside(const Epilogue& e, int row, int col,
+                                                float (&v)[16]) {
+  using TA = __nv_bfloat16;
+  uint4 r[2];
+  if (e.res != nullptr) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const TA*>(e.res) +
+                                                      static_cast<size_t>(row) * e.ldr + col);
+    r[0] = src[0];
+    r[1] = src[1];
+  }
+  if (e.bias != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 16; q += 4) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(e.bias + col + q));
+      v[q] += b.x, v[q + 1] += b.y, v[q + 2] += b.z, v[q + 3] += b.w;
+    }
+  }
+  if (e.z != nullptr) store16(static_cast<TA*>(e.z) + static_cast<size_t>(row) * e.ldz + col, v);
+  act_values<true>(e.act, v);
+  if (e.res != nullptr) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unpack_bf16(r[i], x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[8 * i + q] += x[q];
+    }
+  }
+  store16(static_cast<TA*>(e.c) + static_cast<size_t>(row) * e.ldc + col, v);
 }
 
 // finish8 for two rows (row, row + step) of a bf16 tile that lies wholly inside the output,
@@ -669,7 +720,6 @@ struct PairCfg {
   static constexpr int kStages = 6;
   static constexpr int kBN = 256;
   static constexpr int kTmemCols = 512;
-  static constexpr int kChunk = 16;   // columns staged at a time
   static constexpr int kStgRow = 20;  // floats per staged row: 16 and a pad against conflicts
   static constexpr int kStgBytes = kEpiWarps * 32 * kStgRow * 4;
   static constexpr int kBarBytes = 256;
@@ -841,45 +891,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       tc_fence_after();
       const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                          static_cast<uint32_t>(acc * Cfg::kBN + half * 128);
-      // lane l reads back columns (l & 1) * 8 of rows l / 2 and l / 2 + 16
-      const int rr = lane >> 1, cc = (lane & 1) * 8;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += Cfg::kChunk) {
-        const int row = row0 + rr, col = col0 + c + cc;
-        float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (inside && job.epi.bias != nullptr) load_n(job.epi.bias + col, 8, true, bias);
-        uint32_t r[16];
-        tmem_ld_32x32b_x16(t + c, r);
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t + c, r);
         tmem_ld_wait();
-        if (c + Cfg::kChunk == 128) {  // the accumulator is free for the tile after next
+        if (c + 32 == 128) {  // the accumulator is free for the tile after next
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
         }
+        if (inside && job.epi.wide16) {
 #pragma unroll
-        for (int q = 0; q < 16; q += 4)
-          *reinterpret_cast<float4*>(stg + lane * Cfg::kStgRow + q) =
-              make_float4(__uint_as_float(r[q]), __uint_as_float(r[q + 1]),
-                          __uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]));
-        __syncwarp();
-        float v[2][8];
+          for (int h = 0; h < 32; h += 16) {
+            float v[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          load_n(stg + (rr + 16 * i) * Cfg::kStgRow + cc, 8, true, v[i]);
-        __syncwarp();
-        if (inside) {
-          finish8_inside(job.epi, row, 16, col, bias, v);
+            for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[h + q]);
+            finish16_inside(job.epi, row0 + lane, col0 + c + h, v);
+          }
         } else {
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            if (row + 16 * i < job.epi.rows && col < job.epi.cols) {
-              float u[8];
+          // staged: lane l reads back columns (l & 1) * 8 of rows l / 2 and l / 2 + 16
+          const int rr = lane >> 1, cc = (lane & 1) * 8;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) u[q] = i == 0 ? v[0][q] : v[1][q];
-              finish8<__nv_bfloat16>(job.epi, row + 16 * i, col, u);
+          for (int h = 0; h < 32; h += 16) {
+#pragma unroll
+            for (int q = 0; q < 16; q += 4)
+              *reinterpret_cast<float4*>(stg + lane * Cfg::kStgRow + q) =
+                  make_float4(__uint_as_float(r[h + q]), __uint_as_float(r[h + q + 1]),
+                              __uint_as_float(r[h + q + 2]), __uint_as_float(r[h + q + 3]));
+            __syncwarp();
+            const int col = col0 + c + h + cc;
+            if (inside) {
+              float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[2][8];
+              if (job.epi.bias != nullptr) load_n(job.epi.bias + col, 8, true, bias);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                load_n(stg + (rr + 16 * i) * Cfg::kStgRow + cc, 8, true, v[i]);
+              __syncwarp();
+              finish8_inside(job.epi, row0 + rr, 16, col, bias, v);
+              continue;
             }
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 16) {
+              if (row0 + rr + i < job.epi.rows && col < job.epi.cols) {
+                float v[8];
+                load_n(stg + (rr + i) * Cfg::kStgRow + cc, 8, true, v);
+                finish8<__nv_bfloat16>(job.epi, row0 + rr + i, col, v);
+              }
+            }
+            __syncwarp();
           }
         }
+        __syncwarp();
       }
     }
   }
@@ -1099,6 +1162,12 @@ Epilogue epilogue_of(const LinearGemm& g) {
   e.vec_r = vec_ok(g.res, g.ldr, ab);
   e.vec_z = vec_ok(g.z, g.ldz, ab);
   e.vec_bias = vec_ok(g.bias, 0, 4);
+  auto sector_ok = [](const void* p, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld % 16 == 0;
+  };
+  e.wide16 = !g.c_f32 && !g.act_f32 && sector_ok(g.c, g.ldc) &&
+             (g.z == nullptr || sector_ok(g.z, g.ldz)) && (g.res == nullptr || e.vec_r) &&
+             e.vec_bias;
   return e;
 }
 

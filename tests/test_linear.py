@@ -221,6 +221,32 @@ def test_forward_on_cta_pairs(rows, fin, fout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("pad,off", [(16, 16), (16, 8), (8, 0), (8, 8), (5, 3), (2, 1)])
+@pytest.mark.parametrize("rows,fout", [(2560, 2048), (2500, 2500)])
+def test_outputs_at_each_alignment_on_cta_pairs(rows, fout, pad, off):
+    # 32-, 16- and 2-byte aligned rows are written in different ways; what lies beside them stays
+    fin = 64
+    x, w, b, res, _ = make(rows, fin, fout, torch.bfloat16, pad + off)
+    wide = lambda: torch.full((rows, fout + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    y, z, r = wide(), wide(), wide()
+    cut = lambda t: t[:, off:off + fout]
+    cut(r).copy_(res)
+    c = config(rows, fin, fout, activation=moe.ACT_SILU, y_stride=fout + pad, z_stride=fout + pad,
+               residual_stride=fout + pad)
+    moe.linear(c, x, w, b, cut(r), cut(y), cut(z), workspace(c))
+    moe.sync_check()
+    for t in (y, z):
+        assert (t[:, :off] == 7).all() and (t[:, off + fout:] == 7).all()
+    zr = x.double() @ w.double().t() + b.double()
+    yr = act(moe.ACT_SILU, zr) + res.double()
+    err = (product_error(fin, x.double().abs() @ w.double().abs().t(), False) +
+           2.0 ** -22 * (zr.abs() + 4))
+    assert ((cut(z).double() - zr).abs() <= err + 2.0 ** -8 * zr.abs() * 1.01).all()
+    assert ((cut(y).double() - yr).abs() <=
+            1.13 * err + 2.0 ** -20 * zr.abs() + 2.0 ** -8 * yr.abs() * 1.01).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (5, 0), (5, 3), (1, 1)])
 def test_column_slices_do_not_read_their_neighbours(pad, off, dtype):
