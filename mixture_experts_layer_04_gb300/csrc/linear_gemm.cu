@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Eight epilogue warps, two per TMEM lane quarter with half the columns each: with four, the
 // epilogue of a tile took longer than its MMAs (4096 x 4096 -> 14336 with tanh-GELU and the
-// kept pre-activation: 503 us; with eight 260 us, 1,853 TFLOP/s, the tensor pipe 89% busy).
+// kept pre-activation: 503 us; with eight 258 us, 1,864 TFLOP/s, the tensor pipe 90% busy).
 struct PairCfg {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
