@@ -221,6 +221,17 @@ def test_forward_on_cta_pairs(rows, fin, fout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,fin,fout", [(185, 1024, 5440), (130, 200, 5437), (192, 72, 5440)])
+def test_more_rows_than_a_tile_through_many_features(rows, fin, fout, dtype):
+    forward(rows, fin, fout, dtype, moe.ACT_GELU, seed=rows)
+    forward(rows, fin, fout, dtype, moe.ACT_NONE, bias=False, residual=False, keep=False, pad=5,
+            off=3)
+    if dtype == torch.bfloat16:
+        forward(rows, fin, fout, dtype, moe.ACT_SILU, out_f32=True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("pad,off", [(16, 16), (16, 8), (8, 0), (8, 8), (5, 3), (2, 1)])
 @pytest.mark.parametrize("rows,fout", [(2560, 2048), (2500, 2500)])
 def test_outputs_at_each_alignment_on_cta_pairs(rows, fout, pad, off):
