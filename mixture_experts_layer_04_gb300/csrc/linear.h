@@ -40,7 +40,7 @@ struct LinearGemm {
 bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms);
 
 // One product, or two with operands and results of the same types and no dependence on each
-// other (in one launch where both suit the tile kernel).
+// other (in one launch where both suit the tile kernel and one tile suits both).
 cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
                                 cudaStream_t s);
 

@@ -1099,6 +1099,7 @@ Sides sides_of(const LinearGemm& g, bool swap) {
 struct TileChoice {
   int ba, bn, split;
   bool other;  // the operands lie the other way round than swap_by_rule has them
+  double cost;
 };
 
 // The tile, the split of the reduction and the operands' sides, by an estimate in SM clocks: waves
@@ -1116,31 +1117,37 @@ TileChoice choose_tile(const LinearGemm* jobs, int n, int num_sms) {
   const int planes = jobs[0].planes;
   const int terms = planes == 3 ? 6 : 1;
   const bool forward = n == 1 && !jobs[0].a_mn && !jobs[0].b_mn;
-  TileChoice best{128, 128, 1, false};
-  double best_cost = 1e30;
+  TileChoice best{128, 128, 1, false, 1e30};
   auto consider = [&](int ba, int bn, bool other) {
-    long long tiles = 0;
-    int num_kb = 0;
+    long long tiles[2] = {0, 0};
+    int num_kb[2] = {0, 0};
     for (int i = 0; i < n; ++i) {
       const Sides sd = sides_of(jobs[i], swap_by_rule(jobs[i]) != other);
       if (sd.b_mn && bn < 64) return;  // row-contiguous boxes are 64 rows wide
-      tiles += static_cast<long long>(ceil_div(sd.a, ba)) * ceil_div(sd.b, bn);
-      num_kb = std::max(num_kb, ceil_div(jobs[i].depth, BK));
+      tiles[i] = static_cast<long long>(ceil_div(sd.a, ba)) * ceil_div(sd.b, bn);
+      num_kb[i] = ceil_div(jobs[i].depth, BK);
     }
     const double load = planes * (ba + bn) * 128.0 / 60.0;
     // an MMA of 16 products: its rate, or reading 128 + bn rows of 32 bytes
     const double mma = 4.0 * terms * std::max(0.52 * bn, 32.0 + 0.25 * bn);
     for (int i = 0; i < 4; ++i) {
       const int split = 1 << i;
-      if (split > num_kb) continue;
-      const long long waves = (tiles + room.room[i] - 1) / room.room[i];
-      const double per_tile = ceil_div(num_kb, split) * (load > mma ? load : mma) + 4000.0 +
-                              (split > 1 ? 500.0 + 0.3 * ba * bn : 0.0) + 0.25 * ba * bn / split;
-      const double cost = waves * per_tile * (other ? 1.08 : 1.0);  // only for a clear gain
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = TileChoice{ba, bn, split, other};
+      if (split > num_kb[0]) continue;  // the first job is the longest
+      const long long slots = room.room[i];
+      auto per_tile = [&](int j) {
+        return ceil_div(num_kb[j], split) * (load > mma ? load : mma) + 4000.0 +
+               (split > 1 ? 500.0 + 0.3 * ba * bn : 0.0) + 0.25 * ba * bn / split;
+      };
+      double cost = ((tiles[0] + slots - 1) / slots) * per_tile(0);
+      if (n == 2) {
+        // the second job's tiles run beside the first one's last wave, then in their own
+        const long long free = (slots - tiles[0] % slots) % slots;
+        const long long beside = free * static_cast<long long>(per_tile(0) / per_tile(1));
+        const long long rest = std::max(0ll, tiles[1] - beside);
+        cost += ((rest + slots - 1) / slots) * per_tile(1);
       }
+      if (other) cost *= 1.08;  // only for a clear gain
+      if (cost < best.cost) best = TileChoice{ba, bn, split, other, cost};
     }
   };
   for (int other = 0; other <= (forward ? 1 : 0); ++other)
@@ -1202,12 +1209,11 @@ cudaError_t launch_pairs(const LinearGemm& g, unsigned* err, int num_sms, cudaSt
   return count_launch(cudaGetLastError());
 }
 
-cudaError_t launch_tiles(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
+cudaError_t launch_tiles(const LinearGemm* jobs, int n, const TileChoice& t, unsigned* err,
                          cudaStream_t s) {
   GemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.err = err;
-  const TileChoice t = choose_tile(jobs, n, num_sms);
   long long total = 0;
   for (int i = 0; i < n; ++i) {
     const LinearGemm& g = jobs[i];
@@ -1261,18 +1267,36 @@ cudaError_t launch_tiles(const LinearGemm* jobs, int n, unsigned* err, int num_s
 
 bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms) { return prefer_pairs(g, num_sms); }
 
+// What a second launch costs in the estimate's clocks (half of it on the host, where small calls
+// wait).  Two products share a launch, and with it
+// tile and split, unless their own choices save more than that: a dx of few tiles and a long
+// reduction wants a split that a dW of many tiles and a short one would repay with waves (70 rows,
+// 192 -> 5312, float32: 81 us together, 27 apart; 128 rows, 2048 -> 7168: 172 and 131).  Where the
+// two come close the estimate can be wrong: of 58 shapes timed both ways 16 rows, 128 -> 4096 in
+// bf16 lose most, 12.5 -> 13.5 us.
+constexpr double kLaunchClocks = 8000.0;
+
 cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
                                 cudaStream_t s) {
   if (n == 2 && !prefer_pairs(jobs[0], num_sms) && !prefer_pairs(jobs[1], num_sms)) {
     // the longer tiles first: the shorter ones fill the last wave better
     const int longer = jobs[0].depth >= jobs[1].depth ? 0 : 1;
     const LinearGemm by_depth[2] = {jobs[longer], jobs[1 - longer]};
-    return launch_tiles(by_depth, 2, err, num_sms, s);
+    const TileChoice joint = choose_tile(by_depth, 2, num_sms);
+    const TileChoice apart[2] = {choose_tile(by_depth, 1, num_sms),
+                                 choose_tile(by_depth + 1, 1, num_sms)};
+    if (0.9 * joint.cost <= apart[0].cost + apart[1].cost + kLaunchClocks)
+      return launch_tiles(by_depth, 2, joint, err, s);
+    for (int i = 0; i < 2; ++i) {
+      const cudaError_t e = launch_tiles(by_depth + i, 1, apart[i], err, s);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
   }
   for (int i = 0; i < n; ++i) {
     const cudaError_t e = prefer_pairs(jobs[i], num_sms)
                               ? launch_pairs(jobs[i], err, num_sms, s)
-                              : launch_tiles(jobs + i, 1, err, num_sms, s);
+                              : launch_tiles(jobs + i, 1, choose_tile(jobs + i, 1, num_sms), err, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

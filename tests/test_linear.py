@@ -354,6 +354,16 @@ def test_backward_on_cta_pairs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,fin,fout", [(70, 192, 5312), (60, 64, 8001), (333, 190, 5312),
+                                           (100, 8000, 130)])
+def test_backward_of_long_and_short_reductions(rows, fin, fout, dtype):
+    # one gradient has few tiles and a long reduction, the other many tiles and a short one
+    backward(rows, fin, fout, dtype, moe.ACT_GELU, seed=fout)
+    backward(rows, fin, fout, dtype, moe.ACT_NONE, pad=5, off=3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("pad,off", [(8, 8), (5, 3)])
 def test_backward_of_column_slices(pad, off):
     for dtype in (torch.bfloat16, torch.float32):
