@@ -1267,13 +1267,13 @@ cudaError_t launch_tiles(const LinearGemm* jobs, int n, const TileChoice& t, uns
 
 bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms) { return prefer_pairs(g, num_sms); }
 
-// What a second launch costs in the estimate's clocks (half of it on the host, where small calls
-// wait).  Two products share a launch, and with it
-// tile and split, unless their own choices save more than that: a dx of few tiles and a long
-// reduction wants a split that a dW of many tiles and a short one would repay with waves (70 rows,
-// 192 -> 5312, float32: 81 us together, 27 apart; 128 rows, 2048 -> 7168: 172 and 131).  Where the
-// two come close the estimate can be wrong: of 58 shapes timed both ways 16 rows, 128 -> 4096 in
-// bf16 lose most, 12.5 -> 13.5 us.
+// What a second launch costs in the estimate's clocks: with 4000 more shapes lost by it than with
+// 8000.  Two products share a launch, and with it tile and split, unless their own choices save
+// more than that: a dx of few tiles and a long reduction wants a split that a dW of many tiles and
+// a short one would repay with waves (70 rows, 192 -> 5312, float32: 81 us together, 27 apart; 128
+// rows, 2048 -> 7168: 172 and 131).  Where the two come close the estimate can be wrong: of 58
+// shapes timed both ways 17 gain over 3% and two lose 8%, 16 rows, 128 -> 4096 (12.5 -> 13.5 us)
+// and 1000 rows, 256 -> 4096 (29.7 -> 32.0 us), both bf16.
 constexpr double kLaunchClocks = 8000.0;
 
 cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
