@@ -5,14 +5,17 @@
 // a group whose size is a multiple of NJ never straddles lanes.
 //
 // The choice.  It is defined on 64-bit keys s[e] + bias[e], and 64-bit arithmetic is slow on
-// this GPU (16 clocks per warp instruction), so it is taken in float first and certified:
-// every float score carries a bound on its error.  Where two neighbouring choices (the K-th
-// and the first one left out among them) are closer than the sum of their bounds, the K+1
-// best are put in order by their 64-bit keys, one per lane; groups whose sums cannot be told
-// apart at the border between kept and dropped are compared by 64-bit sums; and only if in
-// such a case the first two experts left out are close to each other too is the whole token
-// chosen again.  Without a bias the keys are ordered as the logits are, so the logits
-// themselves are compared.  Two experts of equal logit and equal bias tie in any precision.
+// this GPU (16 clocks per warp instruction), so it is taken in float first and certified
+// with a bound on the error of every float score.  The bound is the one of the largest score
+// there can be, not those of the two experts compared: an expert further down in the order may
+// have a larger score (and a lower bias) than they, and its key may be off by more than theirs.
+// Where two neighbouring choices (the K-th and the first one left out among them) are closer
+// than two such bounds, the K+1 best are put in order by their 64-bit keys, one per lane; groups
+// whose sums cannot be told apart at the border between kept and dropped are compared by 64-bit
+// sums; and only if in such a case the first two experts left out are close to each other too
+// is the whole token chosen again.  Without a bias the keys are ordered as the logits are, so
+// the logits themselves are compared.  Two experts of equal logit and equal bias tie in any
+// precision.
 //
 // The K+1 best come from each lane's own four best, kept in order in registers as integers:
 // the float's bits made monotone, the last log2(NJ) of them replaced by the register's number
@@ -297,27 +300,27 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// A float score and a bound on its absolute error, in units of 2^-23 of the score: the
-// hardware exponential is off by at most 2 + 1.17 |x| of them.  Logistic function: for l > 0
-// that is damped by 1 - s to 1.1, the sum and the reciprocal add under 3.  Softmax: the sum
-// adds its terms' mean error (|x| averages at most ln 1024) and its additions' roundings, 17
-// in all, the products 2.  Scores under 2^-126 may come out as 0, which the bounds' floor
-// covers.
+// A float score.  Its absolute error, in units of 2^-23 of the score: the hardware exponential
+// is off by at most 2 + 1.17 |x| of them.  Logistic function: for l > 0 that is damped by 1 - s
+// to 1.1, the sum and the reciprocal add under 3: 5 + 1.2 max(-l, 0).  Softmax: the sum adds its
+// terms' mean error (|x| averages at most ln 1024) and its additions' roundings, 17 in all, the
+// products 2: 21 + 1.2 (m - l).  The scores fall faster than these grow, so no score of a row is
+// off by more than the largest there can be: 5 units of 1, 21 units of inv_sum.  Scores under
+// 2^-126 may come out as 0, which the bounds' floor covers.
 template <bool kSig>
 __device__ __forceinline__ float score_of(float l, float m, float inv_sum) {
   if (kSig) return rcp_approx(1.0f + __expf(-l));
   return __expf(l - m) * inv_sum;
 }
 template <bool kSig>
-__device__ __forceinline__ float score_error(float s, float l, float m) {
-  const float units = kSig ? 5.0f + 1.2f * fmaxf(-l, 0.f) : 21.0f + 1.2f * (m - l);
-  return s * units * 0x1p-23f;
+__device__ __forceinline__ float score_error(float inv_sum) {
+  return kSig ? 5.0f * 0x1p-23f : 21.0f * 0x1p-23f * inv_sum;
 }
 constexpr float kErrFloor = 1e-34f;
 
 // One chosen (or next best) expert as a lane holds it.
 struct Pick {
-  float l, b, key, err;
+  float l, b, key;
 };
 
 // Without a bias the order of the scores is the order of the logits, but scores a few 2^-53 of
@@ -329,14 +332,14 @@ __device__ __forceinline__ bool scores_merge(const Pick& a, const Pick& b, float
   return !(gap > 1e-14f) || b.l - m < -600.f;
 }
 
-// Whether a and b, a before b, are too close for their order as ordered keys (rounded to
-// `unit`) to be relied on.
+// Whether a and b, a before b, are too close to rely on a being before b and everything after b
+// in the order of the keys (rounded to `unit`, each with an error of up to `err`).
 template <bool kSig>
 __device__ __forceinline__ bool close(const Pick& a, const Pick& b, bool has_bias, float m,
-                                      float unit) {
+                                      float err, float unit) {
   if (has_bias)
     return !(a.key - b.key >
-             a.err + b.err + 2.0f * kErrFloor + unit * (fabsf(a.key) + fabsf(b.key)));
+             2.0f * (err + kErrFloor) + unit * (fabsf(a.key) + fabsf(b.key)));
   return !(a.l - b.l > unit * (fabsf(a.l) + fabsf(b.l)) + 1e-30f) || scores_merge<kSig>(a, b, m);
 }
 
@@ -404,6 +407,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     for (int j = 0; j < NJ; ++j) sum += __expf(l[j] - m);
     inv_sum = 1.0f / warp_sum(sum);
   }
+
+  const float err = score_error<kSig>(inv_sum);
 
   // `ord` orders the experts by their keys; those at kNone or below are not available
   constexpr uint32_t kLow = NJ - 1, kNone = 0x007fffffu;  // kNone: -inf's
@@ -497,8 +502,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       const float unit = NJ * 0x1p-23f;
       float rounding = mag * unit;
       if (!has_bias) rounding = unit * (kSig ? 0.6f : mag * fabsf(m) + 0.8f * top);
-      const float slack = 2.0f * (2.0f * score_error<kSig>(top, m, m) + 2.0f * kErrFloor +
-                                  mag * 0x1p-22f + rounding);
+      const float slack = 2.0f * (2.0f * err + 2.0f * kErrFloor + mag * 0x1p-22f + rounding);
       if (!(lowest_in - best_out > slack)) {
         // the groups at the border, by 64-bit sums, for the places that the clear ones leave
         const bool in = (live >> lane) & 1u;
@@ -566,13 +570,11 @@ __global__ void __launch_bounds__(32 * kWarps)
     return win * NJ + static_cast<int>(kLow - (taken & kLow));
   };
   auto pick_of = [&](int e) {
-    Pick q{-INFINITY, 0.f, 0.f, 0.f};
+    Pick q{-INFINITY, 0.f, 0.f};
     if (e >= 0) {
       q.l = clean_logit(to_float(row[e]));
       q.b = has_bias ? __ldg(p.bias + e) : 0.f;
-      const float s = score_of<kSig>(q.l, m, inv_sum);
-      q.key = s + q.b;
-      q.err = score_error<kSig>(s, q.l, m);
+      q.key = score_of<kSig>(q.l, m, inv_sum) + q.b;
     }
     return q;
   };
@@ -592,13 +594,12 @@ __global__ void __launch_bounds__(32 * kWarps)
   // certify the order of neighbours
   const Pick me = pick_of(mine);
   const Pick next{__shfl_down_sync(0xffffffffu, me.l, 1), __shfl_down_sync(0xffffffffu, me.b, 1),
-                  __shfl_down_sync(0xffffffffu, me.key, 1),
-                  __shfl_down_sync(0xffffffffu, me.err, 1)};
+                  __shfl_down_sync(0xffffffffu, me.key, 1)};
   const int next_e = __shfl_down_sync(0xffffffffu, mine, 1);
   constexpr float kUnit = (1 + NJ) * 0x1p-23f;
   const bool tie = me.l == next.l && me.b == next.b;  // in any precision
   const bool doubt = __any_sync(0xffffffffu, lane < p.K && next_e >= 0 && !tie &&
-                                                 close<kSig>(me, next, has_bias, m, kUnit));
+                                                 close<kSig>(me, next, has_bias, m, err, kUnit));
   if (doubt) {
     // what comes after the first one left out must be clear of it (a tie is not)
     uint32_t taken = 0u;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int second = win < 0 ? -1 : expert_of(win, taken);
     const Pick q = pick_of(second);
     const bool whole = __shfl_sync(
-        0xffffffffu, second >= 0 && close<kSig>(me, q, has_bias, m, kUnit), p.K);
+        0xffffffffu, second >= 0 && close<kSig>(me, q, has_bias, m, err, kUnit), p.K);
     if (whole) {
       mine = choose64<NJ, TL, kSig>(p, row, m, lane, live);
     } else {
