@@ -62,3 +62,59 @@ def test_large_scores_with_negative_biases_next_to_small_ones(triples, score):
     E = logits.shape[1]
     for K in (1, 2, 3):
         check(moe.RouteConfig.make(T, E, K, 1, 1, 1, score), logits, bias)
+
+
+def tied_rows(T, E, dtype, seed, top=1.0):
+    """Rows with two to five equal logits at low ids, and one expert of a higher id that is one
+    step of the type above them; everything else is clearly below."""
+    rng = np.random.default_rng(seed)
+    L = torch.full((T, E), 0.0)
+    L += torch.tensor(rng.uniform(top - 6.0, top - 2.0, (T, E)), dtype=torch.float32)
+    L = L.to(dtype)
+    v = torch.tensor(top, dtype=dtype)
+    up = torch.tensor(top * (1 + torch.finfo(dtype).eps), dtype=dtype)
+    for t in range(T):
+        n = int(rng.integers(2, 6))
+        at = np.sort(rng.choice(E, n + 1, replace=False))
+        L[t, at[:n]] = v
+        L[t, at[n]] = up
+    return L.cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("E", [20, 60, 256, 1000])
+def test_ties_at_the_border_with_a_better_expert_further_down(E, score):
+    # 1: without a bias a step of the logits is lost in the order's low bits; 20: the logistic
+    # function is 1 in float (and 6e-10 apart in 64 bits)
+    T = 300
+    for dtype, code in ((torch.float32, moe.F32), (torch.bfloat16, moe.BF16)):
+        for top in (1.0, 20.0):
+            logits = tied_rows(T, E, dtype, E, top)
+            for bias in (None, torch.zeros(E, device="cuda"),
+                         torch.full((E,), 0.25, device="cuda")):
+                for K in (1, 2, 3, 5):
+                    check(moe.RouteConfig.make(T, E, K, 1, 1, 1, score, dtype=code), logits, bias)
+
+
+@pytest.mark.gpu
+def test_three_saturated_scores():
+    logits = torch.tensor([[20.0, 20.0, 21.0]], device="cuda")
+    for bias in (None, torch.zeros(3, device="cuda")):
+        ids, _ = check(moe.RouteConfig.make(1, 3, 1, score=moe.SCORE_SIGMOID), logits, bias)
+        assert ids.item() == 2
+    # 64 bits cannot tell 40 from 41 either: the lower id, whichever its logit
+    logits = torch.tensor([[39.5, 41.0, 41.0]], device="cuda")
+    ids, _ = check(moe.RouteConfig.make(1, 3, 1, score=moe.SCORE_SIGMOID), logits)
+    assert ids.item() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", SCORES)
+def test_grouped_choices_with_ties_and_better_experts(score):
+    T, E = 300, 256
+    for top in (1.0, 20.0):
+        logits = tied_rows(T, E, torch.float32, 7, top)
+        for bias in (None, torch.zeros(E, device="cuda")):
+            check(moe.RouteConfig.make(T, E, 2, 8, 4, 2, score), logits, bias)
+            check(moe.RouteConfig.make(T, E, 3, 32, 20, 1, score), logits, bias)
