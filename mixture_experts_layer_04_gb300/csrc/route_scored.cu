@@ -368,6 +368,15 @@ __device__ __noinline__ bool others_close(const RouteParams& p, const TL* row, c
   return __any_sync(0xffffffffu, near);
 }
 
+// A chosen expert's score over one factor common to the token's chosen (of largest logit `top`),
+// which renormalisation takes out again: the logistic function is e^min(l,0) / (1 + e^-|l|), so
+// that nothing overflows and small scores keep their ratio.
+template <bool kSig>
+__device__ __forceinline__ float relative_score(float l, float top) {
+  if (!kSig) return expf(l - top);
+  return __fdividef(expf(fminf(l, 0.f) - fminf(top, 0.f)), 1.0f + expf(-fabsf(l)));
+}
+
 // Descending order of two, and of four.
 __device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
   const uint32_t hi = max(a, b);
@@ -664,8 +673,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   float s = 0.f;
   if (p.renorm) {
     const float top = warp_max(kl);
-    // far below zero the logistic function is exp(l); the common factor cancels
-    if (mine >= 0) s = (kSig && top > -60.f) ? __fdividef(1.0f, 1.0f + expf(-kl)) : expf(kl - top);
+    if (mine >= 0) s = relative_score<kSig>(kl, top);
     const float total = warp_sum(s);
     s = mine >= 0 ? __fdividef(s, total) : 0.f;
   } else if (mine >= 0) {
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (p.renorm) {
       const float top = warp_max(kl);
       float s = 0.f;
-      if (id >= 0) s = (kSig && top > -60.f) ? 1.0f / (1.0f + expf(-kl)) : expf(kl - top);
+      if (id >= 0) s = relative_score<kSig>(kl, top);
       const float total = warp_sum(s);
       const float rho = id >= 0 ? s / total : 0.f;
       const float dot = warp_sum(dw * rho);
