@@ -76,13 +76,28 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+constexpr float kMaxBf16 = 0x1.fep127f;
+
 // Eight values in PL bf16 parts at dst, dst + plane, ...  A value that is not finite goes
-// whole into the first part.
+// whole into the first part.  A finite one that rounding would take past bf16's largest (above
+// 3.39e38) has that for its first part: what is left fits the others.
 template <int PL>
 __device__ __forceinline__ void store_parts(__nv_bfloat16* dst, long long plane, float (&v)[8]) {
 #pragma unroll
   for (int pl = 0; pl < PL; ++pl) {
-    const uint4 u = pack8(v);
+    uint4 u = pack8(v);
+    if (PL > 1 && pl == 0) {
+      float most = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) most = fmaxf(most, fabsf(v[q]));
+      if (most > kMaxBf16) {
+        float t[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          t[q] = fabsf(v[q]) < INFINITY ? fminf(fmaxf(v[q], -kMaxBf16), kMaxBf16) : v[q];
+        u = pack8(t);
+      }
+    }
     *reinterpret_cast<uint4*>(dst + pl * plane) = u;
     if (pl + 1 < PL) {
       float r[8];
