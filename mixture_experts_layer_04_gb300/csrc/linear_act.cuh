@@ -1,9 +1,9 @@
 // Activations of the linear layers and their derivatives, in fp32.
 //
-// kFast forms serve results that are rounded to bf16 (2^-8): the hardware exponential, the
-// approximate division and, for the normal distribution function, the rational approximation
-// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions (absolute error under
-// 7e-8 here), whose exponential the derivative shares.
+// kFast forms serve bf16 operands, whose results are rounded to bf16 (2^-8) in most calls: the
+// hardware exponential, the approximate division and, for the normal distribution function, a
+// polynomial whose exponential the derivative shares.  Their values are good to 2e-5 of their
+// size down to about 2e-37, where the exponential or its reciprocal leaves the normal numbers.
 #pragma once
 
 #include <type_traits>
@@ -25,13 +25,19 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return r;
 }
 
-// Phi(z) for kFast; *e = exp(-z^2 / 2).
+// Phi(z) for kFast; *e = exp(-z^2 / 2).  With x = |z| / sqrt 2, Phi(-|z|) = e^(-x^2) f(x) / 2,
+// and f, which falls from 1 like 1 / x, is t P(t) with t = 1 / (1 + 0.49 x).  P (degree 6) is
+// fitted to f on 0 <= x <= 9.6 for the least of the larger of its relative error over 1e-5 and
+// its share of Phi's absolute error over 7e-8, in a third of both; float arithmetic brings that
+// to 9e-6 of Phi's size over the whole tail and 1.7e-7 absolute.
 __device__ __forceinline__ float normal_cdf_fast(float z, float* e) {
-  const float t = rcp_ftz(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
-  float poly = fmaf(t, 1.061405429f, -1.453152027f);
-  poly = fmaf(t, poly, 1.421413741f);
-  poly = fmaf(t, poly, -0.284496736f);
-  poly = fmaf(t, poly, 0.254829592f);
+  const float t = rcp_ftz(fmaf(0.49f * 0.70710678f, fabsf(z), 1.0f));
+  float poly = fmaf(t, 0.08903342f, -0.37844392f);
+  poly = fmaf(t, poly, 0.45524510f);
+  poly = fmaf(t, poly, -0.0054650893f);
+  poly = fmaf(t, poly, 0.29349263f);
+  poly = fmaf(t, poly, 0.26927288f);
+  poly = fmaf(t, poly, 0.27686502f);
   *e = exp2_ftz(-0.72134752f * z * z);
   const float tail = (0.5f * t) * (poly * *e);  // Phi(-|z|)
   return z < 0.f ? tail : 1.0f - tail;

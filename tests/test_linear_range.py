@@ -1,4 +1,5 @@
-"""Linear layers at the ends of their numerics: the largest float32 values.
+"""Linear layers at the ends of their numerics: the largest float32 values and the
+activations' tails.
 
 The formulas in 64 bits and the tolerances' terms are those of tests/test_linear.py.
 """
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_04_gb300 as moe
-from tests.test_linear import config, workspace
+from tests.test_linear import act, config, slope, workspace
 
 FLT_MAX = torch.finfo(torch.float32).max
 
@@ -82,3 +83,52 @@ def test_infinities_and_nan_still_reach_their_outputs_only():
     bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
     bad[[3, 7, 9]] = True
     assert not torch.isfinite(y[bad]).any() and torch.isfinite(y[~bad]).all()
+
+
+# ------------------------------------------------------------- the activations' tails ----
+
+def grid(lo, hi):
+    """Every bf16 value of lo..hi, in rows of 64."""
+    v = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v[torch.isfinite(v) & (v >= lo) & (v <= hi) & (v.abs() >= 2.0 ** -20)]
+    return v[: v.numel() // 64 * 64].reshape(-1, 64).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("a", [moe.ACT_GELU, moe.ACT_GELU_TANH, moe.ACT_SILU])
+@pytest.mark.parametrize("few", [True, False])
+def test_bf16_activations_are_rounded_once_over_their_whole_range(a, few):
+    """Through an identity, so that z is the input: the value's own error is a few units in the
+    last place of float32 and of the exponential's argument (under 2^-14 of its size down to the
+    smallest normal numbers), then comes the one rounding."""
+    x = grid(-12.9, 12.9)
+    x = x[:8 * (x.shape[0] // 8)]
+    eye = torch.eye(64, device="cuda").bfloat16()
+    parts = x.reshape(-1, 1, 64) if few else x.reshape(1, -1, 64)
+    for xs in parts:
+        for f32 in (False, True):
+            c = config(xs.shape[0], 64, 64, activation=a, out_dtype=moe.F32 if f32 else moe.BF16)
+            y = torch.empty(xs.shape, device="cuda", dtype=torch.float32 if f32 else xs.dtype)
+            moe.linear(c, xs.contiguous(), eye, None, None, y, None, workspace(c))
+            want = act(a, xs.double())
+            tol = (2.0 ** -14 + (0.0 if f32 else 2.0 ** -8)) * want.abs() + 2.0 ** -122
+            if f32:
+                tol = tol + 2.0 ** -22 * xs.double().abs() * (xs > -1.0)
+            assert ((y.double() - want).abs() <= tol).all()
+    moe.sync_check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("a", [moe.ACT_GELU, moe.ACT_GELU_TANH, moe.ACT_SILU])
+def test_bf16_slopes_in_the_tail_are_rounded_once(a):
+    """dz through an identity: dy act'(z), rounded to bf16, exactly the gradient.  Below -3 every
+    slope is away from its zero and its terms do not cancel by more than a factor of three."""
+    z = grid(-12.5, -3.0)
+    eye = torch.eye(64, device="cuda").bfloat16()
+    dy = torch.ones_like(z)
+    c = config(z.shape[0], 64, 64, activation=a)
+    dx = torch.empty_like(z)
+    moe.linear_backward(c, dy, None, eye, z, dx, None, None, workspace(c))
+    moe.sync_check()
+    want = slope(a, z.double())
+    assert ((dx.double() - want).abs() <= (2.0 ** -12 + 2.0 ** -8) * want.abs() + 2.0 ** -118).all()
