@@ -434,7 +434,9 @@ moe_status_t moe_linear_workspace_size(const moe_linear_config_t* cfg, size_t* b
  * Float32 products run on the tensor cores as three bf16 parts per value, with the partial
  * sums added in fp32 registers every 128 values; where an input is infinite or NaN
  * the outputs that it reaches are not finite, and values under 1e-33 keep 16 of their 24
- * bits.  A few rows (1 to 8, by type and size) run on the CUDA cores, where the weights' read
+ * bits.  Bf16 operands: partial sums are added in fp32 registers every 256 values for float32
+ * results, every 16384 for bf16 ones (an accumulator on the tensor cores truncates: values of one
+ * sign come out low by 6e-9 of the sum per value).  A few rows (1 to 8, by type and size) run on the CUDA cores, where the weights' read
  * is what counts.  Outputs must not overlap inputs otherwise. */
 moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x, const void* w,
                         const float* bias, const void* residual, void* y, void* z, void* ws,

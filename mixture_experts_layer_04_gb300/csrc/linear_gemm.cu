@@ -46,6 +46,11 @@ namespace {
 
 constexpr int BK = 64;        // bf16 elements per k-block: one 128-byte swizzle row
 constexpr int kThreads = 192; // TMA warp, MMA warp, four epilogue warps
+// k-blocks that one accumulator takes for a bf16 result, 16384 values.  The tensor core truncates
+// its additions, which leaves a sum of values of one sign low by 6.2e-9 of its size per value
+// (measured from 64 K to 1 M values): 1.0e-4 here, against the result's own rounding of 1.7e-3.
+// DW of 524288 rows in one accumulator would be off by 3.2e-3.
+constexpr int kMaxChunk = 256;
 
 struct Epilogue {
   void* c;
@@ -740,8 +745,12 @@ __device__ __forceinline__ void pair_tile(const Job& p, int idx, int* ta, int* t
 struct PairParams {
   Job job;
   unsigned* err;
+  int chunk;  // k-blocks per accumulator
 };
 
+// kDeep: a tile's reduction is longer than an accumulator may take (kMaxChunk); the epilogue
+// warps add up the chunks in registers.
+template <bool kDeep>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
   using Cfg = PairCfg;
@@ -834,35 +843,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
       const uint32_t a_step = job.a_mn ? 2048u : 32u, b_step = job.b_mn ? 2048u : 32u;
       int stage = 0;
       uint32_t phase = 0;
-      int local = 0;
+      int local = 0;  // accumulators filled
       bool ok = true;
-      for (int idx = pair; ok && idx < total; idx += npairs, ++local) {
-        const int acc = local & 1;
-        if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
-                       p.err))
-          break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::kBN);
-        for (int kb = 0; kb < job.num_kb; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+      for (int idx = pair; ok && idx < total; idx += npairs) {
+        for (int kb = 0; ok && kb < job.num_kb; ++local) {
+          const int acc = local & 1;
+          if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
+                         p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
-          const uint32_t b_base = a_base + Cfg::kABytes;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * Cfg::kBN);
+          const int first = kb, end = kDeep ? min(job.num_kb, kb + p.chunk) : job.num_kb;
+          for (; kb < end; ++kb) {
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
+            const uint32_t b_base = a_base + Cfg::kABytes;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, job.a_mn),
-                             operand_desc(b_base + kk * b_step, job.b_mn), idesc,
-                             (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair(empty_bar(stage), 0x3);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, job.a_mn),
+                               operand_desc(b_base + kk * b_step, job.b_mn), idesc,
+                               kb != first || kk != 0 ? 1u : 0u);
+            tc_commit_pair(empty_bar(stage), 0x3);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
         }
-        if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
       }
       if (!ok || *abort_flag) {
         tc_commit_pair(mma_done_bar, 0x1);
@@ -877,36 +891,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     float* stg = stg_all + (warp - 2) * 32 * Cfg::kStgRow;
     const bool wide = job.epi.vec_c && (job.epi.res == nullptr || job.epi.vec_r) &&
                       (job.epi.z == nullptr || job.epi.vec_z) && job.epi.vec_bias;
-    int local = 0;
-    for (int idx = pair; idx < total; idx += npairs, ++local) {
+    int local = 0;  // accumulators read
+    for (int idx = pair; idx < total; idx += npairs) {
       int ta, tb;
       pair_tile(job, idx, &ta, &tb);
-      const int acc = local & 1;
       const int row0 = ta * 256 + static_cast<int>(rank) * 128 + quad * 32;
       const int col0 = tb * 256 + half * 128;
       const bool inside = wide && row0 + 32 <= job.epi.rows && col0 + 128 <= job.epi.cols;
-      const bool ready =
-          mbar_wait(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err);
-      if (__any_sync(0xffffffffu, !ready)) break;
-      tc_fence_after();
-      const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                         static_cast<uint32_t>(acc * Cfg::kBN + half * 128);
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t + c, r);
-        tmem_ld_wait();
-        if (c + 32 == 128) {  // the accumulator is free for the tile after next
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-        }
+      // 32 neighbouring columns from col0 + c on of this thread's row
+      auto finish = [&](int c, const float (&r)[32]) {
         if (inside && job.epi.wide16) {
 #pragma unroll
           for (int h = 0; h < 32; h += 16) {
             float v[16];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[h + q]);
+            for (int q = 0; q < 16; ++q) v[q] = r[h + q];
             finish16_inside(job.epi, row0 + lane, col0 + c + h, v);
           }
         } else {
@@ -917,8 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 #pragma unroll
             for (int q = 0; q < 16; q += 4)
               *reinterpret_cast<float4*>(stg + lane * Cfg::kStgRow + q) =
-                  make_float4(__uint_as_float(r[h + q]), __uint_as_float(r[h + q + 1]),
-                              __uint_as_float(r[h + q + 2]), __uint_as_float(r[h + q + 3]));
+                  make_float4(r[h + q], r[h + q + 1], r[h + q + 2], r[h + q + 3]);
             __syncwarp();
             const int col = col0 + c + h + cc;
             if (inside) {
@@ -943,6 +941,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
           }
         }
         __syncwarp();
+      };
+      // waits for accumulator `local`, whose columns of this thread start at accumulator()
+      auto filled = [&] {
+        const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
+                                     abort_flag, p.err);
+        if (__any_sync(0xffffffffu, !ready)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto accumulator = [&] {
+        return tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+               static_cast<uint32_t>((local & 1) * Cfg::kBN + half * 128);
+      };
+      auto release_accumulator = [&] {  // it is free for the tile (or chunk) after next
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(local & 1), 0));
+        ++local;
+      };
+      if constexpr (kDeep) {
+        float sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 32; ++q) sum[i][q] = 0.f;
+        bool ok = true;
+        for (int kb = 0; kb < job.num_kb; kb += p.chunk) {
+          ok = filled();
+          if (!ok) break;
+          const uint32_t t = accumulator();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t + i * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) sum[i][q] += __uint_as_float(r[q]);
+          }
+          release_accumulator();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) finish(i * 32, sum[i]);
+      } else {
+        if (!filled()) break;
+        const uint32_t t = accumulator();
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t + c, r);
+          tmem_ld_wait();
+          if (c + 32 == 128) release_accumulator();
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
+          finish(c, v);
+        }
       }
     }
   }
@@ -1200,12 +1255,15 @@ cudaError_t launch_pairs(const LinearGemm& g, unsigned* err, int num_sms, cudaSt
   j.tiles_b = ceil_div(g.cols, 256);
   const long long tiles = static_cast<long long>(j.tiles_a) * j.tiles_b;
   if (tiles >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(linear_pair_kernel, PairCfg::kSmem, &done);
+  p.chunk = kMaxChunk;
+  const bool deep = j.num_kb > kMaxChunk;
+  auto kernel = deep ? linear_pair_kernel<true> : linear_pair_kernel<false>;
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = allow_smem(kernel, PairCfg::kSmem, &done[deep]);
   if (e != cudaSuccess) return e;
   const int pairs = static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
   // a plain launch: see the top of the file
-  linear_pair_kernel<<<dim3(2 * pairs), dim3(PairCfg::kThreads), PairCfg::kSmem, s>>>(p);
+  kernel<<<dim3(2 * pairs), dim3(PairCfg::kThreads), PairCfg::kSmem, s>>>(p);
   return count_launch(cudaGetLastError());
 }
 
@@ -1239,10 +1297,10 @@ cudaError_t launch_tiles(const LinearGemm* jobs, int n, const TileChoice& t, uns
   }
   if (total * t.split >= (1ll << 31)) return cudaErrorInvalidValue;
   p.total = static_cast<int>(total);
-  // bf16 results are rounded far above the tensor core's own error: one chunk.  Float32 ones
-  // leave it after 128 (six products per value, so the drain still hides behind the MMAs) or
-  // 256 values
-  p.chunk = jobs[0].planes == 3 ? 2 : jobs[0].c_f32 ? 4 : 1 << 30;
+  // Float32 results leave the tensor core after 128 (six products per value, so the drain still
+  // hides behind the MMAs) or 256 values; bf16 ones are rounded far above its error up to
+  // kMaxChunk
+  p.chunk = jobs[0].planes == 3 ? 2 : jobs[0].c_f32 ? 4 : kMaxChunk;
   auto go = [&](auto pl) {
     constexpr int PL = decltype(pl)::value;
     if (t.ba == 64) {
