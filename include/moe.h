@@ -419,15 +419,17 @@ typedef struct {
   int64_t x_stride, w_stride, residual_stride, y_stride, z_stride, dx_stride, dw_stride;
 } moe_linear_config_t;
 
-/* Bytes of device workspace that moe_linear and moe_linear_backward need for `cfg` (the
- * larger of the two; 0 is possible).  Scratch, as moe_workspace_size's. */
+/* Bytes of device workspace that moe_linear and moe_linear_backward take for `cfg`: what the
+ * backward needs (dz, column sums, packed operands), never 0.  Scratch, as
+ * moe_workspace_size's. */
 moe_status_t moe_linear_workspace_size(const moe_linear_config_t* cfg, size_t* bytes);
 
 /* y = act(x w^T + bias) + residual, accumulated in fp32, each output rounded once.
  *   x [rows,in] act; w [out,in] act; bias [out] float or NULL; residual [rows,out] act or
  *   NULL; y [rows,out] out_dtype out; z [rows,out] act out or NULL: the value before the
  *   activation, which the backward needs (y is computed from the unrounded value).
- *   ws: moe_linear_workspace_size() bytes, 16-byte aligned (NULL when that is 0).
+ *   ws: moe_linear_workspace_size() bytes, 16-byte aligned; NULL will do for the calls on the
+ *   CUDA cores (below), which use none.
  * y may be residual itself (same type and stride).  Pointers need the alignment of their
  * elements; x and w, whose row stride is a multiple of 16 bytes, must start on a 16-byte
  * boundary (MOE_ERR_MISALIGNED; other strides are copied into the workspace first).
@@ -436,8 +438,10 @@ moe_status_t moe_linear_workspace_size(const moe_linear_config_t* cfg, size_t* b
  * the outputs that it reaches are not finite, and values under 1e-33 keep 16 of their 24
  * bits.  Bf16 operands: partial sums are added in fp32 registers every 256 values for float32
  * results, every 16384 for bf16 ones (an accumulator on the tensor cores truncates: values of one
- * sign come out low by 6e-9 of the sum per value).  A few rows (1 to 8, by type and size) run on the CUDA cores, where the weights' read
- * is what counts.  Outputs must not overlap inputs otherwise. */
+ * sign come out low by 6e-9 of the sum per value).  On the CUDA cores run one row; up to 8 rows
+ * where x or w would be copied into the workspace (float32, or a row stride that is not a
+ * multiple of 16 bytes); up to 4 rows while rows * in_features * out_features <= 2^21: there
+ * the weights' read is what counts.  Outputs must not overlap inputs otherwise. */
 moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x, const void* w,
                         const float* bias, const void* residual, void* y, void* z, void* ws,
                         size_t ws_bytes, moe_stream_t stream);
@@ -446,7 +450,8 @@ moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x, const voi
  *   dx = dz w;  dw = dz^T x;  dbias = the column sums of dz;  (d residual is dy).
  *   dy [rows,out] out_dtype (row stride y_stride); x, w as given to moe_linear; z as it
  *   returned it (NULL without an activation); dx [rows,in] act out or NULL; dw [out,in] act
- *   out or NULL; dbias [out] float out or NULL; ws as for moe_linear.
+ *   out or NULL; dbias [out] float out or NULL; ws: moe_linear_workspace_size() bytes, 16-byte
+ *   aligned (NULL with rows == 0).
  * dz is rounded to act before the products (the operand type of the tensor cores); dbias
  * sums it unrounded.  x may be NULL when dw is, w when dx is.  dy keeps to the rule on 16
  * bytes that x and w have.  With rows == 0, dw and dbias are zeroed. */

@@ -555,13 +555,14 @@ extern "C" moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x
       unaligned(y, act_bytes(cfg->out_dtype)))
     return MOE_ERR_MISALIGNED;
   const LinearPlan plan = make_linear_plan(cfg);
-  if (plan.total > 0 && (ws == nullptr || ws_bytes < plan.total)) return MOE_ERR_WORKSPACE;
-  if (unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
+  const bool few = few_rows(cfg, plan.pack_x || plan.pack_w);  // needs no workspace
+  if (!few && (ws == nullptr || ws_bytes < plan.total)) return MOE_ERR_WORKSPACE;
+  if (!few && unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
   st = check_current_device();
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-  if (few_rows(cfg, plan.pack_x || plan.pack_w)) {
+  if (few) {
     RowsParams p{};
     p.x = x;
     p.w = w;
@@ -658,7 +659,7 @@ extern "C" moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, cons
       (dx != nullptr && bad_operand(w, ld.w, cfg->dtype)) || (has_act && unaligned(z, ab)))
     return MOE_ERR_MISALIGNED;
   const LinearPlan plan = make_linear_plan(cfg);
-  if (plan.total > 0 && (ws == nullptr || ws_bytes < plan.total)) return MOE_ERR_WORKSPACE;
+  if (ws == nullptr || ws_bytes < plan.total) return MOE_ERR_WORKSPACE;
   if (unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
   st = check_current_device();
   if (st != MOE_OK) return st;
