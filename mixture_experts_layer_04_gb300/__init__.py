@@ -206,10 +206,13 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the raw handle of torch's current stream: building a torch.cuda.Stream for it takes
-        # 3 us, as long as a small call's launch
-        from torch import _C
-        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+        import torch
+        try:
+            # the raw handle of torch's current stream: building a torch.cuda.Stream for it takes
+            # 3 us, as long as a small call's launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:  # the names are not public: a torch that has them no longer
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
