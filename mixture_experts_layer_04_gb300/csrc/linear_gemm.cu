@@ -1329,9 +1329,10 @@ bool linear_gemm_on_pairs(const LinearGemm& g, int num_sms) { return prefer_pair
 // 8000.  Two products share a launch, and with it tile and split, unless their own choices save
 // more than that: a dx of few tiles and a long reduction wants a split that a dW of many tiles and
 // a short one would repay with waves (70 rows, 192 -> 5312, float32: 81 us together, 27 apart; 128
-// rows, 2048 -> 7168: 172 and 131).  Where the two come close the estimate can be wrong: of 58
-// shapes timed both ways 17 gain over 3% and two lose 8%, 16 rows, 128 -> 4096 (12.5 -> 13.5 us)
-// and 1000 rows, 256 -> 4096 (29.7 -> 32.0 us), both bf16.
+// rows, 2048 -> 7168: 172 and 131).  Where the two come close the estimate can be wrong: of 24
+// shapes of 8 to 1896 rows within 10% of the border on the side of two launches, 16 gain 5 to 28%
+// by them (80 rows, 200 -> 4616, bf16 19.7 -> 14.2 us), three are equal and five lose 2 to 14%
+// (920 rows, 1920 -> 392, float32 36.3 -> 41.5 us).
 constexpr double kLaunchClocks = 8000.0;
 
 cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, int num_sms,
@@ -1343,7 +1344,7 @@ cudaError_t launch_linear_gemms(const LinearGemm* jobs, int n, unsigned* err, in
     const TileChoice joint = choose_tile(by_depth, 2, num_sms);
     const TileChoice apart[2] = {choose_tile(by_depth, 1, num_sms),
                                  choose_tile(by_depth + 1, 1, num_sms)};
-    if (0.9 * joint.cost <= apart[0].cost + apart[1].cost + kLaunchClocks)
+    if (joint.cost <= apart[0].cost + apart[1].cost + kLaunchClocks)
       return launch_tiles(by_depth, 2, joint, err, s);
     for (int i = 0; i < 2; ++i) {
       const cudaError_t e = launch_tiles(by_depth + i, 1, apart[i], err, s);
