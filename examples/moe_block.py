@@ -3,15 +3,17 @@
     h      = x W_o^T + x                     attention output projection, residual in its epilogue
     logits = h W_r^T                         router logits in float32
     ids, w = route_scored(logits, bias)      sigmoid scores, balance bias, expert groups, top-k
-    rows   = grouped FFN of the dispatched rows of h              (experts frozen)
+    rows   = grouped FFN of the dispatched rows of h       (experts frozen, no gradient to h)
     c      = combine(rows, w)
     z      = h W_1^T + b_1;  u = silu(z)     dense branch
     y      = u W_2^T + c                     second product, the combined experts as residual
 
 The backward gives the gradients of W_o, W_r, W_1, b_1 and W_2: the combine's gradient yields
 the route weights', routing's gradient the logits', and the linear layers take it from there.
-(The experts are frozen, so nothing flows back through their products.)  After each step the
-balance bias moves against the experts' load, as scores-plus-bias routing is trained.
+The experts' rows are a constant of h in it (a stop-gradient): the library has no backward of
+the grouped products, so W_o's gradient is that of the dense branch, the router and the residual
+and leaves out what h does through the experts.  After each step the balance bias moves against
+the experts' load, as scores-plus-bias routing is trained.
 
     python examples/moe_block.py [--tokens T] [--steps N]
 
@@ -97,7 +99,7 @@ class MoEBlock:
         return self.y
 
     def backward(self, x, dy):
-        """Gradients by name, for the x of the last forward."""
+        """Gradients by name, for the x of the last forward, the experts' input held constant."""
         lws = self.lin_ws
         like = torch.empty_like
         du, dw_2 = like(self.u), like(self.w_2)

@@ -5,7 +5,8 @@
 //    bound by reading the weights once.  A block takes two or four output features, its eight
 //    warps split the input features, so each weight row is in flight as a whole; fp32 FMAs,
 //    partial sums joined in shared memory in warp order.  Any alignment and either type.  One
-//    row through 4096 x 4096 bf16 weights: 6.4 us, 5.2 TB/s (7.5 us with every weight from HBM).
+//    row through 4096 x 4096 bf16 weights: 7.5 us with every weight from HBM, 4.5 TB/s (6.4 us
+//    with three copies in turn, which L2 holds in part; 5.1 us with one).
 //  - pack_kernel: an operand the tensor cores cannot read in place.  Float32 values become
 //    three bf16 parts (p0 = bf16(v), p1 = bf16(v - p0), p2 = bf16(v - p0 - p1): 24 bits), and
 //    rows whose stride is not a multiple of 16 bytes are copied to one that is.

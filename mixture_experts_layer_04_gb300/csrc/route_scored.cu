@@ -24,9 +24,9 @@
 // and a step is one warp-wide maximum, a ballot and a shuffle.
 //
 // What bounds it: the row of logits is read once (T*E elements) and K ids and weights are
-// written, but the instructions come first: 917 per token at 256 experts in 8 groups and K = 8,
-// most of them on the half-rate integer and compare pipe (61% busy).  16384 such tokens take
-// 18 us (2.6 us of memory traffic; 18.7 to 21 with inputs rotating), one token 4.3 us, which is its launch.
+// written, but the instructions come first: 924 per token at 256 experts in 8 groups and K = 8,
+// most of them on the half-rate integer and compare pipe (60% busy).  16384 such tokens take
+// 18 to 21 us (2.6 us of memory traffic), one token 4.3 us, which is its launch.
 #include <cfloat>
 #include <type_traits>
 
