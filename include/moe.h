@@ -405,7 +405,8 @@ typedef enum {
   MOE_ACT_RELU = 1,
   MOE_ACT_GELU = 2,
   MOE_ACT_GELU_TANH = 3,
-  MOE_ACT_SILU = 4
+  MOE_ACT_SILU = 4,
+  MOE_ACT_SWIGLU = 5 /* moe_grouped_linear only */
 } moe_activation_t;
 
 typedef struct {
@@ -458,6 +459,65 @@ moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* x, const voi
 moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, const void* dy, const void* x,
                                  const void* w, const void* z, void* dx, void* dw, float* dbias,
                                  void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Matrix products grouped by expert, with their gradients: what trains the experts (and runs
+ * ones of any size).  Rows and offsets are those of moe_permute; the order of the stages is
+ * that of the layer. */
+
+typedef struct {
+  int32_t rows;            /* rows that x, y, z, dy and dx have room for, 0..2^30 */
+  int32_t groups;          /* experts, 1..1024 */
+  int32_t in_features;     /* 1..2^18 */
+  int32_t out_features;    /* 1..2^18; columns of y */
+  int32_t dtype;           /* moe_dtype_t of x, w, z, dy and dw ("act") */
+  int32_t out_dtype;       /* moe_dtype_t of y: dtype, or MOE_F32 */
+  int32_t dx_dtype;        /* moe_dtype_t of dx: dtype, or MOE_F32 */
+  int32_t activation;      /* MOE_ACT_NONE or MOE_ACT_SWIGLU */
+  /* elements between rows, 0 = contiguous; the groups' weights follow one another */
+  int64_t x_stride, w_stride, y_stride, z_stride, dx_stride, dw_stride;
+} moe_grouped_config_t;
+
+/* Bytes of device workspace that moe_grouped_linear and moe_grouped_linear_backward take for
+ * `cfg`, never 0.  Scratch, as moe_workspace_size's. */
+moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg, size_t* bytes);
+
+/* For every row r of group g (offsets[g] <= r < offsets[g+1]):
+ *   z[r] = x[r] w[g]^T, accumulated in fp32;
+ *   y[r] = z[r] (MOE_ACT_NONE), or silu(z[r][c]) * z[r][out + c] for c < out (MOE_ACT_SWIGLU:
+ *   w has 2 out rows per group, the gate's first, as w_gate_up of moe_grouped_ffn),
+ * computed from the unrounded z and rounded once.
+ *   x [rows,in] act; offsets [groups+1] int32 (device), ascending within 0..rows, offsets[0] >= 0;
+ *   w [groups, out or 2 out, in] act; y [rows,out] out_dtype out; z [rows, 2 out] act out or
+ *   NULL (SWIGLU only): what the backward needs; ws: moe_grouped_linear_workspace_size() bytes,
+ *   16-byte aligned.
+ * Rows that belong to no group are not read into any result, and those of y and z are left as
+ * they were; weights of empty groups are not read.  Offsets that descend or leave 0..rows are
+ * held to the largest before them and to rows, and reported by moe_sync_check
+ * (MOE_ERR_INTERNAL).  Pointers need the alignment of their elements; x and w whose row stride is
+ * a multiple of 16 bytes must start on a 16-byte boundary (MOE_ERR_MISALIGNED).  Float32
+ * operands run as three bf16 parts per value, as moe_linear's; partial sums leave the tensor
+ * cores every 128 values (float32 operands), 256 (float32 results) or 16384.
+ * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work. */
+moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
+                                const int32_t* offsets, const void* w, void* y, void* z, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* The gradients of moe_grouped_linear: with dz = dy, or for SWIGLU, with z = (g, u),
+ * dz = (dy u silu'(g), dy silu(g)),
+ *   dx[r] = dz[r] w[g];  dw[g] = sum over the group's rows of dz[r]^T x[r] (0 for an empty one).
+ *   dy [rows,out] act (row stride y_stride); x, offsets, w as given to moe_grouped_linear; z as it
+ *   returned it (NULL without an activation); dx [rows,in] dx_dtype out or NULL, rows that belong
+ *   to no group left as they were; dw [groups, out or 2 out, in] act out or NULL, every element
+ *   written; ws as above (NULL with rows == 0, which zeroes dw).
+ * dz is rounded to act before the products.  x may be NULL when dw is, w when dx is.  dy keeps to
+ * the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds up to the
+ * gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
+ * gradient.  The same inputs give the same bits. */
+moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
+                                         const void* x, const int32_t* offsets, const void* w,
+                                         const void* z, void* dx, void* dw, void* ws,
+                                         size_t ws_bytes, moe_stream_t stream);
 
 /* Intermediates of the last moe_layer_forward that used `ws` (views into ws; valid
  * until ws is reused).  Any output pointer may be NULL.  Useful to check every stage.

@@ -21,6 +21,8 @@ __all__ = [
     "RouteConfig", "SCORE_SOFTMAX", "SCORE_SIGMOID", "route_scored", "route_scored_backward",
     "combine_backward", "LinearConfig", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH",
     "ACT_SILU", "linear_workspace_size", "linear", "linear_backward",
+    "GroupedConfig", "ACT_SWIGLU", "grouped_linear_workspace_size", "grouped_linear",
+    "grouped_linear_backward",
     "sync_check", "debug_wait_timeout", "status_string", "version",
 ]
 
@@ -40,6 +42,7 @@ ACT_RELU = 1
 ACT_GELU = 2
 ACT_GELU_TANH = 3
 ACT_SILU = 4
+ACT_SWIGLU = 5  # grouped_linear only
 
 _STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -124,6 +127,35 @@ class LinearConfig(ctypes.Structure):
                 f"out_dtype={self.out_dtype}, activation={self.activation})")
 
 
+class GroupedConfig(ctypes.Structure):
+    """moe_grouped_config_t: rows, groups, in_features, out_features, dtype, out_dtype, dx_dtype,
+    activation and the row strides in elements (0 = contiguous)."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("groups", ctypes.c_int32), ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32), ("dx_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+        ("w_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("dw_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, rows, groups, in_features, out_features, dtype=BF16, out_dtype=None,
+             dx_dtype=None, activation=ACT_NONE, x_stride=0, w_stride=0, y_stride=0, z_stride=0,
+             dx_stride=0, dw_stride=0):
+        return cls(rows, groups, in_features, out_features, dtype,
+                   dtype if out_dtype is None else out_dtype,
+                   dtype if dx_dtype is None else dx_dtype, activation, x_stride, w_stride,
+                   y_stride, z_stride, dx_stride, dw_stride)
+
+    def __repr__(self):
+        return (f"GroupedConfig(rows={self.rows}, groups={self.groups}, "
+                f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"dtype={self.dtype}, out_dtype={self.out_dtype}, dx_dtype={self.dx_dtype}, "
+                f"activation={self.activation})")
+
+
 def library_path(debug: bool = False) -> str:
     """The release library, or with ``debug`` the bounds-checking build (-DMOE_DEBUG)."""
     return os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -136,6 +168,7 @@ _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoEConfig)
 _RCFG = ctypes.POINTER(RouteConfig)
 _LCFG = ctypes.POINTER(LinearConfig)
+_GCFG = ctypes.POINTER(GroupedConfig)
 _SIGS = {
     "moe_workspace_size": [_CFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_route": [_CFG, _P, _P, _P, _P, _P, _P, _P],
@@ -159,6 +192,9 @@ _SIGS = {
     "moe_linear_workspace_size": [_LCFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_linear": [_LCFG, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_linear_backward": [_LCFG, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_linear_workspace_size": [_GCFG, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_grouped_linear": [_GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_linear_backward": [_GCFG, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_sync_check": [_P],
     "moe_debug_wait_timeout": [ctypes.c_uint, _P, _P],
     "moe_status_string": [ctypes.c_int],
@@ -398,6 +434,29 @@ def linear_backward(cfg, dy, x, w, z, dx, dw, dbias, ws=None, ws_bytes=None, str
                                       _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws),
                                       _ws(ws, ws_bytes), _stream(stream)),
            "moe_linear_backward")
+
+
+def grouped_linear_workspace_size(cfg: GroupedConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_grouped_linear_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_grouped_linear_workspace_size")
+    return n.value
+
+
+def grouped_linear(cfg, x, offsets, w, y, z=None, ws=None, ws_bytes=None, stream=None):
+    """y_r = x_r w_g^T for the rows of every group g, or silu(gate) * up of it (ACT_SWIGLU; z
+    optionally receives the value before the activation)."""
+    _check(load().moe_grouped_linear(ctypes.byref(cfg), _ptr(x), _ptr(offsets), _ptr(w), _ptr(y),
+                                     _ptr(z), _ptr(ws), _ws(ws, ws_bytes), _stream(stream)),
+           "moe_grouped_linear")
+
+
+def grouped_linear_backward(cfg, dy, x, offsets, w, z, dx, dw, ws=None, ws_bytes=None,
+                            stream=None):
+    """dx and dw (each may be None) of grouped_linear; z is what grouped_linear stored."""
+    _check(load().moe_grouped_linear_backward(
+        ctypes.byref(cfg), _ptr(dy), _ptr(x), _ptr(offsets), _ptr(w), _ptr(z), _ptr(dx),
+        _ptr(dw), _ptr(ws), _ws(ws, ws_bytes), _stream(stream)), "moe_grouped_linear_backward")
 
 
 def workspace_views(cfg, ws) -> dict:

@@ -1,0 +1,515 @@
+// moe_grouped_linear and moe_grouped_linear_backward: argument checks, the workspace and the
+// passes around the grouped tensor-core product (grouped_gemm.cu).
+//
+//  - prepare_kernel: operands the tensor cores cannot read in place (float32 values become three
+//    bf16 parts, rows whose stride is not a multiple of 16 bytes are copied to one that is), and
+//    the gradient of SwiGLU, dz = (dy u silu'(g), dy silu(g)), rounded to the operand type of the
+//    products that take it.  Rows that belong to no group and weights of empty groups are passed
+//    over.  Bound by reading dy and z and writing dz.
+#include "common.cuh"
+#include "grouped.h"
+#include "kernels.h"
+#include "linear_act.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+// n of eight values at p, zeros after them; 16-byte loads when `vec` and all eight are there.
+template <typename T>
+__device__ __forceinline__ void load_n(const T* p, int n, bool vec, float (&v)[8]) {
+  if (vec && n >= 8) {
+    load8(p, v);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = q < n ? to_f(p[q]) : 0.f;
+}
+
+constexpr float kMaxBf16 = 0x1.fep127f;
+
+// The next bf16 part of v, and what it leaves.  A value that is not finite goes whole into the
+// first part; a finite one that rounding would take past bf16's largest has that for its first
+// part.
+template <int PL>
+__device__ __forceinline__ __nv_bfloat16 take_part(float* v, bool first) {
+  float t = *v;
+  if (PL > 1 && first && fabsf(t) < INFINITY) t = fminf(fmaxf(t, -kMaxBf16), kMaxBf16);
+  const __nv_bfloat16 h = __float2bfloat16_rn(t);
+  const float r = __bfloat162float(h);
+  *v = fabsf(r) < INFINITY ? *v - r : 0.f;
+  return h;
+}
+
+// n <= 8 values in PL bf16 parts at dst, dst + plane, ...; 16-byte stores when `vec`.
+template <int PL>
+__device__ __forceinline__ void store_parts(__nv_bfloat16* dst, long long plane, int n, bool vec,
+                                            float (&v)[8]) {
+#pragma unroll
+  for (int pl = 0; pl < PL; ++pl) {
+    __nv_bfloat16 h[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[q] = take_part<PL>(&v[q], pl == 0);
+    __nv_bfloat16* d = dst + pl * plane;
+    if (vec && n == 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h[2 * i])) |
+               (static_cast<uint32_t>(__bfloat16_as_ushort(h[2 * i + 1])) << 16);
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < n) d[q] = h[q];
+    }
+  }
+}
+
+// A matrix to copy in parts: rows of `cols` values.  Activations (group_rows == 0): the rows below
+// the last bound; weights: the groups that have rows.
+struct PackTask {
+  const void* src;
+  long long ld;
+  __nv_bfloat16* dst;
+  long long dst_ld, plane;
+  long long rows;
+  int cols, vec, group_rows;
+  int blocks;  // of 256 threads, 0: nothing to pack
+};
+
+struct DzTask {
+  const void* dy;
+  const void* z;
+  long long ldy, ldz;
+  __nv_bfloat16* dz;
+  long long dz_ld, plane;
+  int cols;              // of dy; dz has twice as many
+  int vec_y, vec_z, vec_dz;
+  int blocks;
+};
+
+struct PrepareParams {
+  const int* bounds;
+  int groups;
+  DzTask dz;
+  PackTask x, w;
+};
+
+template <typename T, int PL>
+__device__ __forceinline__ void pack_task(const PackTask& t, const int* bounds, int groups,
+                                          int block) {
+  const int per_row = static_cast<int>(t.dst_ld / 8);
+  const long long rows = t.group_rows == 0 ? bounds[groups] : t.rows;
+  const long long items = rows * per_row;
+  for (long long i = block * 256ll + threadIdx.x; i < items; i += t.blocks * 256ll) {
+    const long long r = i / per_row;
+    const int c = static_cast<int>(i - r * per_row) * 8;
+    if (t.group_rows != 0) {
+      const int g = static_cast<int>(r / t.group_rows);
+      if (bounds[g] == bounds[g + 1]) continue;
+    }
+    float v[8];
+    load_n(static_cast<const T*>(t.src) + r * t.ld + c, t.cols - c, t.vec != 0, v);
+    store_parts<PL>(t.dst + r * t.dst_ld + c, t.plane, 8, true, v);
+  }
+}
+
+template <typename T, int PL>
+__device__ __forceinline__ void dz_task(const DzTask& t, int rows, int block) {
+  const int per_row = (t.cols + 7) / 8;
+  const long long items = static_cast<long long>(rows) * per_row;
+  const long long step = t.blocks * 256ll;
+  for (long long i = block * 256ll + threadIdx.x; i < items; i += step) {
+    const long long r = i / per_row;
+    const int c = static_cast<int>(i - r * per_row) * 8, n = min(8, t.cols - c);
+    float dy[8], gate[8], up[8];
+    load_n(static_cast<const T*>(t.dy) + r * t.ldy + c, n, t.vec_y != 0, dy);
+    const T* z = static_cast<const T*>(t.z) + r * t.ldz + c;
+    load_n(z, n, t.vec_z != 0, gate);
+    load_n(z + t.cols, n, t.vec_z != 0, up);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float slope = act_slope<PL == 1>(MOE_ACT_SILU, gate[q]);
+      const float value = act_value<PL == 1>(MOE_ACT_SILU, gate[q]);
+      gate[q] = dy[q] * up[q] * slope;
+      up[q] = dy[q] * value;
+    }
+    __nv_bfloat16* dst = t.dz + r * t.dz_ld + c;
+    store_parts<PL>(dst, t.plane, n, t.vec_dz != 0, gate);
+    store_parts<PL>(dst + t.cols, t.plane, n, t.vec_dz != 0, up);
+  }
+}
+
+template <typename T, int PL>
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
+  grid_dep_wait();
+  grid_dep_trigger();
+  int b = static_cast<int>(blockIdx.x);
+  if (b < p.dz.blocks) {
+    dz_task<T, PL>(p.dz, p.bounds[p.groups], b);
+    return;
+  }
+  b -= p.dz.blocks;
+  if (b < p.x.blocks) pack_task<T, PL>(p.x, p.bounds, p.groups, b);
+  else pack_task<T, PL>(p.w, p.bounds, p.groups, b - p.x.blocks);
+}
+
+cudaError_t launch_prepare(const PrepareParams& p, bool f32, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.dz.blocks + p.x.blocks + p.w.blocks));
+  return f32 ? launch_pdl(prepare_kernel<float, 3>, grid, dim3(256), 0, s, p)
+             : launch_pdl(prepare_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s, p);
+}
+
+// --------------------------------------------------------------------- host ----
+
+struct Shape {
+  long long x, w, y, z, dx, dw;  // row strides
+  int w_rows;                    // rows of a group's weights, columns of z
+  bool swiglu, f32;
+};
+
+Shape shape_of(const moe_grouped_config_t* c) {
+  auto pick = [](long long s, long long n) { return s != 0 ? s : n; };
+  Shape s;
+  s.swiglu = c->activation == MOE_ACT_SWIGLU;
+  s.f32 = c->dtype == MOE_F32;
+  s.w_rows = c->out_features * (s.swiglu ? 2 : 1);
+  s.x = pick(c->x_stride, c->in_features);
+  s.w = pick(c->w_stride, c->in_features);
+  s.y = pick(c->y_stride, c->out_features);
+  s.z = pick(c->z_stride, s.w_rows);
+  s.dx = pick(c->dx_stride, c->in_features);
+  s.dw = pick(c->dw_stride, c->in_features);
+  return s;
+}
+
+moe_status_t check_grouped_config(const moe_grouped_config_t* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->rows < 0 || c->rows > (1 << 30)) return MOE_ERR_INVALID_ARG;
+  if (c->groups < 1 || c->groups > 1024) return MOE_ERR_INVALID_ARG;
+  if (c->in_features < 1 || c->in_features > (1 << 18)) return MOE_ERR_INVALID_ARG;
+  if (c->out_features < 1 || c->out_features > (1 << 18)) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->out_dtype != c->dtype && c->out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (c->dx_dtype != c->dtype && c->dx_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (c->activation != MOE_ACT_NONE && c->activation != MOE_ACT_SWIGLU)
+    return c->activation < 0 || c->activation > MOE_ACT_SWIGLU ? MOE_ERR_INVALID_ARG
+                                                               : MOE_ERR_UNSUPPORTED;
+  const Shape s = shape_of(c);
+  const long long most = 1ll << 31;
+  const struct {
+    long long stride, least;
+  } q[] = {{c->x_stride, c->in_features},  {c->w_stride, c->in_features},
+           {c->y_stride, c->out_features}, {c->z_stride, s.w_rows},
+           {c->dx_stride, c->in_features}, {c->dw_stride, c->in_features}};
+  for (const auto& v : q)
+    if (v.stride != 0 && (v.stride < v.least || v.stride > most)) return MOE_ERR_INVALID_ARG;
+  // tiles of a product are numbered in 31 bits (the smallest tile: 32 rows, 64 features)
+  const long long rows = c->rows / 32 + c->groups;
+  const long long widest = c->in_features > c->out_features ? c->in_features : c->out_features;
+  const long long wg = (s.w_rows + 127ll) / 128 * ((c->in_features + 127ll) / 128) * c->groups;
+  if (rows * (widest / 64 + 1) >= (1ll << 30) || wg >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+inline bool odd_stride(long long stride, int dtype) {
+  return stride * static_cast<long long>(act_bytes(dtype)) % 16 != 0;
+}
+inline long long pad8(long long n) { return (n + 7) / 8 * 8; }
+inline bool unaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+inline bool vec_ok(const void* p, long long ld, int dtype) {
+  return !unaligned(p, 16) && !odd_stride(ld, dtype);
+}
+// An operand's pointer: the alignment of an element, and a 16-byte boundary when its stride says
+// that it is read in place.
+inline bool bad_operand(const void* p, long long ld, int dtype) {
+  return unaligned(p, odd_stride(ld, dtype) ? act_bytes(dtype) : 16);
+}
+inline moe_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// Workspace: the plan (bounds, tiles of rows, tensor maps), packed x and w, dz in operand form.
+struct Layout {
+  bool pack_x, pack_w, make_dz;
+  int planes, tile_rows;
+  size_t bounds, count, tiles, maps, x, w, dz, total;
+};
+
+Layout layout_of(const moe_grouped_config_t* c) {
+  const Shape s = shape_of(c);
+  Layout l;
+  l.planes = s.f32 ? 3 : 1;
+  l.tile_rows = grouped_tile_rows(c->rows, c->groups, l.planes);
+  l.pack_x = s.f32 || odd_stride(s.x, c->dtype);
+  l.pack_w = s.f32 || odd_stride(s.w, c->dtype);
+  l.make_dz = s.f32 || s.swiglu || odd_stride(s.y, c->dtype);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) & ~static_cast<size_t>(255);
+    return at;
+  };
+  const size_t rows = c->rows, groups = c->groups, planes = l.planes;
+  l.bounds = take((groups + 1) * 4);
+  l.count = take(4);
+  l.tiles = take(grouped_max_tiles(c->rows, c->groups, l.tile_rows) * 16);
+  l.maps = take(groups * 2 * 128);
+  l.x = take(l.pack_x ? planes * rows * pad8(c->in_features) * 2 : 0);
+  l.w = take(l.pack_w ? planes * groups * s.w_rows * pad8(c->in_features) * 2 : 0);
+  l.dz = take(l.make_dz ? planes * rows * pad8(s.w_rows) * 2 : 0);
+  l.total = o + 256;  // the start is moved up to a multiple of 256
+  return l;
+}
+
+struct Workspace {
+  char* base;
+  explicit Workspace(void* ws)
+      : base(reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 255) &
+                                     ~static_cast<uintptr_t>(255))) {}
+  template <typename T>
+  T* at(size_t off) const {
+    return reinterpret_cast<T*>(base + off);
+  }
+  GroupPlan plan(const Layout& l) const {
+    return GroupPlan{at<int>(l.bounds), at<int4>(l.tiles), at<int>(l.count), at<void>(l.maps)};
+  }
+};
+
+int blocks_for(long long items, int num_sms) {
+  const long long blocks = (items + 255) / 256, most = 16ll * num_sms;
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+struct Operand {
+  const void* p;
+  long long ld, plane;
+};
+
+// The matrix in place, or packed into `dst` by the task it fills in.
+Operand operand(const void* src, long long ld, long long rows, int cols, int group_rows, int dtype,
+                bool pack, void* dst, int num_sms, PackTask* t) {
+  if (!pack) return Operand{src, ld, 0};
+  t->src = src;
+  t->ld = ld;
+  t->dst = static_cast<__nv_bfloat16*>(dst);
+  t->dst_ld = pad8(cols);
+  t->plane = t->dst_ld * rows;
+  t->rows = rows;
+  t->cols = cols;
+  t->vec = vec_ok(src, ld, dtype);
+  t->group_rows = group_rows;
+  t->blocks = blocks_for(t->plane / 8, num_sms);
+  return Operand{dst, t->dst_ld, t->plane};
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg,
+                                                          size_t* bytes) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_grouped_linear_workspace_size");
+  if (st != MOE_OK) return st;
+  st = check_grouped_config(cfg);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = layout_of(cfg).total;
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
+                                           const int32_t* offsets, const void* w, void* y, void* z,
+                                           void* ws, size_t ws_bytes, moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_grouped_linear");
+  if (st != MOE_OK) return st;
+  st = check_grouped_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->rows == 0) return MOE_OK;
+  const Shape sh = shape_of(cfg);
+  if (x == nullptr || offsets == nullptr || w == nullptr || y == nullptr ||
+      (z != nullptr && !sh.swiglu))
+    return MOE_ERR_INVALID_ARG;
+  if (bad_operand(x, sh.x, cfg->dtype) || bad_operand(w, sh.w, cfg->dtype) ||
+      unaligned(offsets, 4) || unaligned(y, act_bytes(cfg->out_dtype)) ||
+      unaligned(z, act_bytes(cfg->dtype)))
+    return MOE_ERR_MISALIGNED;
+  const Layout l = layout_of(cfg);
+  if (ws == nullptr || ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+  if (unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = device_num_sms();
+  const Workspace at(ws);
+  const GroupPlan plan = at.plan(l);
+  unsigned* err = device_error_word();
+  if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan, nullptr, err, s) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  PrepareParams pp{};
+  pp.bounds = plan.bounds;
+  pp.groups = cfg->groups;
+  const Operand ox = operand(x, sh.x, cfg->rows, cfg->in_features, 0, cfg->dtype, l.pack_x,
+                             at.at<void>(l.x), sms, &pp.x);
+  const Operand ow = operand(w, sh.w, static_cast<long long>(cfg->groups) * sh.w_rows,
+                             cfg->in_features, sh.w_rows, cfg->dtype, l.pack_w, at.at<void>(l.w),
+                             sms, &pp.w);
+  if (pp.x.blocks + pp.w.blocks > 0 && launch_prepare(pp, sh.f32, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  GroupedProduct g{};
+  g.kind = GroupedKind::kForward;
+  g.groups = cfg->groups;
+  g.total_rows = cfg->rows;
+  g.planes = l.planes;
+  g.depth = cfg->in_features;
+  g.features = cfg->out_features;
+  g.swiglu = sh.swiglu;
+  g.a = ox.p;
+  g.lda = ox.ld;
+  g.a_plane = ox.plane;
+  g.b = ow.p;
+  g.ldb = ow.ld;
+  g.b_plane = ow.plane;
+  g.c = y;
+  g.c_f32 = cfg->out_dtype == MOE_F32;
+  g.ldc = sh.y;
+  g.z = z;
+  g.z_f32 = sh.f32;
+  g.ldz = sh.z;
+  return status_of(launch_grouped_product(g, plan, err, sms, s));
+}
+
+extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
+                                                    const void* x, const int32_t* offsets,
+                                                    const void* w, const void* z, void* dx,
+                                                    void* dw, void* ws, size_t ws_bytes,
+                                                    moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_grouped_linear_backward");
+  if (st != MOE_OK) return st;
+  st = check_grouped_config(cfg);
+  if (st != MOE_OK) return st;
+  const Shape sh = shape_of(cfg);
+  const size_t ab = act_bytes(cfg->dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (unaligned(dx, act_bytes(cfg->dx_dtype)) || unaligned(dw, ab)) return MOE_ERR_MISALIGNED;
+  if (cfg->rows == 0) {
+    if (dw == nullptr) return MOE_OK;
+    st = check_current_device();
+    if (st != MOE_OK) return st;
+    return status_of(cudaMemset2DAsync(dw, sh.dw * ab, 0, cfg->in_features * ab,
+                                       static_cast<size_t>(cfg->groups) * sh.w_rows, s));
+  }
+  if (dy == nullptr || offsets == nullptr || (dx == nullptr && dw == nullptr) ||
+      (dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) ||
+      (sh.swiglu && z == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (bad_operand(dy, sh.y, cfg->dtype) || (dw != nullptr && bad_operand(x, sh.x, cfg->dtype)) ||
+      (dx != nullptr && bad_operand(w, sh.w, cfg->dtype)) || unaligned(offsets, 4) ||
+      (sh.swiglu && unaligned(z, ab)))
+    return MOE_ERR_MISALIGNED;
+  const Layout l = layout_of(cfg);
+  if (ws == nullptr || ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+  if (unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  const int sms = device_num_sms();
+  const Workspace at(ws);
+  const GroupPlan plan = at.plan(l);
+  unsigned* err = device_error_word();
+
+  PrepareParams pp{};
+  pp.bounds = plan.bounds;
+  pp.groups = cfg->groups;
+  Operand ox{}, ow{}, odz{dy, sh.y, 0};
+  if (dw != nullptr)
+    ox = operand(x, sh.x, cfg->rows, cfg->in_features, 0, cfg->dtype, l.pack_x, at.at<void>(l.x),
+                 sms, &pp.x);
+  if (dx != nullptr)
+    ow = operand(w, sh.w, static_cast<long long>(cfg->groups) * sh.w_rows, cfg->in_features,
+                 sh.w_rows, cfg->dtype, l.pack_w, at.at<void>(l.w), sms, &pp.w);
+  PackTask pack_dy{};
+  if (l.make_dz && !sh.swiglu) {
+    odz = operand(dy, sh.y, cfg->rows, cfg->out_features, 0, cfg->dtype, true, at.at<void>(l.dz),
+                  sms, &pack_dy);
+  } else if (l.make_dz) {
+    DzTask& t = pp.dz;
+    t.dy = dy;
+    t.z = z;
+    t.ldy = sh.y;
+    t.ldz = sh.z;
+    t.dz = at.at<__nv_bfloat16>(l.dz);
+    t.dz_ld = pad8(sh.w_rows);
+    t.plane = t.dz_ld * cfg->rows;
+    t.cols = cfg->out_features;
+    const bool eights = cfg->out_features % 8 == 0;
+    t.vec_y = vec_ok(dy, sh.y, cfg->dtype);
+    t.vec_z = eights && vec_ok(z, sh.z, cfg->dtype);
+    t.vec_dz = eights;
+    t.blocks = blocks_for(static_cast<long long>(cfg->rows) * ((t.cols + 7) / 8), sms);
+    odz = Operand{t.dz, t.dz_ld, t.plane};
+  }
+
+  GroupedProduct q{};
+  q.groups = cfg->groups;
+  q.total_rows = cfg->rows;
+  q.planes = l.planes;
+  q.a = odz.p;
+  q.lda = odz.ld;
+  q.a_plane = odz.plane;
+  q.features = cfg->in_features;
+  GroupedProduct gx = q, gw = q;
+  gx.kind = GroupedKind::kInputGrad;
+  gx.depth = sh.w_rows;
+  gx.b = ow.p;
+  gx.ldb = ow.ld;
+  gx.b_plane = ow.plane;
+  gx.c = dx;
+  gx.c_f32 = cfg->dx_dtype == MOE_F32;
+  gx.ldc = sh.dx;
+  gw.kind = GroupedKind::kWeightGrad;
+  gw.rows = sh.w_rows;
+  gw.b = ox.p;
+  gw.ldb = ox.ld;
+  gw.b_plane = ox.plane;
+  gw.c = dw;
+  gw.c_f32 = sh.f32;
+  gw.ldc = sh.dw;
+  gw.c_group = sh.dw * sh.w_rows;
+
+  if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan,
+                        dw != nullptr ? &gw : nullptr, err, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (pack_dy.blocks > 0) {
+    PrepareParams first{};
+    first.bounds = pp.bounds;
+    first.groups = pp.groups;
+    first.x = pack_dy;
+    if (launch_prepare(first, sh.f32, s) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (pp.dz.blocks + pp.x.blocks + pp.w.blocks > 0 && launch_prepare(pp, sh.f32, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (dx != nullptr && launch_grouped_product(gx, plan, err, sms, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (dw != nullptr && launch_grouped_product(gw, plan, err, sms, s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}

@@ -1,0 +1,863 @@
+// The matrix products grouped by expert on the 5th-generation tensor cores: the forward, the
+// gradient of its input and the gradient of the weights, over groups of rows whose sizes are known
+// on the device only.
+//
+//   forward          C_r  = sum_k A[r,k] B_g[f,k]      rows r of group g; reduction over inputs
+//   input gradient   C_r  = sum_n A[r,n] B_g[n,f]      the same rows; reduction over outputs
+//   weight gradient  C_g  = sum_r A[r,n] B[r,f]        reduction over the group's rows
+//
+// One persistent kernel for all three: TMA loads either operand layout in 128-byte swizzled boxes
+// (k-contiguous, or row-contiguous for the weights of the input gradient and both operands of the
+// weight gradient) and the descriptors name the layout, so nothing is transposed in memory.
+//  - Tiles of rows start at a group's first row and run over its end; the rows past it belong to
+//    the next group (a row of the result depends on its own row of A alone) and are not stored.
+//  - The reduction of the weight gradient must end with the group: what follows may be another
+//    group's infinity or NaN, so masking one operand would not do.  Every group has its own pair
+//    of tensor maps, copies of the call's map whose number of rows is the group's end: TMA then
+//    fills the rest of the last block with zeros.  The plan kernel writes them.
+//  - A float32 result leaves the tensor core every 256 values (float32 operands, six products per
+//    value: 128), a bf16 one every 16384, and is added up in registers: the tensor core truncates
+//    its additions.
+//
+// CTA pairs (256 x 256 tiles) where groups have many rows; single CTAs with the weights on the
+// side of 128 and the rows on a side of 32 or 64 where they have few, which are bound by reading
+// the weights; single CTAs with 128 x 128 tiles for float32.
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "common.cuh"
+#include "grouped.h"
+#include "linear_act.cuh"
+#include "tc_operand.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 64;
+constexpr int kMaxChunk = 256;  // k-blocks per accumulator of a bf16 result
+constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
+
+template <int CTAS, int BN, int PL, bool SWAP>
+struct GroupedCfg {
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kBRows = BN / CTAS;
+  static constexpr int kABytes = 128 * BK * 2, kBBytes = kBRows * BK * 2;
+  static constexpr int kStageBytes = PL * (kABytes + kBBytes);
+  static constexpr int kStgBytes = SWAP ? 0 : kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
+  static constexpr int kBarBytes = 256;
+  static constexpr int kRaw = (232448 - 1024 - kBarBytes - kStgBytes) / kStageBytes;
+  static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
+  static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kTileRows = SWAP ? BN : 128 * CTAS;
+  static constexpr int kTileFeatures = SWAP ? 128 : BN;
+  static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier region");
+};
+
+struct GroupedParams {
+  CUtensorMap tm_a, tm_b;  // as the sides of the tile: with swapped sides A is the weights
+  CUtensorMap tm_c, tm_z;
+  GroupPlan plan;
+  GroupedKind kind;
+  int groups, num_kb, chunk;
+  int tiles_a;       // weight gradient: tiles along the rows of C_g
+  int tiles_b;       // tiles along the features
+  int rows;          // weight gradient: rows of C_g
+  int features, swiglu;
+  int a_mn, b_mn;
+  int a_step, b_step;  // third coordinate per plane (weights: groups, activations: 1)
+  void* c;
+  void* z;
+  long long ldc, c_group, ldz;
+  int c_f32, tma_c, tma_z, vec_c, vec_z;
+  unsigned* err;
+};
+
+struct Tile {
+  int group, row0, row_end, feat0;
+  int k0, num_kb;  // first row of the reduction (weight gradient), k-blocks
+};
+
+template <typename Cfg>
+__device__ __forceinline__ int total_tiles(const GroupedParams& p) {
+  return p.kind == GroupedKind::kWeightGrad ? p.groups * p.tiles_a * p.tiles_b
+                                            : *p.plan.count * p.tiles_b;
+}
+
+// Tiles of up to kRowChunk tiles of rows of a group share every tile of features in turn.
+template <typename Cfg>
+__device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx) {
+  Tile t;
+  const int step = p.swiglu ? Cfg::kTileFeatures / 2 : Cfg::kTileFeatures;
+  if (p.kind != GroupedKind::kWeightGrad) {
+    const int4 e = __ldg(p.plan.tiles + idx / p.tiles_b);
+    const int in = idx - e.z * p.tiles_b;
+    const int f = in / e.w;
+    t.group = e.x;
+    t.row0 = e.y + (in - f * e.w) * Cfg::kTileRows;
+    t.row_end = __ldg(p.plan.bounds + e.x + 1);
+    t.feat0 = f * step;
+    t.k0 = 0;
+    t.num_kb = p.num_kb;
+  } else {
+    const int per = p.tiles_a * p.tiles_b;
+    t.group = idx / per;
+    const int in = idx - t.group * per;
+    const int c = in / (kRowChunk * p.tiles_b);
+    const int rest = in - c * kRowChunk * p.tiles_b;
+    const int h = min(kRowChunk, p.tiles_a - c * kRowChunk);
+    const int f = rest / h;
+    t.row0 = (c * kRowChunk + rest - f * h) * Cfg::kTileRows;
+    t.row_end = p.rows;
+    t.feat0 = f * step;
+    t.k0 = __ldg(p.plan.bounds + t.group);
+    t.num_kb = (__ldg(p.plan.bounds + t.group + 1) - t.k0 + BK - 1) / BK;
+  }
+  return t;
+}
+
+// ------------------------------------------------------------------- loading ----
+
+template <int CTAS>
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, uint32_t bar, int c0,
+                                         int c1, int c2) {
+  if constexpr (CTAS == 2) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+  else tma_load_3d(dst, map, bar, c0, c1, c2);
+}
+
+// One k-block (from k on) of ROWS operand rows from row on.
+template <int CTAS, int ROWS>
+__device__ __forceinline__ void load_rows(uint32_t dst, const void* map, uint32_t bar, int mn,
+                                          int row, int k, int third) {
+  if (!mn) {
+    load_box<CTAS>(dst, map, bar, k, row, third);
+  } else {
+#pragma unroll
+    for (int c = 0; c < ROWS; c += 64) load_box<CTAS>(dst + c * 128u, map, bar, row + c, k, third);
+  }
+}
+
+__device__ __forceinline__ void acquire_map(const void* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(map))
+               : "memory");
+}
+
+// ------------------------------------------------------------------- storing ----
+
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int c0, int c1,
+                                             int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A warp's staging: 32 rows of 128 bytes, the 16-byte pieces of row r at piece ^ (r & 7), which is
+// the 128-byte swizzle of a TMA box.  A lane writes its own row.
+__device__ __forceinline__ void stage_f32(uint8_t* stg, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void stage_bf16(uint8_t* stg, int lane, int c0, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stg + lane * 128 + (((c0 + c) ^ (lane & 7)) << 4)) =
+        make_uint4(pack2(v[8 * c], v[8 * c + 1]), pack2(v[8 * c + 2], v[8 * c + 3]),
+                   pack2(v[8 * c + 4], v[8 * c + 5]), pack2(v[8 * c + 6], v[8 * c + 7]));
+}
+
+// Where a piece of 32 rows x 128 bytes of an output goes: rows of a group's matrix (C, third = the
+// group), or of one half of z, whose map has the halves before the rows (third = the half).
+struct Out {
+  const CUtensorMap* map;
+  char* base;  // of the group or half
+  long long ld;
+  int cols, third, is_z, tma, vec;
+};
+
+// The staged piece to rows row0.. (below row_end) and columns col.. of the output: by TMA where
+// all 32 rows are the group's, else by the lanes, eight to a row.  TMA clips columns past the end
+// in 16-byte steps only: a row that ends inside one is left to the lanes.
+template <typename T>
+__device__ __forceinline__ void put_piece(const Out& o, uint8_t* stg, int lane, int row0,
+                                          int row_end, int col, bool whole) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  if (whole && o.tma && (col + 8 * N <= o.cols || o.cols % N == 0)) {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(o.map, smem_u32(stg), col, o.is_z ? o.third : row0, o.is_z ? row0 : o.third);
+      bulk_commit();
+    }
+    return;
+  }
+  __syncwarp();
+  const int piece = lane & 7, c = col + piece * N;
+  const int n = min(N, o.cols - c);
+#pragma unroll 1
+  for (int r = lane >> 3; r < 32; r += 4) {
+    if (row0 + r >= row_end || n <= 0) break;
+    const uint8_t* src = stg + r * 128 + ((piece ^ (r & 7)) << 4);
+    T* dst = reinterpret_cast<T*>(o.base) + static_cast<long long>(row0 + r) * o.ld + c;
+    if (o.vec && n == N) {
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+    } else {
+      for (int q = 0; q < n; ++q) dst[q] = reinterpret_cast<const T*>(src)[q];
+    }
+  }
+}
+
+// -------------------------------------------------------------------- kernel ----
+
+template <int CTAS, int BN, int PL, bool SWAP>
+__global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
+    grouped_kernel(const __grid_constant__ GroupedParams p) {
+  using Cfg = GroupedCfg<CTAS, BN, PL, SWAP>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* stg_all = smem + S * Cfg::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stg_all + Cfg::kStgBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t mma_done_bar = bar0 + 8u * (2 * S + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), CTAS * Cfg::kEpiWarps);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    if (p.kind != GroupedKind::kWeightGrad) {
+      tma_prefetch_desc(&p.tm_a);
+      tma_prefetch_desc(&p.tm_b);
+    }
+    tma_prefetch_desc(&p.tm_c);
+  }
+  if (warp == 1) {
+    if constexpr (CTAS == 2) {
+      tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync_all();  // the peer's barriers exist before use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  if constexpr (CTAS == 1) {
+    grid_dep_wait();
+    grid_dep_trigger();
+  }
+
+  const int total = total_tiles<Cfg>(p);
+  const int first = static_cast<int>(blockIdx.x) / CTAS;
+  const int step = static_cast<int>(gridDim.x) / CTAS;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer ----
+    const bool leader = elect_one_sync();
+    int stage = 0, issued = 0;  // (issued stops counting at S)
+    uint32_t phase = 0;
+    if (leader) {
+      bool ok = true;
+      int map_group = -1;
+      const CUtensorMap* tm_a = &p.tm_a;
+      const CUtensorMap* tm_b = &p.tm_b;
+      for (int idx = first; ok && idx < total; idx += step) {
+        const Tile t = tile_at<Cfg>(p, idx);
+        int a_row, b_row, a_third, b_third;
+        if (p.kind == GroupedKind::kWeightGrad) {
+          a_row = t.row0 + static_cast<int>(rank) * 128;
+          b_row = t.feat0 + static_cast<int>(rank) * Cfg::kBRows;
+          a_third = b_third = 0;
+          if (t.group != map_group && t.num_kb > 0) {
+            map_group = t.group;
+            tm_a = static_cast<const CUtensorMap*>(p.plan.maps) + 2 * t.group;
+            tm_b = tm_a + 1;
+            acquire_map(tm_a);
+            acquire_map(tm_b);
+          }
+        } else if constexpr (SWAP) {
+          a_row = t.feat0;
+          b_row = t.row0;
+          a_third = t.group;
+          b_third = 0;
+        } else {
+          a_row = t.row0 + static_cast<int>(rank) * 128;
+          // with swiglu the odd CTA has the up half's rows
+          b_row = p.swiglu ? t.feat0 + static_cast<int>(rank) * p.features
+                           : t.feat0 + static_cast<int>(rank) * Cfg::kBRows;
+          a_third = 0;
+          b_third = t.group;
+        }
+        for (int kb = 0; kb < t.num_kb; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+          const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CTAS * Cfg::kStageBytes);
+          const int k = t.k0 + kb * BK;
+#pragma unroll
+          for (int pl = 0; pl < PL; ++pl) {
+            const uint32_t da = dst + pl * Cfg::kABytes;
+            const uint32_t db = dst + PL * Cfg::kABytes + pl * Cfg::kBBytes;
+            const int ta = a_third + pl * p.a_step, tb = b_third + pl * p.b_step;
+            if constexpr (SWAP) {
+              if (p.swiglu) {  // 16 gate rows, then the same 16 up rows, for each 32 lanes
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  load_box<CTAS>(da + q * 4096u, tm_a, fb, k, a_row + 16 * q, ta);
+                  load_box<CTAS>(da + q * 4096u + 2048u, tm_a, fb, k, p.features + a_row + 16 * q,
+                                 ta);
+                }
+              } else {
+                load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
+              }
+              load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
+            } else {
+              load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
+              if (CTAS == 1 && p.swiglu) {  // gate and up halves of the tile
+                load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
+                load_box<CTAS>(db + Cfg::kBBytes / 2, tm_b, fb, k, p.features + b_row, tb);
+              } else {
+                load_rows<CTAS, Cfg::kBRows>(db, tm_b, fb, p.b_mn, b_row, k, tb);
+              }
+            }
+          }
+          issued = min(issued + 1, S);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // (both CTAs' loads complete on the even CTA's barriers)
+    drain_stages<S>(leader, lane, stage, phase, issued, empty_bar, full_bar, rank == 0, abort_flag,
+                    p.err);
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA ----
+    if (rank == 0 && elect_one_sync()) {
+      const uint32_t idesc = idesc_bf16_f32(128 * CTAS, BN) |
+                             (static_cast<uint32_t>(p.a_mn) << 15) |
+                             (static_cast<uint32_t>(p.b_mn) << 16);
+      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+      auto commit = [&](uint32_t bar) {
+        if constexpr (CTAS == 2) tc_commit_pair(bar, 0x3);
+        else tc_commit(bar);
+      };
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;  // accumulators filled
+      bool ok = true;
+      for (int idx = first; ok && idx < total; idx += step) {
+        const int num_kb = tile_at<Cfg>(p, idx).num_kb;
+        for (int kb = 0; ok && kb < num_kb; ++local) {
+          const int acc = local & 1;
+          if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
+                         p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+          const int end = min(num_kb, kb + p.chunk);
+          uint32_t accumulate = 0;
+          for (; kb < end; ++kb) {
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
+            const uint32_t b_base = a_base + PL * Cfg::kABytes;
+            // smallest products first
+            constexpr int kTerms = PL == 3 ? 6 : 1;
+            constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+            for (int q = 0; q < kTerms; ++q) {
+              const int qa = PL == 3 ? pa[q] : 0, qb = PL == 3 ? pb[q] : 0;
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t da = operand_desc(a_base + qa * Cfg::kABytes + kk * a_step, p.a_mn);
+                const uint64_t db = operand_desc(b_base + qb * Cfg::kBBytes + kk * b_step, p.b_mn);
+                if constexpr (CTAS == 2) tc_mma_bf16_pair(d, da, db, idesc, accumulate);
+                else tc_mma_bf16(d, da, db, idesc, accumulate);
+                accumulate = 1u;
+              }
+            }
+            commit(empty_bar(stage));
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) commit(tfull_bar(acc));
+        }
+      }
+      if (!ok || *abort_flag) {
+        if constexpr (CTAS == 2) tc_commit_pair(mma_done_bar, 0x1);
+        else tc_commit(mma_done_bar);
+        volatile int no_abort = 0;
+        mbar_wait(mma_done_bar, 0, &no_abort, p.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue ----
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    constexpr int W = BN / 2;               // columns of the accumulator that a warp takes
+    constexpr int P = W >= 32 ? 32 : W;     // columns per load
+    constexpr int NP = W / P;
+    int local = 0;  // accumulators read
+    float sum[NP][P];
+    for (int idx = first; idx < total; idx += step) {
+      const Tile t = tile_at<Cfg>(p, idx);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int q = 0; q < P; ++q) sum[i][q] = 0.f;
+      bool ok = true;
+      for (int kb = 0; kb < t.num_kb; kb += p.chunk, ++local) {
+        const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
+                                     abort_flag, p.err);
+        ok = !__any_sync(0xffffffffu, !ready);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                             static_cast<uint32_t>((local & 1) * BN);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          // with swiglu (sides not swapped) the first half of a warp's columns are the gate's
+          const int col = !SWAP && p.swiglu ? (i / ((NP + 1) / 2)) * W + half * (W / 2) +
+                                                  (i % ((NP + 1) / 2)) * P
+                                            : half * W + i * P;
+          uint32_t r[P];
+          if constexpr (P == 32) tmem_ld_32x32b_x32(acc + col, r);
+          else tmem_ld_32x32b_x16(acc + col, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < P; ++q) sum[i][q] += __uint_as_float(r[q]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CTAS == 2) mbar_arrive_cluster(mapa_shared(tempty_bar(local & 1), 0));
+          else mbar_arrive(tempty_bar(local & 1));
+        }
+      }
+      if (!ok) break;
+
+      if constexpr (SWAP) {
+        // lanes are features, columns are rows of the groups
+        const int f = p.swiglu ? t.feat0 + quad * 16 + (lane & 15) : t.feat0 + quad * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+          const int row = t.row0 + half * W + q;
+          if (row >= t.row_end) break;
+          float v = sum[q / P][q % P];
+          if (p.swiglu) {
+            const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+            if (p.z != nullptr && f < p.features) {
+              const long long at = static_cast<long long>(row) * p.ldz + (lane >> 4) * p.features + f;
+              static_cast<__nv_bfloat16*>(p.z)[at] = __float2bfloat16_rn(v);
+            }
+            v = act_value<true>(MOE_ACT_SILU, v) * other;
+          }
+          if (f < p.features && (!p.swiglu || lane < 16)) {
+            const long long at = static_cast<long long>(row) * p.ldc + f;
+            if (p.c_f32) static_cast<float*>(p.c)[at] = v;
+            else static_cast<__nv_bfloat16*>(p.c)[at] = __float2bfloat16_rn(v);
+          }
+        }
+      } else {
+        uint8_t* stg = stg_all + (warp - 2) * 4096;
+        const int row0 = t.row0 + static_cast<int>(rank) * 128 + quad * 32;
+        if (row0 >= t.row_end) continue;
+        const bool weight_grad = p.kind == GroupedKind::kWeightGrad;
+        // rows past a weight's last are clipped by TMA, those past a group's end would not be
+        const bool whole = weight_grad || row0 + 32 <= t.row_end;
+        Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
+        if (weight_grad) {
+          oc.third = t.group;
+          oc.base += static_cast<long long>(t.group) * p.c_group * (p.c_f32 ? 4 : 2);
+        }
+        // N pieces of 32 columns, sum[I0..], to columns col.. of the output
+        auto emit = [&](const Out& o, bool f32, int col, auto i0, auto n) {
+          constexpr int I0 = decltype(i0)::value, N = decltype(n)::value;
+          auto reuse = [&] {  // the last piece has left the staging
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          };
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (col + 32 * i >= o.cols) break;
+            if (PL == 3 || f32) {
+              reuse();
+              stage_f32(stg, lane, sum[I0 + i]);
+              put_piece<float>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
+            } else if (i % 2 == 0) {
+              reuse();
+              stage_bf16(stg, lane, 0, sum[I0 + i]);
+              stage_bf16(stg, lane, 4, sum[I0 + (i + 1) % N]);
+              put_piece<__nv_bfloat16>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
+            }
+          }
+        };
+        using std::integral_constant;
+        constexpr integral_constant<int, 0> zero{};
+        constexpr integral_constant<int, NP / 2> mid{};
+        constexpr integral_constant<int, NP> all{};
+        if (!p.swiglu) {
+          emit(oc, p.c_f32 != 0, t.feat0 + half * W, zero, all);
+        } else {
+          const int col = t.feat0 + half * (W / 2);
+          if (p.z != nullptr) {
+            Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
+            emit(oz, false, col, zero, mid);
+            oz.third = 1;
+            oz.base += static_cast<long long>(p.features) * (PL == 3 ? 4 : 2);
+            emit(oz, false, col, mid, mid);
+          }
+#pragma unroll
+          for (int i = 0; i < NP / 2; ++i)
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+              sum[i][q] = act_value<PL == 1>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
+          emit(oc, p.c_f32 != 0, col, zero, mid);
+        }
+      }
+    }
+    if (!SWAP && lane == 0) bulk_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync_all();  // no peer still reads or arrives here
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (CTAS == 2) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+    else tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+  __syncwarp();
+  if constexpr (CTAS == 2) cluster_sync_all();  // the pair gives its TMEM back before either leaves
+}
+
+// ---------------------------------------------------------------------- plan ----
+
+struct PlanParams {
+  const int32_t* offsets;
+  GroupPlan plan;
+  int rows, groups, tile_rows;
+  unsigned* err;
+  CUtensorMap tm_a, tm_b;  // whole operands of the weight gradient
+};
+
+constexpr int kPlanThreads = 1024;
+
+// Every block reads the offsets (at most 1025) and makes them ascend within 0..rows: a running
+// maximum, so that bad ones cannot lead a kernel out of its buffers (reported through the error
+// word).  Block 0 writes the bounds and the table of the tiles of rows; all blocks share the
+// groups' tensor maps.
+__global__ void __launch_bounds__(kPlanThreads) group_plan_kernel(
+    const __grid_constant__ PlanParams p) {
+  __shared__ int s_bound[kPlanThreads + 1];
+  __shared__ int s_first[kPlanThreads + 1];
+  __shared__ int scratch[32];
+  __shared__ alignas(128) uint32_t s_map[kPlanThreads / 32][32];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  // entry t + 1 of the bounds; the first is held to 0..rows by itself
+  const int start = min(max(p.offsets[0], 0), p.rows);
+  const int given = t < p.groups ? p.offsets[t + 1] : start;
+  int bound = max(min(max(given, 0), p.rows), start);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, bound, o);
+    if (lane >= o) bound = max(bound, n);
+  }
+  if (lane == 31) scratch[warp] = bound;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) bound = max(bound, scratch[w]);
+  if (t == 0) s_bound[0] = start;
+  s_bound[t + 1] = bound;
+  if (blockIdx.x == 0 && ((t < p.groups && given != bound) || (t == 0 && p.offsets[0] != start)))
+    report_error(p.err, MOE_DEVERR_BOUNDS);
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+    const int size = t < p.groups ? s_bound[t + 1] - s_bound[t] : 0;
+    const int tiles = (size + p.tile_rows - 1) / p.tile_rows;
+    int total;
+    const int before = block_exclusive_scan(tiles, scratch, &total);
+    s_first[t] = before;
+    if (t == 0) {
+      s_first[kPlanThreads] = total;
+      *p.plan.count = total;
+      p.plan.bounds[0] = s_bound[0];
+    }
+    if (t < p.groups) p.plan.bounds[t + 1] = s_bound[t + 1];
+    __syncthreads();
+    for (int i = t; i < total; i += kPlanThreads) {
+      int lo = 0, hi = p.groups;  // the last group whose first tile is not past i
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (s_first[m] <= i) lo = m;
+        else hi = m;
+      }
+      const int end = lo + 1 < kPlanThreads ? s_first[lo + 1] : total;
+      const int chunk = s_first[lo] + (i - s_first[lo]) / kRowChunk * kRowChunk;
+      p.plan.tiles[i] = make_int4(lo, s_bound[lo] + (chunk - s_first[lo]) * p.tile_rows, chunk,
+                                  min(kRowChunk, end - chunk));
+    }
+  }
+  if (p.plan.maps == nullptr) return;
+  const int warps = gridDim.x * (kPlanThreads / 32);
+  for (int i = blockIdx.x * (kPlanThreads / 32) + warp; i < 2 * p.groups; i += warps) {
+    const CUtensorMap* from = i & 1 ? &p.tm_b : &p.tm_a;
+    s_map[warp][lane] = reinterpret_cast<const uint32_t*>(from)[lane];
+    __syncwarp();
+    const uint32_t sm = smem_u32(s_map[warp]);
+    if (lane == 0) {
+      // (a map with no rows is never used)
+      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(sm),
+                   "r"(max(s_bound[(i >> 1) + 1], 1))
+                   : "memory");
+    }
+    __syncwarp();
+    asm volatile(
+        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
+        "[%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(
+            static_cast<CUtensorMap*>(p.plan.maps) + i)),
+        "r"(sm)
+        : "memory");
+    __syncwarp();
+  }
+}
+
+// ---------------------------------------------------------------------- host ----
+
+inline int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
+
+bool encode(CUtensorMap* m, bool f32, const void* base, const cuuint64_t (&dims)[3],
+            const cuuint64_t (&strides)[2], int box0, int box1, int box2) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1),
+                             static_cast<cuuint32_t>(box2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand as [third][outer][inner] with boxes of 64 inner elements x box_rows.
+bool operand_map(CUtensorMap* m, const void* base, long long inner, long long outer,
+                 long long third, long long ld, long long third_stride, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(third)};
+  const cuuint64_t strides[2] = {
+      static_cast<cuuint64_t>(ld) * 2,
+      static_cast<cuuint64_t>(third > 1 ? third_stride : ld * outer) * 2};
+  return encode(m, false, base, dims, strides, BK, box_rows, 1);
+}
+
+// An output as dims[2] x dims[1] x dims[0] values with strides (in values) of the outer two, boxes
+// of 128 bytes x 32 rows, the rows dimension `row_dim`; false if TMA cannot take it.
+bool output_map(CUtensorMap* m, bool f32, const void* base, const long long (&dims)[3],
+                const long long (&ld)[2], int row_dim) {
+  const long long sz = f32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(base) & 15u) != 0 || ld[0] * sz % 16 != 0 || ld[1] * sz % 16 != 0)
+    return false;
+  const cuuint64_t d[3] = {static_cast<cuuint64_t>(dims[0]), static_cast<cuuint64_t>(dims[1]),
+                           static_cast<cuuint64_t>(dims[2])};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld[0] * sz),
+                                 static_cast<cuuint64_t>(ld[1] * sz)};
+  return encode(m, f32, base, d, strides, static_cast<int>(128 / sz), row_dim == 1 ? 32 : 1,
+                row_dim == 2 ? 32 : 1);
+}
+
+inline bool vec_ok(const void* p, long long ld, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * bytes % 16 == 0;
+}
+
+template <int CTAS, int BN, int PL, bool SWAP>
+cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+  using Cfg = GroupedCfg<CTAS, BN, PL, SWAP>;
+  const bool weight_grad = g.kind == GroupedKind::kWeightGrad;
+  const long long rows = g.total_rows;
+  if (!weight_grad) {
+    // sides: activations k-contiguous, weights k-contiguous or (input gradient) row-contiguous
+    const bool mn = g.kind == GroupedKind::kInputGrad;
+    const long long w_rows = mn ? g.depth : g.swiglu ? 2ll * g.features : g.features;
+    const long long w_inner = mn ? g.features : g.depth;
+    const int w_side = SWAP ? 128 : Cfg::kBRows;
+    const int w_box = mn ? BK : g.swiglu && SWAP ? 16 : g.swiglu && CTAS == 1 ? w_side / 2 : w_side;
+    const int x_box = SWAP ? BN : 128;
+    CUtensorMap* tx = SWAP ? &p->tm_b : &p->tm_a;
+    CUtensorMap* tw = SWAP ? &p->tm_a : &p->tm_b;
+    if (!operand_map(tx, g.a, g.depth, rows, g.planes, g.lda, g.a_plane, x_box) ||
+        !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.planes) * g.groups, g.ldb,
+                     g.ldb * w_rows, w_box))
+      return cudaErrorInvalidValue;
+    (SWAP ? p->a_mn : p->b_mn) = mn;
+    p->a_step = SWAP ? g.groups : 1;
+    p->b_step = SWAP ? 1 : g.groups;
+    p->num_kb = ceil_div(g.depth, BK);
+  } else {
+    p->a_mn = p->b_mn = 1;
+    p->a_step = p->b_step = 1;
+    p->tiles_a = ceil_div(g.rows, Cfg::kTileRows);
+  }
+  p->tiles_b = ceil_div(g.features, g.swiglu ? Cfg::kTileFeatures / 2 : Cfg::kTileFeatures);
+  if (!SWAP) {
+    const long long c_rows = weight_grad ? g.rows : rows;
+    p->tma_c = output_map(&p->tm_c, g.c_f32, g.c, {g.features, c_rows, weight_grad ? g.groups : 1},
+                          {g.ldc, weight_grad ? g.c_group : g.ldc * c_rows}, 1);
+    p->tma_z = g.z != nullptr && output_map(&p->tm_z, g.z_f32, g.z, {g.features, 2, rows},
+                                            {g.features, g.ldz}, 2);
+  }
+  p->vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2) &&
+             (!weight_grad || g.c_group * (g.c_f32 ? 4 : 2) % 16 == 0);
+  p->vec_z = vec_ok(g.z, g.ldz, g.z_f32 ? 4 : 2) && g.features * (g.z_f32 ? 4 : 2) % 16 == 0;
+  const long long bound =
+      weight_grad ? static_cast<long long>(g.groups) * p->tiles_a * p->tiles_b
+                  : static_cast<long long>(grouped_max_tiles(g.total_rows, g.groups, Cfg::kTileRows)) *
+                        p->tiles_b;
+  if (bound >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
+  auto kernel = grouped_kernel<CTAS, BN, PL, SWAP>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(kernel, Cfg::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const int slots = num_sms / CTAS;
+  const unsigned grid = static_cast<unsigned>(bound < slots ? bound : slots) * CTAS;
+  cudaLaunchConfig_t lc;
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = dim3(grid);
+  lc.blockDim = dim3(Cfg::kThreads);
+  lc.dynamicSmemBytes = Cfg::kSmem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (CTAS == 2) {  // in stream order, without overlap with its neighbours
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return count_launch(cudaLaunchKernelEx(&lc, kernel, *p));
+}
+
+}  // namespace
+
+int grouped_tile_rows(int total_rows, int groups, int planes) {
+  if (planes == 3) return 128;
+  const long long mean = (static_cast<long long>(total_rows) + groups - 1) / groups;
+  return mean <= 32 ? 32 : mean <= 64 ? 64 : 256;
+}
+
+size_t grouped_max_tiles(int total_rows, int groups, int tile_rows) {
+  return static_cast<size_t>(total_rows / tile_rows) +
+         static_cast<size_t>(std::min(groups, total_rows));
+}
+
+cudaError_t launch_group_plan(const int32_t* offsets, int rows, int groups, int tile_rows,
+                              const GroupPlan& plan, const GroupedProduct* wg, unsigned* err,
+                              cudaStream_t s) {
+  PlanParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.offsets = offsets;
+  p.plan = plan;
+  p.rows = rows;
+  p.groups = groups;
+  p.tile_rows = tile_rows;
+  p.err = err;
+  unsigned blocks = 1;
+  if (wg != nullptr) {
+    // both row-contiguous: [planes][rows][inner], boxes of 64 x 64
+    if (!operand_map(&p.tm_a, wg->a, wg->rows, rows, wg->planes, wg->lda, wg->a_plane, BK) ||
+        !operand_map(&p.tm_b, wg->b, wg->features, rows, wg->planes, wg->ldb, wg->b_plane, BK))
+      return cudaErrorInvalidValue;
+    blocks = static_cast<unsigned>(ceil_div(2ll * groups, kPlanThreads / 32));
+  } else {
+    p.plan.maps = nullptr;
+  }
+  return launch_pdl(group_plan_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, p);
+}
+
+cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& plan, unsigned* err,
+                                int num_sms, cudaStream_t s) {
+  GroupedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.plan = plan;
+  p.kind = g.kind;
+  p.groups = g.groups;
+  p.rows = g.rows;
+  p.features = g.features;
+  p.swiglu = g.swiglu;
+  p.c = g.c;
+  p.z = g.z;
+  p.ldc = g.ldc;
+  p.c_group = g.c_group;
+  p.ldz = g.ldz;
+  p.c_f32 = g.c_f32;
+  p.err = err;
+  p.chunk = g.planes == 3 ? 2 : g.c_f32 ? 4 : kMaxChunk;
+  if (g.planes == 3) return launch<1, 128, 3, false>(&p, g, num_sms, s);
+  if (g.kind == GroupedKind::kWeightGrad) return launch<2, 256, 1, false>(&p, g, num_sms, s);
+  switch (grouped_tile_rows(g.total_rows, g.groups, g.planes)) {
+    case 32: return launch<1, 32, 1, true>(&p, g, num_sms, s);
+    case 64: return launch<1, 64, 1, true>(&p, g, num_sms, s);
+    default: return launch<2, 256, 1, false>(&p, g, num_sms, s);
+  }
+}
+
+}  // namespace moe

@@ -35,11 +35,10 @@
 #include <mutex>
 #include <type_traits>
 
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "linear.h"
 #include "linear_act.cuh"
+#include "tc_operand.cuh"
 
 namespace moe {
 namespace {
@@ -341,15 +340,6 @@ __device__ __forceinline__ void finish8_inside(const Epilogue& e, int row, int s
 
 // --------------------------------------------------------- operands in smem ----
 
-// Descriptor of a 128-byte-swizzled operand tile (see the layouts above): k-contiguous tiles
-// have 1024 bytes between 8-row atoms (the other offset is not used), row-contiguous ones
-// 1024 bytes between atoms of 8 k and 8192 between chunks of 64 rows.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
-  uint64_t d = smem_desc_sw128(saddr);
-  if (mn) d = (d & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(8192u >> 4) << 16);
-  return d;
-}
-
 // One k-block of `rows` (a multiple of 64 when row-contiguous) operand rows from r0 on.
 __device__ __forceinline__ void load_operand(uint32_t dst, const void* map, uint32_t bar, int mn,
                                              int r0, int rows, int kb, int plane) {
@@ -368,34 +358,6 @@ __device__ __forceinline__ void load_operand_pair(uint32_t dst, const void* map,
     tma_load_3d_pair(dst, map, bar, r0, kb * BK, 0);
     tma_load_3d_pair(dst + 8192u, map, bar, r0 + 64, kb * BK, 0);
   }
-}
-
-// The producer warp's last act: no load or commit may still be in flight when the CTA gives up
-// its shared memory.  The commits of the last min(issued, S) stages arrive after their loads and
-// MMAs; each lane waits for one of them (one after the other they cost 0.1 us each).  If the
-// pipeline gave up, the loads alone are waited for, where they complete on this CTA's barriers.
-// stage, phase, issued: the issuing lane's (`leader`) state after its last load.
-template <int S, typename Empty, typename Full>
-__device__ __forceinline__ void drain_stages(bool leader, int lane, int stage, uint32_t phase,
-                                             int issued, Empty empty_bar, Full full_bar,
-                                             bool own_loads, volatile int* abort_flag,
-                                             unsigned* err) {
-  const int src = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
-  stage = __shfl_sync(0xffffffffu, stage, src);
-  phase = __shfl_sync(0xffffffffu, phase, src);
-  const int n = min(__shfl_sync(0xffffffffu, issued, src), S);
-  static_assert(S <= 32, "one lane per stage");
-  if (lane < n) {
-    int s = stage - n + lane;
-    if (s < 0) {
-      s += S;
-      phase ^= 1u;
-    }
-    volatile int no_abort = 0;
-    if (!mbar_wait(empty_bar(s), phase, abort_flag, err) && own_loads)
-      mbar_wait(full_bar(s), phase, &no_abort, err);
-  }
-  __syncwarp();
 }
 
 // ---------------------------------------------------------- one tile per CTA ----
@@ -1012,20 +974,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 
 // ---------------------------------------------------------------------- host ----
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 // The operand's planes as [planes][outer][inner] with boxes of 64 inner elements x box_rows.
 // What lies past an edge reads as zero.
 bool operand_map(CUtensorMap* m, const void* base, int rows, int depth, int mn, long long ld,
@@ -1043,19 +991,6 @@ bool operand_map(CUtensorMap* m, const void* base, int rows, int depth, int mn, 
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Raises a kernel's dynamic shared memory limit, once per device (`done` belongs to the kernel).
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
-  return e;
 }
 
 // A cluster launch of `split` CTAs per tile.
