@@ -519,6 +519,95 @@ moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const 
                                          const void* z, void* dx, void* dw, void* ws,
                                          size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * What stands between two blocks: the norm after a block's output, its gate and scales, the
+ * residual sum and the norm before the next block, in one pass; with its gradients. */
+
+/* moe_block_norm_config_t.gate: none, a factor per row, or the logistic function of one. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_VALUE = 1, MOE_GATE_LOGISTIC = 2 } moe_gate_t;
+
+typedef struct {
+  int32_t rows;          /* tokens, 0..2^30 */
+  int32_t width;         /* 1..65536 */
+  int32_t dtype;         /* moe_dtype_t of x, residual, sum, y and their gradients ("act") */
+  int32_t gate;          /* moe_gate_t */
+  float eps;             /* added to the mean squares, finite and > 0 */
+  float residual_scale;  /* finite */
+  float branch_scale;    /* finite */
+  /* elements between rows, 0 = contiguous; dsum has sum's, dy has y's */
+  int64_t x_stride, residual_stride, sum_stride, y_stride, dx_stride, dresidual_stride;
+} moe_block_norm_config_t;
+
+/* Bytes of device workspace that moe_block_norm_backward takes for `cfg`, never 0. */
+moe_status_t moe_block_norm_workspace_size(const moe_block_norm_config_t* cfg, size_t* bytes);
+
+/* For every row t, with R(v) = 1 / sqrt(mean of v^2 + eps):
+ *   p   = x[t] R(x[t]) post_weight        (post_weight NULL: p = x[t]);
+ *   s   = residual_scale * residual[t] + branch_scale * gate[t] * channel_scale * p;
+ *   sum[t] = s;   y[t] = s R(s) norm_weight,
+ * in fp32, y from the unrounded s, each output rounded once.
+ *   x [rows,width] act; residual [rows,width] act or NULL (0); post_weight, channel_scale,
+ *   norm_weight [width] float or NULL; gate [rows] float, NULL with MOE_GATE_NONE; sum [rows,width]
+ *   act out or NULL; y [rows,width] act out or NULL (with norm_weight).
+ * sum may be residual or x itself (same stride).  Pointers need the alignment of their elements.
+ * One launch, no workspace. */
+moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
+                            const void* residual, const float* post_weight, const float* gate,
+                            const float* channel_scale, const float* norm_weight, void* sum,
+                            void* y, moe_stream_t stream);
+
+/* The gradients of moe_block_norm at the stored sum, from dy (of y) and dsum (of sum, what
+ * reaches it by other ways); either may be NULL, not both:
+ *   ds        = dsum + R(s) (dy norm_weight - s R(s)^2 mean(dy norm_weight s));
+ *   dresidual = residual_scale * ds;   dnorm_weight = sum over rows of dy s R(s);
+ *   dp        = ds branch_scale gate channel_scale, and through the norm of x to dx likewise;
+ *   dgate     = its sum over the row (times g (1 - g) with MOE_GATE_LOGISTIC);
+ *   dpost_weight, dchannel_scale: sums over the rows.
+ *   x, sum, post_weight, gate, channel_scale, norm_weight as in the forward (x may be NULL where
+ *   nothing needs it, sum and norm_weight when dy is); dx, dresidual [rows,width] act out; dgate
+ *   [rows], dpost_weight, dchannel_scale, dnorm_weight [width] float out; each output may be NULL.
+ *   ws: moe_block_norm_workspace_size() bytes, 16-byte aligned; NULL will do when no vector's
+ *   gradient is asked for.
+ * dresidual may be dsum itself (same stride).  With rows == 0 the vectors' gradients are zeroed.
+ * The same inputs give the same bits. */
+moe_status_t moe_block_norm_backward(const moe_block_norm_config_t* cfg, const void* dy,
+                                     const void* dsum, const void* x, const void* sum,
+                                     const float* post_weight, const float* gate,
+                                     const float* channel_scale, const float* norm_weight,
+                                     void* dx, void* dresidual, float* dgate, float* dpost_weight,
+                                     float* dchannel_scale, float* dnorm_weight, void* ws,
+                                     size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The global norm of a step's gradients, and clipping. */
+
+typedef struct {
+  const void* grad;   /* [size] dtype, contiguous */
+  void* out;          /* [size] out_dtype: grad itself (same type), another array, or NULL */
+  int64_t size;       /* 0..2^40 */
+  int32_t dtype;      /* moe_dtype_t */
+  int32_t out_dtype;  /* moe_dtype_t */
+} moe_grad_t;
+
+/* Bytes of device workspace that moe_clip_grad_norm takes for a list of n tensors, never 0. */
+moe_status_t moe_clip_grad_norm_workspace_size(int n, size_t* bytes);
+
+/* norm = grad_scale * the 2-norm over all elements of all n tensors;
+ * out  = grad * grad_scale * min(1, max_norm / (norm + eps)) where out is not NULL.
+ * Squares are summed in 64 bits, those outside float's range included; the factor is rounded to
+ * float once, each output once.  A norm that is NaN makes every output NaN; an infinite one makes
+ * the factor 0.  max_norm may be infinite (the scale alone).  In place, where the factor is 1,
+ * nothing is written.
+ *   grads: n entries in HOST memory, read during the call only (0 <= n <= 2^20); norm [1] float
+ *   out (device) or NULL; ws: moe_clip_grad_norm_workspace_size() bytes, 16-byte aligned.
+ * grad_scale > 0 and finite (1 over a loss scale), max_norm > 0, eps >= 0.  Pointers need the
+ * alignment of their elements; arrays on 16-byte boundaries are read and written 16 bytes at a
+ * time.  No two entries may share results, nor results of one lie in gradients of another.  Two
+ * launches for up to 512 tensors.  The same inputs give the same bits. */
+moe_status_t moe_clip_grad_norm(const moe_grad_t* grads, int n, float grad_scale, float max_norm,
+                                float eps, float* norm, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
 /* Intermediates of the last moe_layer_forward that used `ws` (views into ws; valid
  * until ws is reused).  Any output pointer may be NULL.  Useful to check every stage.
  * x_perm is not written by decode-sized bf16 layers (T <= 16, E <= 256, K <= 16), whose

@@ -22,7 +22,9 @@ __all__ = [
     "combine_backward", "LinearConfig", "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH",
     "ACT_SILU", "linear_workspace_size", "linear", "linear_backward",
     "GroupedConfig", "ACT_SWIGLU", "grouped_linear_workspace_size", "grouped_linear",
-    "grouped_linear_backward",
+    "grouped_linear_backward", "BlockNormConfig", "GATE_NONE", "GATE_VALUE", "GATE_LOGISTIC",
+    "block_norm_workspace_size", "block_norm", "block_norm_backward",
+    "GradList", "clip_grad_norm_workspace_size", "clip_grad_norm",
     "sync_check", "debug_wait_timeout", "status_string", "version",
 ]
 
@@ -43,6 +45,10 @@ ACT_GELU = 2
 ACT_GELU_TANH = 3
 ACT_SILU = 4
 ACT_SWIGLU = 5  # grouped_linear only
+# moe_block_norm_config_t.gate
+GATE_NONE = 0
+GATE_VALUE = 1
+GATE_LOGISTIC = 2
 
 _STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
@@ -156,6 +162,73 @@ class GroupedConfig(ctypes.Structure):
                 f"activation={self.activation})")
 
 
+class BlockNormConfig(ctypes.Structure):
+    """moe_block_norm_config_t: rows, width, dtype, gate, eps, residual_scale, branch_scale and the
+    row strides in elements (0 = contiguous)."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+        ("branch_scale", ctypes.c_float), ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("dresidual_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, rows, width, dtype=BF16, eps=1e-6, residual_scale=1.0, branch_scale=1.0,
+             gate=GATE_NONE, x_stride=0, residual_stride=0, sum_stride=0, y_stride=0, dx_stride=0,
+             dresidual_stride=0):
+        return cls(rows, width, dtype, gate, eps, residual_scale, branch_scale, x_stride,
+                   residual_stride, sum_stride, y_stride, dx_stride, dresidual_stride)
+
+    def __repr__(self):
+        return (f"BlockNormConfig(rows={self.rows}, width={self.width}, dtype={self.dtype}, "
+                f"gate={self.gate}, eps={self.eps}, residual_scale={self.residual_scale}, "
+                f"branch_scale={self.branch_scale})")
+
+
+class _Grad(ctypes.Structure):
+    """moe_grad_t."""
+
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("size", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class GradList:
+    """The tensors of clip_grad_norm, contiguous bf16 or float32; outs: as many tensors of the same
+    sizes (the gradients themselves to clip in place), or None for the norm alone.  Holds the
+    tensors, whose storage it names."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            raise ValueError("as many results as gradients")
+        self.array = (_Grad * max(1, len(self.grads)))()
+        for i, g in enumerate(self.grads):
+            o = None if self.outs is None else self.outs[i]
+            for t in (g, o):
+                if t is not None and not t.is_contiguous():
+                    raise ValueError("gradients and results must be contiguous")
+            if o is not None and o.numel() != g.numel():
+                raise ValueError("a result of another size than its gradient")
+            self.array[i] = _Grad(g.data_ptr(), None if o is None else o.data_ptr(), g.numel(),
+                                  _dtype_of(g), _dtype_of(g if o is None else o))
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def _dtype_of(t) -> int:
+    name = str(t.dtype)
+    if name == "torch.bfloat16":
+        return BF16
+    if name == "torch.float32":
+        return F32
+    raise ValueError(f"bfloat16 or float32, not {name}")
+
+
 def library_path(debug: bool = False) -> str:
     """The release library, or with ``debug`` the bounds-checking build (-DMOE_DEBUG)."""
     return os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -169,6 +242,7 @@ _CFG = ctypes.POINTER(MoEConfig)
 _RCFG = ctypes.POINTER(RouteConfig)
 _LCFG = ctypes.POINTER(LinearConfig)
 _GCFG = ctypes.POINTER(GroupedConfig)
+_NCFG = ctypes.POINTER(BlockNormConfig)
 _SIGS = {
     "moe_workspace_size": [_CFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_route": [_CFG, _P, _P, _P, _P, _P, _P, _P],
@@ -195,6 +269,12 @@ _SIGS = {
     "moe_grouped_linear_workspace_size": [_GCFG, ctypes.POINTER(ctypes.c_size_t)],
     "moe_grouped_linear": [_GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_grouped_linear_backward": [_GCFG, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_block_norm_workspace_size": [_NCFG, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_block_norm": [_NCFG] + [_P] * 9,
+    "moe_block_norm_backward": [_NCFG] + [_P] * 15 + [ctypes.c_size_t, _P],
+    "moe_clip_grad_norm_workspace_size": [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_clip_grad_norm": [_P, ctypes.c_int, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P,
+                           _P, ctypes.c_size_t, _P],
     "moe_sync_check": [_P],
     "moe_debug_wait_timeout": [ctypes.c_uint, _P, _P],
     "moe_status_string": [ctypes.c_int],
@@ -457,6 +537,51 @@ def grouped_linear_backward(cfg, dy, x, offsets, w, z, dx, dw, ws=None, ws_bytes
     _check(load().moe_grouped_linear_backward(
         ctypes.byref(cfg), _ptr(dy), _ptr(x), _ptr(offsets), _ptr(w), _ptr(z), _ptr(dx),
         _ptr(dw), _ptr(ws), _ws(ws, ws_bytes), _stream(stream)), "moe_grouped_linear_backward")
+
+
+def block_norm_workspace_size(cfg: BlockNormConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_block_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_block_norm_workspace_size")
+    return n.value
+
+
+def block_norm(cfg, x, residual, post_weight, gate, channel_scale, norm_weight, sum, y,
+               stream=None):
+    """sum = residual_scale * residual + branch_scale * gate * channel_scale * postnorm(x) and
+    y = norm(sum) * norm_weight (either may be None)."""
+    _check(load().moe_block_norm(ctypes.byref(cfg), _ptr(x), _ptr(residual), _ptr(post_weight),
+                                 _ptr(gate), _ptr(channel_scale), _ptr(norm_weight), _ptr(sum),
+                                 _ptr(y), _stream(stream)), "moe_block_norm")
+
+
+def block_norm_backward(cfg, dy, dsum, x, sum, post_weight, gate, channel_scale, norm_weight, dx,
+                        dresidual, dgate, dpost_weight, dchannel_scale, dnorm_weight, ws=None,
+                        ws_bytes=None, stream=None):
+    """The gradients of block_norm (each output may be None) from dy and dsum (one may be None)."""
+    _check(load().moe_block_norm_backward(
+        ctypes.byref(cfg), _ptr(dy), _ptr(dsum), _ptr(x), _ptr(sum), _ptr(post_weight), _ptr(gate),
+        _ptr(channel_scale), _ptr(norm_weight), _ptr(dx), _ptr(dresidual), _ptr(dgate),
+        _ptr(dpost_weight), _ptr(dchannel_scale), _ptr(dnorm_weight), _ptr(ws),
+        _ws(ws, ws_bytes), _stream(stream)), "moe_block_norm_backward")
+
+
+def clip_grad_norm_workspace_size(grads) -> int:
+    """For a GradList, or a number of tensors."""
+    n = ctypes.c_size_t(0)
+    count = grads if isinstance(grads, int) else len(grads)
+    _check(load().moe_clip_grad_norm_workspace_size(count, ctypes.byref(n)),
+           "moe_clip_grad_norm_workspace_size")
+    return n.value
+
+
+def clip_grad_norm(grads: GradList, max_norm, norm, ws, grad_scale=1.0, eps=1e-6, ws_bytes=None,
+                   stream=None):
+    """norm[0] = grad_scale * 2-norm of all gradients; results = gradients * grad_scale *
+    min(1, max_norm / (norm + eps))."""
+    _check(load().moe_clip_grad_norm(ctypes.addressof(grads.array), len(grads), grad_scale,
+                                     max_norm, eps, _ptr(norm), _ptr(ws), _ws(ws, ws_bytes),
+                                     _stream(stream)), "moe_clip_grad_norm")
 
 
 def workspace_views(cfg, ws) -> dict:

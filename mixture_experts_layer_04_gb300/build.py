@@ -32,7 +32,8 @@ LIB_PATH_DEBUG = os.path.join(BUILD_DEBUG, LIB_NAME)
 SOURCES = ["api.cu", "route.cu", "permute.cu", "combine.cu", "gemm_tc.cu",
            "permute_noalloc.cu", "route_cluster.cu", "capacity.cu", "quant.cu",
            "gemm_tf32.cu", "route_scored.cu", "combine_grad.cu",
-           "linear.cu", "linear_gemm.cu", "grouped.cu", "grouped_gemm.cu"]
+           "linear.cu", "linear_gemm.cu", "grouped.cu", "grouped_gemm.cu",
+           "block_norm.cu", "grad_norm.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [
     GENCODE, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1,0 +1,726 @@
+// moe_block_norm and moe_block_norm_backward: what stands between two blocks of a transformer --
+// the norm after a block's output, its gate and scales, the residual sum, and the norm before the
+// next block -- in one pass over the rows.
+//
+// With p = x rx wp (rx the reciprocal root mean square of x) or x, g the row's gate, c the column's
+// product of branch scale, channel scale and wp:
+//   s = a res + g rx x c;   y = s rs wn.
+// Backward, ds the gradient of s:
+//   ds  = dsum + rs (dy wn - s rs^2 D1 / W),          D1 = sum of dy wn s;
+//   dx  = g rx (ds c - x rx^2 D2 / W),                D2 = sum of ds c x  (no second term without
+//   dgate = rx D2 (times the logistic's slope),            the norm after the block)
+// and all three vectors' gradients come from two column sums, of dy s rs and of g rx ds x.
+//
+// Bound by memory: a row is read once into registers, reduced twice across its threads (the second
+// sum needs the first: adding up squares and cross terms in one pass would cancel where block and
+// residual do), and written once.  A group of threads takes a row, eight columns each (rows of over
+// 8192 columns are read again in each pass); the columns' vectors stay in its registers
+// from row to row.  The column sums stay in registers too and leave as one partial per block,
+// which a second launch adds up in order.
+#include <initializer_list>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "topk.cuh"
+
+namespace moe {
+namespace {
+
+// Eight values of a row as they lie in memory.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+  __device__ __forceinline__ void set(int q, __nv_bfloat16 v) {
+    const uint32_t b = __bfloat16_as_ushort(v);
+    w[q >> 1] |= q & 1 ? b << 16 : b;
+  }
+  __device__ __forceinline__ float get(int q) const {
+    return __uint_as_float(q & 1 ? w[q >> 1] & 0xffff0000u : w[q >> 1] << 16);
+  }
+};
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = 0.f;
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(int q, float x) { v[q] = x; }
+  __device__ __forceinline__ float get(int q) const { return v[q]; }
+};
+
+__device__ __forceinline__ void store_eight(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_eight(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+
+struct NormParams {
+  const void *x, *residual, *sum_in, *dy, *dsum;
+  const float *post, *gate, *scale, *norm;
+  void *sum, *y, *dx, *dresidual;
+  float* dgate;
+  float* parts;  // column sums: [blocks][2][width]
+  long long ldx, ldr, lds, ldy, lddx, lddr;
+  int rows, width, gate_kind;
+  int threads;  // per row
+  float eps, residual_scale, branch_scale;
+};
+
+// The threads of one row: eight columns each, `i` times.  Vec: neighbouring columns, 16-byte
+// accesses; else every `threads`-th column.
+template <bool Vec>
+struct Columns {
+  int t, threads, width;
+  __device__ __forceinline__ int at(int i, int q) const {
+    return Vec ? (i * threads + t) * 8 + q : (i * 8 + q) * threads + t;
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, int i, Eight<T>& e) const {
+    if constexpr (Vec) {
+      if (at(i, 0) < width) e.load(row + at(i, 0));
+      else e.zero();
+    } else {
+      e.zero();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (at(i, q) < width) e.set(q, row[at(i, q)]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int i, const float (&v)[8]) const {
+    if constexpr (Vec) {
+      if (at(i, 0) < width) store_eight(row + at(i, 0), v);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (at(i, q) < width) store_one(row + at(i, q), v[q]);
+    }
+  }
+  // a vector's values, `none` where there is no vector
+  __device__ __forceinline__ void vector(const float* p, int i, float none, float (&v)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = p == nullptr ? none : at(i, q) < width ? __ldg(p + at(i, q)) : 0.f;
+  }
+};
+
+// Sums of N values over the threads of a row; every thread gets them.  `part` is this group's
+// shared memory (N floats per warp), `turn` alternates between two such areas.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* part, int group, int threads) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if (threads == 32) return;
+  const int warps = threads >> 5, warp = (threadIdx.x % threads) >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[warp * N + k] = v[k];
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? part[lane * N + k] : 0.f);
+}
+
+__device__ __forceinline__ float gate_of(const NormParams& p, int row, float* slope) {
+  *slope = 1.f;
+  if (p.gate_kind == MOE_GATE_NONE) return 1.f;
+  const float v = p.gate[row];
+  if (p.gate_kind == MOE_GATE_VALUE) return v;
+  const float t = expf(-fabsf(v)), r = 1.f / (1.f + t);
+  *slope = t * r * r;  // of the logistic function, without the cancellation in 1 - g
+  return v >= 0.f ? r : t * r;
+}
+
+__device__ __forceinline__ float root(float squares, float width, float eps) {
+  return 1.f / sqrtf(squares / width + eps);
+}
+
+constexpr int kMaxThreads = 1024;
+// Partial sums of the warps: at most kMaxThreads / 32 of them, 3 values, two areas.
+constexpr int kPartFloats = kMaxThreads / 32 * 3;
+
+// V: columns a thread keeps, in eights; 0: rows are read again in each pass.  NT: threads at most.
+template <typename T, int V, bool Vec, int NT>
+__global__ void __launch_bounds__(NT)
+    block_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float part[2][kPartFloats];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
+  const Columns<Vec> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const int n = V > 0 ? V : (p.width + 8 * p.threads - 1) / (8 * p.threads);
+  const float width = static_cast<float>(p.width);
+  float* mine[2] = {part[0] + group * (p.threads >> 5) * 3, part[1] + group * (p.threads >> 5) * 3};
+  constexpr int R = V > 0 ? V : 1;
+  float c[R][8], wn[R][8];
+  auto vectors = [&](int i, float (&cv)[8], float (&nv)[8]) {
+    float post[8], scale[8];
+    col.vector(p.post, i, 1.f, post);
+    col.vector(p.scale, i, 1.f, scale);
+    col.vector(p.norm, i, 1.f, nv);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) cv[q] = p.branch_scale * scale[q] * post[q];
+  };
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) vectors(i, c[i], wn[i]);
+  }
+  Eight<T> x[R], res[R];
+  auto load_row = [&](int row, int i, Eight<T>& ex, Eight<T>& er) {
+    col.load(static_cast<const T*>(p.x) + row * p.ldx, i, ex);
+    if (p.residual != nullptr) col.load(static_cast<const T*>(p.residual) + row * p.ldr, i, er);
+    else er.zero();
+  };
+  const int step = gridDim.x * groups;
+  int row = blockIdx.x * groups + group;
+  if constexpr (V > 0) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) load_row(row, i, x[i], res[i]);
+    }
+  }
+  for (; row < p.rows; row += step) {
+    float slope;
+    float f = gate_of(p, row, &slope);
+    if (p.post != nullptr) {
+      float sq[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        if constexpr (V == 0) col.load(static_cast<const T*>(p.x) + row * p.ldx, i, x[0]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float v = x[V > 0 ? i : 0].get(q);
+          sq[0] = fmaf(v, v, sq[0]);
+        }
+      }
+      row_sum<1>(sq, mine[0], group, p.threads);
+      f *= root(sq[0], width, p.eps);
+    }
+    float s[R][8];
+    auto make = [&](int i, const Eight<T>& ex, const Eight<T>& er, const float (&cv)[8],
+                    float (&sv)[8]) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        sv[q] = fmaf(f * ex.get(q), cv[q], p.residual_scale * er.get(q));
+    };
+    float sq[1] = {0.f};
+    if constexpr (V > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        make(i, x[i], res[i], c[i], s[i]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sq[0] = fmaf(s[i][q], s[i][q], sq[0]);
+        // the next row is on its way while this one is reduced
+        if (row + step < p.rows) load_row(row + step, i, x[i], res[i]);
+        if (p.sum != nullptr) col.store(static_cast<T*>(p.sum) + row * p.lds, i, s[i]);
+      }
+    } else if (p.y != nullptr) {
+      for (int i = 0; i < n; ++i) {
+        vectors(i, c[0], wn[0]);
+        load_row(row, i, x[0], res[0]);
+        make(i, x[0], res[0], c[0], s[0]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sq[0] = fmaf(s[0][q], s[0][q], sq[0]);
+      }
+    }
+    float rs = 0.f;
+    if (p.y != nullptr) {
+      row_sum<1>(sq, mine[1], group, p.threads);
+      rs = root(sq[0], width, p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if constexpr (V == 0) {
+        vectors(i, c[0], wn[0]);
+        load_row(row, i, x[0], res[0]);
+        make(i, x[0], res[0], c[0], s[0]);
+        if (p.sum != nullptr) col.store(static_cast<T*>(p.sum) + row * p.lds, i, s[0]);
+      }
+      if (p.y != nullptr) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = s[V > 0 ? i : 0][q] * rs * wn[V > 0 ? i : 0][q];
+        col.store(static_cast<T*>(p.y) + row * p.ldy, i, v);
+      }
+    }
+    if (p.y == nullptr || p.post == nullptr) {
+      // one reduction a row: its area must not be written again before every warp has read it
+      if (p.threads > 32 && (p.y != nullptr || p.post != nullptr))
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.threads) : "memory");
+    }
+  }
+}
+
+// A row's sums: of x^2, s^2 and dy wn s; then of ds c x.
+template <typename T, int V, bool Vec, int NT>
+__global__ void __launch_bounds__(NT)
+    block_norm_grad_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float part[2][kPartFloats];
+  extern __shared__ float columns[];  // V > 0: [groups - 1][2][width]
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
+  const Columns<Vec> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const int n = V > 0 ? V : (p.width + 8 * p.threads - 1) / (8 * p.threads);
+  const float width = static_cast<float>(p.width);
+  float* mine[2] = {part[0] + group * (p.threads >> 5) * 3, part[1] + group * (p.threads >> 5) * 3};
+  constexpr int R = V > 0 ? V : 1;
+  float* out = p.parts == nullptr ? nullptr
+                                  : p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.width;
+  float c[R][8], wn[R][8], sum_n[R][8], sum_a[R][8];
+  auto vectors = [&](int i, float (&cv)[8], float (&nv)[8]) {
+    float post[8], scale[8];
+    col.vector(p.post, i, 1.f, post);
+    col.vector(p.scale, i, 1.f, scale);
+    col.vector(p.norm, i, 0.f, nv);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) cv[q] = p.branch_scale * scale[q] * post[q];
+  };
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      vectors(i, c[i], wn[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum_n[i][q] = sum_a[i][q] = 0.f;
+    }
+  } else if (out != nullptr) {  // the block's partial sums live in memory (one group a block)
+    for (int k = threadIdx.x; k < 2 * p.width; k += blockDim.x) out[k] = 0.f;
+    __syncthreads();
+  }
+  Eight<T> x[R], s[R], dy[R], ds[R];
+  auto load_one = [&](const void* base, long long ld, int row, int i, Eight<T>& e) {
+    if (base != nullptr) col.load(static_cast<const T*>(base) + row * ld, i, e);
+    else e.zero();
+  };
+  auto load_row = [&](int row, int i) {
+    constexpr bool keep = V > 0;
+    load_one(p.x, p.ldx, row, i, x[keep ? i : 0]);
+    load_one(p.sum_in, p.lds, row, i, s[keep ? i : 0]);
+    load_one(p.dy, p.ldy, row, i, dy[keep ? i : 0]);
+    load_one(p.dsum, p.lds, row, i, ds[keep ? i : 0]);
+    if constexpr (!keep) vectors(i, c[0], wn[0]);
+  };
+  const int step = gridDim.x * groups;
+  for (int row = blockIdx.x * groups + group; row < p.rows; row += step) {
+    float slope;
+    const float g = gate_of(p, row, &slope);
+    float sums[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      load_row(row, i);
+      const int k = V > 0 ? i : 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float vx = x[k].get(q), vs = s[k].get(q);
+        sums[0] = fmaf(vx, vx, sums[0]);
+        sums[1] = fmaf(vs, vs, sums[1]);
+        sums[2] = fmaf(dy[k].get(q) * wn[k][q], vs, sums[2]);
+      }
+    }
+    row_sum<3>(sums, mine[0], group, p.threads);
+    const float rx = p.post != nullptr ? root(sums[0], width, p.eps) : 1.f;
+    const float rs = p.dy != nullptr ? root(sums[1], width, p.eps) : 0.f;
+    const float d1 = rs * rs * (sums[2] / width);
+    auto grad = [&](int k, int q) {  // ds
+      return fmaf(rs, fmaf(-s[k].get(q), d1, dy[k].get(q) * wn[k][q]), ds[k].get(q));
+    };
+    float dot[1] = {0.f};
+    const bool need_dot = p.post != nullptr || p.dgate != nullptr;
+    if (need_dot) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        if constexpr (V == 0) load_row(row, i);
+        const int k = V > 0 ? i : 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dot[0] = fmaf(grad(k, q) * c[k][q], x[k].get(q), dot[0]);
+      }
+      row_sum<1>(dot, mine[1], group, p.threads);
+      if (p.dgate != nullptr && col.t == 0) p.dgate[row] = rx * dot[0] * slope;
+    }
+    const float d2 = p.post != nullptr ? rx * rx * (dot[0] / width) : 0.f;
+    const float f = g * rx;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if constexpr (V == 0) load_row(row, i);
+      const int k = V > 0 ? i : 0;
+      float v[8], an[8], aa[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[q] = grad(k, q);
+        an[q] = dy[k].get(q) * s[k].get(q) * rs;
+        aa[q] = f * v[q] * x[k].get(q);
+        if constexpr (V > 0) {
+          sum_n[i][q] += an[q];
+          sum_a[i][q] += aa[q];
+        } else if (out != nullptr && col.at(i, q) < p.width) {
+          out[col.at(i, q)] += an[q];
+          out[p.width + col.at(i, q)] += aa[q];
+        }
+      }
+      if (p.dresidual != nullptr) {
+        float r[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] = p.residual_scale * v[q];
+        col.store(static_cast<T*>(p.dresidual) + row * p.lddr, i, r);
+      }
+      if (p.dx != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = f * fmaf(-x[k].get(q), d2, v[q] * c[k][q]);
+        col.store(static_cast<T*>(p.dx) + row * p.lddx, i, v);
+      }
+    }
+    // one reduction a row: its area must not be written again before every warp has read it
+    if (!need_dot && p.threads > 32)
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.threads) : "memory");
+  }
+  if constexpr (V > 0) {
+    if (out == nullptr) return;
+    // the groups' sums, in order
+    if (group > 0) {
+      float* to = columns + static_cast<size_t>(group - 1) * 2 * p.width;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (col.at(i, q) < p.width) {
+            to[col.at(i, q)] = sum_n[i][q];
+            to[p.width + col.at(i, q)] = sum_a[i][q];
+          }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int at = col.at(i, q);
+        if (at >= p.width) continue;
+        float a = sum_n[i][q], b = sum_a[i][q];
+        for (int k = 0; k + 1 < groups; ++k) {
+          a += columns[static_cast<size_t>(k) * 2 * p.width + at];
+          b += columns[(static_cast<size_t>(k) * 2 + 1) * p.width + at];
+        }
+        out[at] = a;
+        out[p.width + at] = b;
+      }
+  }
+}
+
+// The blocks' column sums, added in order, and the vectors' gradients: 32 columns per block, each
+// of its 16 warps adds every sixteenth partial.
+struct VectorParams {
+  const float* parts;
+  const float *post, *scale;
+  float *dpost, *dscale, *dnorm;
+  int blocks, width;
+  float branch_scale;
+};
+constexpr int kVectorWarps = 16;
+__global__ void __launch_bounds__(32 * kVectorWarps)
+    norm_vectors_kernel(const __grid_constant__ VectorParams p) {
+  __shared__ float s[2][kVectorWarps][32];
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float n = 0.f, a = 0.f;
+  if (c < p.width) {
+#pragma unroll 4
+    for (int b = warp; b < p.blocks; b += kVectorWarps) {
+      n += p.parts[static_cast<size_t>(b) * 2 * p.width + c];
+      a += p.parts[(static_cast<size_t>(b) * 2 + 1) * p.width + c];
+    }
+  }
+  s[0][warp][lane] = n;
+  s[1][warp][lane] = a;
+  __syncthreads();
+  if (warp != 0 || c >= p.width) return;
+  n = a = 0.f;
+#pragma unroll
+  for (int w = 0; w < kVectorWarps; ++w) {
+    n += s[0][w][lane];
+    a += s[1][w][lane];
+  }
+  a *= p.branch_scale;
+  if (p.dnorm != nullptr) p.dnorm[c] = n;
+  if (p.dscale != nullptr) p.dscale[c] = a * (p.post != nullptr ? p.post[c] : 1.f);
+  if (p.dpost != nullptr) p.dpost[c] = a * (p.scale != nullptr ? p.scale[c] : 1.f);
+}
+
+// --------------------------------------------------------------------- host ----
+
+// How rows lie on threads: `threads` per row, `groups` rows per block at a time.
+struct Shape {
+  int keep, threads, groups;
+};
+Shape shape_of(int width, int block) {
+  Shape s;
+  s.keep = width <= 8 * kMaxThreads ? 1 : 0;
+  const int per = s.keep ? 8 : 64;
+  const int threads = ((width + per - 1) / per + 31) / 32 * 32;
+  s.threads = threads < kMaxThreads ? threads : kMaxThreads;
+  const int groups = block / s.threads;
+  // (a group of several warps has a named barrier of its own: 15 beside the block's)
+  s.groups = s.keep == 0 || groups < 1 ? 1 : groups < 15 ? groups : s.threads == 32 ? 16 : 15;
+  return s;
+}
+
+moe_status_t check_norm_config(const moe_block_norm_config_t* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->rows < 0 || c->rows > (1 << 30)) return MOE_ERR_INVALID_ARG;
+  if (c->width < 1 || c->width > 65536) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->gate < MOE_GATE_NONE || c->gate > MOE_GATE_LOGISTIC) return MOE_ERR_INVALID_ARG;
+  const float most = 3.402823466e38f;
+  auto finite = [&](float v) { return v >= -most && v <= most; };
+  if (!(c->eps > 0.f) || !finite(c->eps) || !finite(c->residual_scale) || !finite(c->branch_scale))
+    return MOE_ERR_INVALID_ARG;
+  for (long long s : {c->x_stride, c->residual_stride, c->sum_stride, c->y_stride, c->dx_stride,
+                      c->dresidual_stride})
+    if (s != 0 && (s < c->width || s > (1ll << 31))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Blocks of the backward: their number sets that of the partial column sums.
+constexpr int kGradBlock = 512;
+int grad_blocks(const moe_block_norm_config_t* c, int num_sms) {
+  const Shape s = shape_of(c->width, kGradBlock);
+  const long long need = (static_cast<long long>(c->rows) + s.groups - 1) / s.groups;
+  const long long most = static_cast<long long>(num_sms) * (s.threads * s.groups <= 512 ? 2 : 1);
+  return static_cast<int>(need < most ? need : most);
+}
+// For the workspace's size, which must not depend on the device: no GPU has more.
+constexpr int kMostSms = 160;
+
+inline bool unaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+inline moe_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+long long pick(long long s, int width) { return s != 0 ? s : width; }
+
+NormParams params_of(const moe_block_norm_config_t* c, int threads) {
+  NormParams p{};
+  p.ldx = pick(c->x_stride, c->width);
+  p.ldr = pick(c->residual_stride, c->width);
+  p.lds = pick(c->sum_stride, c->width);
+  p.ldy = pick(c->y_stride, c->width);
+  p.lddx = pick(c->dx_stride, c->width);
+  p.lddr = pick(c->dresidual_stride, c->width);
+  p.rows = c->rows;
+  p.width = c->width;
+  p.gate_kind = c->gate;
+  p.threads = threads;
+  p.eps = c->eps;
+  p.residual_scale = c->residual_scale;
+  p.branch_scale = c->branch_scale;
+  return p;
+}
+
+// 16-byte accesses to every array, null ones aside.
+struct Array {
+  const void* p;
+  long long ld;
+};
+bool all_vec(int width, int dtype, std::initializer_list<Array> arrays) {
+  const long long bytes = static_cast<long long>(act_bytes(dtype));
+  if (width % 8 != 0) return false;
+  for (const Array& a : arrays)
+    if (a.p != nullptr && (unaligned(a.p, 16) || a.ld * bytes % 16 != 0)) return false;
+  return true;
+}
+
+template <typename T, bool Vec>
+cudaError_t launch_forward(const NormParams& p, int keep, unsigned blocks, unsigned threads,
+                           cudaStream_t s) {
+  auto kernel = !keep            ? block_norm_kernel<T, 0, Vec, kMaxThreads>
+                : threads <= 256 ? block_norm_kernel<T, 1, Vec, 256>
+                                 : block_norm_kernel<T, 1, Vec, kMaxThreads>;
+  return launch_pdl(kernel, dim3(blocks), dim3(threads), 0, s, p);
+}
+template <typename T, bool Vec>
+cudaError_t launch_backward(const NormParams& p, int keep, unsigned blocks, unsigned threads,
+                            size_t smem, cudaStream_t s) {
+  auto kernel = !keep            ? block_norm_grad_kernel<T, 0, Vec, kMaxThreads>
+                : threads <= 512 ? block_norm_grad_kernel<T, 1, Vec, 512>
+                                 : block_norm_grad_kernel<T, 1, Vec, kMaxThreads>;
+  return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, p);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status_t moe_block_norm_workspace_size(const moe_block_norm_config_t* cfg,
+                                                      size_t* bytes) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_block_norm_workspace_size");
+  if (st != MOE_OK) return st;
+  st = check_norm_config(cfg);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  const size_t blocks = static_cast<size_t>(grad_blocks(cfg, kMostSms));
+  *bytes = blocks * 2 * cfg->width * 4 + 16;
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
+                                       const void* residual, const float* post_weight,
+                                       const float* gate, const float* channel_scale,
+                                       const float* norm_weight, void* sum, void* y,
+                                       moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_block_norm");
+  if (st != MOE_OK) return st;
+  st = check_norm_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->rows == 0) return MOE_OK;
+  if (x == nullptr || (sum == nullptr && y == nullptr) ||
+      (gate == nullptr) != (cfg->gate == MOE_GATE_NONE) ||
+      (norm_weight == nullptr) != (y == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ab = act_bytes(cfg->dtype);
+  for (const void* q : {x, residual, static_cast<const void*>(sum), static_cast<const void*>(y)})
+    if (unaligned(q, ab)) return MOE_ERR_MISALIGNED;
+  for (const float* q : {post_weight, gate, channel_scale, norm_weight})
+    if (unaligned(q, 4)) return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  const int sms = device_num_sms();
+  const Shape sh = shape_of(cfg->width, 256);
+  NormParams p = params_of(cfg, sh.threads);
+  p.x = x;
+  p.residual = residual;
+  p.post = post_weight;
+  p.gate = gate;
+  p.scale = channel_scale;
+  p.norm = norm_weight;
+  p.sum = sum;
+  p.y = y;
+  const bool vec = all_vec(cfg->width, cfg->dtype,
+                           {{x, p.ldx}, {residual, p.ldr}, {sum, p.lds}, {y, p.ldy}});
+  const int block = sh.threads * sh.groups;
+  const long long need = (static_cast<long long>(cfg->rows) + sh.groups - 1) / sh.groups;
+  const long long most = static_cast<long long>(sms) * (kMaxThreads / block);
+  const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
+  const unsigned threads = static_cast<unsigned>(block);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cfg->dtype == MOE_BF16)
+    return status_of(vec ? launch_forward<__nv_bfloat16, true>(p, sh.keep, blocks, threads, s)
+                         : launch_forward<__nv_bfloat16, false>(p, sh.keep, blocks, threads, s));
+  return status_of(vec ? launch_forward<float, true>(p, sh.keep, blocks, threads, s)
+                       : launch_forward<float, false>(p, sh.keep, blocks, threads, s));
+}
+
+extern "C" moe_status_t moe_block_norm_backward(
+    const moe_block_norm_config_t* cfg, const void* dy, const void* dsum, const void* x,
+    const void* sum, const float* post_weight, const float* gate, const float* channel_scale,
+    const float* norm_weight, void* dx, void* dresidual, float* dgate, float* dpost_weight,
+    float* dchannel_scale, float* dnorm_weight, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  using namespace moe;
+  moe_status_t st = fault_point("moe_block_norm_backward");
+  if (st != MOE_OK) return st;
+  st = check_norm_config(cfg);
+  if (st != MOE_OK) return st;
+  const size_t ab = act_bytes(cfg->dtype);
+  for (const void* q : {dy, dsum, x, sum, static_cast<const void*>(dx),
+                        static_cast<const void*>(dresidual)})
+    if (unaligned(q, ab)) return MOE_ERR_MISALIGNED;
+  for (const float* q : {post_weight, gate, channel_scale, norm_weight,
+                         static_cast<const float*>(dgate), static_cast<const float*>(dpost_weight),
+                         static_cast<const float*>(dchannel_scale),
+                         static_cast<const float*>(dnorm_weight)})
+    if (unaligned(q, 4)) return MOE_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cfg->rows == 0) {
+    if (dpost_weight == nullptr && dchannel_scale == nullptr && dnorm_weight == nullptr)
+      return MOE_OK;
+    st = check_current_device();
+    if (st != MOE_OK) return st;
+    for (float* q : {dpost_weight, dchannel_scale, dnorm_weight})
+      if (q != nullptr &&
+          cudaMemsetAsync(q, 0, static_cast<size_t>(cfg->width) * 4, s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const bool vectors = dpost_weight != nullptr || dchannel_scale != nullptr || dnorm_weight != nullptr;
+  const bool own = dpost_weight != nullptr || dchannel_scale != nullptr || dgate != nullptr;
+  if ((dy == nullptr && dsum == nullptr) ||
+      (!vectors && dx == nullptr && dresidual == nullptr && dgate == nullptr) ||
+      (dy != nullptr && (sum == nullptr || norm_weight == nullptr)) ||
+      (gate == nullptr) != (cfg->gate == MOE_GATE_NONE) ||
+      (dgate != nullptr && gate == nullptr) || (dpost_weight != nullptr && post_weight == nullptr) ||
+      (dnorm_weight != nullptr && dy == nullptr) ||
+      (x == nullptr && (own || (dx != nullptr && post_weight != nullptr))))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = device_num_sms();
+  const size_t need = static_cast<size_t>(grad_blocks(cfg, kMostSms)) * 2 * cfg->width * 4 + 16;
+  if (vectors && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (vectors && unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
+  st = check_current_device();
+  if (st != MOE_OK) return st;
+  const Shape sh = shape_of(cfg->width, kGradBlock);
+  NormParams p = params_of(cfg, sh.threads);
+  // (read only where something needs it)
+  p.x = own || (dx != nullptr && post_weight != nullptr) ? x : nullptr;
+  p.sum_in = dy != nullptr ? sum : nullptr;
+  p.dy = dy;
+  p.dsum = dsum;
+  p.post = p.x != nullptr ? post_weight : nullptr;
+  p.gate = gate;
+  p.scale = channel_scale;
+  p.norm = norm_weight;
+  p.dx = dx;
+  p.dresidual = dresidual;
+  p.dgate = dgate;
+  p.parts = vectors ? static_cast<float*>(ws) : nullptr;
+  const int blocks = grad_blocks(cfg, sms < kMostSms ? sms : kMostSms);
+  const unsigned threads = static_cast<unsigned>(sh.threads * sh.groups);
+  const size_t smem =
+      vectors && sh.keep > 0 ? static_cast<size_t>(sh.groups - 1) * 2 * cfg->width * 4 : 0;
+  const bool vec = all_vec(cfg->width, cfg->dtype,
+                           {{p.x, p.ldx}, {p.sum_in, p.lds}, {dy, p.ldy}, {dsum, p.lds},
+                            {dx, p.lddx}, {dresidual, p.lddr}});
+  const unsigned grid = static_cast<unsigned>(blocks);
+  const cudaError_t e =
+      cfg->dtype == MOE_BF16
+          ? (vec ? launch_backward<__nv_bfloat16, true>(p, sh.keep, grid, threads, smem, s)
+                 : launch_backward<__nv_bfloat16, false>(p, sh.keep, grid, threads, smem, s))
+          : (vec ? launch_backward<float, true>(p, sh.keep, grid, threads, smem, s)
+                 : launch_backward<float, false>(p, sh.keep, grid, threads, smem, s));
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  if (!vectors) return MOE_OK;
+  VectorParams v{};
+  v.parts = static_cast<const float*>(ws);
+  v.post = post_weight;
+  v.scale = channel_scale;
+  v.dpost = dpost_weight;
+  v.dscale = dchannel_scale;
+  v.dnorm = dnorm_weight;
+  v.blocks = blocks;
+  v.width = cfg->width;
+  v.branch_scale = cfg->branch_scale;
+  return status_of(launch_pdl(norm_vectors_kernel,
+                              dim3(static_cast<unsigned>((cfg->width + 31) / 32)),
+                              dim3(32 * kVectorWarps), 0, s, v));
+}
