@@ -510,7 +510,8 @@ moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
  *   returned it (NULL without an activation); dx [rows,in] dx_dtype out or NULL, rows that belong
  *   to no group left as they were; dw [groups, out or 2 out, in] act out or NULL, every element
  *   written; ws as above (NULL with rows == 0, which zeroes dw).
- * dz is rounded to act before the products.  x may be NULL when dw is, w when dx is.  dy keeps to
+ * dz is rounded to act before the products (for a float32 dx of a bf16 SWIGLU layer it is held in
+ * 16 bits instead, as two bf16 parts).  x may be NULL when dw is, w when dx is.  dy keeps to
  * the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds up to the
  * gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
  * gradient.  The same inputs give the same bits. */

@@ -102,6 +102,7 @@ struct DzTask {
   __nv_bfloat16* dz;
   long long dz_ld, plane;
   int cols;              // of dy; dz has twice as many
+  int parts;
   int vec_y, vec_z, vec_dz;
   int blocks;
 };
@@ -133,6 +134,13 @@ __device__ __forceinline__ void pack_task(const PackTask& t, const int* bounds, 
 }
 
 template <typename T, int PL>
+__device__ __forceinline__ void store_dz(__nv_bfloat16* dst, const DzTask& t, int n,
+                                         float (&v)[8]) {
+  if (PL == 3 || t.parts == 1) store_parts<PL>(dst, t.plane, n, t.vec_dz != 0, v);
+  else store_parts<2>(dst, t.plane, n, t.vec_dz != 0, v);
+}
+
+template <typename T, int PL>
 __device__ __forceinline__ void dz_task(const DzTask& t, int rows, int block) {
   const int per_row = (t.cols + 7) / 8;
   const long long items = static_cast<long long>(rows) * per_row;
@@ -153,8 +161,8 @@ __device__ __forceinline__ void dz_task(const DzTask& t, int rows, int block) {
       up[q] = dy[q] * value;
     }
     __nv_bfloat16* dst = t.dz + r * t.dz_ld + c;
-    store_parts<PL>(dst, t.plane, n, t.vec_dz != 0, gate);
-    store_parts<PL>(dst + t.cols, t.plane, n, t.vec_dz != 0, up);
+    store_dz<T, PL>(dst, t, n, gate);
+    store_dz<T, PL>(dst + t.cols, t, n, up);
   }
 }
 
@@ -248,15 +256,19 @@ inline moe_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK 
 // Workspace: the plan (bounds, tiles of rows, tensor maps), packed x and w, dz in operand form.
 struct Layout {
   bool pack_x, pack_w, make_dz;
-  int planes, tile_rows;
+  int parts;     // bf16 parts of an operand's value
+  int dz_parts;  // and of dz
+  int tile_rows;
   size_t bounds, count, tiles, maps, x, w, dz, total;
 };
 
 Layout layout_of(const moe_grouped_config_t* c) {
   const Shape s = shape_of(c);
   Layout l;
-  l.planes = s.f32 ? 3 : 1;
-  l.tile_rows = grouped_tile_rows(c->rows, c->groups, l.planes);
+  l.parts = s.f32 ? 3 : 1;
+  // a float32 dx of bf16 layers: dz rounded to bf16 would leave it 2^-9 off; two parts keep 16 bits
+  l.dz_parts = s.f32 ? 3 : s.swiglu && c->dx_dtype == MOE_F32 ? 2 : 1;
+  l.tile_rows = grouped_tile_rows(c->rows, c->groups, s.f32);
   l.pack_x = s.f32 || odd_stride(s.x, c->dtype);
   l.pack_w = s.f32 || odd_stride(s.w, c->dtype);
   l.make_dz = s.f32 || s.swiglu || odd_stride(s.y, c->dtype);
@@ -266,14 +278,14 @@ Layout layout_of(const moe_grouped_config_t* c) {
     o += (bytes + 255) & ~static_cast<size_t>(255);
     return at;
   };
-  const size_t rows = c->rows, groups = c->groups, planes = l.planes;
+  const size_t rows = c->rows, groups = c->groups, parts = l.parts;
   l.bounds = take((groups + 1) * 4);
   l.count = take(4);
   l.tiles = take(grouped_max_tiles(c->rows, c->groups, l.tile_rows) * 16);
   l.maps = take(groups * 2 * 128);
-  l.x = take(l.pack_x ? planes * rows * pad8(c->in_features) * 2 : 0);
-  l.w = take(l.pack_w ? planes * groups * s.w_rows * pad8(c->in_features) * 2 : 0);
-  l.dz = take(l.make_dz ? planes * rows * pad8(s.w_rows) * 2 : 0);
+  l.x = take(l.pack_x ? parts * rows * pad8(c->in_features) * 2 : 0);
+  l.w = take(l.pack_w ? parts * groups * s.w_rows * pad8(c->in_features) * 2 : 0);
+  l.dz = take(l.make_dz ? l.dz_parts * rows * pad8(s.w_rows) * 2 : 0);
   l.total = o + 256;  // the start is moved up to a multiple of 256
   return l;
 }
@@ -378,7 +390,7 @@ extern "C" moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, cons
   g.kind = GroupedKind::kForward;
   g.groups = cfg->groups;
   g.total_rows = cfg->rows;
-  g.planes = l.planes;
+  g.a_parts = g.b_parts = l.parts;
   g.depth = cfg->in_features;
   g.features = cfg->out_features;
   g.swiglu = sh.swiglu;
@@ -460,6 +472,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
     t.dz_ld = pad8(sh.w_rows);
     t.plane = t.dz_ld * cfg->rows;
     t.cols = cfg->out_features;
+    t.parts = dx != nullptr ? l.dz_parts : l.parts;
     const bool eights = cfg->out_features % 8 == 0;
     t.vec_y = vec_ok(dy, sh.y, cfg->dtype);
     t.vec_z = eights && vec_ok(z, sh.z, cfg->dtype);
@@ -471,7 +484,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   GroupedProduct q{};
   q.groups = cfg->groups;
   q.total_rows = cfg->rows;
-  q.planes = l.planes;
+  q.a_parts = q.b_parts = l.parts;
   q.a = odz.p;
   q.lda = odz.ld;
   q.a_plane = odz.plane;
@@ -479,6 +492,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   GroupedProduct gx = q, gw = q;
   gx.kind = GroupedKind::kInputGrad;
   gx.depth = sh.w_rows;
+  gx.a_parts = l.dz_parts;
   gx.b = ow.p;
   gx.ldb = ow.ld;
   gx.b_plane = ow.plane;

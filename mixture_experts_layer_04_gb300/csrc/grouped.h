@@ -20,12 +20,14 @@ struct GroupPlan {
   void* maps;     // tensor maps of every group's rows, [groups][2], or null
 };
 
-// One grouped product.  Operands are bf16, in `planes` parts (1, or 3 for float32 values), with
-// rows at 16-byte boundaries.  A: activations [total rows][a_inner]; B: weights
+// One grouped product.  Operands are bf16, in parts whose sum is the value (1; 3 each for float32
+// values; 2 of A for a gradient that a float32 result wants exact to 16 bits), with rows at 16-byte
+// boundaries.  A: activations [total rows][a_inner]; B: weights
 // [groups][w_rows][w_inner], or for the weight gradient activations [total rows][b_inner].
 struct GroupedProduct {
   GroupedKind kind;
-  int groups, total_rows, planes;
+  int groups, total_rows;
+  int a_parts, b_parts;
   int depth;           // reduction (forward, input gradient); unused by the weight gradient
   int rows;            // weight gradient: rows of C_g
   int features;        // columns of C
@@ -43,7 +45,7 @@ struct GroupedProduct {
 };
 
 // Rows that a tile of the forward or input-gradient product takes, by the rule in grouped_gemm.cu.
-int grouped_tile_rows(int total_rows, int groups, int planes);
+int grouped_tile_rows(int total_rows, int groups, bool f32);
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows);
 
 // Reads the offsets; with `weight_grad` (may be null) also writes its operands' maps.

@@ -38,13 +38,14 @@ constexpr int BK = 64;
 constexpr int kMaxChunk = 256;  // k-blocks per accumulator of a bf16 result
 constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
 
-template <int CTAS, int BN, int PL, bool SWAP>
+// PA, PB: bf16 parts per value on the A and on the B side.
+template <int CTAS, int BN, int PA, int PB, bool SWAP>
 struct GroupedCfg {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kBRows = BN / CTAS;
   static constexpr int kABytes = 128 * BK * 2, kBBytes = kBRows * BK * 2;
-  static constexpr int kStageBytes = PL * (kABytes + kBBytes);
+  static constexpr int kStageBytes = PA * kABytes + PB * kBBytes;
   static constexpr int kStgBytes = SWAP ? 0 : kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
   static constexpr int kBarBytes = 256;
   static constexpr int kRaw = (232448 - 1024 - kBarBytes - kStgBytes) / kStageBytes;
@@ -231,10 +232,10 @@ __device__ __forceinline__ void put_piece(const Out& o, uint8_t* stg, int lane, 
 
 // -------------------------------------------------------------------- kernel ----
 
-template <int CTAS, int BN, int PL, bool SWAP>
-__global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
+template <int CTAS, int BN, int PA, int PB, bool SWAP>
+__global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 1)
     grouped_kernel(const __grid_constant__ GroupedParams p) {
-  using Cfg = GroupedCfg<CTAS, BN, PL, SWAP>;
+  using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -340,10 +341,9 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CTAS * Cfg::kStageBytes);
           const int k = t.k0 + kb * BK;
 #pragma unroll
-          for (int pl = 0; pl < PL; ++pl) {
+          for (int pl = 0; pl < PA; ++pl) {
             const uint32_t da = dst + pl * Cfg::kABytes;
-            const uint32_t db = dst + PL * Cfg::kABytes + pl * Cfg::kBBytes;
-            const int ta = a_third + pl * p.a_step, tb = b_third + pl * p.b_step;
+            const int ta = a_third + pl * p.a_step;
             if constexpr (SWAP) {
               if (p.swiglu) {  // 16 gate rows, then the same 16 up rows, for each 32 lanes
 #pragma unroll
@@ -355,15 +355,21 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
               } else {
                 load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
               }
-              load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
             } else {
               load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
-              if (CTAS == 1 && p.swiglu) {  // gate and up halves of the tile
-                load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
-                load_box<CTAS>(db + Cfg::kBBytes / 2, tm_b, fb, k, p.features + b_row, tb);
-              } else {
-                load_rows<CTAS, Cfg::kBRows>(db, tm_b, fb, p.b_mn, b_row, k, tb);
-              }
+            }
+          }
+#pragma unroll
+          for (int pl = 0; pl < PB; ++pl) {
+            const uint32_t db = dst + PA * Cfg::kABytes + pl * Cfg::kBBytes;
+            const int tb = b_third + pl * p.b_step;
+            if constexpr (SWAP) {
+              load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
+            } else if (CTAS == 1 && p.swiglu) {  // gate and up halves of the tile
+              load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
+              load_box<CTAS>(db + Cfg::kBBytes / 2, tm_b, fb, k, p.features + b_row, tb);
+            } else {
+              load_rows<CTAS, Cfg::kBRows>(db, tm_b, fb, p.b_mn, b_row, k, tb);
             }
           }
           issued = min(issued + 1, S);
@@ -413,13 +419,16 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
             }
             tc_fence_after();
             const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
-            const uint32_t b_base = a_base + PL * Cfg::kABytes;
-            // smallest products first
-            constexpr int kTerms = PL == 3 ? 6 : 1;
+            const uint32_t b_base = a_base + PA * Cfg::kABytes;
+            // smallest products first; of three parts each, those above 2^-24
+            constexpr bool kThree = PA == 3 && PB == 3;
+            constexpr int kTerms = kThree ? 6 : PA * PB;
             constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
+            static_assert(kThree || PA * PB <= 2, "parts");
 #pragma unroll
             for (int q = 0; q < kTerms; ++q) {
-              const int qa = PL == 3 ? pa[q] : 0, qb = PL == 3 ? pb[q] : 0;
+              const int qa = kThree ? pa[q] : PA - 1 - (PA > 1 ? q : 0);
+              const int qb = kThree ? pb[q] : PB - 1 - (PB > 1 ? q : 0);
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
                 const uint64_t da = operand_desc(a_base + qa * Cfg::kABytes + kk * a_step, p.a_mn);
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             if (col + 32 * i >= o.cols) break;
-            if (PL == 3 || f32) {
+            if (PA == 3 || f32) {
               reuse();
               stage_f32(stg, lane, sum[I0 + i]);
               put_piece<float>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
@@ -559,14 +568,14 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PL, SWAP>::kThreads, 1)
             Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
             emit(oz, false, col, zero, mid);
             oz.third = 1;
-            oz.base += static_cast<long long>(p.features) * (PL == 3 ? 4 : 2);
+            oz.base += static_cast<long long>(p.features) * (PA == 3 ? 4 : 2);
             emit(oz, false, col, mid, mid);
           }
 #pragma unroll
           for (int i = 0; i < NP / 2; ++i)
 #pragma unroll
             for (int q = 0; q < P; ++q)
-              sum[i][q] = act_value<PL == 1>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
+              sum[i][q] = act_value<PA != 3>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
           emit(oc, p.c_f32 != 0, col, zero, mid);
         }
       }
@@ -725,9 +734,9 @@ inline bool vec_ok(const void* p, long long ld, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * bytes % 16 == 0;
 }
 
-template <int CTAS, int BN, int PL, bool SWAP>
+template <int CTAS, int BN, int PA, int PB, bool SWAP>
 cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
-  using Cfg = GroupedCfg<CTAS, BN, PL, SWAP>;
+  using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
   const bool weight_grad = g.kind == GroupedKind::kWeightGrad;
   const long long rows = g.total_rows;
   if (!weight_grad) {
@@ -740,8 +749,8 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
     const int x_box = SWAP ? BN : 128;
     CUtensorMap* tx = SWAP ? &p->tm_b : &p->tm_a;
     CUtensorMap* tw = SWAP ? &p->tm_a : &p->tm_b;
-    if (!operand_map(tx, g.a, g.depth, rows, g.planes, g.lda, g.a_plane, x_box) ||
-        !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.planes) * g.groups, g.ldb,
+    if (!operand_map(tx, g.a, g.depth, rows, g.a_parts, g.lda, g.a_plane, x_box) ||
+        !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.b_parts) * g.groups, g.ldb,
                      g.ldb * w_rows, w_box))
       return cudaErrorInvalidValue;
     (SWAP ? p->a_mn : p->b_mn) = mn;
@@ -769,7 +778,7 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
                   : static_cast<long long>(grouped_max_tiles(g.total_rows, g.groups, Cfg::kTileRows)) *
                         p->tiles_b;
   if (bound >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
-  auto kernel = grouped_kernel<CTAS, BN, PL, SWAP>;
+  auto kernel = grouped_kernel<CTAS, BN, PA, PB, SWAP>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(kernel, Cfg::kSmem, &done);
   if (e != cudaSuccess) return e;
@@ -798,8 +807,8 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
 
 }  // namespace
 
-int grouped_tile_rows(int total_rows, int groups, int planes) {
-  if (planes == 3) return 128;
+int grouped_tile_rows(int total_rows, int groups, bool f32) {
+  if (f32) return 128;
   const long long mean = (static_cast<long long>(total_rows) + groups - 1) / groups;
   return mean <= 32 ? 32 : mean <= 64 ? 64 : 256;
 }
@@ -823,8 +832,8 @@ cudaError_t launch_group_plan(const int32_t* offsets, int rows, int groups, int 
   unsigned blocks = 1;
   if (wg != nullptr) {
     // both row-contiguous: [planes][rows][inner], boxes of 64 x 64
-    if (!operand_map(&p.tm_a, wg->a, wg->rows, rows, wg->planes, wg->lda, wg->a_plane, BK) ||
-        !operand_map(&p.tm_b, wg->b, wg->features, rows, wg->planes, wg->ldb, wg->b_plane, BK))
+    if (!operand_map(&p.tm_a, wg->a, wg->rows, rows, wg->a_parts, wg->lda, wg->a_plane, BK) ||
+        !operand_map(&p.tm_b, wg->b, wg->features, rows, wg->b_parts, wg->ldb, wg->b_plane, BK))
       return cudaErrorInvalidValue;
     blocks = static_cast<unsigned>(ceil_div(2ll * groups, kPlanThreads / 32));
   } else {
@@ -850,13 +859,21 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& pla
   p.ldz = g.ldz;
   p.c_f32 = g.c_f32;
   p.err = err;
-  p.chunk = g.planes == 3 ? 2 : g.c_f32 ? 4 : kMaxChunk;
-  if (g.planes == 3) return launch<1, 128, 3, false>(&p, g, num_sms, s);
-  if (g.kind == GroupedKind::kWeightGrad) return launch<2, 256, 1, false>(&p, g, num_sms, s);
-  switch (grouped_tile_rows(g.total_rows, g.groups, g.planes)) {
-    case 32: return launch<1, 32, 1, true>(&p, g, num_sms, s);
-    case 64: return launch<1, 64, 1, true>(&p, g, num_sms, s);
-    default: return launch<2, 256, 1, false>(&p, g, num_sms, s);
+  const bool f32 = g.a_parts == 3;
+  p.chunk = f32 ? 2 : g.c_f32 ? 4 : kMaxChunk;
+  if (f32) return launch<1, 128, 3, 3, false>(&p, g, num_sms, s);
+  if (g.kind == GroupedKind::kWeightGrad) return launch<2, 256, 1, 1, false>(&p, g, num_sms, s);
+  const bool two = g.a_parts == 2;
+  switch (grouped_tile_rows(g.total_rows, g.groups, false)) {
+    case 32:
+      return two ? launch<1, 32, 1, 2, true>(&p, g, num_sms, s)
+                 : launch<1, 32, 1, 1, true>(&p, g, num_sms, s);
+    case 64:
+      return two ? launch<1, 64, 1, 2, true>(&p, g, num_sms, s)
+                 : launch<1, 64, 1, 1, true>(&p, g, num_sms, s);
+    default:
+      return two ? launch<2, 256, 2, 1, false>(&p, g, num_sms, s)
+                 : launch<2, 256, 1, 1, false>(&p, g, num_sms, s);
   }
 }
 

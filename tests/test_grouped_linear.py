@@ -5,7 +5,7 @@ itself.  The tensor core adds 16 products at a time and truncates: at most 2^-22
 float32 addition per chunk of at most 2^-24 of S: ACC(n) = (n / 16 + n / 128 + 2) 2^-22.  Float32
 operands are three bf16 parts (2^-24 of each value left, twice) and six products per value, added in
 as many steps: 6 ACC(n) + 2^-22.  dz is rounded to bf16 once (2^-8 of itself, and so of S of the
-products that take it), SwiGLU's fast exponential is good to 2e-5.  What a sum of independent
+products that take it; 2^-17 where dx is float32), SwiGLU's fast exponential is good to 2e-5.  What a sum of independent
 roundings comes to is checked in L2: a product p_i whose factor is rounded is off by e_i p_i, with
 e_i at most 2^-8 and 2^-8 / sqrt(3) in the root mean square, so sum e_i p_i has the root mean square
 2^-8 / sqrt(3) sqrt(sum p_i^2) (not a share of the sum itself, whose terms may cancel), and the
@@ -135,7 +135,7 @@ class Case:
         return torch.cat([dy * u * (s + g * s * (1 - s)), dy * g * s], dim=1)
 
     def check_backward(self, dx, dw):
-        rounded = (HALF + 4e-5 if self.dtype == BF16 else 2.0 ** -21) if self.act else 0.0
+        off = (HALF + 4e-5 if self.dtype == BF16 else 2.0 ** -21) if self.act else 0.0
         if dx is not None:
             self.unowned(dx, self.fin)
         if dw is not None:
@@ -144,10 +144,12 @@ class Case:
         for e, at, w in self.groups():
             seen.add(e)
             d, x = self.dz(at), self.x[at].double()
-            for got, a, b, t in (
-                    (dx[at] if dx is not None else None, d, w, self.dxt),
+            two = self.dtype == BF16 and self.dxt == F32 and self.act  # dz in two parts for dx
+            for got, a, b, t, rounded in (
+                    (dx[at] if dx is not None else None, d, w, self.dxt,
+                     2.0 ** -17 + 4e-5 if two else off),
                     (dw[e * self.N:(e + 1) * self.N] if dw is not None else None, d.t(), x,
-                     self.dtype)):
+                     self.dtype, off)):
                 if got is not None:
                     got, ref, S, n = got[:, :self.fin], a @ b, a.abs() @ b.abs(), a.shape[1]
                     assert_close(got, ref, S * (acc(n, self.dtype) + rounded) * (1 + HALF)
