@@ -17,10 +17,12 @@
 // 8192 columns are read again in each pass); the columns' vectors stay in its registers
 // from row to row.  The column sums stay in registers too and leave as one partial per block,
 // which a second launch adds up in order.
+#include <atomic>
 #include <initializer_list>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_operand.cuh"
 #include "topk.cuh"
 
 namespace moe {
@@ -86,7 +88,9 @@ struct NormParams {
   long long ldx, ldr, lds, ldy, lddx, lddr;
   int rows, width, gate_kind;
   int threads;  // per row
+  int depth;    // rows on their way per group of threads (ring kernels)
   float eps, residual_scale, branch_scale;
+  unsigned* err;
 };
 
 // The threads of one row: eight columns each, `i` times.  Vec: neighbouring columns, 16-byte
@@ -127,8 +131,10 @@ struct Columns {
   }
 };
 
-// Sums of N values over the threads of a row; every thread gets them.  `part` is this group's
-// shared memory (N floats per warp), `turn` alternates between two such areas.
+// Sums of N values over the threads of a row; every thread gets them.  `part`: this group's shared
+// memory, 4 floats per warp.  (Halving the values among the lanes as they are added up takes half
+// the instructions and two more dependent steps, and is slower: 16384 rows of 7168 177 us instead
+// of 167, the backward of 8192 rows of 2048 63 instead of 59.)
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int group, int threads) {
 #pragma unroll
@@ -144,23 +150,90 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* part, int group, i
   for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? part[lane * N + k] : 0.f);
 }
 
-__device__ __forceinline__ float gate_of(const NormParams& p, int row, float* slope) {
+// The gate of a row whose entry is v, and the logistic's slope there.
+__device__ __forceinline__ float gate_from(int kind, float v, float* slope) {
   *slope = 1.f;
-  if (p.gate_kind == MOE_GATE_NONE) return 1.f;
-  const float v = p.gate[row];
-  if (p.gate_kind == MOE_GATE_VALUE) return v;
-  const float t = expf(-fabsf(v)), r = 1.f / (1.f + t);
+  if (kind == MOE_GATE_NONE) return 1.f;
+  if (kind == MOE_GATE_VALUE) return v;
+  const float t = expf(-fabsf(v)), r = __fdividef(1.f, 1.f + t);
   *slope = t * r * r;  // of the logistic function, without the cancellation in 1 - g
   return v >= 0.f ? r : t * r;
 }
 
-__device__ __forceinline__ float root(float squares, float width, float eps) {
-  return 1.f / sqrtf(squares / width + eps);
+__device__ __forceinline__ float gate_of(const NormParams& p, int row, float* slope) {
+  return gate_from(p.gate_kind, p.gate != nullptr ? p.gate[row] : 0.f, slope);
+}
+
+__device__ __forceinline__ float root(float squares, float inv_width, float eps) {
+  return rsqrtf(fmaf(squares, inv_width, eps));
 }
 
 constexpr int kMaxThreads = 1024;
-// Partial sums of the warps: at most kMaxThreads / 32 of them, 3 values, two areas.
-constexpr int kPartFloats = kMaxThreads / 32 * 3;
+constexpr int kMaxDepth = 8, kMostGroups = 16;
+
+// Rows on their way to a group of threads: `depth` slots of shared memory, each with the row of up
+// to N arrays (null ones have no place), copied in bulk and counted on the slot's barrier.
+template <typename T, int N>
+struct Ring {
+  const T* src[N];
+  long long ld[N];
+  uint32_t base, slot_bytes, bar0;
+  uint8_t* smem;
+  int row_bytes, depth;
+  volatile int* abort_flag;
+  unsigned* err;
+
+  __device__ __forceinline__ void issue(int row, int slot) const {
+    const uint32_t bar = bar0 + 8u * slot;
+    mbar_arrive_expect_tx(bar, slot_bytes);
+    uint32_t dst = base + slot * slot_bytes;
+#pragma unroll
+    for (int a = 0; a < N; ++a)
+      if (src[a] != nullptr) {
+        bulk_copy_g2s(dst, src[a] + row * ld[a], static_cast<uint32_t>(row_bytes), bar);
+        dst += row_bytes;
+      }
+  }
+  __device__ __forceinline__ bool wait(int slot, uint32_t phase) const {
+    return mbar_wait(bar0 + 8u * slot, phase, abort_flag, err);
+  }
+  // column `at` on of the slot's rows (zeros for null arrays and past the end)
+  __device__ __forceinline__ void read(int slot, int at, bool in, Eight<T> (&e)[N]) const {
+    const T* from = reinterpret_cast<const T*>(smem + slot * slot_bytes) + at;
+#pragma unroll
+    for (int a = 0; a < N; ++a) {
+      if (src[a] != nullptr && in) e[a].load(from);
+      else e[a].zero();
+      if (src[a] != nullptr) from += row_bytes / static_cast<int>(sizeof(T));
+    }
+  }
+};
+
+// Sets a group's ring up and sends for its first rows.  Every thread of the block calls it.
+template <typename T, int N>
+__device__ __forceinline__ void start_ring(Ring<T, N>& r, uint8_t* rings, uint64_t* bars, int width,
+                                           int depth, int group, int groups, bool leader, int row,
+                                           int step, int rows) {
+  int arrays = 0;
+#pragma unroll
+  for (int a = 0; a < N; ++a) arrays += r.src[a] != nullptr;
+  r.row_bytes = width * static_cast<int>(sizeof(T));
+  r.slot_bytes = static_cast<uint32_t>(arrays * r.row_bytes);
+  r.depth = depth;
+  r.smem = rings + static_cast<size_t>(group) * depth * r.slot_bytes;
+  r.base = smem_u32(r.smem);
+  r.bar0 = smem_u32(bars + group * kMaxDepth);
+  if (leader)
+    for (int k = 0; k < depth; ++k) mbar_init(r.bar0 + 8u * k, 1);
+  fence_mbar_init();
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_trigger();
+  if (leader)
+    for (int k = 0; k < depth && row + k * step < rows; ++k) r.issue(row + k * step, k);
+}
+// Partial sums of the warps: at most kMaxThreads / 32 of them, 4 values, two areas.
+constexpr int kPartFloats = kMaxThreads / 32 * 4;
 
 // V: columns a thread keeps, in eights; 0: rows are read again in each pass.  NT: threads at most.
 template <typename T, int V, bool Vec, int NT>
@@ -172,8 +245,8 @@ __global__ void __launch_bounds__(NT)
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
   const Columns<Vec> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
   const int n = V > 0 ? V : (p.width + 8 * p.threads - 1) / (8 * p.threads);
-  const float width = static_cast<float>(p.width);
-  float* mine[2] = {part[0] + group * (p.threads >> 5) * 3, part[1] + group * (p.threads >> 5) * 3};
+  const float inv_width = 1.f / static_cast<float>(p.width);
+  float* mine[2] = {part[0] + group * (p.threads >> 5) * 4, part[1] + group * (p.threads >> 5) * 4};
   constexpr int R = V > 0 ? V : 1;
   float c[R][8], wn[R][8];
   auto vectors = [&](int i, float (&cv)[8], float (&nv)[8]) {
@@ -217,7 +290,7 @@ __global__ void __launch_bounds__(NT)
         }
       }
       row_sum<1>(sq, mine[0], group, p.threads);
-      f *= root(sq[0], width, p.eps);
+      f *= root(sq[0], inv_width, p.eps);
     }
     float s[R][8];
     auto make = [&](int i, const Eight<T>& ex, const Eight<T>& er, const float (&cv)[8],
@@ -249,7 +322,7 @@ __global__ void __launch_bounds__(NT)
     float rs = 0.f;
     if (p.y != nullptr) {
       row_sum<1>(sq, mine[1], group, p.threads);
-      rs = root(sq[0], width, p.eps);
+      rs = root(sq[0], inv_width, p.eps);
     }
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -274,6 +347,42 @@ __global__ void __launch_bounds__(NT)
   }
 }
 
+// The block's column sums to its partial: the groups' sums, in order.  Every thread of the block
+// calls it; columns: [groups - 1][2][width].
+template <int V, typename C>
+__device__ __forceinline__ void leave_columns(const NormParams& p, const C& col, float* columns,
+                                              int group, int groups, const float (&sum_n)[V][8],
+                                              const float (&sum_a)[V][8]) {
+  float* out = p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.width;
+  if (group > 0) {
+    float* to = columns + static_cast<size_t>(group - 1) * 2 * p.width;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (col.at(i, q) < p.width) {
+          to[col.at(i, q)] = sum_n[i][q];
+          to[p.width + col.at(i, q)] = sum_a[i][q];
+        }
+  }
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int at = col.at(i, q);
+      if (at >= p.width) continue;
+      float a = sum_n[i][q], b = sum_a[i][q];
+      for (int k = 0; k + 1 < groups; ++k) {
+        a += columns[static_cast<size_t>(k) * 2 * p.width + at];
+        b += columns[(static_cast<size_t>(k) * 2 + 1) * p.width + at];
+      }
+      out[at] = a;
+      out[p.width + at] = b;
+    }
+}
+
 // A row's sums: of x^2, s^2 and dy wn s; then of ds c x.
 template <typename T, int V, bool Vec, int NT>
 __global__ void __launch_bounds__(NT)
@@ -285,8 +394,8 @@ __global__ void __launch_bounds__(NT)
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
   const Columns<Vec> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
   const int n = V > 0 ? V : (p.width + 8 * p.threads - 1) / (8 * p.threads);
-  const float width = static_cast<float>(p.width);
-  float* mine[2] = {part[0] + group * (p.threads >> 5) * 3, part[1] + group * (p.threads >> 5) * 3};
+  const float inv_width = 1.f / static_cast<float>(p.width);
+  float* mine[2] = {part[0] + group * (p.threads >> 5) * 4, part[1] + group * (p.threads >> 5) * 4};
   constexpr int R = V > 0 ? V : 1;
   float* out = p.parts == nullptr ? nullptr
                                   : p.parts + static_cast<size_t>(blockIdx.x) * 2 * p.width;
@@ -341,9 +450,9 @@ __global__ void __launch_bounds__(NT)
       }
     }
     row_sum<3>(sums, mine[0], group, p.threads);
-    const float rx = p.post != nullptr ? root(sums[0], width, p.eps) : 1.f;
-    const float rs = p.dy != nullptr ? root(sums[1], width, p.eps) : 0.f;
-    const float d1 = rs * rs * (sums[2] / width);
+    const float rx = p.post != nullptr ? root(sums[0], inv_width, p.eps) : 1.f;
+    const float rs = p.dy != nullptr ? root(sums[1], inv_width, p.eps) : 0.f;
+    const float d1 = rs * rs * (sums[2] * inv_width);
     auto grad = [&](int k, int q) {  // ds
       return fmaf(rs, fmaf(-s[k].get(q), d1, dy[k].get(q) * wn[k][q]), ds[k].get(q));
     };
@@ -360,7 +469,7 @@ __global__ void __launch_bounds__(NT)
       row_sum<1>(dot, mine[1], group, p.threads);
       if (p.dgate != nullptr && col.t == 0) p.dgate[row] = rx * dot[0] * slope;
     }
-    const float d2 = p.post != nullptr ? rx * rx * (dot[0] / width) : 0.f;
+    const float d2 = p.post != nullptr ? rx * rx * (dot[0] * inv_width) : 0.f;
     const float f = g * rx;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -397,36 +506,280 @@ __global__ void __launch_bounds__(NT)
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.threads) : "memory");
   }
   if constexpr (V > 0) {
-    if (out == nullptr) return;
-    // the groups' sums, in order
-    if (group > 0) {
-      float* to = columns + static_cast<size_t>(group - 1) * 2 * p.width;
+    if (out != nullptr) leave_columns<V>(p, col, columns, group, groups, sum_n, sum_a);
+  }
+}
+
+// Eight values of a vector: in registers, or (KEEP false) in shared memory.
+template <bool KEEP>
+struct Vector {
+  float v[KEEP ? 8 : 1];
+  __device__ __forceinline__ void get(const float* p, float (&out)[8]) const {
+    if constexpr (KEEP) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (col.at(i, q) < p.width) {
-            to[col.at(i, q)] = sum_n[i][q];
-            to[p.width + col.at(i, q)] = sum_a[i][q];
-          }
+      for (int q = 0; q < 8; ++q) out[q] = v[q];
+    } else {
+      const float4 a = reinterpret_cast<const float4*>(p)[0];
+      const float4 b = reinterpret_cast<const float4*>(p)[1];
+      out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+      out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
     }
-    __syncthreads();
-    if (group > 0) return;
+  }
+};
+
+// The forward over many rows.  The first sum of the next row is taken with the second sum of the
+// present one, so that a row costs one barrier.  V: eights of columns per thread; a thread's
+// instructions for a row (two sums, the gate, addresses) cost as much as eight columns' own, so
+// two where rows have them.
+template <typename T, int V>
+__global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float part[2][kPartFloats];
+  __shared__ uint64_t bars[kMostGroups * kMaxDepth];
+  __shared__ int gave_up;
+  extern __shared__ __align__(128) uint8_t rings[];
+  const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
+  const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const float inv_width = 1.f / static_cast<float>(p.width);
+  const int step = gridDim.x * groups;
+  int row = blockIdx.x * groups + group;
+  Ring<T, 2> ring;
+  if (threadIdx.x == 0) gave_up = 0;
+  ring.src[0] = static_cast<const T*>(p.x);
+  ring.src[1] = static_cast<const T*>(p.residual);
+  ring.ld[0] = p.ldx;
+  ring.ld[1] = p.ldr;
+  ring.abort_flag = &gave_up;
+  ring.err = p.err;
+  start_ring(ring, rings, bars, p.width, p.depth, group, groups, col.t == 0, row, step, p.rows);
+  float c[V][8], wn[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float post[8], scale[8];
+    col.vector(p.post, i, 1.f, post);
+    col.vector(p.scale, i, 1.f, scale);
+    col.vector(p.norm, i, 1.f, wn[i]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c[i][q] = p.branch_scale * scale[q] * post[q];
+  }
+  Eight<T> cur[V][2];
+  int slot = 0, area = 0;
+  uint32_t phase = 0;
+  float sums[2] = {0.f, 0.f};  // of s^2, of the next row's x^2
+  float gate = 1.f, slope;
+  // (a row's gate is loaded a row ahead of its use)
+  auto gate_entry = [&](int r) { return p.gate != nullptr && r < p.rows ? p.gate[r] : 0.f; };
+  float entry = gate_entry(row);
+  bool ok = row < p.rows;
+  auto next_row = [&](int r) {
+    gate = gate_from(p.gate_kind, entry, &slope);
+    entry = gate_entry(r + step);
+    if (!ring.wait(slot, phase)) return false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int at = col.at(i, 0);
+      ring.read(slot, at, at < p.width, cur[i]);
+      if (p.post != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[1] = fmaf(cur[i][0].get(q), cur[i][0].get(q), sums[1]);
+      }
+    }
+    return true;
+  };
+  auto reduce = [&] {
+    row_sum<2>(sums, part[area] + group * (p.threads >> 5) * 2, group, p.threads);
+    area ^= 1;
+  };
+  if (ok) {
+    ok = next_row(row);
+    reduce();
+  }
+  for (; ok; row += step) {
+    const float f = p.post != nullptr ? gate * root(sums[1], inv_width, p.eps) : gate;
+    // the barrier has passed, so every thread has this row out of its slot
+    if (p.threads == 32) __syncwarp();
+    if (col.t == 0 && row + p.depth * step < p.rows) ring.issue(row + p.depth * step, slot);
+    if (++slot == p.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    float s[V][8];
+    sums[0] = sums[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const int at = col.at(i, q);
-        if (at >= p.width) continue;
-        float a = sum_n[i][q], b = sum_a[i][q];
-        for (int k = 0; k + 1 < groups; ++k) {
-          a += columns[static_cast<size_t>(k) * 2 * p.width + at];
-          b += columns[(static_cast<size_t>(k) * 2 + 1) * p.width + at];
-        }
-        out[at] = a;
-        out[p.width + at] = b;
+        s[i][q] = fmaf(f * cur[i][0].get(q), c[i][q], p.residual_scale * cur[i][1].get(q));
+        sums[0] = fmaf(s[i][q], s[i][q], sums[0]);
       }
+    const bool more = row + step < p.rows;
+    if (more) ok = next_row(row + step);
+    if (p.sum != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) col.store(static_cast<T*>(p.sum) + row * p.lds, i, s[i]);
+    }
+    reduce();
+    if (p.y != nullptr) {
+      const float rs = root(sums[0], inv_width, p.eps);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[i][q] *= rs * wn[i][q];
+        col.store(static_cast<T*>(p.y) + row * p.ldy, i, s[i]);
+      }
+    }
+    ok = ok && more;
   }
+}
+
+// The backward over many rows: the first sums of the next row are taken with the dot product of the
+// present one.  V: eights of columns per thread; with two, c and wn lie in shared memory.
+template <typename T, int V>
+__global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
+    const __grid_constant__ NormParams p) {
+  __shared__ float part[2][kPartFloats];
+  __shared__ uint64_t bars[kMostGroups * kMaxDepth];
+  __shared__ int gave_up;
+  // the rings, then (V > 1) c and wn; after the last row the groups' sums: [groups - 1][2][width]
+  extern __shared__ __align__(128) uint8_t rings[];
+  float* columns = reinterpret_cast<float*>(rings);
+  const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
+  const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const float inv_width = 1.f / static_cast<float>(p.width);
+  const int step = gridDim.x * groups;
+  int row = blockIdx.x * groups + group;
+  Ring<T, 4> ring;
+  if (threadIdx.x == 0) gave_up = 0;
+  ring.src[0] = static_cast<const T*>(p.x);
+  ring.src[1] = static_cast<const T*>(p.sum_in);
+  ring.src[2] = static_cast<const T*>(p.dy);
+  ring.src[3] = static_cast<const T*>(p.dsum);
+  ring.ld[0] = p.ldx;
+  ring.ld[1] = ring.ld[3] = p.lds;
+  ring.ld[2] = p.ldy;
+  ring.abort_flag = &gave_up;
+  ring.err = p.err;
+  start_ring(ring, rings, bars, p.width, p.depth, group, groups, col.t == 0, row, step, p.rows);
+  float* shared_c = reinterpret_cast<float*>(rings + static_cast<size_t>(groups) * p.depth *
+                                                         ring.slot_bytes);
+  const float* shared_w = shared_c + p.width;
+  Vector<V == 1> c[V], wn[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float post[8], scale[8], norm[8];
+    col.vector(p.post, i, 1.f, post);
+    col.vector(p.scale, i, 1.f, scale);
+    col.vector(p.norm, i, 0.f, norm);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float v = p.branch_scale * scale[q] * post[q];
+      if constexpr (V == 1) {
+        c[i].v[q] = v;
+        wn[i].v[q] = norm[q];
+      } else if (col.at(i, q) < p.width) {  // (read by the thread that wrote it)
+        shared_c[col.at(i, q)] = v;
+        shared_c[p.width + col.at(i, q)] = norm[q];
+      }
+    }
+  }
+  float sum_n[V][8], sum_a[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum_n[i][q] = sum_a[i][q] = 0.f;
+  Eight<T> cur[V][4];
+  int slot = 0, area = 0;
+  uint32_t phase = 0;
+  float sums[4] = {0.f, 0.f, 0.f, 0.f};  // of ds c x; the next row's x^2, s^2, dy wn s
+  float gate = 1.f, slope = 1.f;
+  // (a row's gate is loaded a row ahead of its use)
+  auto gate_entry = [&](int r) { return p.gate != nullptr && r < p.rows ? p.gate[r] : 0.f; };
+  float entry = gate_entry(row);
+  bool ok = row < p.rows;
+  auto next_row = [&](int r, Eight<T> (&e)[V][4]) {
+    gate = gate_from(p.gate_kind, entry, &slope);
+    entry = gate_entry(r + step);
+    if (!ring.wait(slot, phase)) return false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int at = col.at(i, 0);
+      ring.read(slot, at, at < p.width, e[i]);
+      if (at >= p.width) continue;
+      float w[8];
+      wn[i].get(shared_w + at, w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float vx = e[i][0].get(q), vs = e[i][1].get(q);
+        sums[1] = fmaf(vx, vx, sums[1]);
+        sums[2] = fmaf(vs, vs, sums[2]);
+        sums[3] = fmaf(e[i][2].get(q) * w[q], vs, sums[3]);
+      }
+    }
+    return true;
+  };
+  auto reduce = [&] {
+    row_sum<4>(sums, part[area] + group * (p.threads >> 5) * 4, group, p.threads);
+    area ^= 1;
+  };
+  if (ok) {
+    ok = next_row(row, cur);
+    reduce();
+  }
+  for (; ok; row += step) {
+    const float rx = p.post != nullptr ? root(sums[1], inv_width, p.eps) : 1.f;
+    const float rs = p.dy != nullptr ? root(sums[2], inv_width, p.eps) : 0.f;
+    const float d1 = rs * rs * (sums[3] * inv_width);
+    const float f = gate * rx, gate_slope = rx * slope;
+    // the barrier has passed, so every thread has this row out of its slot
+    if (p.threads == 32) __syncwarp();
+    if (col.t == 0 && row + p.depth * step < p.rows) ring.issue(row + p.depth * step, slot);
+    if (++slot == p.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    float v[V][8];
+    Eight<T> x[V];
+    sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int at = col.at(i, 0);
+      float cv[8], w[8];
+      if (at >= p.width) continue;
+      c[i].get(shared_c + at, cv);
+      wn[i].get(shared_w + at, w);
+      x[i] = cur[i][0];
+      float r[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float s = cur[i][1].get(q), dy = cur[i][2].get(q);
+        v[i][q] = fmaf(rs, fmaf(-s, d1, dy * w[q]), cur[i][3].get(q));
+        sum_n[i][q] = fmaf(dy * s, rs, sum_n[i][q]);
+        sum_a[i][q] = fmaf(f * v[i][q], x[i].get(q), sum_a[i][q]);
+        r[q] = p.residual_scale * v[i][q];
+        v[i][q] *= cv[q];
+        sums[0] = fmaf(v[i][q], x[i].get(q), sums[0]);
+      }
+      if (p.dresidual != nullptr)
+        col.store(static_cast<T*>(p.dresidual) + row * p.lddr, i, r);
+    }
+    const bool more = row + step < p.rows;
+    if (more) ok = next_row(row + step, cur);
+    reduce();
+    if (p.dgate != nullptr && col.t == 0) p.dgate[row] = gate_slope * sums[0];
+    if (p.dx != nullptr) {
+      const float d2 = p.post != nullptr ? rx * rx * (sums[0] * inv_width) : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (col.at(i, 0) >= p.width) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[i][q] = f * fmaf(-x[i].get(q), d2, v[i][q]);
+        col.store(static_cast<T*>(p.dx) + row * p.lddx, i, v[i]);
+      }
+    }
+    ok = ok && more;
+  }
+  if (p.parts == nullptr) return;
+  __syncthreads();  // every group's last row has left its slot
+  leave_columns<V>(p, col, columns, group, groups, sum_n, sum_a);
 }
 
 // The blocks' column sums, added in order, and the vectors' gradients: 32 columns per block, each
@@ -509,11 +862,36 @@ constexpr int kGradBlock = 512;
 int grad_blocks(const moe_block_norm_config_t* c, int num_sms) {
   const Shape s = shape_of(c->width, kGradBlock);
   const long long need = (static_cast<long long>(c->rows) + s.groups - 1) / s.groups;
-  const long long most = static_cast<long long>(num_sms) * (s.threads * s.groups <= 512 ? 2 : 1);
-  return static_cast<int>(need < most ? need : most);
+  return static_cast<int>(need < num_sms ? need : num_sms);
 }
 // For the workspace's size, which must not depend on the device: no GPU has more.
 constexpr int kMostSms = 160;
+
+// The ring kernels' shape: 512 threads at most, rows of `two_from` columns and more 16 columns a
+// thread.  The backward has them where rows would not fit otherwise: 8192 rows of 2048 take 64 us
+// with 16 columns a thread.
+constexpr int kRowsBlock = 512;
+constexpr int kTwoEights = 512;
+constexpr int kGradTwoEights = 8 * 512 + 1;
+Shape rows_shape(int width, int two_from) {
+  Shape s;
+  s.keep = width <= 16 * kRowsBlock;
+  const int per = width < two_from ? 8 : 16;
+  s.threads = ((width + per - 1) / per + 31) / 32 * 32;
+  const int groups = kRowsBlock / s.threads;
+  const int most = s.threads == 32 ? kMostGroups : kMostGroups - 1;  // (named barriers: 1 to 15)
+  s.groups = groups < 1 ? 1 : groups < most ? groups : most;
+  return s;
+}
+
+// Rows in a group's ring, 0: read directly (few rows a group, or rows that bulk copies cannot take).
+constexpr int kRingBytes = 196608;
+int ring_depth(const Shape& s, bool vec, int rows, int blocks, int slot_bytes, int other) {
+  if (!s.keep || !vec || slot_bytes == 0) return 0;
+  const int fits = (kRingBytes - other) / (slot_bytes * s.groups);
+  const int depth = fits < kMaxDepth ? fits : kMaxDepth;
+  return depth >= 2 && rows / (blocks * s.groups) >= 2 ? depth : 0;
+}
 
 inline bool unaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 inline moe_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -551,20 +929,48 @@ bool all_vec(int width, int dtype, std::initializer_list<Array> arrays) {
   return true;
 }
 
-template <typename T, bool Vec>
-cudaError_t launch_forward(const NormParams& p, int keep, unsigned blocks, unsigned threads,
-                           cudaStream_t s) {
-  auto kernel = !keep            ? block_norm_kernel<T, 0, Vec, kMaxThreads>
-                : threads <= 256 ? block_norm_kernel<T, 1, Vec, 256>
-                                 : block_norm_kernel<T, 1, Vec, kMaxThreads>;
+template <typename K>
+cudaError_t launch_rows(K kernel, const NormParams& p, unsigned blocks, unsigned threads,
+                        size_t smem, std::atomic<unsigned long long>* done, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = allow_smem(kernel, kRingBytes, done);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, p);
+}
+
+template <typename T>
+cudaError_t launch_forward(const NormParams& p, int keep, bool vec, unsigned blocks,
+                           unsigned threads, size_t smem, cudaStream_t s) {
+  static std::atomic<unsigned long long> done[2];
+  if (p.depth > 0)
+    return p.width < kTwoEights
+               ? launch_rows(block_norm_rows_kernel<T, 1>, p, blocks, threads, smem, &done[0], s)
+               : launch_rows(block_norm_rows_kernel<T, 2>, p, blocks, threads, smem, &done[1], s);
+  auto kernel = keep ? (vec ? block_norm_kernel<T, 1, true, kMaxThreads>
+                            : block_norm_kernel<T, 1, false, kMaxThreads>)
+                     : (vec ? block_norm_kernel<T, 0, true, kMaxThreads>
+                            : block_norm_kernel<T, 0, false, kMaxThreads>);
   return launch_pdl(kernel, dim3(blocks), dim3(threads), 0, s, p);
 }
-template <typename T, bool Vec>
-cudaError_t launch_backward(const NormParams& p, int keep, unsigned blocks, unsigned threads,
-                            size_t smem, cudaStream_t s) {
-  auto kernel = !keep            ? block_norm_grad_kernel<T, 0, Vec, kMaxThreads>
-                : threads <= 512 ? block_norm_grad_kernel<T, 1, Vec, 512>
-                                 : block_norm_grad_kernel<T, 1, Vec, kMaxThreads>;
+template <typename T>
+cudaError_t launch_backward(const NormParams& p, int keep, bool vec, unsigned blocks,
+                            unsigned threads, size_t smem, cudaStream_t s) {
+  static std::atomic<unsigned long long> done[2];
+  if (p.depth > 0)
+    return p.width < kGradTwoEights
+               ? launch_rows(block_norm_grad_rows_kernel<T, 1>, p, blocks, threads, smem, &done[0],
+                             s)
+               : launch_rows(block_norm_grad_rows_kernel<T, 2>, p, blocks, threads, smem, &done[1],
+                             s);
+  if (keep && threads <= 512)
+    return launch_pdl(vec ? block_norm_grad_kernel<T, 1, true, 512>
+                          : block_norm_grad_kernel<T, 1, false, 512>,
+                      dim3(blocks), dim3(threads), smem, s, p);
+  auto kernel = keep ? (vec ? block_norm_grad_kernel<T, 1, true, kMaxThreads>
+                            : block_norm_grad_kernel<T, 1, false, kMaxThreads>)
+                     : (vec ? block_norm_grad_kernel<T, 0, true, kMaxThreads>
+                            : block_norm_grad_kernel<T, 0, false, kMaxThreads>);
   return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, p);
 }
 
@@ -607,8 +1013,26 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
   st = check_current_device();
   if (st != MOE_OK) return st;
   const int sms = device_num_sms();
-  const Shape sh = shape_of(cfg->width, 256);
+  // one group's rows follow one another through its ring, so a block per SM; without one, blocks
+  // of a few groups fill the SMs
+  const bool sums = post_weight != nullptr || y != nullptr;
+  const long long ab2 = static_cast<long long>(ab);
+  const NormParams q = params_of(cfg, 0);
+  const bool vec = all_vec(cfg->width, cfg->dtype,
+                           {{x, q.ldx}, {residual, q.ldr}, {sum, q.lds}, {y, q.ldy}});
+  const int slot = static_cast<int>((residual != nullptr ? 2 : 1) * cfg->width * ab2);
+  Shape sh = rows_shape(cfg->width, kTwoEights);
+  const int depth = sums ? ring_depth(sh, vec, cfg->rows, sms, slot, 0) : 0;
+  long long most = sms;
+  if (depth == 0) {
+    sh = shape_of(cfg->width, 256);
+    most = static_cast<long long>(sms) * (kMaxThreads / (sh.threads * sh.groups));
+  }
+  const int block = sh.threads * sh.groups;
+  const long long need = (static_cast<long long>(cfg->rows) + sh.groups - 1) / sh.groups;
   NormParams p = params_of(cfg, sh.threads);
+  p.depth = depth;
+  p.err = device_error_word();
   p.x = x;
   p.residual = residual;
   p.post = post_weight;
@@ -617,19 +1041,13 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
   p.norm = norm_weight;
   p.sum = sum;
   p.y = y;
-  const bool vec = all_vec(cfg->width, cfg->dtype,
-                           {{x, p.ldx}, {residual, p.ldr}, {sum, p.lds}, {y, p.ldy}});
-  const int block = sh.threads * sh.groups;
-  const long long need = (static_cast<long long>(cfg->rows) + sh.groups - 1) / sh.groups;
-  const long long most = static_cast<long long>(sms) * (kMaxThreads / block);
   const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
   const unsigned threads = static_cast<unsigned>(block);
+  const size_t smem = static_cast<size_t>(depth) * slot * sh.groups;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cfg->dtype == MOE_BF16)
-    return status_of(vec ? launch_forward<__nv_bfloat16, true>(p, sh.keep, blocks, threads, s)
-                         : launch_forward<__nv_bfloat16, false>(p, sh.keep, blocks, threads, s));
-  return status_of(vec ? launch_forward<float, true>(p, sh.keep, blocks, threads, s)
-                       : launch_forward<float, false>(p, sh.keep, blocks, threads, s));
+  return status_of(cfg->dtype == MOE_BF16
+                       ? launch_forward<__nv_bfloat16>(p, sh.keep, vec, blocks, threads, smem, s)
+                       : launch_forward<float>(p, sh.keep, vec, blocks, threads, smem, s));
 }
 
 extern "C" moe_status_t moe_block_norm_backward(
@@ -679,7 +1097,7 @@ extern "C" moe_status_t moe_block_norm_backward(
   if (vectors && unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
   st = check_current_device();
   if (st != MOE_OK) return st;
-  const Shape sh = shape_of(cfg->width, kGradBlock);
+  Shape sh = shape_of(cfg->width, kGradBlock);
   NormParams p = params_of(cfg, sh.threads);
   // (read only where something needs it)
   p.x = own || (dx != nullptr && post_weight != nullptr) ? x : nullptr;
@@ -694,20 +1112,35 @@ extern "C" moe_status_t moe_block_norm_backward(
   p.dresidual = dresidual;
   p.dgate = dgate;
   p.parts = vectors ? static_cast<float*>(ws) : nullptr;
-  const int blocks = grad_blocks(cfg, sms < kMostSms ? sms : kMostSms);
-  const unsigned threads = static_cast<unsigned>(sh.threads * sh.groups);
-  const size_t smem =
-      vectors && sh.keep > 0 ? static_cast<size_t>(sh.groups - 1) * 2 * cfg->width * 4 : 0;
   const bool vec = all_vec(cfg->width, cfg->dtype,
                            {{p.x, p.ldx}, {p.sum_in, p.lds}, {dy, p.ldy}, {dsum, p.lds},
                             {dx, p.lddx}, {dresidual, p.lddr}});
+  int arrays = 0;
+  for (const void* q : {p.x, p.sum_in, dy, dsum}) arrays += q != nullptr;
+  const int slot = arrays * cfg->width * static_cast<int>(ab);
+  const Shape rs = rows_shape(cfg->width, kGradTwoEights);
+  const int vector_bytes = cfg->width >= kGradTwoEights ? 2 * cfg->width * 4 : 0;  // c and wn
+  int blocks = grad_blocks(cfg, sms < kMostSms ? sms : kMostSms);
+  p.depth = ring_depth(rs, vec, cfg->rows, blocks, slot, vector_bytes);
+  if (p.depth > 0) {
+    sh = rs;
+    p.threads = sh.threads;
+    const int most = (cfg->rows + sh.groups - 1) / sh.groups;
+    if (blocks > most) blocks = most;
+  }
+  const unsigned threads = static_cast<unsigned>(sh.threads * sh.groups);
+  p.err = device_error_word();
+  // the groups' column sums take the rings' place in the end
+  const size_t column_sums =
+      vectors && sh.keep ? static_cast<size_t>(sh.groups - 1) * 2 * cfg->width * 4 : 0;
+  const size_t ring =
+      p.depth > 0 ? static_cast<size_t>(p.depth) * slot * sh.groups + vector_bytes : 0;
+  const size_t smem = ring > column_sums ? ring : column_sums;
   const unsigned grid = static_cast<unsigned>(blocks);
   const cudaError_t e =
       cfg->dtype == MOE_BF16
-          ? (vec ? launch_backward<__nv_bfloat16, true>(p, sh.keep, grid, threads, smem, s)
-                 : launch_backward<__nv_bfloat16, false>(p, sh.keep, grid, threads, smem, s))
-          : (vec ? launch_backward<float, true>(p, sh.keep, grid, threads, smem, s)
-                 : launch_backward<float, false>(p, sh.keep, grid, threads, smem, s));
+          ? launch_backward<__nv_bfloat16>(p, sh.keep, vec, grid, threads, smem, s)
+          : launch_backward<float>(p, sh.keep, vec, grid, threads, smem, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (!vectors) return MOE_OK;
   VectorParams v{};

@@ -11,9 +11,9 @@
 // the first, because the last ones read are what L2 still holds.
 //
 // Squares: eight elements are squared and added in float, and those sums added in pairs of floats
-// (the 64-bit units manage an addition per eight bf16 elements at two thirds of their rate, so
-// they join the chunks only).  Where a square would leave float's range (above 2^120, or the
-// largest element below 2^-55 and not 0) the eight are squared in 64 bits.  Bound by memory.
+// (an addition in 64 bits per eight bf16 elements would take two thirds of what the 64-bit units
+// can do).  Where a square would leave float's range (above 2^96, or the largest element below
+// 2^-55 and not 0) the eight are squared in 64 bits.  Bound by memory.
 #include <cmath>
 
 #include "common.cuh"
@@ -22,10 +22,11 @@
 namespace moe {
 namespace {
 
-constexpr int kPerLaunch = 512;   // tensors: 24 bytes each in the kernel's parameters
+constexpr int kPerLaunch = 512;  // tensors: 32 bytes each in the kernel's parameters
+constexpr int kFewTensors = 64;  // a list that short has a kernel with as short a parameter
 constexpr int kThreads = 512;
-constexpr int kChunk = 32768;     // elements
-constexpr int kBlocksPerSm = 4;   // of the sum, one partial sum each
+constexpr int kLeastChunk = 4096, kMostChunk = 32768;  // elements
+constexpr int kSumBlocks = 2, kScaleBlocks = 4;  // per SM; the sum wants registers for its loads
 constexpr int kMostBlocks = 1024;
 
 struct Entry {
@@ -34,27 +35,26 @@ struct Entry {
   int first_chunk;
   int types;  // bit 0: grad is bf16, bit 1: out is bf16
 };
-struct Batch {
-  Entry e[kPerLaunch];
-  // elements past a tensor's whole chunks are found from its size
-  long long size[kPerLaunch];
-};
+// CAP: tensors that a launch's list has room for.
+template <int CAP>
 struct ClipParams {
-  Batch batch;
+  Entry e[CAP];
+  long long size[CAP];
   double* parts;
   float* norm;
-  int tensors, chunks;
+  int tensors, chunks, chunk;
   int parts_before;  // partial sums of the launches before this one
   int parts_total;
   float scale, max_norm, eps;
 };
-static_assert(sizeof(ClipParams) <= 32764, "kernel parameters");
+static_assert(sizeof(ClipParams<kPerLaunch>) <= 32764, "kernel parameters");
 
-__device__ __forceinline__ int find(const ClipParams& p, int chunk) {
+template <int CAP>
+__device__ __forceinline__ int find(const ClipParams<CAP>& p, int chunk) {
   int lo = 0, hi = p.tensors;
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    if (p.batch.e[m].first_chunk <= chunk) lo = m;
+    if (p.e[m].first_chunk <= chunk) lo = m;
     else hi = m;
   }
   return lo;
@@ -87,11 +87,17 @@ struct Raw8 {
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// A thread's sum over a chunk: hi + lo is exact but for lo's own roundings (2^-48 of the sum),
-// `rest` takes what leaves float's range.
+// A thread's sum: hi + lo is exact but for lo's own roundings (2^-48 of the sum), `rest` takes what
+// leaves float's range.
 struct Squares {
   float hi = 0.f, lo = 0.f;
   double rest = 0.0;
+  // hi + lo += s + l
+  __device__ __forceinline__ void join(float s, float l) {
+    const float t = __fadd_rn(hi, s), b = __fsub_rn(t, hi);
+    lo += l + __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(s, b));
+    hi = t;
+  }
   __device__ __forceinline__ void add(const float (&v)[8]) {
     float most = 0.f, s = 0.f;
 #pragma unroll
@@ -99,25 +105,39 @@ struct Squares {
       most = fmaxf(most, fabsf(v[q]));
       s = fmaf(v[q], v[q], s);
     }
-    // (a NaN is not below the limit; a chunk has at most 64 such sums a thread)
-    if (s < 0x1p120f && (most > 0x1p-55f || most == 0.f)) {
-      const float t = __fadd_rn(hi, s), b = __fsub_rn(t, hi);
-      lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(s, b));
-      hi = t;
+    // (a NaN is not below the limit; 2^31 such sums stay below float's largest)
+    if (s < 0x1p96f && (most > 0x1p-55f || most == 0.f)) {
+      join(s, 0.f);
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         rest = fma(static_cast<double>(v[q]), static_cast<double>(v[q]), rest);
     }
   }
-  __device__ __forceinline__ double total() const {
-    return static_cast<double>(hi) + static_cast<double>(lo) + rest;
+  // the block's total, in thread 0
+  __device__ __forceinline__ double total() {
+    __shared__ double part[kThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+      join(h, l);
+    }
+    if (__any_sync(0xffffffffu, rest != 0.0)) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    }
+    if ((threadIdx.x & 31) == 0)
+      part[threadIdx.x >> 5] = static_cast<double>(hi) + static_cast<double>(lo) + rest;
+    __syncthreads();
+    double sum = 0.0;
+    if (threadIdx.x == 0)
+      for (int w = 0; w < kThreads / 32; ++w) sum += part[w];
+    return sum;
   }
 };
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* g, int n) {
-  Squares sum;
+__device__ __forceinline__ void chunk_squares(const T* g, int n, Squares& sum) {
   int done = 0;
   if ((reinterpret_cast<uintptr_t>(g) & 15u) == 0) {
     const int vecs = n / 8;
@@ -143,37 +163,26 @@ __device__ __forceinline__ double chunk_squares(const T* g, int n) {
     for (int q = 0; q < 8; ++q) v[q] = i + q * kThreads < n ? to_f(g[i + q * kThreads]) : 0.f;
     sum.add(v);
   }
-  return sum.total();
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double s[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v += s[w];
-  return v;
-}
-
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(
-    const __grid_constant__ ClipParams p) {
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kSumBlocks) grad_squares_kernel(
+    const __grid_constant__ ClipParams<CAP> p) {
   grid_dep_wait();
   grid_dep_trigger();
-  double sum = 0.0;
+  Squares sum;
   for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
     const int t = find(p, c);
-    const long long at = static_cast<long long>(c - p.batch.e[t].first_chunk) * kChunk;
-    const long long left = p.batch.size[t] - at;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
-    sum += p.batch.e[t].types & 1
-               ? chunk_squares(static_cast<const __nv_bfloat16*>(p.batch.e[t].grad) + at, n)
-               : chunk_squares(static_cast<const float*>(p.batch.e[t].grad) + at, n);
+    const long long at = static_cast<long long>(c - p.e[t].first_chunk) * p.chunk;
+    const long long left = p.size[t] - at;
+    const int n = static_cast<int>(left < p.chunk ? left : p.chunk);
+    if (p.e[t].types & 1)
+      chunk_squares(static_cast<const __nv_bfloat16*>(p.e[t].grad) + at, n, sum);
+    else
+      chunk_squares(static_cast<const float*>(p.e[t].grad) + at, n, sum);
   }
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) p.parts[p.parts_before + blockIdx.x] = sum;
+  const double total = sum.total();
+  if (threadIdx.x == 0) p.parts[p.parts_before + blockIdx.x] = total;
 }
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
@@ -218,26 +227,51 @@ __device__ __forceinline__ void chunk_scale(const T* g, O* out, int n, float f) 
   for (int i = done + threadIdx.x; i < n; i += kThreads) store1(out + i, to_f(g[i]) * f);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(
-    const __grid_constant__ ClipParams p) {
+// Newton's step in 64 bits from a float estimate, which doubles its 22 bits; far from 1 the
+// library's routines.
+__device__ __forceinline__ bool moderate(double v) { return v > 0x1p-100 && v < 0x1p100; }
+__device__ __forceinline__ double root_of(double v) {
+  if (!moderate(v)) return sqrt(v);
+  const double y = static_cast<double>(rsqrtf(static_cast<float>(v))), r = v * y;
+  return fma(fma(-r, r, v), 0.5 * y, r);
+}
+__device__ __forceinline__ double quotient(double a, double b) {
+  if (!moderate(a) || !moderate(b)) return a / b;
+  const double y = static_cast<double>(1.f / static_cast<float>(b)), q = a * y;
+  return fma(fma(-q, b, a), y, q);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(
+    const __grid_constant__ ClipParams<CAP> p) {
   grid_dep_wait();
   grid_dep_trigger();
-  double total = 0.0;
-  for (int i = threadIdx.x; i < p.parts_total; i += kThreads) total += p.parts[i];
-  total = block_sum(total);
-  const double norm = sqrt(total) * static_cast<double>(p.scale);
-  if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
-  if (p.chunks == 0) return;
-  const double room = static_cast<double>(p.max_norm) / (norm + static_cast<double>(p.eps));
-  // (a norm that is NaN makes the factor NaN; an infinite one makes it 0)
-  const float f = static_cast<float>(static_cast<double>(p.scale) * (room < 1.0 || room != room ? room : 1.0));
+  // One warp adds the partial sums and one thread takes the root: the 64-bit units do two
+  // operations a clock (in all 512 threads this took 6 us).
+  __shared__ float factor;
+  if (threadIdx.x < 32) {
+    double total = 0.0;
+    for (int i = threadIdx.x; i < p.parts_total; i += 32) total += p.parts[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (threadIdx.x == 0) {
+      const double norm = root_of(total) * static_cast<double>(p.scale);
+      if (p.norm != nullptr && blockIdx.x == 0) *p.norm = static_cast<float>(norm);
+      const double room = quotient(static_cast<double>(p.max_norm), norm + static_cast<double>(p.eps));
+      // (a norm that is NaN makes the factor NaN; an infinite one makes it 0)
+      factor = static_cast<float>(static_cast<double>(p.scale) *
+                                  (room < 1.0 || room != room ? room : 1.0));
+    }
+  }
+  __syncthreads();
+  const float f = factor;
   for (int c = p.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
     const int t = find(p, c);
-    const Entry& e = p.batch.e[t];
+    const Entry& e = p.e[t];
     if (f == 1.f && e.grad == e.out) continue;  // in place, nothing to change
-    const long long at = static_cast<long long>(c - e.first_chunk) * kChunk;
-    const long long left = p.batch.size[t] - at;
-    const int n = static_cast<int>(left < kChunk ? left : kChunk);
+    const long long at = static_cast<long long>(c - e.first_chunk) * p.chunk;
+    const long long left = p.size[t] - at;
+    const int n = static_cast<int>(left < p.chunk ? left : p.chunk);
     switch (e.types) {
       case 0:
         chunk_scale(static_cast<const float*>(e.grad) + at, static_cast<float*>(e.out) + at, n, f);
@@ -278,6 +312,78 @@ moe_status_t check_tensors(const moe_grad_t* grads, int n) {
 
 inline long long launches_for(int n) { return n == 0 ? 1 : (n + kPerLaunch - 1) / kPerLaunch; }
 
+template <int CAP>
+moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float max_norm, float eps,
+                      float* norm, void* ws, cudaStream_t s) {
+  const int sms = device_num_sms();
+  auto blocks_of = [&](int chunks, int per_sm) {
+    const int most = sms * per_sm < kMostBlocks ? sms * per_sm : kMostBlocks;
+    return chunks < most ? (chunks > 0 ? chunks : 1) : most;
+  };
+  const long long launches = n == 0 ? 1 : (n + CAP - 1) / CAP;
+  ClipParams<CAP> p;
+  p.parts = static_cast<double*>(ws);
+  p.scale = grad_scale;
+  p.max_norm = max_norm;
+  p.eps = eps;
+  // chunks small enough that a short list fills the blocks (23 tensors of 300 K elements: 18.0 us
+  // with 32768 elements, 9.9 with 4096), large enough that a block seldom looks for its tensor
+  long long total = 0;
+  for (int i = 0; i < n; ++i) total += grads[i].size;
+  p.chunk = kLeastChunk;
+  while (p.chunk < kMostChunk && total / p.chunk > 32ll * sms) p.chunk *= 2;
+  // one batch of the list: tensors with elements, and with results where `scaling`
+  auto fill = [&](long long batch, bool scaling) -> bool {
+    p.tensors = 0;
+    long long chunks = 0;
+    const int end = static_cast<int>((batch + 1) * CAP < n ? (batch + 1) * CAP : n);
+    for (int i = static_cast<int>(batch * CAP); i < end; ++i) {
+      const moe_grad_t& g = grads[i];
+      if (g.size == 0 || (scaling && g.out == nullptr)) continue;
+      Entry& e = p.e[p.tensors];
+      e.grad = g.grad;
+      e.out = g.out;
+      e.first_chunk = static_cast<int>(chunks);
+      e.types = (g.dtype == MOE_BF16 ? 1 : 0) | (g.out_dtype == MOE_BF16 ? 2 : 0);
+      p.size[p.tensors++] = g.size;
+      chunks += (g.size + p.chunk - 1) / p.chunk;
+      if (chunks >= (1ll << 30)) return false;
+    }
+    p.chunks = static_cast<int>(chunks);
+    return true;
+  };
+  for (long long b = 0; b < launches; ++b)
+    if (!fill(b, false)) return MOE_ERR_UNSUPPORTED;
+  int parts = 0;
+  for (long long b = 0; b < launches; ++b) {
+    fill(b, false);
+    p.norm = nullptr;
+    p.parts_before = parts;
+    p.parts_total = 0;
+    if (p.chunks == 0) continue;
+    const int blocks = blocks_of(p.chunks, kSumBlocks);
+    if (launch_pdl(grad_squares_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                   s, p) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    parts += blocks;
+  }
+  // scaled last list first, for what L2 still holds; the first launch writes the norm
+  float* out = norm;
+  for (long long b = launches - 1; b >= 0; --b) {
+    fill(b, true);
+    if (p.chunks == 0 && (out == nullptr || b > 0)) continue;
+    p.norm = out;
+    p.parts_before = 0;
+    p.parts_total = parts;
+    const int blocks = blocks_of(p.chunks, kScaleBlocks);
+    if (launch_pdl(grad_scale_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
+                   p) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    out = nullptr;
+  }
+  return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -306,68 +412,12 @@ extern "C" moe_status_t moe_clip_grad_norm(const moe_grad_t* grads, int n, float
   for (int i = 0; i < n; ++i) any_out |= grads[i].out != nullptr && grads[i].size > 0;
   if (norm == nullptr && !any_out) return MOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(norm) % 4 != 0) return MOE_ERR_MISALIGNED;
-  const long long launches = launches_for(n);
-  if (ws == nullptr || ws_bytes < static_cast<size_t>(launches) * kMostBlocks * sizeof(double))
+  if (ws == nullptr || ws_bytes < static_cast<size_t>(launches_for(n)) * kMostBlocks * sizeof(double))
     return MOE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) return MOE_ERR_MISALIGNED;
   st = check_current_device();
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = device_num_sms();
-  const int most = sms * kBlocksPerSm < kMostBlocks ? sms * kBlocksPerSm : kMostBlocks;
-  ClipParams p;
-  p.parts = static_cast<double*>(ws);
-  p.scale = grad_scale;
-  p.max_norm = max_norm;
-  p.eps = eps;
-  // one batch of the list: tensors with elements, and with results where `scaling`
-  auto fill = [&](long long batch, bool scaling) -> bool {
-    p.tensors = 0;
-    long long chunks = 0;
-    const int end = static_cast<int>((batch + 1) * kPerLaunch < n ? (batch + 1) * kPerLaunch : n);
-    for (int i = static_cast<int>(batch * kPerLaunch); i < end; ++i) {
-      const moe_grad_t& g = grads[i];
-      if (g.size == 0 || (scaling && g.out == nullptr)) continue;
-      Entry& e = p.batch.e[p.tensors];
-      e.grad = g.grad;
-      e.out = g.out;
-      e.first_chunk = static_cast<int>(chunks);
-      e.types = (g.dtype == MOE_BF16 ? 1 : 0) | (g.out_dtype == MOE_BF16 ? 2 : 0);
-      p.batch.size[p.tensors++] = g.size;
-      chunks += (g.size + kChunk - 1) / kChunk;
-      if (chunks >= (1ll << 30)) return false;
-    }
-    p.chunks = static_cast<int>(chunks);
-    return true;
-  };
-  for (long long b = 0; b < launches; ++b)
-    if (!fill(b, false)) return MOE_ERR_UNSUPPORTED;
-  int parts = 0;
-  for (long long b = 0; b < launches; ++b) {
-    fill(b, false);
-    p.norm = nullptr;
-    p.parts_before = parts;
-    p.parts_total = 0;
-    const int blocks = p.chunks < most ? p.chunks : most;
-    if (blocks == 0) continue;
-    if (launch_pdl(grad_squares_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
-                   p) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    parts += blocks;
-  }
-  // scaled last list first, for what L2 still holds; the first launch writes the norm
-  float* out = norm;
-  for (long long b = launches - 1; b >= 0; --b) {
-    fill(b, true);
-    if (p.chunks == 0 && (out == nullptr || b > 0)) continue;
-    p.norm = out;
-    p.parts_before = 0;
-    p.parts_total = parts;
-    const int blocks = p.chunks < most ? (p.chunks > 0 ? p.chunks : 1) : most;
-    if (launch_pdl(grad_scale_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
-                   p) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    out = nullptr;
-  }
-  return MOE_OK;
+  return n <= kFewTensors ? run_clip<kFewTensors>(grads, n, grad_scale, max_norm, eps, norm, ws, s)
+                          : run_clip<kPerLaunch>(grads, n, grad_scale, max_norm, eps, norm, ws, s);
 }
