@@ -15,7 +15,7 @@ enum class GroupedKind : int {
 struct GroupPlan {
   int* bounds;    // [groups + 1], the offsets clamped to ascend within 0..rows
   int4* tiles;    // per tile of rows: {group, first row of its chunk, first tile of its chunk,
-                  //                    tiles in its chunk}
+                  //                    tiles in its chunk | rows of each << 4}
   int* count;     // tiles of rows
   void* maps;     // tensor maps of every group's rows, [groups][2], or null
 };

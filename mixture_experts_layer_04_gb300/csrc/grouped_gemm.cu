@@ -13,8 +13,9 @@
 //    the next group (a row of the result depends on its own row of A alone) and are not stored.
 //  - The reduction of the weight gradient must end with the group: what follows may be another
 //    group's infinity or NaN, so masking one operand would not do.  Every group has its own pair
-//    of tensor maps, copies of the call's map whose number of rows is the group's end: TMA then
-//    fills the rest of the last block with zeros.  The plan kernel writes them.
+//    of tensor maps, copies of the call's maps whose number of rows is the group's end: TMA then
+//    fills the rest of the block that the end cuts with zeros.  The plan kernel writes them; the
+//    blocks before the last use the call's own.
 //  - A float32 result leaves the tensor core every 256 values (float32 operands, six products per
 //    value: 128), a bf16 one every 16384, and is added up in registers: the tensor core truncates
 //    its additions.
@@ -37,6 +38,7 @@ namespace {
 constexpr int BK = 64;
 constexpr int kMaxChunk = 256;  // k-blocks per accumulator of a bf16 result
 constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
+constexpr int kWideRows = 256, kWideStep = 32;  // rows of a tile of grouped_wide_kernel
 
 // PA, PB: bf16 parts per value on the A and on the B side.
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
@@ -60,6 +62,8 @@ struct GroupedCfg {
 struct GroupedParams {
   CUtensorMap tm_a, tm_b;  // as the sides of the tile: with swapped sides A is the weights
   CUtensorMap tm_c, tm_z;
+  CUtensorMap tm_rows[3];  // wide kernel: B's map with boxes of 64, 32 and 16 rows (tm_b: 128)
+  int w_blocks;            // wide kernel, swiglu: tm_a takes both halves' blocks of 16 rows
   GroupPlan plan;
   GroupedKind kind;
   int groups, num_kb, chunk;
@@ -78,7 +82,9 @@ struct GroupedParams {
 
 struct Tile {
   int group, row0, row_end, feat0;
+  int rows;        // of the tile (forward and input gradient)
   int k0, num_kb;  // first row of the reduction (weight gradient), k-blocks
+  int cut_kb;      // the block that the group's end cuts (weight gradient), or -1
 };
 
 template <typename Cfg>
@@ -95,16 +101,19 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx) {
   if (p.kind != GroupedKind::kWeightGrad) {
     const int4 e = __ldg(p.plan.tiles + idx / p.tiles_b);
     const int in = idx - e.z * p.tiles_b;
-    const int f = in / e.w;
+    const int tiles = e.w & 15, f = in / tiles;
     t.group = e.x;
-    t.row0 = e.y + (in - f * e.w) * Cfg::kTileRows;
+    t.rows = e.w >> 4;
+    t.row0 = e.y + (in - f * tiles) * t.rows;
     t.row_end = __ldg(p.plan.bounds + e.x + 1);
     t.feat0 = f * step;
     t.k0 = 0;
     t.num_kb = p.num_kb;
+    t.cut_kb = -1;
   } else {
     const int per = p.tiles_a * p.tiles_b;
     t.group = idx / per;
+    t.rows = 0;
     const int in = idx - t.group * per;
     const int c = in / (kRowChunk * p.tiles_b);
     const int rest = in - c * kRowChunk * p.tiles_b;
@@ -114,7 +123,9 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx) {
     t.row_end = p.rows;
     t.feat0 = f * step;
     t.k0 = __ldg(p.plan.bounds + t.group);
-    t.num_kb = (__ldg(p.plan.bounds + t.group + 1) - t.k0 + BK - 1) / BK;
+    const int size = __ldg(p.plan.bounds + t.group + 1) - t.k0;
+    t.num_kb = (size + BK - 1) / BK;
+    t.cut_kb = size % BK != 0 ? t.num_kb - 1 : -1;
   }
   return t;
 }
@@ -162,6 +173,9 @@ __device__ __forceinline__ void bulk_commit() {
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -198,6 +212,26 @@ struct Out {
   int cols, third, is_z, tma, vec;
 };
 
+// Rows first.. of a staged piece (`count` of them, a multiple of 4) to memory, eight lanes to a row.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const Out& o, const uint8_t* stg, int lane, int first,
+                                          int count, int row0, int row_end, int col) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  const int piece = lane & 7, c = col + piece * N;
+  const int n = min(N, o.cols - c);
+#pragma unroll 1
+  for (int r = first + (lane >> 3); r < first + count; r += 4) {
+    if (row0 + r >= row_end || n <= 0) break;
+    const uint8_t* src = stg + r * 128 + ((piece ^ (r & 7)) << 4);
+    T* dst = reinterpret_cast<T*>(o.base) + static_cast<long long>(row0 + r) * o.ld + c;
+    if (o.vec && n == N) {
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+    } else {
+      for (int q = 0; q < n; ++q) dst[q] = reinterpret_cast<const T*>(src)[q];
+    }
+  }
+}
+
 // The staged piece to rows row0.. (below row_end) and columns col.. of the output: by TMA where
 // all 32 rows are the group's, else by the lanes, eight to a row.  TMA clips columns past the end
 // in 16-byte steps only: a row that ends inside one is left to the lanes.
@@ -215,18 +249,25 @@ __device__ __forceinline__ void put_piece(const Out& o, uint8_t* stg, int lane, 
     return;
   }
   __syncwarp();
-  const int piece = lane & 7, c = col + piece * N;
-  const int n = min(N, o.cols - c);
-#pragma unroll 1
-  for (int r = lane >> 3; r < 32; r += 4) {
-    if (row0 + r >= row_end || n <= 0) break;
-    const uint8_t* src = stg + r * 128 + ((piece ^ (r & 7)) << 4);
-    T* dst = reinterpret_cast<T*>(o.base) + static_cast<long long>(row0 + r) * o.ld + c;
-    if (o.vec && n == N) {
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-    } else {
-      for (int q = 0; q < n; ++q) dst[q] = reinterpret_cast<const T*>(src)[q];
-    }
+  copy_rows<T>(o, stg, lane, 0, 32, row0, row_end, col);
+}
+
+// A step of the wide kernel in float: the fragments of 32 rows (columns of the accumulator) and 16
+// or 32 lanes, lane f of them at float f0 + f of a row of the piece.
+__device__ __forceinline__ void put_f32(uint8_t* at, int lane, int f0, const float (&v)[32],
+                                        int lanes) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (16 * half >= lanes) break;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // e & 1: the row, e >> 1: lanes 8 on
+        const int f = f0 + 16 * half + 8 * (e >> 1) + (lane >> 2);
+        const int row = 8 * j + 2 * (lane & 3) + (e & 1);
+        *reinterpret_cast<float*>(at + row * 128 + (((f >> 2) ^ (row & 7)) << 4) + (f & 3) * 4) =
+            v[16 * half + 4 * j + e];
+      }
   }
 }
 
@@ -265,10 +306,8 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    if (p.kind != GroupedKind::kWeightGrad) {
-      tma_prefetch_desc(&p.tm_a);
-      tma_prefetch_desc(&p.tm_b);
-    }
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
     tma_prefetch_desc(&p.tm_c);
   }
   if (warp == 1) {
@@ -301,23 +340,15 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
-      int map_group = -1;
-      const CUtensorMap* tm_a = &p.tm_a;
-      const CUtensorMap* tm_b = &p.tm_b;
       for (int idx = first; ok && idx < total; idx += step) {
         const Tile t = tile_at<Cfg>(p, idx);
+        const CUtensorMap* tm_a = &p.tm_a;
+        const CUtensorMap* tm_b = &p.tm_b;
         int a_row, b_row, a_third, b_third;
         if (p.kind == GroupedKind::kWeightGrad) {
           a_row = t.row0 + static_cast<int>(rank) * 128;
           b_row = t.feat0 + static_cast<int>(rank) * Cfg::kBRows;
           a_third = b_third = 0;
-          if (t.group != map_group && t.num_kb > 0) {
-            map_group = t.group;
-            tm_a = static_cast<const CUtensorMap*>(p.plan.maps) + 2 * t.group;
-            tm_b = tm_a + 1;
-            acquire_map(tm_a);
-            acquire_map(tm_b);
-          }
         } else if constexpr (SWAP) {
           a_row = t.feat0;
           b_row = t.row0;
@@ -335,6 +366,12 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
+          }
+          if (kb == t.cut_kb) {
+            tm_a = static_cast<const CUtensorMap*>(p.plan.maps) + 2 * t.group;
+            tm_b = tm_a + 1;
+            acquire_map(tm_a);
+            acquire_map(tm_b);
           }
           const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
           const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
@@ -594,6 +631,385 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
   if constexpr (CTAS == 2) cluster_sync_all();  // the pair gives its TMEM back before either leaves
 }
 
+// ------------------------------------------- weights on the side of 256 (pairs) ----
+
+// The forward and the input gradient of groups with many rows.  A CTA pair's tile is 256 features
+// (the weights are the MMA's A side) times a group's share of up to 256 rows in steps of 32: the
+// MMA's N follows the group, so a group of 524 rows costs three tiles of 192 instead of three of
+// 256.  Per stage 16 KB of weights and up to 16 KB (two parts: 32 KB) of rows in each CTA.
+//
+// The accumulator has features in its lanes and rows in its columns.  The epilogue reads it in 16 x
+// 8 fragments and stores them transposed (stmatrix), 32 rows at a time, into 128-byte rows that TMA
+// takes to memory; four warps (one per 32 lanes) share a piece, two such sets take turns.  With
+// swiglu every 32 lanes are 16 gate features and the same 16 up features, so a thread has both.
+template <int PB>
+struct WideCfg {
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kABytes = 128 * BK * 2, kBBytes = 128 * BK * 2;
+  static constexpr int kStageBytes = kABytes + PB * kBBytes;
+  static constexpr int kStgBytes = 2 * 16384;  // a set of warps: two pieces of 8 KB, or one of 16
+  static constexpr int kBarBytes = 256;
+  static constexpr int kStages = (232448 - 1024 - kBarBytes - kStgBytes) / kStageBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
+  static constexpr int kTileRows = kWideRows, kTileFeatures = 256;
+  static constexpr int kTmemCols = 512;
+};
+
+// Four 8 x 8 matrices of 16-bit values, transposed: thread t holds of matrix i the values
+// (row 2 (t % 4), column t / 4) and (row 2 (t % 4) + 1, column t / 4) in r[i] and gives, for
+// i = t / 8, the address of row t % 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Whether `ok` holds in all of the 128 threads that call it with barrier `id`.
+__device__ __forceinline__ bool all_of_set(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, %2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "r"(id)
+      : "memory");
+  return all != 0;
+}
+
+template <int PB>
+__global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
+    grouped_wide_kernel(const __grid_constant__ GroupedParams p) {
+  using Cfg = WideCfg<PB>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* stg_all = smem + S * Cfg::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stg_all + Cfg::kStgBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t mma_done_bar = bar0 + 8u * (2 * S + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * Cfg::kEpiWarps);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+    tma_prefetch_desc(&p.tm_c);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total = total_tiles<Cfg>(p);
+  const int first = static_cast<int>(blockIdx.x) >> 1, step = static_cast<int>(gridDim.x) >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer ----
+    const bool leader = elect_one_sync();
+    int stage = 0, issued = 0;  // (issued stops counting at S)
+    uint32_t phase = 0;
+    if (leader) {
+      bool ok = true;
+      for (int idx = first; ok && idx < total; idx += step) {
+        const Tile t = tile_at<Cfg>(p, idx);
+        const int mine = t.rows >> 1;  // rows that this CTA loads
+        const int x_row = t.row0 + rank * mine;
+        const int w_row = t.feat0 + rank * (p.swiglu ? 64 : 128);
+        const uint32_t bytes = static_cast<uint32_t>(2 * Cfg::kABytes + PB * t.rows * 128);
+        for (int kb = 0; kb < t.num_kb; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const uint32_t da = smem_u32(smem) + stage * Cfg::kStageBytes, db = da + Cfg::kABytes;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), bytes);
+          const int k = kb * BK;
+          if (p.w_blocks) {
+            tma_load_5d_pair(da, &p.tm_a, fb, k, 0, 0, w_row >> 4, t.group);
+          } else if (p.swiglu) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              tma_load_3d_pair(da + q * 4096u, &p.tm_a, fb, k, w_row + 16 * q, t.group);
+              tma_load_3d_pair(da + q * 4096u + 2048u, &p.tm_a, fb, k, p.features + w_row + 16 * q,
+                               t.group);
+            }
+          } else {
+            load_rows<2, 128>(da, &p.tm_a, fb, p.a_mn, w_row, k, t.group);
+          }
+#pragma unroll
+          for (int pl = 0; pl < PB; ++pl) {
+            const uint32_t dx = db + pl * Cfg::kBBytes;
+            if (mine == 128) {
+              tma_load_3d_pair(dx, &p.tm_b, fb, k, x_row, pl);
+            } else {  // 64, 32 and 16 rows as the share has them
+              int r = 0;
+#pragma unroll
+              for (int b = 0; b < 3; ++b)
+                if (mine & (64 >> b)) {
+                  tma_load_3d_pair(dx + r * 128u, &p.tm_rows[b], fb, k, x_row + r, pl);
+                  r += 64 >> b;
+                }
+            }
+          }
+          issued = min(issued + 1, S);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    // (both CTAs' loads complete on the even CTA's barriers)
+    drain_stages<S>(leader, lane, stage, phase, issued, empty_bar, full_bar, rank == 0, abort_flag,
+                    p.err);
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA ----
+    if (rank == 0 && elect_one_sync()) {
+      const uint32_t a_step = p.a_mn ? 2048u : 32u;
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;  // accumulators filled
+      bool ok = true;
+      for (int idx = first; ok && idx < total; idx += step) {
+        const Tile t = tile_at<Cfg>(p, idx);
+        const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(p.a_mn) << 15) |
+                               (static_cast<uint32_t>(t.rows >> 3) << 17);
+        for (int kb = 0; ok && kb < t.num_kb; ++local) {
+          const int acc = local & 1;
+          if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
+                         p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * 256);
+          const int end = min(t.num_kb, kb + p.chunk);
+          uint32_t accumulate = 0;
+          for (; kb < end; ++kb) {
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(smem) + stage * Cfg::kStageBytes;
+            const uint32_t b_base = a_base + Cfg::kABytes;
+#pragma unroll
+            for (int pl = PB - 1; pl >= 0; --pl) {  // the smaller part first
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                tc_mma_bf16_pair(d, operand_desc(a_base + kk * a_step, p.a_mn),
+                                 operand_desc(b_base + pl * Cfg::kBBytes + kk * 32u, 0), idesc,
+                                 accumulate);
+                accumulate = 1u;
+              }
+            }
+            tc_commit_pair(empty_bar(stage), 0x3);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) tc_commit_pair(tfull_bar(acc), 0x3);
+        }
+      }
+      if (!ok || *abort_flag) {
+        tc_commit_pair(mma_done_bar, 0x1);
+        volatile int no_abort = 0;
+        mbar_wait(mma_done_bar, 0, &no_abort, p.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue ----
+    const int quad = warp & 3, set = (warp - 2) >> 2;
+    uint8_t* stg_set = stg_all + set * 16384;
+    const bool issuer = threadIdx.x == static_cast<unsigned>(64 + set * 128);
+    auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(set + 1) : "memory"); };
+    const bool big = p.c_f32 && !p.swiglu;  // pieces of 16 KB, one at a time
+    int turn = 0;
+    int local = 0;  // accumulators read
+    for (int idx = first; idx < total; idx += step) {
+      const Tile t = tile_at<Cfg>(p, idx);
+      float sum[4][32];  // per 32 rows: lanes 0-15, then 16-31, as tmem_ld_16x256b_x4 has them
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 32; ++q) sum[i][q] = 0.f;
+      bool ok = true;
+      for (int kb = 0; kb < t.num_kb; kb += p.chunk, ++local) {
+        const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
+                                     abort_flag, p.err);
+        ok = !__any_sync(0xffffffffu, !ready);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                             static_cast<uint32_t>((local & 1) * 256);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = (2 * i + set) * 32;
+          if (col < t.rows) {
+            uint32_t lo[16], hi[16];
+            tmem_ld_16x256b_x4(acc + col, lo);
+            tmem_ld_16x256b_x4(acc + col + (16u << 16), hi);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              sum[i][q] += __uint_as_float(lo[q]);
+              sum[i][16 + q] += __uint_as_float(hi[q]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(local & 1), 0));
+      }
+      // a set's warps meet below, so they give up together
+      if (!all_of_set(set + 1, ok)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row0 = t.row0 + (2 * i + set) * 32;
+        if ((2 * i + set) * 32 >= t.rows || row0 >= t.row_end) continue;
+        const bool whole = row0 + 32 <= t.row_end;
+        // The next piece's staging, free of the store that used it last.
+        auto begin = [&]() -> uint8_t* {
+          if (issuer) {
+            if (big) bulk_wait_read();
+            else bulk_wait_read_but_one();
+          }
+          meet();
+          uint8_t* at = stg_set + (big ? 0 : (turn & 1) * 8192);
+          ++turn;
+          return at;
+        };
+        // Boxes of 128 bytes x 32 rows at `at`, to columns col0, col0 + width, ...
+        auto finish = [&](const Out& o, uint8_t* at, int boxes, int col0, auto type, bool halves) {
+          using T = decltype(type);
+          constexpr int N = 16 / static_cast<int>(sizeof(T)), kWidth = 8 * N;
+          fence_async_shared();
+          meet();
+          for (int b = 0; b < boxes; ++b) {
+            Out ob = o;
+            int col = col0 + b * kWidth;
+            if (halves) {  // box b is z's half b
+              col = col0;
+              ob.third = b;
+              ob.base += b * static_cast<long long>(o.cols) * static_cast<long long>(sizeof(T));
+            }
+            if (col >= o.cols) continue;
+            const bool tma = whole && o.tma && (col + kWidth <= o.cols || o.cols % N == 0);
+            if (tma) {
+              if (issuer)
+                tma_store_3d(o.map, smem_u32(at + b * 4096), col, o.is_z ? ob.third : row0,
+                             o.is_z ? row0 : ob.third);
+            } else {
+              copy_rows<T>(ob, at + b * 4096, lane, quad * 8, 8, row0, t.row_end, col);
+            }
+          }
+          if (issuer) bulk_commit();
+        };
+        // 32 rows x 32 lanes in bf16: `chunk` is the place of 8 lanes among a row's 16-byte pieces
+        auto put_bf16 = [&](uint8_t* at, int box, int chunk, uint32_t (&m)[4], int row) {
+          // (box and chunk are those of the matrix whose row this thread addresses)
+          const uint32_t addr = smem_u32(at) + box * 4096u + row * 128u +
+                                (static_cast<uint32_t>(chunk ^ (row & 7)) << 4);
+          stmatrix_x4_trans(addr, m[0], m[1], m[2], m[3]);
+        };
+        const int mat = lane >> 3, in = lane & 7;
+        if (!p.swiglu) {
+          Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
+          const int col0 = t.feat0 + rank * 128;
+          uint8_t* at = begin();
+          if (!p.c_f32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
+                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
+                               pack2(sum[i][16 + 4 * j], sum[i][17 + 4 * j]),
+                               pack2(sum[i][18 + 4 * j], sum[i][19 + 4 * j])};
+              put_bf16(at, quad >> 1, (quad & 1) * 4 + mat, m, 8 * j + in);
+            }
+            finish(oc, at, 2, col0, __nv_bfloat16{}, false);
+          } else {
+            put_f32(at + quad * 4096, lane, 0, sum[i], 32);
+            finish(oc, at, 4, col0, float{}, false);
+          }
+        } else {
+          const int col0 = t.feat0 + rank * 64;
+          if (p.z != nullptr) {
+            Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
+            uint8_t* at = begin();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
+                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
+                               pack2(sum[i][16 + 4 * j], sum[i][17 + 4 * j]),
+                               pack2(sum[i][18 + 4 * j], sum[i][19 + 4 * j])};
+              put_bf16(at, mat >> 1, quad * 2 + (mat & 1), m, 8 * j + in);
+            }
+            finish(oz, at, 2, col0, __nv_bfloat16{}, true);
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            sum[i][q] = act_value<true>(MOE_ACT_SILU, sum[i][q]) * sum[i][16 + q];
+          Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
+          uint8_t* at = begin();
+          if (!p.c_f32) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {  // 16 rows x 16 features
+              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
+                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
+                               pack2(sum[i][4 * j + 4], sum[i][4 * j + 5]),
+                               pack2(sum[i][4 * j + 6], sum[i][4 * j + 7])};
+              put_bf16(at, 0, quad * 2 + (mat & 1), m, 8 * (j + (mat >> 1)) + in);
+            }
+            finish(oc, at, 1, col0, __nv_bfloat16{}, false);
+          } else {
+            put_f32(at + (quad >> 1) * 4096, lane, (quad & 1) * 16, sum[i], 16);
+            finish(oc, at, 2, col0, float{}, false);
+          }
+        }
+      }
+    }
+    if (issuer) bulk_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no peer still reads this CTA's shared memory or arrives on it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+  __syncwarp();
+  cluster_sync_all();  // the pair gives its TMEM back before either CTA leaves
+}
+
 // ---------------------------------------------------------------------- plan ----
 
 struct PlanParams {
@@ -659,8 +1075,13 @@ __global__ void __launch_bounds__(kPlanThreads) group_plan_kernel(
       }
       const int end = lo + 1 < kPlanThreads ? s_first[lo + 1] : total;
       const int chunk = s_first[lo] + (i - s_first[lo]) / kRowChunk * kRowChunk;
-      p.plan.tiles[i] = make_int4(lo, s_bound[lo] + (chunk - s_first[lo]) * p.tile_rows, chunk,
-                                  min(kRowChunk, end - chunk));
+      // rows of the group's tiles: even shares, where a tile need not be full
+      const int tiles = end - s_first[lo], size = s_bound[lo + 1] - s_bound[lo];
+      const int rows = p.tile_rows == kWideRows
+                           ? ((size + tiles - 1) / tiles + kWideStep - 1) / kWideStep * kWideStep
+                           : p.tile_rows;
+      p.plan.tiles[i] = make_int4(lo, s_bound[lo] + (chunk - s_first[lo]) * rows, chunk,
+                                  min(kRowChunk, end - chunk) | rows << 4);
     }
   }
   if (p.plan.maps == nullptr) return;
@@ -715,6 +1136,29 @@ bool operand_map(CUtensorMap* m, const void* base, long long inner, long long ou
   return encode(m, false, base, dims, strides, BK, box_rows, 1);
 }
 
+// A swiglu layer's weights as [groups][blocks of 16][halves][16][inner], boxes of four blocks of both
+// halves: 16 gate rows, the same 16 up rows, and so on.
+bool halves_map(CUtensorMap* m, const GroupedProduct& g) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t ld = static_cast<cuuint64_t>(g.ldb) * 2, half = ld * g.features;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(g.depth), 16, 2,
+                              static_cast<cuuint64_t>(g.features / 16),
+                              static_cast<cuuint64_t>(g.groups)};
+  const cuuint64_t strides[4] = {ld, half, 16 * ld, 2 * half};
+  const cuuint32_t box[5] = {BK, 16, 2, 4, 1}, estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(g.b), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand of the weight gradient, row-contiguous: [parts][rows][inner], boxes of 64 x 64.
+bool rows_map(CUtensorMap* m, const GroupedProduct& g, bool a) {
+  return a ? operand_map(m, g.a, g.rows, g.total_rows, g.a_parts, g.lda, g.a_plane, BK)
+           : operand_map(m, g.b, g.features, g.total_rows, g.b_parts, g.ldb, g.b_plane, BK);
+}
+
 // An output as dims[2] x dims[1] x dims[0] values with strides (in values) of the outer two, boxes
 // of 128 bytes x 32 rows, the rows dimension `row_dim`; false if TMA cannot take it.
 bool output_map(CUtensorMap* m, bool f32, const void* base, const long long (&dims)[3],
@@ -734,9 +1178,32 @@ inline bool vec_ok(const void* p, long long ld, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * bytes % 16 == 0;
 }
 
-template <int CTAS, int BN, int PA, int PB, bool SWAP>
-cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
-  using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
+// How a kernel's tile lies: rows and features of it, and the boxes that its operands are loaded in.
+struct TileShape {
+  int rows, features;        // of a tile (swiglu: twice the features of C)
+  bool swap;                 // the weights are operand A
+  int x_box, w_box, w_box_swiglu;
+  int ctas, threads, smem;
+  bool staged;               // C and z leave by TMA
+};
+
+template <typename Cfg, int CTAS, int BN, bool SWAP>
+constexpr TileShape plain_shape() {
+  return TileShape{Cfg::kTileRows, Cfg::kTileFeatures, SWAP, SWAP ? BN : 128,
+                   SWAP ? 128 : Cfg::kBRows,
+                   SWAP ? 16 : CTAS == 1 ? Cfg::kBRows / 2 : Cfg::kBRows,
+                   CTAS, Cfg::kThreads, Cfg::kSmem, !SWAP};
+}
+template <int PB>
+constexpr TileShape wide_shape() {
+  using Cfg = WideCfg<PB>;
+  return TileShape{kWideRows, Cfg::kTileFeatures, true, 128, 128, 16, 2, Cfg::kThreads, Cfg::kSmem,
+                   true};
+}
+
+template <typename K>
+cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long>* done,
+                   GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
   const bool weight_grad = g.kind == GroupedKind::kWeightGrad;
   const long long rows = g.total_rows;
   if (!weight_grad) {
@@ -744,26 +1211,27 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
     const bool mn = g.kind == GroupedKind::kInputGrad;
     const long long w_rows = mn ? g.depth : g.swiglu ? 2ll * g.features : g.features;
     const long long w_inner = mn ? g.features : g.depth;
-    const int w_side = SWAP ? 128 : Cfg::kBRows;
-    const int w_box = mn ? BK : g.swiglu && SWAP ? 16 : g.swiglu && CTAS == 1 ? w_side / 2 : w_side;
-    const int x_box = SWAP ? BN : 128;
-    CUtensorMap* tx = SWAP ? &p->tm_b : &p->tm_a;
-    CUtensorMap* tw = SWAP ? &p->tm_a : &p->tm_b;
-    if (!operand_map(tx, g.a, g.depth, rows, g.a_parts, g.lda, g.a_plane, x_box) ||
-        !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.b_parts) * g.groups, g.ldb,
-                     g.ldb * w_rows, w_box))
+    const int w_box = mn ? BK : g.swiglu ? ts.w_box_swiglu : ts.w_box;
+    CUtensorMap* tx = ts.swap ? &p->tm_b : &p->tm_a;
+    CUtensorMap* tw = ts.swap ? &p->tm_a : &p->tm_b;
+    if (!operand_map(tx, g.a, g.depth, rows, g.a_parts, g.lda, g.a_plane, ts.x_box))
       return cudaErrorInvalidValue;
-    (SWAP ? p->a_mn : p->b_mn) = mn;
-    p->a_step = SWAP ? g.groups : 1;
-    p->b_step = SWAP ? 1 : g.groups;
+    if (p->w_blocks ? !halves_map(tw, g)
+                    : !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.b_parts) * g.groups, g.ldb,
+                                   g.ldb * w_rows, w_box))
+      return cudaErrorInvalidValue;
+    (ts.swap ? p->a_mn : p->b_mn) = mn;
+    p->a_step = ts.swap ? g.groups : 1;
+    p->b_step = ts.swap ? 1 : g.groups;
     p->num_kb = ceil_div(g.depth, BK);
   } else {
+    if (!rows_map(&p->tm_a, g, true) || !rows_map(&p->tm_b, g, false)) return cudaErrorInvalidValue;
     p->a_mn = p->b_mn = 1;
     p->a_step = p->b_step = 1;
-    p->tiles_a = ceil_div(g.rows, Cfg::kTileRows);
+    p->tiles_a = ceil_div(g.rows, ts.rows);
   }
-  p->tiles_b = ceil_div(g.features, g.swiglu ? Cfg::kTileFeatures / 2 : Cfg::kTileFeatures);
-  if (!SWAP) {
+  p->tiles_b = ceil_div(g.features, g.swiglu ? ts.features / 2 : ts.features);
+  if (ts.staged) {
     const long long c_rows = weight_grad ? g.rows : rows;
     p->tma_c = output_map(&p->tm_c, g.c_f32, g.c, {g.features, c_rows, weight_grad ? g.groups : 1},
                           {g.ldc, weight_grad ? g.c_group : g.ldc * c_rows}, 1);
@@ -775,23 +1243,21 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
   p->vec_z = vec_ok(g.z, g.ldz, g.z_f32 ? 4 : 2) && g.features * (g.z_f32 ? 4 : 2) % 16 == 0;
   const long long bound =
       weight_grad ? static_cast<long long>(g.groups) * p->tiles_a * p->tiles_b
-                  : static_cast<long long>(grouped_max_tiles(g.total_rows, g.groups, Cfg::kTileRows)) *
+                  : static_cast<long long>(grouped_max_tiles(g.total_rows, g.groups, ts.rows)) *
                         p->tiles_b;
   if (bound >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
-  auto kernel = grouped_kernel<CTAS, BN, PA, PB, SWAP>;
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(kernel, Cfg::kSmem, &done);
+  const cudaError_t e = allow_smem(kernel, ts.smem, done);
   if (e != cudaSuccess) return e;
-  const int slots = num_sms / CTAS;
-  const unsigned grid = static_cast<unsigned>(bound < slots ? bound : slots) * CTAS;
+  const int slots = num_sms / ts.ctas;
+  const unsigned grid = static_cast<unsigned>(bound < slots ? bound : slots) * ts.ctas;
   cudaLaunchConfig_t lc;
   std::memset(&lc, 0, sizeof(lc));
   lc.gridDim = dim3(grid);
-  lc.blockDim = dim3(Cfg::kThreads);
-  lc.dynamicSmemBytes = Cfg::kSmem;
+  lc.blockDim = dim3(static_cast<unsigned>(ts.threads));
+  lc.dynamicSmemBytes = static_cast<size_t>(ts.smem);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
-  if (CTAS == 2) {  // in stream order, without overlap with its neighbours
+  if (ts.ctas == 2) {  // in stream order, without overlap with its neighbours
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
@@ -805,12 +1271,30 @@ cudaError_t launch(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaS
   return count_launch(cudaLaunchKernelEx(&lc, kernel, *p));
 }
 
+template <int CTAS, int BN, int PA, int PB, bool SWAP>
+cudaError_t launch_plain(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  return launch(grouped_kernel<CTAS, BN, PA, PB, SWAP>,
+                plain_shape<GroupedCfg<CTAS, BN, PA, PB, SWAP>, CTAS, BN, SWAP>(), &done, p, g,
+                num_sms, s);
+}
+template <int PB>
+cudaError_t launch_wide(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  for (int b = 0; b < 3; ++b)
+    if (!operand_map(&p->tm_rows[b], g.a, g.depth, g.total_rows, g.a_parts, g.lda, g.a_plane,
+                     64 >> b))
+      return cudaErrorInvalidValue;
+  p->w_blocks = g.swiglu && g.features % 16 == 0;
+  return launch(grouped_wide_kernel<PB>, wide_shape<PB>(), &done, p, g, num_sms, s);
+}
+
 }  // namespace
 
 int grouped_tile_rows(int total_rows, int groups, bool f32) {
   if (f32) return 128;
   const long long mean = (static_cast<long long>(total_rows) + groups - 1) / groups;
-  return mean <= 32 ? 32 : mean <= 64 ? 64 : 256;
+  return mean <= 32 ? 32 : mean <= 64 ? 64 : kWideRows;
 }
 
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows) {
@@ -831,9 +1315,7 @@ cudaError_t launch_group_plan(const int32_t* offsets, int rows, int groups, int 
   p.err = err;
   unsigned blocks = 1;
   if (wg != nullptr) {
-    // both row-contiguous: [planes][rows][inner], boxes of 64 x 64
-    if (!operand_map(&p.tm_a, wg->a, wg->rows, rows, wg->a_parts, wg->lda, wg->a_plane, BK) ||
-        !operand_map(&p.tm_b, wg->b, wg->features, rows, wg->b_parts, wg->ldb, wg->b_plane, BK))
+    if (!rows_map(&p.tm_a, *wg, true) || !rows_map(&p.tm_b, *wg, false))
       return cudaErrorInvalidValue;
     blocks = static_cast<unsigned>(ceil_div(2ll * groups, kPlanThreads / 32));
   } else {
@@ -861,19 +1343,18 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& pla
   p.err = err;
   const bool f32 = g.a_parts == 3;
   p.chunk = f32 ? 2 : g.c_f32 ? 4 : kMaxChunk;
-  if (f32) return launch<1, 128, 3, 3, false>(&p, g, num_sms, s);
-  if (g.kind == GroupedKind::kWeightGrad) return launch<2, 256, 1, 1, false>(&p, g, num_sms, s);
+  if (f32) return launch_plain<1, 128, 3, 3, false>(&p, g, num_sms, s);
+  if (g.kind == GroupedKind::kWeightGrad) return launch_plain<2, 256, 1, 1, false>(&p, g, num_sms, s);
   const bool two = g.a_parts == 2;
   switch (grouped_tile_rows(g.total_rows, g.groups, false)) {
     case 32:
-      return two ? launch<1, 32, 1, 2, true>(&p, g, num_sms, s)
-                 : launch<1, 32, 1, 1, true>(&p, g, num_sms, s);
+      return two ? launch_plain<1, 32, 1, 2, true>(&p, g, num_sms, s)
+                 : launch_plain<1, 32, 1, 1, true>(&p, g, num_sms, s);
     case 64:
-      return two ? launch<1, 64, 1, 2, true>(&p, g, num_sms, s)
-                 : launch<1, 64, 1, 1, true>(&p, g, num_sms, s);
+      return two ? launch_plain<1, 64, 1, 2, true>(&p, g, num_sms, s)
+                 : launch_plain<1, 64, 1, 1, true>(&p, g, num_sms, s);
     default:
-      return two ? launch<2, 256, 2, 1, false>(&p, g, num_sms, s)
-                 : launch<2, 256, 1, 1, false>(&p, g, num_sms, s);
+      return two ? launch_wide<2>(&p, g, num_sms, s) : launch_wide<1>(&p, g, num_sms, s);
   }
 }
 
