@@ -93,26 +93,34 @@ __device__ __forceinline__ int total_tiles(const GroupedParams& p) {
                                             : *p.plan.count * p.tiles_b;
 }
 
+// What tile idx's place is read from, to be loaded while the tile before it is worked on: the
+// table's entry of its rows, or (weight gradient) the ends of its group.
+__device__ __forceinline__ int4 fetch_tile(const GroupedParams& p, int idx) {
+  if (p.kind != GroupedKind::kWeightGrad) return __ldg(p.plan.tiles + idx / p.tiles_b);
+  const int g = idx / (p.tiles_a * p.tiles_b);
+  return make_int4(__ldg(p.plan.bounds + g), __ldg(p.plan.bounds + g + 1), g, 0);
+}
+
 // Tiles of up to kRowChunk tiles of rows of a group share every tile of features in turn.
+// row_end is not set in a ragged product: row_end_of.
 template <typename Cfg>
-__device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx) {
+__device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const int4& e) {
   Tile t;
   const int step = p.swiglu ? Cfg::kTileFeatures / 2 : Cfg::kTileFeatures;
   if (p.kind != GroupedKind::kWeightGrad) {
-    const int4 e = __ldg(p.plan.tiles + idx / p.tiles_b);
     const int in = idx - e.z * p.tiles_b;
     const int tiles = e.w & 15, f = in / tiles;
     t.group = e.x;
     t.rows = e.w >> 4;
     t.row0 = e.y + (in - f * tiles) * t.rows;
-    t.row_end = __ldg(p.plan.bounds + e.x + 1);
+    t.row_end = 0;
     t.feat0 = f * step;
     t.k0 = 0;
     t.num_kb = p.num_kb;
     t.cut_kb = -1;
   } else {
     const int per = p.tiles_a * p.tiles_b;
-    t.group = idx / per;
+    t.group = e.z;
     t.rows = 0;
     const int in = idx - t.group * per;
     const int c = in / (kRowChunk * p.tiles_b);
@@ -122,12 +130,16 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx) {
     t.row0 = (c * kRowChunk + rest - f * h) * Cfg::kTileRows;
     t.row_end = p.rows;
     t.feat0 = f * step;
-    t.k0 = __ldg(p.plan.bounds + t.group);
-    const int size = __ldg(p.plan.bounds + t.group + 1) - t.k0;
+    t.k0 = e.x;
+    const int size = e.y - t.k0;
     t.num_kb = (size + BK - 1) / BK;
     t.cut_kb = size % BK != 0 ? t.num_kb - 1 : -1;
   }
   return t;
+}
+
+__device__ __forceinline__ int row_end_of(const GroupedParams& p, const Tile& t) {
+  return p.kind == GroupedKind::kWeightGrad ? p.rows : __ldg(p.plan.bounds + t.group + 1);
 }
 
 // ------------------------------------------------------------------- loading ----
@@ -183,8 +195,35 @@ __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// A warp's staging: 32 rows of 128 bytes, the 16-byte pieces of row r at piece ^ (r & 7), which is
-// the 128-byte swizzle of a TMA box.  A lane writes its own row.
+// tcgen05.ld into floats; the values are there after tmem_ld_wait.  keep and after_wait hold their
+// uses behind that wait, which does not name the registers.
+__device__ __forceinline__ void tmem_ld_columns(uint32_t addr, float (&v)[32]) {
+  tmem_ld_32x32b_x32(addr, reinterpret_cast<uint32_t (&)[32]>(v));
+}
+__device__ __forceinline__ void tmem_ld_columns(uint32_t addr, float (&v)[16]) {
+  tmem_ld_32x32b_x16(addr, reinterpret_cast<uint32_t (&)[16]>(v));
+}
+__device__ __forceinline__ float after_wait(float v) {
+  asm volatile("" : "+f"(v));
+  return v;
+}
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t addr, float (&v)[32], int at) {
+  uint32_t r[16];
+  tmem_ld_16x256b_x4(addr, r);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) v[at + q] = __uint_as_float(r[q]);
+}
+template <int A, int B>
+__device__ __forceinline__ void keep(float (&v)[A][B]) {
+#pragma unroll
+  for (int i = 0; i < A; ++i)
+#pragma unroll
+    for (int q = 0; q < B; ++q) asm volatile("" : "+f"(v[i][q]));
+}
+
+// A staged piece: rows of 128 bytes, the 16-byte parts of row r at part ^ (r & 7), which is TMA's
+// 128-byte swizzle.  (Rows of 64 bytes leave no faster than those of 128: half the rate.)
+// A lane's own row: 32 floats, or 32 values in bf16 from part c0 on.
 __device__ __forceinline__ void stage_f32(uint8_t* stg, int lane, const float (&v)[32]) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
@@ -203,8 +242,8 @@ __device__ __forceinline__ void stage_bf16(uint8_t* stg, int lane, int c0, const
                    pack2(v[8 * c + 4], v[8 * c + 5]), pack2(v[8 * c + 6], v[8 * c + 7]));
 }
 
-// Where a piece of 32 rows x 128 bytes of an output goes: rows of a group's matrix (C, third = the
-// group), or of one half of z, whose map has the halves before the rows (third = the half).
+// Where a piece of an output goes: rows of a group's matrix (C, third = the group), or of one half
+// of z, whose map has the halves before the rows (third = the half).
 struct Out {
   const CUtensorMap* map;
   char* base;  // of the group or half
@@ -212,17 +251,17 @@ struct Out {
   int cols, third, is_z, tma, vec;
 };
 
-// Rows first.. of a staged piece (`count` of them, a multiple of 4) to memory, eight lanes to a row.
+// Rows first.. of a staged piece (`count` of them) to memory, eight lanes to a row.
 template <typename T>
 __device__ __forceinline__ void copy_rows(const Out& o, const uint8_t* stg, int lane, int first,
                                           int count, int row0, int row_end, int col) {
   constexpr int N = 16 / static_cast<int>(sizeof(T));
-  const int piece = lane & 7, c = col + piece * N;
+  const int part = lane & 7, c = col + part * N;
   const int n = min(N, o.cols - c);
 #pragma unroll 1
   for (int r = first + (lane >> 3); r < first + count; r += 4) {
     if (row0 + r >= row_end || n <= 0) break;
-    const uint8_t* src = stg + r * 128 + ((piece ^ (r & 7)) << 4);
+    const uint8_t* src = stg + r * 128 + ((part ^ (r & 7)) << 4);
     T* dst = reinterpret_cast<T*>(o.base) + static_cast<long long>(row0 + r) * o.ld + c;
     if (o.vec && n == N) {
       *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
@@ -232,14 +271,20 @@ __device__ __forceinline__ void copy_rows(const Out& o, const uint8_t* stg, int 
   }
 }
 
-// The staged piece to rows row0.. (below row_end) and columns col.. of the output: by TMA where
-// all 32 rows are the group's, else by the lanes, eight to a row.  TMA clips columns past the end
-// in 16-byte steps only: a row that ends inside one is left to the lanes.
+// Whether TMA may take a piece from column col on: it clips columns past the end in 16-byte steps
+// only, so a row that ends inside one is left to the lanes.
+template <typename T>
+__device__ __forceinline__ bool tma_takes(const Out& o, int col) {
+  constexpr int N = 16 / static_cast<int>(sizeof(T));
+  return o.tma && (col + 8 * N <= o.cols || o.cols % N == 0);
+}
+
+// A warp's staged piece to rows row0.. (below row_end) and columns col.. of the output: by TMA
+// where all 32 rows are the group's, else by the lanes.
 template <typename T>
 __device__ __forceinline__ void put_piece(const Out& o, uint8_t* stg, int lane, int row0,
                                           int row_end, int col, bool whole) {
-  constexpr int N = 16 / static_cast<int>(sizeof(T));
-  if (whole && o.tma && (col + 8 * N <= o.cols || o.cols % N == 0)) {
+  if (whole && tma_takes<T>(o, col)) {
     fence_async_shared();
     __syncwarp();
     if (lane == 0) {
@@ -252,21 +297,21 @@ __device__ __forceinline__ void put_piece(const Out& o, uint8_t* stg, int lane, 
   copy_rows<T>(o, stg, lane, 0, 32, row0, row_end, col);
 }
 
-// A step of the wide kernel in float: the fragments of 32 rows (columns of the accumulator) and 16
-// or 32 lanes, lane f of them at float f0 + f of a row of the piece.
-__device__ __forceinline__ void put_f32(uint8_t* at, int lane, int f0, const float (&v)[32],
-                                        int lanes) {
+// Sixteen rows of the wide kernel's fragments in float: rows 8 j0.. of the 32, 16 or 32 lanes, lane
+// f of them at float f0 + f of a row of the piece.
+__device__ __forceinline__ void put_f32(uint8_t* at, int lane, int f0, const float (&v)[32], int j0,
+                                        int first_row, int lanes) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (16 * half >= lanes) break;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {  // e & 1: the row, e >> 1: lanes 8 on
         const int f = f0 + 16 * half + 8 * (e >> 1) + (lane >> 2);
-        const int row = 8 * j + 2 * (lane & 3) + (e & 1);
-        *reinterpret_cast<float*>(at + row * 128 + (((f >> 2) ^ (row & 7)) << 4) + (f & 3) * 4) =
-            v[16 * half + 4 * j + e];
+        const int row = first_row + 8 * j + 2 * (lane & 3) + (e & 1);
+        *reinterpret_cast<float*>(at + row * 128 + (((f >> 2) ^ (row & 7)) << 4) +
+                                  (f & 3) * 4) = v[16 * half + 4 * (j0 + j) + e];
       }
   }
 }
@@ -340,8 +385,10 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
+      int4 entry = first < total ? fetch_tile(p, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const Tile t = tile_at<Cfg>(p, idx);
+        const Tile t = tile_at<Cfg>(p, idx, entry);
+        if (idx + step < total) entry = fetch_tile(p, idx + step);
         const CUtensorMap* tm_a = &p.tm_a;
         const CUtensorMap* tm_b = &p.tm_b;
         int a_row, b_row, a_third, b_third;
@@ -436,8 +483,10 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
       uint32_t phase = 0;
       int local = 0;  // accumulators filled
       bool ok = true;
+      int4 entry = first < total ? fetch_tile(p, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const int num_kb = tile_at<Cfg>(p, idx).num_kb;
+        const int num_kb = tile_at<Cfg>(p, idx, entry).num_kb;
+        if (idx + step < total) entry = fetch_tile(p, idx + step);
         for (int kb = 0; ok && kb < num_kb; ++local) {
           const int acc = local & 1;
           if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
@@ -494,19 +543,24 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue ----
-    const int quad = warp & 3, half = (warp - 2) >> 2;
-    constexpr int W = BN / 2;               // columns of the accumulator that a warp takes
-    constexpr int P = W >= 32 ? 32 : W;     // columns per load
+    const int quad = warp & 3, part = (warp - 2) >> 2;
+    constexpr int W = BN / (Cfg::kEpiWarps / 4);  // columns of the accumulator that a warp takes
+    constexpr int P = W >= 32 ? 32 : W;           // columns per load
     constexpr int NP = W / P;
     int local = 0;  // accumulators read
     float sum[NP][P];
+    int4 entry = first < total ? fetch_tile(p, first) : int4{};
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = tile_at<Cfg>(p, idx);
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int q = 0; q < P; ++q) sum[i][q] = 0.f;
+      Tile t = tile_at<Cfg>(p, idx, entry);
+      t.row_end = row_end_of(p, t);
+      if (idx + step < total) entry = fetch_tile(p, idx + step);
       bool ok = true;
+      if (t.num_kb == 0) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int q = 0; q < P; ++q) sum[i][q] = 0.f;
+      }
       for (int kb = 0; kb < t.num_kb; kb += p.chunk, ++local) {
         const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
                                      abort_flag, p.err);
@@ -515,18 +569,26 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         tc_fence_after();
         const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                              static_cast<uint32_t>((local & 1) * BN);
+        // with swiglu (sides not swapped) the first half of a warp's columns are the gate's
+        auto column = [&](int i) {
+          return !SWAP && p.swiglu ? (i / ((NP + 1) / 2)) * W + part * (W / 2) +
+                                         (i % ((NP + 1) / 2)) * P
+                                   : part * W + i * P;
+        };
+        if (kb == 0) {  // straight into the sums, all on their way at once
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          // with swiglu (sides not swapped) the first half of a warp's columns are the gate's
-          const int col = !SWAP && p.swiglu ? (i / ((NP + 1) / 2)) * W + half * (W / 2) +
-                                                  (i % ((NP + 1) / 2)) * P
-                                            : half * W + i * P;
-          uint32_t r[P];
-          if constexpr (P == 32) tmem_ld_32x32b_x32(acc + col, r);
-          else tmem_ld_32x32b_x16(acc + col, r);
+          for (int i = 0; i < NP; ++i) tmem_ld_columns(acc + column(i), sum[i]);
           tmem_ld_wait();
+          keep(sum);
+        } else {
 #pragma unroll
-          for (int q = 0; q < P; ++q) sum[i][q] += __uint_as_float(r[q]);
+          for (int i = 0; i < NP; ++i) {
+            float r[P];
+            tmem_ld_columns(acc + column(i), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < P; ++q) sum[i][q] += after_wait(r[q]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -542,7 +604,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         const int f = p.swiglu ? t.feat0 + quad * 16 + (lane & 15) : t.feat0 + quad * 32 + lane;
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-          const int row = t.row0 + half * W + q;
+          const int row = t.row0 + part * W + q;
           if (row >= t.row_end) break;
           float v = sum[q / P][q % P];
           if (p.swiglu) {
@@ -571,26 +633,24 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
           oc.third = t.group;
           oc.base += static_cast<long long>(t.group) * p.c_group * (p.c_f32 ? 4 : 2);
         }
-        // N pieces of 32 columns, sum[I0..], to columns col.. of the output
-        auto emit = [&](const Out& o, bool f32, int col, auto i0, auto n) {
+        // N times 32 columns, sum[I0..], to columns col.. of the output: float in three-part
+        // products, else bf16
+        auto emit = [&](const Out& o, int col, auto i0, auto n) {
           constexpr int I0 = decltype(i0)::value, N = decltype(n)::value;
-          auto reuse = [&] {  // the last piece has left the staging
-            if (lane == 0) bulk_wait_read();
-            __syncwarp();
-          };
+          using T = std::conditional_t<PA == 3, float, __nv_bfloat16>;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             if (col + 32 * i >= o.cols) break;
-            if (PA == 3 || f32) {
-              reuse();
+            if (PA != 3 && i % 2 != 0) continue;
+            if (lane == 0) bulk_wait_read();  // the last piece has left the staging
+            __syncwarp();
+            if constexpr (PA == 3) {
               stage_f32(stg, lane, sum[I0 + i]);
-              put_piece<float>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
-            } else if (i % 2 == 0) {
-              reuse();
+            } else {
               stage_bf16(stg, lane, 0, sum[I0 + i]);
               stage_bf16(stg, lane, 4, sum[I0 + (i + 1) % N]);
-              put_piece<__nv_bfloat16>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
             }
+            put_piece<T>(o, stg, lane, row0, t.row_end, col + 32 * i, whole);
           }
         };
         using std::integral_constant;
@@ -598,22 +658,22 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         constexpr integral_constant<int, NP / 2> mid{};
         constexpr integral_constant<int, NP> all{};
         if (!p.swiglu) {
-          emit(oc, p.c_f32 != 0, t.feat0 + half * W, zero, all);
+          emit(oc, t.feat0 + part * W, zero, all);
         } else {
-          const int col = t.feat0 + half * (W / 2);
+          const int col = t.feat0 + part * (W / 2);
           if (p.z != nullptr) {
             Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
-            emit(oz, false, col, zero, mid);
+            emit(oz, col, zero, mid);
             oz.third = 1;
             oz.base += static_cast<long long>(p.features) * (PA == 3 ? 4 : 2);
-            emit(oz, false, col, mid, mid);
+            emit(oz, col, mid, mid);
           }
 #pragma unroll
           for (int i = 0; i < NP / 2; ++i)
 #pragma unroll
             for (int q = 0; q < P; ++q)
               sum[i][q] = act_value<PA != 3>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
-          emit(oc, p.c_f32 != 0, col, zero, mid);
+          emit(oc, col, zero, mid);
         }
       }
     }
@@ -648,7 +708,9 @@ struct WideCfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kABytes = 128 * BK * 2, kBBytes = 128 * BK * 2;
   static constexpr int kStageBytes = kABytes + PB * kBBytes;
-  static constexpr int kStgBytes = 2 * 16384;  // a set of warps: two pieces of 8 KB, or one of 16
+  // a set's staging: two pieces of 32 rows x 128 features in bf16, or one in float
+  static constexpr int kSetBytes = 16384;
+  static constexpr int kStgBytes = kEpiWarps / 4 * kSetBytes;
   static constexpr int kBarBytes = 256;
   static constexpr int kStages = (232448 - 1024 - kBarBytes - kStgBytes) / kStageBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
@@ -737,12 +799,18 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
+      int4 entry = first < total ? fetch_tile(p, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const Tile t = tile_at<Cfg>(p, idx);
+        const Tile t = tile_at<Cfg>(p, idx, entry);
+        if (idx + step < total) entry = fetch_tile(p, idx + step);
         const int mine = t.rows >> 1;  // rows that this CTA loads
         const int x_row = t.row0 + rank * mine;
         const int w_row = t.feat0 + rank * (p.swiglu ? 64 : 128);
-        const uint32_t bytes = static_cast<uint32_t>(2 * Cfg::kABytes + PB * t.rows * 128);
+        // one box, of 16 to 128 rows: several smaller ones for the exact share cost more than the
+        // rows they save (8192 rows in 8 groups, 14336 -> 4096: 648 us and 603)
+        const int size = mine > 64 ? 0 : mine > 32 ? 1 : mine > 16 ? 2 : 3;
+        const CUtensorMap* rows_map = size == 0 ? &p.tm_b : &p.tm_rows[size - 1];
+        const uint32_t bytes = static_cast<uint32_t>(2 * (Cfg::kABytes + PB * ((128 >> size) * 128)));
         for (int kb = 0; kb < t.num_kb; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
             ok = false;
@@ -766,18 +834,7 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
           }
 #pragma unroll
           for (int pl = 0; pl < PB; ++pl) {
-            const uint32_t dx = db + pl * Cfg::kBBytes;
-            if (mine == 128) {
-              tma_load_3d_pair(dx, &p.tm_b, fb, k, x_row, pl);
-            } else {  // 64, 32 and 16 rows as the share has them
-              int r = 0;
-#pragma unroll
-              for (int b = 0; b < 3; ++b)
-                if (mine & (64 >> b)) {
-                  tma_load_3d_pair(dx + r * 128u, &p.tm_rows[b], fb, k, x_row + r, pl);
-                  r += 64 >> b;
-                }
-            }
+            tma_load_3d_pair(db + pl * Cfg::kBBytes, rows_map, fb, k, x_row, pl);
           }
           issued = min(issued + 1, S);
           if (++stage == S) {
@@ -799,8 +856,10 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
       uint32_t phase = 0;
       int local = 0;  // accumulators filled
       bool ok = true;
+      int4 entry = first < total ? fetch_tile(p, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const Tile t = tile_at<Cfg>(p, idx);
+        const Tile t = tile_at<Cfg>(p, idx, entry);
+        if (idx + step < total) entry = fetch_tile(p, idx + step);
         const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(p.a_mn) << 15) |
                                (static_cast<uint32_t>(t.rows >> 3) << 17);
         for (int kb = 0; ok && kb < t.num_kb; ++local) {
@@ -851,19 +910,21 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue ----
     const int quad = warp & 3, set = (warp - 2) >> 2;
-    uint8_t* stg_set = stg_all + set * 16384;
+    constexpr int kSets = Cfg::kEpiWarps / 4, NS = 8 / kSets;  // steps of 32 rows per set
+    uint8_t* const stg_set = stg_all + set * Cfg::kSetBytes;
+    uint8_t* stg = stg_set;
+    const bool big = p.c_f32 && !p.swiglu;  // one piece at a time
+    int turn = 0;
     const bool issuer = threadIdx.x == static_cast<unsigned>(64 + set * 128);
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(set + 1) : "memory"); };
-    const bool big = p.c_f32 && !p.swiglu;  // pieces of 16 KB, one at a time
-    int turn = 0;
     int local = 0;  // accumulators read
+    int4 entry = first < total ? fetch_tile(p, first) : int4{};
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = tile_at<Cfg>(p, idx);
-      float sum[4][32];  // per 32 rows: lanes 0-15, then 16-31, as tmem_ld_16x256b_x4 has them
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 32; ++q) sum[i][q] = 0.f;
+      Tile t = tile_at<Cfg>(p, idx, entry);
+      t.row_end = row_end_of(p, t);
+      if (idx + step < total) entry = fetch_tile(p, idx + step);
+      // per 32 rows: lanes 0-15, then 16-31, as tmem_ld_16x256b_x4 has them
+      float sum[NS][32];
       bool ok = true;
       for (int kb = 0; kb < t.num_kb; kb += p.chunk, ++local) {
         const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
@@ -872,21 +933,30 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                             static_cast<uint32_t>((local & 1) * 256);
+                             static_cast<uint32_t>((local & 1) * 256 + set * 32);
+        if (kb == 0) {  // straight into the sums
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = (2 * i + set) * 32;
-          if (col < t.rows) {
-            uint32_t lo[16], hi[16];
-            tmem_ld_16x256b_x4(acc + col, lo);
-            tmem_ld_16x256b_x4(acc + col + (16u << 16), hi);
-            tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              sum[i][q] += __uint_as_float(lo[q]);
-              sum[i][16 + q] += __uint_as_float(hi[q]);
+          for (int i = 0; i < NS; ++i)
+            if ((kSets * i + set) * 32 < t.rows) {
+              tmem_ld_fragments(acc + i * kSets * 32, sum[i], 0);
+              tmem_ld_fragments(acc + i * kSets * 32 + (16u << 16), sum[i], 16);
             }
-          }
+          tmem_ld_wait();
+          keep(sum);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+            if ((kSets * i + set) * 32 < t.rows) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t r[16];
+                tmem_ld_16x256b_x4(acc + i * kSets * 32 + (h ? 16u << 16 : 0u), r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                  sum[i][16 * h + q] += after_wait(__uint_as_float(r[q]));
+              }
+            }
         }
         tc_fence_before();
         __syncwarp();
@@ -894,107 +964,103 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
       }
       // a set's warps meet below, so they give up together
       if (!all_of_set(set + 1, ok)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row0 = t.row0 + (2 * i + set) * 32;
-        if ((2 * i + set) * 32 >= t.rows || row0 >= t.row_end) continue;
+      const int mat = lane >> 3, in = lane & 7;
+      Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
+      // the staging is free of the store that used it last
+      auto begin = [&] {
+        if (issuer) {
+          if (big) bulk_wait_read();
+          else bulk_wait_read_but_one();
+        }
+        meet();
+        if (!big) stg = stg_set + (turn++ & 1) * 8192;
+      };
+      // Boxes of 128 bytes x 32 rows to columns col0, col0 + width, ...
+      auto finish = [&](const Out& o, int boxes, int row0, int col0, auto type, bool halves) {
+        using T = decltype(type);
+        constexpr int kWidth = 128 / static_cast<int>(sizeof(T));
         const bool whole = row0 + 32 <= t.row_end;
-        // The next piece's staging, free of the store that used it last.
-        auto begin = [&]() -> uint8_t* {
-          if (issuer) {
-            if (big) bulk_wait_read();
-            else bulk_wait_read_but_one();
+        fence_async_shared();
+        meet();
+        for (int b = 0; b < boxes; ++b) {
+          Out ob = o;
+          int col = col0 + b * kWidth;
+          if (halves) {  // box b is z's half b
+            col = col0;
+            ob.third = b;
+            ob.base += b * static_cast<long long>(o.cols) * static_cast<long long>(sizeof(T));
           }
-          meet();
-          uint8_t* at = stg_set + (big ? 0 : (turn & 1) * 8192);
-          ++turn;
-          return at;
-        };
-        // Boxes of 128 bytes x 32 rows at `at`, to columns col0, col0 + width, ...
-        auto finish = [&](const Out& o, uint8_t* at, int boxes, int col0, auto type, bool halves) {
-          using T = decltype(type);
-          constexpr int N = 16 / static_cast<int>(sizeof(T)), kWidth = 8 * N;
-          fence_async_shared();
-          meet();
-          for (int b = 0; b < boxes; ++b) {
-            Out ob = o;
-            int col = col0 + b * kWidth;
-            if (halves) {  // box b is z's half b
-              col = col0;
-              ob.third = b;
-              ob.base += b * static_cast<long long>(o.cols) * static_cast<long long>(sizeof(T));
-            }
-            if (col >= o.cols) continue;
-            const bool tma = whole && o.tma && (col + kWidth <= o.cols || o.cols % N == 0);
-            if (tma) {
-              if (issuer)
-                tma_store_3d(o.map, smem_u32(at + b * 4096), col, o.is_z ? ob.third : row0,
-                             o.is_z ? row0 : ob.third);
-            } else {
-              copy_rows<T>(ob, at + b * 4096, lane, quad * 8, 8, row0, t.row_end, col);
-            }
-          }
-          if (issuer) bulk_commit();
-        };
-        // 32 rows x 32 lanes in bf16: `chunk` is the place of 8 lanes among a row's 16-byte pieces
-        auto put_bf16 = [&](uint8_t* at, int box, int chunk, uint32_t (&m)[4], int row) {
-          // (box and chunk are those of the matrix whose row this thread addresses)
-          const uint32_t addr = smem_u32(at) + box * 4096u + row * 128u +
-                                (static_cast<uint32_t>(chunk ^ (row & 7)) << 4);
-          stmatrix_x4_trans(addr, m[0], m[1], m[2], m[3]);
-        };
-        const int mat = lane >> 3, in = lane & 7;
-        if (!p.swiglu) {
-          Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
-          const int col0 = t.feat0 + rank * 128;
-          uint8_t* at = begin();
-          if (!p.c_f32) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
-                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
-                               pack2(sum[i][16 + 4 * j], sum[i][17 + 4 * j]),
-                               pack2(sum[i][18 + 4 * j], sum[i][19 + 4 * j])};
-              put_bf16(at, quad >> 1, (quad & 1) * 4 + mat, m, 8 * j + in);
-            }
-            finish(oc, at, 2, col0, __nv_bfloat16{}, false);
+          if (col >= o.cols) continue;
+          uint8_t* at = stg + b * 4096;
+          if (whole && tma_takes<T>(o, col)) {
+            if (issuer)
+              tma_store_3d(o.map, smem_u32(at), col, o.is_z ? ob.third : row0,
+                           o.is_z ? row0 : ob.third);
           } else {
-            put_f32(at + quad * 4096, lane, 0, sum[i], 32);
-            finish(oc, at, 4, col0, float{}, false);
+            copy_rows<T>(ob, at, lane, quad * 8, 8, row0, t.row_end, col);
+          }
+        }
+        if (issuer) bulk_commit();
+      };
+      // four matrices of 8 rows x 8 lanes: this thread addresses `row` of one of them, whose lanes
+      // are the row's 16-byte part `part` in box `box`
+      auto put_bf16 = [&](int box, int part, int row, uint32_t a, uint32_t b, uint32_t c,
+                          uint32_t d) {
+        stmatrix_x4_trans(smem_u32(stg) + box * 4096u + row * 128u +
+                              (static_cast<uint32_t>(part ^ (row & 7)) << 4),
+                          a, b, c, d);
+      };
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int row0 = t.row0 + (kSets * i + set) * 32;
+        if ((kSets * i + set) * 32 >= t.rows || row0 >= t.row_end) continue;
+        float(&v)[32] = sum[i];
+        auto put_all = [&](auto place) {  // 32 rows x 32 lanes in bf16
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            place(8 * j + in, pack2(v[4 * j], v[4 * j + 1]), pack2(v[4 * j + 2], v[4 * j + 3]),
+                  pack2(v[16 + 4 * j], v[17 + 4 * j]), pack2(v[18 + 4 * j], v[19 + 4 * j]));
+        };
+        if (!p.swiglu) {
+          const int col0 = t.feat0 + rank * 128;
+          if (!p.c_f32) {
+            begin();
+            put_all([&](int row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+              put_bf16(quad >> 1, (quad & 1) * 4 + mat, row, a, b, c, d);
+            });
+            finish(oc, 2, row0, col0, __nv_bfloat16{}, false);
+          } else {
+            begin();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              put_f32(stg + quad * 4096, lane, 0, v, 2 * h, 16 * h, 32);
+            finish(oc, 4, row0, col0, float{}, false);
           }
         } else {
           const int col0 = t.feat0 + rank * 64;
           if (p.z != nullptr) {
             Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
-            uint8_t* at = begin();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
-                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
-                               pack2(sum[i][16 + 4 * j], sum[i][17 + 4 * j]),
-                               pack2(sum[i][18 + 4 * j], sum[i][19 + 4 * j])};
-              put_bf16(at, mat >> 1, quad * 2 + (mat & 1), m, 8 * j + in);
-            }
-            finish(oz, at, 2, col0, __nv_bfloat16{}, true);
+            begin();
+            put_all([&](int row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+              put_bf16(mat >> 1, quad * 2 + (mat & 1), row, a, b, c, d);
+            });
+            finish(oz, 2, row0, col0, __nv_bfloat16{}, true);
           }
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            sum[i][q] = act_value<true>(MOE_ACT_SILU, sum[i][q]) * sum[i][16 + q];
-          Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
-          uint8_t* at = begin();
+          for (int q = 0; q < 16; ++q) v[q] = act_value<true>(MOE_ACT_SILU, v[q]) * v[16 + q];
+          begin();
           if (!p.c_f32) {
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {  // 16 rows x 16 features
-              uint32_t m[4] = {pack2(sum[i][4 * j], sum[i][4 * j + 1]),
-                               pack2(sum[i][4 * j + 2], sum[i][4 * j + 3]),
-                               pack2(sum[i][4 * j + 4], sum[i][4 * j + 5]),
-                               pack2(sum[i][4 * j + 6], sum[i][4 * j + 7])};
-              put_bf16(at, 0, quad * 2 + (mat & 1), m, 8 * (j + (mat >> 1)) + in);
-            }
-            finish(oc, at, 1, col0, __nv_bfloat16{}, false);
+            for (int j = 0; j < 4; j += 2)  // 16 rows x 16 features
+              put_bf16(0, quad * 2 + (mat & 1), 8 * (j + (mat >> 1)) + in,
+                       pack2(v[4 * j], v[4 * j + 1]), pack2(v[4 * j + 2], v[4 * j + 3]),
+                       pack2(v[4 * j + 4], v[4 * j + 5]), pack2(v[4 * j + 6], v[4 * j + 7]));
+            finish(oc, 1, row0, col0, __nv_bfloat16{}, false);
           } else {
-            put_f32(at + (quad >> 1) * 4096, lane, (quad & 1) * 16, sum[i], 16);
-            finish(oc, at, 2, col0, float{}, false);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              put_f32(stg + (quad >> 1) * 4096, lane, (quad & 1) * 16, v, 2 * h, 16 * h, 16);
+            finish(oc, 2, row0, col0, float{}, false);
           }
         }
       }
