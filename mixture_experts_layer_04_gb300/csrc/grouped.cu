@@ -108,29 +108,48 @@ struct DzTask {
 };
 
 struct PrepareParams {
-  const int* bounds;
-  int groups;
+  const int32_t* offsets;
+  int rows, groups;
   DzTask dz;
   PackTask x, w;
 };
 
-template <typename T, int PL>
-__device__ __forceinline__ void pack_task(const PackTask& t, const int* bounds, int groups,
-                                          int block) {
-  const int per_row = static_cast<int>(t.dst_ld / 8);
-  const long long rows = t.group_rows == 0 ? bounds[groups] : t.rows;
+// Calls f(row, eight of columns) for the items that are this thread's; 32-bit divisions where they
+// do (64-bit ones cost more than the rest of an item).
+template <typename F>
+__device__ __forceinline__ void each_item(long long rows, int per_row, int block, int blocks, F f) {
   const long long items = rows * per_row;
-  for (long long i = block * 256ll + threadIdx.x; i < items; i += t.blocks * 256ll) {
-    const long long r = i / per_row;
-    const int c = static_cast<int>(i - r * per_row) * 8;
-    if (t.group_rows != 0) {
-      const int g = static_cast<int>(r / t.group_rows);
-      if (bounds[g] == bounds[g + 1]) continue;
+  const long long step = blocks * 256ll;
+  if (items + step <= 0xffffffffll) {
+    for (uint32_t i = block * 256u + threadIdx.x; i < static_cast<uint32_t>(items);
+         i += static_cast<uint32_t>(step)) {
+      const uint32_t r = i / static_cast<uint32_t>(per_row);
+      f(static_cast<long long>(r), static_cast<int>(i - r * static_cast<uint32_t>(per_row)));
     }
-    float v[8];
-    load_n(static_cast<const T*>(t.src) + r * t.ld + c, t.cols - c, t.vec != 0, v);
-    store_parts<PL>(t.dst + r * t.dst_ld + c, t.plane, 8, true, v);
+    return;
   }
+  for (long long i = block * 256ll + threadIdx.x; i < items; i += step) {
+    const long long r = i / per_row;
+    f(r, static_cast<int>(i - r * per_row));
+  }
+}
+
+template <typename T, int PL>
+__device__ __forceinline__ void pack_task(const PackTask& t, const PrepareParams& p, int used,
+                                          int block) {
+  each_item(t.group_rows == 0 ? used : t.rows, static_cast<int>(t.dst_ld / 8), block, t.blocks,
+            [&](long long r, int piece) {
+              const int c = piece * 8;
+              if (t.group_rows != 0) {
+                const int g = static_cast<int>(static_cast<uint32_t>(r) /
+                                               static_cast<uint32_t>(t.group_rows));
+                // (where offsets are held, a group with rows still has an offset above the last)
+                if (p.offsets[g + 1] <= p.offsets[g]) return;
+              }
+              float v[8];
+              load_n(static_cast<const T*>(t.src) + r * t.ld + c, t.cols - c, t.vec != 0, v);
+              store_parts<PL>(t.dst + r * t.dst_ld + c, t.plane, 8, true, v);
+            });
 }
 
 template <typename T, int PL>
@@ -141,13 +160,9 @@ __device__ __forceinline__ void store_dz(__nv_bfloat16* dst, const DzTask& t, in
 }
 
 template <typename T, int PL>
-__device__ __forceinline__ void dz_task(const DzTask& t, int rows, int block) {
-  const int per_row = (t.cols + 7) / 8;
-  const long long items = static_cast<long long>(rows) * per_row;
-  const long long step = t.blocks * 256ll;
-  for (long long i = block * 256ll + threadIdx.x; i < items; i += step) {
-    const long long r = i / per_row;
-    const int c = static_cast<int>(i - r * per_row) * 8, n = min(8, t.cols - c);
+__device__ __forceinline__ void dz_task(const DzTask& t, int used, int block) {
+  each_item(used, (t.cols + 7) / 8, block, t.blocks, [&](long long r, int piece) {
+    const int c = piece * 8, n = min(8, t.cols - c);
     float dy[8], gate[8], up[8];
     load_n(static_cast<const T*>(t.dy) + r * t.ldy + c, n, t.vec_y != 0, dy);
     const T* z = static_cast<const T*>(t.z) + r * t.ldz + c;
@@ -163,21 +178,33 @@ __device__ __forceinline__ void dz_task(const DzTask& t, int rows, int block) {
     __nv_bfloat16* dst = t.dz + r * t.dz_ld + c;
     store_dz<T, PL>(dst, t, n, gate);
     store_dz<T, PL>(dst + t.cols, t, n, up);
-  }
+  });
 }
 
+// Launched behind the plan kernel, on which it does not depend: the plan lets it start once what
+// came before the call is complete, and it waits for the plan at its end, for the products' sake.
 template <typename T, int PL>
 __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
-  grid_dep_wait();
+  __shared__ int s_used;
   grid_dep_trigger();
+  if (threadIdx.x == 0) s_used = 0;
+  __syncthreads();
+  // the end of the last group: the largest offset, held to the rows
+  int used = 0;
+  for (int i = threadIdx.x; i <= p.groups; i += 256) used = max(used, p.offsets[i]);
+  used = __reduce_max_sync(0xffffffffu, used);
+  if ((threadIdx.x & 31) == 0) atomicMax(&s_used, used);
+  __syncthreads();
+  used = min(s_used, p.rows);
   int b = static_cast<int>(blockIdx.x);
   if (b < p.dz.blocks) {
-    dz_task<T, PL>(p.dz, p.bounds[p.groups], b);
-    return;
+    dz_task<T, PL>(p.dz, used, b);
+  } else {
+    b -= p.dz.blocks;
+    if (b < p.x.blocks) pack_task<T, PL>(p.x, p, used, b);
+    else pack_task<T, PL>(p.w, p, used, b - p.x.blocks);
   }
-  b -= p.dz.blocks;
-  if (b < p.x.blocks) pack_task<T, PL>(p.x, p.bounds, p.groups, b);
-  else pack_task<T, PL>(p.w, p.bounds, p.groups, b - p.x.blocks);
+  grid_dep_wait();
 }
 
 cudaError_t launch_prepare(const PrepareParams& p, bool f32, cudaStream_t s) {
@@ -300,7 +327,8 @@ struct Workspace {
     return reinterpret_cast<T*>(base + off);
   }
   GroupPlan plan(const Layout& l) const {
-    return GroupPlan{at<int>(l.bounds), at<int4>(l.tiles), at<int>(l.count), at<void>(l.maps)};
+    return GroupPlan{at<int>(l.bounds), at<int4>(l.tiles), at<int>(l.count), at<void>(l.maps),
+                     nullptr};
   }
 };
 
@@ -371,21 +399,25 @@ extern "C" moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, cons
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = device_num_sms();
   const Workspace at(ws);
-  const GroupPlan plan = at.plan(l);
+  GroupPlan plan = at.plan(l);
   unsigned* err = device_error_word();
-  if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan, nullptr, err, s) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
   PrepareParams pp{};
-  pp.bounds = plan.bounds;
+  pp.offsets = offsets;
+  pp.rows = cfg->rows;
   pp.groups = cfg->groups;
   const Operand ox = operand(x, sh.x, cfg->rows, cfg->in_features, 0, cfg->dtype, l.pack_x,
                              at.at<void>(l.x), sms, &pp.x);
   const Operand ow = operand(w, sh.w, static_cast<long long>(cfg->groups) * sh.w_rows,
                              cfg->in_features, sh.w_rows, cfg->dtype, l.pack_w, at.at<void>(l.w),
                              sms, &pp.w);
-  if (pp.x.blocks + pp.w.blocks > 0 && launch_prepare(pp, sh.f32, s) != cudaSuccess)
+  const bool prepare = pp.x.blocks + pp.w.blocks > 0;
+  if (!prepare && grouped_plans_itself(l.tile_rows, sh.f32)) {
+    plan.offsets = offsets;
+  } else if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan, nullptr, err,
+                               s) != cudaSuccess) {
     return MOE_ERR_CUDA;
+  }
+  if (prepare && launch_prepare(pp, sh.f32, s) != cudaSuccess) return MOE_ERR_CUDA;
   GroupedProduct g{};
   g.kind = GroupedKind::kForward;
   g.groups = cfg->groups;
@@ -445,11 +477,12 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   if (st != MOE_OK) return st;
   const int sms = device_num_sms();
   const Workspace at(ws);
-  const GroupPlan plan = at.plan(l);
+  GroupPlan plan = at.plan(l);
   unsigned* err = device_error_word();
 
   PrepareParams pp{};
-  pp.bounds = plan.bounds;
+  pp.offsets = offsets;
+  pp.rows = cfg->rows;
   pp.groups = cfg->groups;
   Operand ox{}, ow{}, odz{dy, sh.y, 0};
   if (dw != nullptr)
@@ -509,13 +542,19 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   gw.ldc = sh.dw;
   gw.c_group = sh.dw * sh.w_rows;
 
-  if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan,
-                        dw != nullptr ? &gw : nullptr, err, s) != cudaSuccess)
+  // a float32 weight gradient fills the SMs that the input gradient leaves idle (both wait for the
+  // packing alone); the others take CTA pairs, which run in stream order
+  gw.beside = sh.f32 && dx != nullptr;
+  const bool prepare = pack_dy.blocks + pp.dz.blocks + pp.x.blocks + pp.w.blocks > 0;
+  if (dw == nullptr && !prepare && grouped_plans_itself(l.tile_rows, sh.f32)) {
+    plan.offsets = offsets;
+  } else if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan,
+                               dw != nullptr ? &gw : nullptr, err, s) != cudaSuccess) {
     return MOE_ERR_CUDA;
+  }
   if (pack_dy.blocks > 0) {
-    PrepareParams first{};
-    first.bounds = pp.bounds;
-    first.groups = pp.groups;
+    PrepareParams first = pp;
+    first.w = PackTask{};
     first.x = pack_dy;
     if (launch_prepare(first, sh.f32, s) != cudaSuccess) return MOE_ERR_CUDA;
   }

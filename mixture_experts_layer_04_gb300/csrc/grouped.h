@@ -18,6 +18,7 @@ struct GroupPlan {
                   //                    tiles in its chunk | rows of each << 4}
   int* count;     // tiles of rows
   void* maps;     // tensor maps of every group's rows, [groups][2], or null
+  const int32_t* offsets;  // not null: no plan was made, the product's kernel reads the offsets
 };
 
 // One grouped product.  Operands are bf16, in parts whose sum is the value (1; 3 each for float32
@@ -39,6 +40,7 @@ struct GroupedProduct {
   void* c;
   int c_f32;
   long long ldc, c_group;  // c_group: elements between the groups of a weight gradient
+  int beside;              // needs nothing of the launch before it but what that one needed itself
   void* z;                 // forward with swiglu: [total rows][2 features] or null
   int z_f32;
   long long ldz;
@@ -46,6 +48,8 @@ struct GroupedProduct {
 
 // Rows that a tile of the forward or input-gradient product takes, by the rule in grouped_gemm.cu.
 int grouped_tile_rows(int total_rows, int groups, bool f32);
+// Whether the forward and input-gradient kernels for these tiles can do without a plan.
+bool grouped_plans_itself(int tile_rows, bool f32);
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows);
 
 // Reads the offsets; with `weight_grad` (may be null) also writes its operands' maps.

@@ -38,6 +38,7 @@ namespace {
 constexpr int BK = 64;
 constexpr int kMaxChunk = 256;  // k-blocks per accumulator of a bf16 result
 constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
+constexpr int kMostGroups = 1024;
 constexpr int kWideRows = 256, kWideStep = 32;  // rows of a tile of grouped_wide_kernel
 
 // PA, PB: bf16 parts per value on the A and on the B side.
@@ -50,9 +51,12 @@ struct GroupedCfg {
   static constexpr int kStageBytes = PA * kABytes + PB * kBBytes;
   static constexpr int kStgBytes = SWAP ? 0 : kEpiWarps * 4096;  // 32 rows of 128 bytes per warp
   static constexpr int kBarBytes = 256;
-  static constexpr int kRaw = (232448 - 1024 - kBarBytes - kStgBytes) / kStageBytes;
+  // the groups' bounds and first tiles, where the kernel plans for itself
+  static constexpr int kTableBytes = SWAP ? 2 * (kMostGroups + 4) * 4 + 128 : 0;
+  static constexpr int kRaw =
+      (232448 - 1024 - kBarBytes - kStgBytes - kTableBytes) / kStageBytes;
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStgBytes + kBarBytes + kTableBytes;
   static constexpr int kTmemCols = 2 * BN;
   static constexpr int kTileRows = SWAP ? BN : 128 * CTAS;
   static constexpr int kTileFeatures = SWAP ? 128 : BN;
@@ -66,7 +70,8 @@ struct GroupedParams {
   int w_blocks;            // wide kernel, swiglu: tm_a takes both halves' blocks of 16 rows
   GroupPlan plan;
   GroupedKind kind;
-  int groups, num_kb, chunk;
+  int groups, total_rows, num_kb, chunk;
+  int beside;        // starts without waiting for the launch before it, and waits at its end
   int tiles_a;       // weight gradient: tiles along the rows of C_g
   int tiles_b;       // tiles along the features
   int rows;          // weight gradient: rows of C_g
@@ -87,15 +92,110 @@ struct Tile {
   int cut_kb;      // the block that the group's end cuts (weight gradient), or -1
 };
 
-template <typename Cfg>
-__device__ __forceinline__ int total_tiles(const GroupedParams& p) {
-  return p.kind == GroupedKind::kWeightGrad ? p.groups * p.tiles_a * p.tiles_b
-                                            : *p.plan.count * p.tiles_b;
+// The plan in shared memory of a kernel that plans for itself (bound null: the plan kernel's).
+struct Table {
+  int* bound;  // [groups + 1]
+  int* first;  // [groups + 1]: first tile of rows of each group, then their number
+};
+
+__device__ __forceinline__ int total_tiles(const GroupedParams& p, const Table& table) {
+  if (p.kind == GroupedKind::kWeightGrad) return p.groups * p.tiles_a * p.tiles_b;
+  return (table.bound != nullptr ? table.first[p.groups] : *p.plan.count) * p.tiles_b;
+}
+
+// The last group whose first tile is not past tile i (so one that has tiles).
+__device__ __forceinline__ int group_of_tile(const int* first, int groups, int i) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (first[m] <= i) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+
+// Tile i of rows as the table of tiles has it.
+__device__ __forceinline__ int4 table_entry(const Table& t, int groups, int i, int tile_rows) {
+  const int g = group_of_tile(t.first, groups, i);
+  const int first = t.first[g], tiles = t.first[g + 1] - first;
+  const int chunk = first + (i - first) / kRowChunk * kRowChunk;
+  // rows of the group's tiles: even shares, where a tile need not be full
+  const int size = t.bound[g + 1] - t.bound[g];
+  const int rows = tile_rows == kWideRows
+                       ? ((size + tiles - 1) / tiles + kWideStep - 1) / kWideStep * kWideStep
+                       : tile_rows;
+  return make_int4(g, t.bound[g] + (chunk - first) * rows, chunk,
+                   min(kRowChunk, first + tiles - chunk) | rows << 4);
+}
+
+// Reads the offsets (at most 1025) and makes them ascend within 0..rows: a running maximum, so that
+// bad ones cannot lead a kernel out of its buffers; `report`: one block tells of them through the
+// error word.  Then the groups' first tiles.  Every thread of the block calls it; PER groups a
+// thread; scratch: 32 ints.
+template <int PER>
+__device__ __forceinline__ void make_table(const int32_t* offsets, int rows, int groups,
+                                           int tile_rows, const Table& t, int* scratch, bool report,
+                                           unsigned* err) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int start = min(max(offsets[0], 0), rows);
+  int given[PER], bound[PER];
+  int most = start;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    given[k] = g < groups ? offsets[g + 1] : start;
+    most = max(most, min(max(given[k], 0), rows));
+    bound[k] = most;
+  }
+  int before = most;  // running maximum over the threads up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before = max(before, n);
+  }
+  if (lane == 31) scratch[warp] = before;
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = start;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before = max(before, scratch[w]);
+  bool bad = tid == 0 && offsets[0] != start;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    bound[k] = max(bound[k], before);
+    if (g < groups) {
+      t.bound[g + 1] = bound[k];
+      bad |= given[k] != bound[k];
+    }
+  }
+  if (tid == 0) t.bound[0] = start;
+  if (report && bad) report_error(err, MOE_DEVERR_BOUNDS);
+  __syncthreads();
+  int tiles[PER], sum = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    tiles[k] = g < groups ? (t.bound[g + 1] - t.bound[g] + tile_rows - 1) / tile_rows : 0;
+    sum += tiles[k];
+  }
+  int total;
+  int at = block_exclusive_scan(sum, scratch, &total);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int g = tid * PER + k;
+    if (g < groups) t.first[g] = at;
+    at += tiles[k];
+  }
+  if (tid == 0) t.first[groups] = total;
+  __syncthreads();
 }
 
 // What tile idx's place is read from, to be loaded while the tile before it is worked on: the
 // table's entry of its rows, or (weight gradient) the ends of its group.
-__device__ __forceinline__ int4 fetch_tile(const GroupedParams& p, int idx) {
+template <typename Cfg>
+__device__ __forceinline__ int4 fetch_tile(const GroupedParams& p, const Table& table, int idx) {
+  if (table.bound != nullptr)
+    return table_entry(table, p.groups, idx / p.tiles_b, Cfg::kTileRows);
   if (p.kind != GroupedKind::kWeightGrad) return __ldg(p.plan.tiles + idx / p.tiles_b);
   const int g = idx / (p.tiles_a * p.tiles_b);
   return make_int4(__ldg(p.plan.bounds + g), __ldg(p.plan.bounds + g + 1), g, 0);
@@ -138,7 +238,9 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const i
   return t;
 }
 
-__device__ __forceinline__ int row_end_of(const GroupedParams& p, const Tile& t) {
+__device__ __forceinline__ int row_end_of(const GroupedParams& p, const Table& table,
+                                          const Tile& t) {
+  if (table.bound != nullptr) return table.bound[t.group + 1];
   return p.kind == GroupedKind::kWeightGrad ? p.rows : __ldg(p.plan.bounds + t.group + 1);
 }
 
@@ -370,11 +472,22 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   if constexpr (CTAS == 1) {
-    grid_dep_wait();
+    if (!p.beside) grid_dep_wait();
     grid_dep_trigger();
   }
+  Table table{nullptr, nullptr};
+  if constexpr (SWAP) {
+    if (p.plan.offsets != nullptr) {
+      int* room = reinterpret_cast<int*>(stg_all + Cfg::kStgBytes + Cfg::kBarBytes);
+      table.bound = room + 32;
+      table.first = table.bound + kMostGroups + 4;
+      constexpr int kPer = (kMostGroups + Cfg::kThreads - 1) / Cfg::kThreads;
+      make_table<kPer>(p.plan.offsets, p.total_rows, p.groups, Cfg::kTileRows, table, room,
+                       blockIdx.x == 0, p.err);
+    }
+  }
 
-  const int total = total_tiles<Cfg>(p);
+  const int total = total_tiles(p, table);
   const int first = static_cast<int>(blockIdx.x) / CTAS;
   const int step = static_cast<int>(gridDim.x) / CTAS;
 
@@ -385,10 +498,10 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
-      int4 entry = first < total ? fetch_tile(p, first) : int4{};
+      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
         const Tile t = tile_at<Cfg>(p, idx, entry);
-        if (idx + step < total) entry = fetch_tile(p, idx + step);
+        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
         const CUtensorMap* tm_a = &p.tm_a;
         const CUtensorMap* tm_b = &p.tm_b;
         int a_row, b_row, a_third, b_third;
@@ -483,10 +596,10 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
       uint32_t phase = 0;
       int local = 0;  // accumulators filled
       bool ok = true;
-      int4 entry = first < total ? fetch_tile(p, first) : int4{};
+      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
         const int num_kb = tile_at<Cfg>(p, idx, entry).num_kb;
-        if (idx + step < total) entry = fetch_tile(p, idx + step);
+        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
         for (int kb = 0; ok && kb < num_kb; ++local) {
           const int acc = local & 1;
           if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
@@ -549,11 +662,11 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     constexpr int NP = W / P;
     int local = 0;  // accumulators read
     float sum[NP][P];
-    int4 entry = first < total ? fetch_tile(p, first) : int4{};
+    int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
     for (int idx = first; idx < total; idx += step) {
       Tile t = tile_at<Cfg>(p, idx, entry);
-      t.row_end = row_end_of(p, t);
-      if (idx + step < total) entry = fetch_tile(p, idx + step);
+      t.row_end = row_end_of(p, table, t);
+      if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
       bool ok = true;
       if (t.num_kb == 0) {
 #pragma unroll
@@ -689,6 +802,8 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
   }
   __syncwarp();
   if constexpr (CTAS == 2) cluster_sync_all();  // the pair gives its TMEM back before either leaves
+  // who waits for this launch waits for the one before it, too
+  if (CTAS == 1 && p.beside) grid_dep_wait();
 }
 
 // ------------------------------------------- weights on the side of 256 (pairs) ----
@@ -789,7 +904,8 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int total = total_tiles<Cfg>(p);
+  const Table table{nullptr, nullptr};
+  const int total = total_tiles(p, table);
   const int first = static_cast<int>(blockIdx.x) >> 1, step = static_cast<int>(gridDim.x) >> 1;
 
   if (warp == 0) {
@@ -799,10 +915,10 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
-      int4 entry = first < total ? fetch_tile(p, first) : int4{};
+      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
         const Tile t = tile_at<Cfg>(p, idx, entry);
-        if (idx + step < total) entry = fetch_tile(p, idx + step);
+        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
         const int mine = t.rows >> 1;  // rows that this CTA loads
         const int x_row = t.row0 + rank * mine;
         const int w_row = t.feat0 + rank * (p.swiglu ? 64 : 128);
@@ -856,10 +972,10 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
       uint32_t phase = 0;
       int local = 0;  // accumulators filled
       bool ok = true;
-      int4 entry = first < total ? fetch_tile(p, first) : int4{};
+      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
         const Tile t = tile_at<Cfg>(p, idx, entry);
-        if (idx + step < total) entry = fetch_tile(p, idx + step);
+        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
         const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(p.a_mn) << 15) |
                                (static_cast<uint32_t>(t.rows >> 3) << 17);
         for (int kb = 0; ok && kb < t.num_kb; ++local) {
@@ -918,11 +1034,11 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
     const bool issuer = threadIdx.x == static_cast<unsigned>(64 + set * 128);
     auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(set + 1) : "memory"); };
     int local = 0;  // accumulators read
-    int4 entry = first < total ? fetch_tile(p, first) : int4{};
+    int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
     for (int idx = first; idx < total; idx += step) {
       Tile t = tile_at<Cfg>(p, idx, entry);
-      t.row_end = row_end_of(p, t);
-      if (idx + step < total) entry = fetch_tile(p, idx + step);
+      t.row_end = row_end_of(p, table, t);
+      if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
       // per 32 rows: lanes 0-15, then 16-31, as tmem_ld_16x256b_x4 has them
       float sum[NS][32];
       bool ok = true;
@@ -1086,69 +1202,29 @@ struct PlanParams {
   CUtensorMap tm_a, tm_b;  // whole operands of the weight gradient
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = kMostGroups;
 
-// Every block reads the offsets (at most 1025) and makes them ascend within 0..rows: a running
-// maximum, so that bad ones cannot lead a kernel out of its buffers (reported through the error
-// word).  Block 0 writes the bounds and the table of the tiles of rows; all blocks share the
-// groups' tensor maps.
+// Every block makes the table for itself; block 0 writes the bounds and the table of the tiles of
+// rows, and all blocks share the groups' tensor maps.
 __global__ void __launch_bounds__(kPlanThreads) group_plan_kernel(
     const __grid_constant__ PlanParams p) {
-  __shared__ int s_bound[kPlanThreads + 1];
-  __shared__ int s_first[kPlanThreads + 1];
+  __shared__ int s_bound[kMostGroups + 1], s_first[kMostGroups + 1];
   __shared__ int scratch[32];
   __shared__ alignas(128) uint32_t s_map[kPlanThreads / 32][32];
   grid_dep_wait();
   grid_dep_trigger();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  // entry t + 1 of the bounds; the first is held to 0..rows by itself
-  const int start = min(max(p.offsets[0], 0), p.rows);
-  const int given = t < p.groups ? p.offsets[t + 1] : start;
-  int bound = max(min(max(given, 0), p.rows), start);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, bound, o);
-    if (lane >= o) bound = max(bound, n);
-  }
-  if (lane == 31) scratch[warp] = bound;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) bound = max(bound, scratch[w]);
-  if (t == 0) s_bound[0] = start;
-  s_bound[t + 1] = bound;
-  if (blockIdx.x == 0 && ((t < p.groups && given != bound) || (t == 0 && p.offsets[0] != start)))
-    report_error(p.err, MOE_DEVERR_BOUNDS);
-  __syncthreads();
-
+  const Table table{s_bound, s_first};
+  make_table<1>(p.offsets, p.rows, p.groups, p.tile_rows, table, scratch, blockIdx.x == 0, p.err);
   if (blockIdx.x == 0) {
-    const int size = t < p.groups ? s_bound[t + 1] - s_bound[t] : 0;
-    const int tiles = (size + p.tile_rows - 1) / p.tile_rows;
-    int total;
-    const int before = block_exclusive_scan(tiles, scratch, &total);
-    s_first[t] = before;
+    const int total = s_first[p.groups];
     if (t == 0) {
-      s_first[kPlanThreads] = total;
       *p.plan.count = total;
       p.plan.bounds[0] = s_bound[0];
     }
     if (t < p.groups) p.plan.bounds[t + 1] = s_bound[t + 1];
-    __syncthreads();
-    for (int i = t; i < total; i += kPlanThreads) {
-      int lo = 0, hi = p.groups;  // the last group whose first tile is not past i
-      while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (s_first[m] <= i) lo = m;
-        else hi = m;
-      }
-      const int end = lo + 1 < kPlanThreads ? s_first[lo + 1] : total;
-      const int chunk = s_first[lo] + (i - s_first[lo]) / kRowChunk * kRowChunk;
-      // rows of the group's tiles: even shares, where a tile need not be full
-      const int tiles = end - s_first[lo], size = s_bound[lo + 1] - s_bound[lo];
-      const int rows = p.tile_rows == kWideRows
-                           ? ((size + tiles - 1) / tiles + kWideStep - 1) / kWideStep * kWideStep
-                           : p.tile_rows;
-      p.plan.tiles[i] = make_int4(lo, s_bound[lo] + (chunk - s_first[lo]) * rows, chunk,
-                                  min(kRowChunk, end - chunk) | rows << 4);
-    }
+    for (int i = t; i < total; i += kPlanThreads)
+      p.plan.tiles[i] = table_entry(table, p.groups, i, p.tile_rows);
   }
   if (p.plan.maps == nullptr) return;
   const int warps = gridDim.x * (kPlanThreads / 32);
@@ -1363,6 +1439,8 @@ int grouped_tile_rows(int total_rows, int groups, bool f32) {
   return mean <= 32 ? 32 : mean <= 64 ? 64 : kWideRows;
 }
 
+bool grouped_plans_itself(int tile_rows, bool f32) { return !f32 && tile_rows < kWideRows; }
+
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows) {
   return static_cast<size_t>(total_rows / tile_rows) +
          static_cast<size_t>(std::min(groups, total_rows));
@@ -1397,6 +1475,8 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& pla
   p.plan = plan;
   p.kind = g.kind;
   p.groups = g.groups;
+  p.total_rows = g.total_rows;
+  p.beside = g.beside;
   p.rows = g.rows;
   p.features = g.features;
   p.swiglu = g.swiglu;
