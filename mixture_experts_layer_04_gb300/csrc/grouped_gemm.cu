@@ -16,7 +16,7 @@
 //    of tensor maps, copies of the call's maps whose number of rows is the group's end: TMA then
 //    fills the rest of the block that the end cuts with zeros.  The plan kernel writes them; the
 //    blocks before the last use the call's own.
-//  - A float32 result leaves the tensor core every 256 values (float32 operands, six products per
+//  - A float32 result leaves the tensor core every 512 values (float32 operands, six products per
 //    value: 128), a bf16 one every 16384, and is added up in registers: the tensor core truncates
 //    its additions.
 //
@@ -36,7 +36,11 @@ namespace moe {
 namespace {
 
 constexpr int BK = 64;
-constexpr int kMaxChunk = 256;  // k-blocks per accumulator of a bf16 result
+// K-blocks per accumulator: of a bf16 result, of a float one, of float operands.  An accumulator of
+// values of one sign falls short by 6.2e-9 of its size per value: 3.2e-6 over 512 values.  Draining
+// it every 256 values (4) cost the two-part input gradient 13400 clocks a tile, as much as half of
+// its MMAs.
+constexpr int kMaxChunk = 256, kFloatChunk = 8, kPartsChunk = 2;
 constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
 constexpr int kMostGroups = 1024;
 constexpr int kWideRows = 256, kWideStep = 32;  // rows of a tile of grouped_wide_kernel
@@ -1063,14 +1067,14 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < NS; ++i)
             if ((kSets * i + set) * 32 < t.rows) {
+              uint32_t lo[16], hi[16];
+              tmem_ld_16x256b_x4(acc + i * kSets * 32, lo);
+              tmem_ld_16x256b_x4(acc + i * kSets * 32 + (16u << 16), hi);
+              tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t r[16];
-                tmem_ld_16x256b_x4(acc + i * kSets * 32 + (h ? 16u << 16 : 0u), r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 16; ++q)
-                  sum[i][16 * h + q] += after_wait(__uint_as_float(r[q]));
+              for (int q = 0; q < 16; ++q) {
+                sum[i][q] += after_wait(__uint_as_float(lo[q]));
+                sum[i][16 + q] += after_wait(__uint_as_float(hi[q]));
               }
             }
         }
@@ -1488,7 +1492,7 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& pla
   p.c_f32 = g.c_f32;
   p.err = err;
   const bool f32 = g.a_parts == 3;
-  p.chunk = f32 ? 2 : g.c_f32 ? 4 : kMaxChunk;
+  p.chunk = f32 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk;
   if (f32) return launch_plain<1, 128, 3, 3, false>(&p, g, num_sms, s);
   if (g.kind == GroupedKind::kWeightGrad) return launch_plain<2, 256, 1, 1, false>(&p, g, num_sms, s);
   const bool two = g.a_parts == 2;
