@@ -10,9 +10,9 @@
 
 The backward gives the gradients of W_o, W_r, W_1, b_1 and W_2: the combine's gradient yields
 the route weights', routing's gradient the logits', and the linear layers take it from there.
-The experts' rows are a constant of h in it (a stop-gradient): the library has no backward of
-the grouped products, so W_o's gradient is that of the dense branch, the router and the residual
-and leaves out what h does through the experts.  After each step the balance bias moves against
+The experts' rows are a constant of h in it (a stop-gradient: they are frozen here, moe_train.py
+trains them), so W_o's gradient is that of the dense branch, the router and the residual and
+leaves out what h does through the experts.  After each step the balance bias moves against
 the experts' load, as scores-plus-bias routing is trained.
 
     python examples/moe_block.py [--tokens T] [--steps N]

@@ -569,7 +569,7 @@ moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
  *   [rows], dpost_weight, dchannel_scale, dnorm_weight [width] float out; each output may be NULL.
  *   ws: moe_block_norm_workspace_size() bytes, 16-byte aligned; NULL will do when no vector's
  *   gradient is asked for.
- * dresidual may be dsum itself (same stride).  With rows == 0 the vectors' gradients are zeroed.
+ * dx or dresidual may be dsum itself (same stride).  With rows == 0 the vectors' gradients are zeroed.
  * The same inputs give the same bits. */
 moe_status_t moe_block_norm_backward(const moe_block_norm_config_t* cfg, const void* dy,
                                      const void* dsum, const void* x, const void* sum,

@@ -63,6 +63,47 @@ struct Eight<float> {
   __device__ __forceinline__ float get(int q) const { return v[q]; }
 };
 
+// Two floats in a register pair: GB300 does a multiply-add of both in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ Pair both(float a) { return pair(a, a); }
+__device__ __forceinline__ float first(Pair p) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  return a;
+}
+__device__ __forceinline__ float second(Pair p) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+  return b;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ Pair pair_of(const Eight<T>& e, int i) {
+  return pair(e.get(2 * i), e.get(2 * i + 1));
+}
+__device__ __forceinline__ float add_up(Pair p) { return first(p) + second(p); }
+__device__ __forceinline__ void spread(const Pair (&v)[4], float (&out)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[2 * i] = first(v[i]);
+    out[2 * i + 1] = second(v[i]);
+  }
+}
+
 __device__ __forceinline__ void store_eight(__nv_bfloat16* p, const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -113,10 +154,10 @@ struct Columns {
         if (at(i, q) < width) e.set(q, row[at(i, q)]);
     }
   }
-  template <typename T>
+  template <bool FULL = false, typename T>
   __device__ __forceinline__ void store(T* row, int i, const float (&v)[8]) const {
     if constexpr (Vec) {
-      if (at(i, 0) < width) store_eight(row + at(i, 0), v);
+      if (FULL || at(i, 0) < width) store_eight(row + at(i, 0), v);
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -136,16 +177,30 @@ struct Columns {
 // the instructions and two more dependent steps, and is slower: 16384 rows of 7168 177 us instead
 // of 167, the backward of 8192 rows of 2048 63 instead of 59.)
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* part, int group, int threads) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float* part, int group, int threads,
+                                        int warp) {
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
   if (threads == 32) return;
-  const int warps = threads >> 5, warp = (threadIdx.x % threads) >> 5, lane = threadIdx.x & 31;
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < N; ++k) part[warp * N + k] = v[k];
   }
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+  if (N == 4 && warps <= 8) {  // every thread adds the few warps' sums up by itself
+    float4 sum = *reinterpret_cast<const float4*>(part);
+#pragma unroll
+    for (int w = 1; w < 8; ++w)
+      if (w < warps) {
+        const float4 x = *reinterpret_cast<const float4*>(part + 4 * w);
+        sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+      }
+    const float s[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = s[k];
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? part[lane * N + k] : 0.f);
 }
@@ -197,9 +252,18 @@ struct Ring {
   __device__ __forceinline__ bool wait(int slot, uint32_t phase) const {
     return mbar_wait(bar0 + 8u * slot, phase, abort_flag, err);
   }
-  // column `at` on of the slot's rows (zeros for null arrays and past the end)
+  // column `at` on of the slot's rows (zeros for null arrays and past the end; FULL: there are none)
+  template <bool FULL>
   __device__ __forceinline__ void read(int slot, int at, bool in, Eight<T> (&e)[N]) const {
     const T* from = reinterpret_cast<const T*>(smem + slot * slot_bytes) + at;
+    if constexpr (FULL) {
+#pragma unroll
+      for (int a = 0; a < N; ++a) {
+        e[a].load(from);
+        from += row_bytes / static_cast<int>(sizeof(T));
+      }
+      return;
+    }
 #pragma unroll
     for (int a = 0; a < N; ++a) {
       if (src[a] != nullptr && in) e[a].load(from);
@@ -239,7 +303,7 @@ constexpr int kPartFloats = kMaxThreads / 32 * 4;
 template <typename T, int V, bool Vec, int NT>
 __global__ void __launch_bounds__(NT)
     block_norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float part[2][kPartFloats];
+  __shared__ __align__(16) float part[2][kPartFloats];
   grid_dep_wait();
   grid_dep_trigger();
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
@@ -289,7 +353,7 @@ __global__ void __launch_bounds__(NT)
           sq[0] = fmaf(v, v, sq[0]);
         }
       }
-      row_sum<1>(sq, mine[0], group, p.threads);
+      row_sum<1>(sq, mine[0], group, p.threads, col.t >> 5);
       f *= root(sq[0], inv_width, p.eps);
     }
     float s[R][8];
@@ -321,7 +385,7 @@ __global__ void __launch_bounds__(NT)
     }
     float rs = 0.f;
     if (p.y != nullptr) {
-      row_sum<1>(sq, mine[1], group, p.threads);
+      row_sum<1>(sq, mine[1], group, p.threads, col.t >> 5);
       rs = root(sq[0], inv_width, p.eps);
     }
 #pragma unroll
@@ -387,7 +451,7 @@ __device__ __forceinline__ void leave_columns(const NormParams& p, const C& col,
 template <typename T, int V, bool Vec, int NT>
 __global__ void __launch_bounds__(NT)
     block_norm_grad_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float part[2][kPartFloats];
+  __shared__ __align__(16) float part[2][kPartFloats];
   extern __shared__ float columns[];  // V > 0: [groups - 1][2][width]
   grid_dep_wait();
   grid_dep_trigger();
@@ -449,7 +513,7 @@ __global__ void __launch_bounds__(NT)
         sums[2] = fmaf(dy[k].get(q) * wn[k][q], vs, sums[2]);
       }
     }
-    row_sum<3>(sums, mine[0], group, p.threads);
+    row_sum<3>(sums, mine[0], group, p.threads, col.t >> 5);
     const float rx = p.post != nullptr ? root(sums[0], inv_width, p.eps) : 1.f;
     const float rs = p.dy != nullptr ? root(sums[1], inv_width, p.eps) : 0.f;
     const float d1 = rs * rs * (sums[2] * inv_width);
@@ -466,7 +530,7 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
         for (int q = 0; q < 8; ++q) dot[0] = fmaf(grad(k, q) * c[k][q], x[k].get(q), dot[0]);
       }
-      row_sum<1>(dot, mine[1], group, p.threads);
+      row_sum<1>(dot, mine[1], group, p.threads, col.t >> 5);
       if (p.dgate != nullptr && col.t == 0) p.dgate[row] = rx * dot[0] * slope;
     }
     const float d2 = p.post != nullptr ? rx * rx * (dot[0] * inv_width) : 0.f;
@@ -531,14 +595,17 @@ struct Vector {
 // present one, so that a row costs one barrier.  V: eights of columns per thread; a thread's
 // instructions for a row (two sums, the gate, addresses) cost as much as eight columns' own, so
 // two where rows have them.
-template <typename T, int V>
+// FULL: residual, sum and y are all there and the threads' columns are the row's: the checks of
+// that would be a quarter of the instructions.
+template <typename T, int V, bool FULL>
 __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float part[2][kPartFloats];
+  __shared__ __align__(16) float part[2][kPartFloats];
   __shared__ uint64_t bars[kMostGroups * kMaxDepth];
   __shared__ int gave_up;
   extern __shared__ __align__(128) uint8_t rings[];
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
   const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const int warp = col.t >> 5;
   const float inv_width = 1.f / static_cast<float>(p.width);
   const int step = gridDim.x * groups;
   int row = blockIdx.x * groups + group;
@@ -551,15 +618,19 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   ring.abort_flag = &gave_up;
   ring.err = p.err;
   start_ring(ring, rings, bars, p.width, p.depth, group, groups, col.t == 0, row, step, p.rows);
-  float c[V][8], wn[V][8];
+  Pair c[V][4], wn[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float post[8], scale[8];
+    float post[8], scale[8], norm[8];
     col.vector(p.post, i, 1.f, post);
     col.vector(p.scale, i, 1.f, scale);
-    col.vector(p.norm, i, 1.f, wn[i]);
+    col.vector(p.norm, i, 1.f, norm);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) c[i][q] = p.branch_scale * scale[q] * post[q];
+    for (int q = 0; q < 4; ++q) {
+      c[i][q] = pair(p.branch_scale * scale[2 * q] * post[2 * q],
+                     p.branch_scale * scale[2 * q + 1] * post[2 * q + 1]);
+      wn[i][q] = pair(norm[2 * q], norm[2 * q + 1]);
+    }
   }
   Eight<T> cur[V][2];
   int slot = 0, area = 0;
@@ -574,19 +645,24 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
     gate = gate_from(p.gate_kind, entry, &slope);
     entry = gate_entry(r + step);
     if (!ring.wait(slot, phase)) return false;
+    Pair square = both(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = col.at(i, 0);
-      ring.read(slot, at, at < p.width, cur[i]);
+      ring.template read<FULL>(slot, at, at < p.width, cur[i]);
       if (p.post != nullptr) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sums[1] = fmaf(cur[i][0].get(q), cur[i][0].get(q), sums[1]);
+        for (int q = 0; q < 4; ++q) {
+          const Pair x = pair_of(cur[i][0], q);
+          square = fma2(x, x, square);
+        }
       }
     }
+    sums[1] = add_up(square);
     return true;
   };
   auto reduce = [&] {
-    row_sum<2>(sums, part[area] + group * (p.threads >> 5) * 2, group, p.threads);
+    row_sum<2>(sums, part[area] + group * (p.threads >> 5) * 2, group, p.threads, warp);
     area ^= 1;
   };
   if (ok) {
@@ -602,29 +678,38 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
       slot = 0;
       phase ^= 1u;
     }
-    float s[V][8];
-    sums[0] = sums[1] = 0.f;
+    Pair s[V][4], square = both(0.f);
+    const Pair f2 = both(f), scale2 = both(p.residual_scale);
+    sums[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        s[i][q] = fmaf(f * cur[i][0].get(q), c[i][q], p.residual_scale * cur[i][1].get(q));
-        sums[0] = fmaf(s[i][q], s[i][q], sums[0]);
+      for (int q = 0; q < 4; ++q) {
+        s[i][q] = fma2(mul2(f2, pair_of(cur[i][0], q)), c[i][q],
+                       mul2(scale2, pair_of(cur[i][1], q)));
+        square = fma2(s[i][q], s[i][q], square);
       }
+    sums[0] = add_up(square);
     const bool more = row + step < p.rows;
     if (more) ok = next_row(row + step);
-    if (p.sum != nullptr) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) col.store(static_cast<T*>(p.sum) + row * p.lds, i, s[i]);
-    }
-    reduce();
-    if (p.y != nullptr) {
-      const float rs = root(sums[0], inv_width, p.eps);
+    if (FULL || p.sum != nullptr) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        float v[8];
+        spread(s[i], v);
+        col.template store<FULL>(static_cast<T*>(p.sum) + row * p.lds, i, v);
+      }
+    }
+    reduce();
+    if (FULL || p.y != nullptr) {
+      const Pair rs = both(root(sums[0], inv_width, p.eps));
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s[i][q] *= rs * wn[i][q];
-        col.store(static_cast<T*>(p.y) + row * p.ldy, i, s[i]);
+      for (int i = 0; i < V; ++i) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[i][q] = mul2(mul2(s[i][q], rs), wn[i][q]);
+        spread(s[i], v);
+        col.template store<FULL>(static_cast<T*>(p.y) + row * p.ldy, i, v);
       }
     }
     ok = ok && more;
@@ -633,10 +718,11 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
 
 // The backward over many rows: the first sums of the next row are taken with the dot product of the
 // present one.  V: eights of columns per thread; with two, c and wn lie in shared memory.
-template <typename T, int V>
-__global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
+// FULL: every array is there and the threads' columns are the row's, as in the forward.
+template <typename T, int V, int NT, bool FULL>
+__global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
     const __grid_constant__ NormParams p) {
-  __shared__ float part[2][kPartFloats];
+  __shared__ __align__(16) float part[2][kPartFloats];
   __shared__ uint64_t bars[kMostGroups * kMaxDepth];
   __shared__ int gave_up;
   // the rings, then (V > 1) c and wn; after the last row the groups' sums: [groups - 1][2][width]
@@ -644,6 +730,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
   float* columns = reinterpret_cast<float*>(rings);
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
   const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const int warp = col.t >> 5;
   const float inv_width = 1.f / static_cast<float>(p.width);
   const int step = gridDim.x * groups;
   int row = blockIdx.x * groups + group;
@@ -681,11 +768,11 @@ __global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
       }
     }
   }
-  float sum_n[V][8], sum_a[V][8];
+  Pair sum_n[V][4], sum_a[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum_n[i][q] = sum_a[i][q] = 0.f;
+    for (int q = 0; q < 4; ++q) sum_n[i][q] = sum_a[i][q] = both(0.f);
   Eight<T> cur[V][4];
   int slot = 0, area = 0;
   uint32_t phase = 0;
@@ -699,25 +786,29 @@ __global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
     gate = gate_from(p.gate_kind, entry, &slope);
     entry = gate_entry(r + step);
     if (!ring.wait(slot, phase)) return false;
+    Pair xx = both(0.f), ss = xx, ds = xx;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = col.at(i, 0);
-      ring.read(slot, at, at < p.width, e[i]);
-      if (at >= p.width) continue;
+      ring.template read<FULL>(slot, at, at < p.width, e[i]);
+      if (!FULL && at >= p.width) continue;
       float w[8];
       wn[i].get(shared_w + at, w);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float vx = e[i][0].get(q), vs = e[i][1].get(q);
-        sums[1] = fmaf(vx, vx, sums[1]);
-        sums[2] = fmaf(vs, vs, sums[2]);
-        sums[3] = fmaf(e[i][2].get(q) * w[q], vs, sums[3]);
+      for (int q = 0; q < 4; ++q) {
+        const Pair vx = pair_of(e[i][0], q), vs = pair_of(e[i][1], q);
+        xx = fma2(vx, vx, xx);
+        ss = fma2(vs, vs, ss);
+        ds = fma2(mul2(pair_of(e[i][2], q), pair(w[2 * q], w[2 * q + 1])), vs, ds);
       }
     }
+    sums[1] = add_up(xx);
+    sums[2] = add_up(ss);
+    sums[3] = add_up(ds);
     return true;
   };
   auto reduce = [&] {
-    row_sum<4>(sums, part[area] + group * (p.threads >> 5) * 4, group, p.threads);
+    row_sum<4>(sums, part[area] + group * (p.threads >> 5) * 4, group, p.threads, warp);
     area ^= 1;
   };
   if (ok) {
@@ -726,7 +817,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
   }
   for (; ok; row += step) {
     const float rx = p.post != nullptr ? root(sums[1], inv_width, p.eps) : 1.f;
-    const float rs = p.dy != nullptr ? root(sums[2], inv_width, p.eps) : 0.f;
+    const float rs = FULL || p.dy != nullptr ? root(sums[2], inv_width, p.eps) : 0.f;
     const float d1 = rs * rs * (sums[3] * inv_width);
     const float f = gate * rx, gate_slope = rx * slope;
     // the barrier has passed, so every thread has this row out of its slot
@@ -736,50 +827,64 @@ __global__ void __launch_bounds__(512) block_norm_grad_rows_kernel(
       slot = 0;
       phase ^= 1u;
     }
-    float v[V][8];
+    Pair v[V][4], dot = both(0.f);
+    const Pair rs2 = both(rs), d12 = both(-d1), f2 = both(f), scale2 = both(p.residual_scale);
     Eight<T> x[V];
-    sums[0] = sums[1] = sums[2] = sums[3] = 0.f;
+    sums[1] = sums[2] = sums[3] = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = col.at(i, 0);
       float cv[8], w[8];
-      if (at >= p.width) continue;
+      if (!FULL && at >= p.width) continue;
       c[i].get(shared_c + at, cv);
       wn[i].get(shared_w + at, w);
       x[i] = cur[i][0];
-      float r[8];
+      Pair r[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float s = cur[i][1].get(q), dy = cur[i][2].get(q);
-        v[i][q] = fmaf(rs, fmaf(-s, d1, dy * w[q]), cur[i][3].get(q));
-        sum_n[i][q] = fmaf(dy * s, rs, sum_n[i][q]);
-        sum_a[i][q] = fmaf(f * v[i][q], x[i].get(q), sum_a[i][q]);
-        r[q] = p.residual_scale * v[i][q];
-        v[i][q] *= cv[q];
-        sums[0] = fmaf(v[i][q], x[i].get(q), sums[0]);
+      for (int q = 0; q < 4; ++q) {
+        const Pair s = pair_of(cur[i][1], q), dy = pair_of(cur[i][2], q), vx = pair_of(x[i], q);
+        const Pair ds = fma2(rs2, fma2(s, d12, mul2(dy, pair(w[2 * q], w[2 * q + 1]))),
+                             pair_of(cur[i][3], q));
+        sum_n[i][q] = fma2(mul2(dy, s), rs2, sum_n[i][q]);
+        sum_a[i][q] = fma2(mul2(f2, ds), vx, sum_a[i][q]);
+        r[q] = mul2(scale2, ds);
+        v[i][q] = mul2(ds, pair(cv[2 * q], cv[2 * q + 1]));
+        dot = fma2(v[i][q], vx, dot);
       }
-      if (p.dresidual != nullptr)
-        col.store(static_cast<T*>(p.dresidual) + row * p.lddr, i, r);
+      if (FULL || p.dresidual != nullptr) {
+        float out[8];
+        spread(r, out);
+        col.template store<FULL>(static_cast<T*>(p.dresidual) + row * p.lddr, i, out);
+      }
     }
+    sums[0] = add_up(dot);
     const bool more = row + step < p.rows;
     if (more) ok = next_row(row + step, cur);
     reduce();
     if (p.dgate != nullptr && col.t == 0) p.dgate[row] = gate_slope * sums[0];
-    if (p.dx != nullptr) {
-      const float d2 = p.post != nullptr ? rx * rx * (sums[0] * inv_width) : 0.f;
+    if (FULL || p.dx != nullptr) {
+      const Pair d2 = both(p.post != nullptr ? -rx * rx * (sums[0] * inv_width) : 0.f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (col.at(i, 0) >= p.width) continue;
+        if (!FULL && col.at(i, 0) >= p.width) continue;
+        float out[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[i][q] = f * fmaf(-x[i].get(q), d2, v[i][q]);
-        col.store(static_cast<T*>(p.dx) + row * p.lddx, i, v[i]);
+        for (int q = 0; q < 4; ++q) v[i][q] = mul2(f2, fma2(pair_of(x[i], q), d2, v[i][q]));
+        spread(v[i], out);
+        col.template store<FULL>(static_cast<T*>(p.dx) + row * p.lddx, i, out);
       }
     }
     ok = ok && more;
   }
   if (p.parts == nullptr) return;
   __syncthreads();  // every group's last row has left its slot
-  leave_columns<V>(p, col, columns, group, groups, sum_n, sum_a);
+  float n8[V][8], a8[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    spread(sum_n[i], n8[i]);
+    spread(sum_a[i], a8[i]);
+  }
+  leave_columns<V>(p, col, columns, group, groups, n8, a8);
 }
 
 // The blocks' column sums, added in order, and the vectors' gradients: 32 columns per block, each
@@ -867,21 +972,29 @@ int grad_blocks(const moe_block_norm_config_t* c, int num_sms) {
 // For the workspace's size, which must not depend on the device: no GPU has more.
 constexpr int kMostSms = 160;
 
-// The ring kernels' shape: 512 threads at most, rows of `two_from` columns and more 16 columns a
-// thread.  The backward has them where rows would not fit otherwise: 8192 rows of 2048 take 64 us
-// with 16 columns a thread.
+// The ring kernels' shape: `block` threads at most, rows of `two_from` columns and more 16 columns a
+// thread.
 constexpr int kRowsBlock = 512;
 constexpr int kTwoEights = 512;
-constexpr int kGradTwoEights = 8 * 512 + 1;
-Shape rows_shape(int width, int two_from) {
+Shape rows_shape(int width, int two_from, int block) {
   Shape s;
   s.keep = width <= 16 * kRowsBlock;
   const int per = width < two_from ? 8 : 16;
   s.threads = ((width + per - 1) / per + 31) / 32 * 32;
-  const int groups = kRowsBlock / s.threads;
+  const int groups = block / s.threads;
   const int most = s.threads == 32 ? kMostGroups : kMostGroups - 1;  // (named barriers: 1 to 15)
   s.groups = groups < 1 ? 1 : groups < most ? groups : most;
   return s;
+}
+
+// The backward's.  With 16 columns a thread it would like more than the 128 registers that 512
+// threads leave, so rows that fill no more than 448 threads are compiled for that many (8192 bf16
+// rows of 7168: 206 us for 512 threads, 151 for 448).  Float32 rows would spill even so and have 8
+// columns a thread where 512 threads reach.
+constexpr int kGradBlock448 = 448;
+int grad_two_from(int dtype) { return dtype == MOE_F32 ? 8 * kRowsBlock + 1 : kTwoEights; }
+Shape grad_rows_shape(int width, int dtype) {
+  return rows_shape(width, grad_two_from(dtype), kRowsBlock);
 }
 
 // Rows in a group's ring, 0: read directly (few rows a group, or rows that bulk copies cannot take).
@@ -939,14 +1052,27 @@ cudaError_t launch_rows(K kernel, const NormParams& p, unsigned blocks, unsigned
   return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, p);
 }
 
+// Whether the threads' columns are just the row's.
+bool whole_rows(const NormParams& p, int per_thread) { return p.threads * per_thread == p.width; }
+
 template <typename T>
 cudaError_t launch_forward(const NormParams& p, int keep, bool vec, unsigned blocks,
                            unsigned threads, size_t smem, cudaStream_t s) {
-  static std::atomic<unsigned long long> done[2];
-  if (p.depth > 0)
-    return p.width < kTwoEights
-               ? launch_rows(block_norm_rows_kernel<T, 1>, p, blocks, threads, smem, &done[0], s)
-               : launch_rows(block_norm_rows_kernel<T, 2>, p, blocks, threads, smem, &done[1], s);
+  static std::atomic<unsigned long long> done[4];
+  if (p.depth > 0) {
+    const bool there = p.residual != nullptr && p.sum != nullptr && p.y != nullptr;
+    if (p.width < kTwoEights)
+      return there && whole_rows(p, 8)
+                 ? launch_rows(block_norm_rows_kernel<T, 1, true>, p, blocks, threads, smem,
+                               &done[0], s)
+                 : launch_rows(block_norm_rows_kernel<T, 1, false>, p, blocks, threads, smem,
+                               &done[1], s);
+    return there && whole_rows(p, 16)
+               ? launch_rows(block_norm_rows_kernel<T, 2, true>, p, blocks, threads, smem, &done[2],
+                             s)
+               : launch_rows(block_norm_rows_kernel<T, 2, false>, p, blocks, threads, smem,
+                             &done[3], s);
+  }
   auto kernel = keep ? (vec ? block_norm_kernel<T, 1, true, kMaxThreads>
                             : block_norm_kernel<T, 1, false, kMaxThreads>)
                      : (vec ? block_norm_kernel<T, 0, true, kMaxThreads>
@@ -956,13 +1082,27 @@ cudaError_t launch_forward(const NormParams& p, int keep, bool vec, unsigned blo
 template <typename T>
 cudaError_t launch_backward(const NormParams& p, int keep, bool vec, unsigned blocks,
                             unsigned threads, size_t smem, cudaStream_t s) {
-  static std::atomic<unsigned long long> done[2];
-  if (p.depth > 0)
-    return p.width < kGradTwoEights
-               ? launch_rows(block_norm_grad_rows_kernel<T, 1>, p, blocks, threads, smem, &done[0],
-                             s)
-               : launch_rows(block_norm_grad_rows_kernel<T, 2>, p, blocks, threads, smem, &done[1],
-                             s);
+  static std::atomic<unsigned long long> done[6];
+  if (p.depth > 0) {
+    const bool there = p.x != nullptr && p.dy != nullptr && p.dsum != nullptr && p.dx != nullptr &&
+                       p.dresidual != nullptr;
+    if (p.width < grad_two_from(sizeof(T) == 4 ? MOE_F32 : MOE_BF16))
+      return there && whole_rows(p, 8)
+                 ? launch_rows(block_norm_grad_rows_kernel<T, 1, 512, true>, p, blocks, threads,
+                               smem, &done[0], s)
+                 : launch_rows(block_norm_grad_rows_kernel<T, 1, 512, false>, p, blocks, threads,
+                               smem, &done[1], s);
+    const bool full = there && whole_rows(p, 16);
+    if (threads <= kGradBlock448)
+      return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, true>, p, blocks,
+                                threads, smem, &done[2], s)
+                  : launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, false>, p, blocks,
+                                threads, smem, &done[3], s);
+    return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, 512, true>, p, blocks, threads,
+                              smem, &done[4], s)
+                : launch_rows(block_norm_grad_rows_kernel<T, 2, 512, false>, p, blocks, threads,
+                              smem, &done[5], s);
+  }
   if (keep && threads <= 512)
     return launch_pdl(vec ? block_norm_grad_kernel<T, 1, true, 512>
                           : block_norm_grad_kernel<T, 1, false, 512>,
@@ -1021,7 +1161,7 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
   const bool vec = all_vec(cfg->width, cfg->dtype,
                            {{x, q.ldx}, {residual, q.ldr}, {sum, q.lds}, {y, q.ldy}});
   const int slot = static_cast<int>((residual != nullptr ? 2 : 1) * cfg->width * ab2);
-  Shape sh = rows_shape(cfg->width, kTwoEights);
+  Shape sh = rows_shape(cfg->width, kTwoEights, kRowsBlock);
   const int depth = sums ? ring_depth(sh, vec, cfg->rows, sms, slot, 0) : 0;
   long long most = sms;
   if (depth == 0) {
@@ -1118,8 +1258,8 @@ extern "C" moe_status_t moe_block_norm_backward(
   int arrays = 0;
   for (const void* q : {p.x, p.sum_in, dy, dsum}) arrays += q != nullptr;
   const int slot = arrays * cfg->width * static_cast<int>(ab);
-  const Shape rs = rows_shape(cfg->width, kGradTwoEights);
-  const int vector_bytes = cfg->width >= kGradTwoEights ? 2 * cfg->width * 4 : 0;  // c and wn
+  const Shape rs = grad_rows_shape(cfg->width, cfg->dtype);
+  const int vector_bytes = cfg->width >= grad_two_from(cfg->dtype) ? 2 * cfg->width * 4 : 0;  // c and wn
   int blocks = grad_blocks(cfg, sms < kMostSms ? sms : kMostSms);
   p.depth = ring_depth(rs, vec, cfg->rows, blocks, slot, vector_bytes);
   if (p.depth > 0) {

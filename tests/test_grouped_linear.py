@@ -3,11 +3,10 @@
 Tolerances.  S is the sum of the products' absolute values.  A bf16 result is rounded once: 2^-8 of
 itself.  The tensor core adds 16 products at a time and truncates: at most 2^-22 of S a step, and a
 float32 addition per chunk of 128 values or more of at most 2^-24 of S: ACC(n) = (n / 16 + n / 128 +
-2) 2^-22.  Float32
-operands are three bf16 parts (2^-24 of each value left, twice) and six products per value, added in
-as many steps: 6 ACC(n) + 2^-22.  dz is rounded to bf16 once (2^-8 of itself, and so of S of the
-products that take it; 2^-17 where dx is float32), SwiGLU's fast exponential is good to 2e-5.  What a sum of independent
-roundings comes to is checked in L2: a product p_i whose factor is rounded is off by e_i p_i, with
+2) 2^-22.  Float32 operands are three bf16 parts (2^-24 of each value left, twice) and six products
+per value, added in as many steps: 6 ACC(n) + 2^-22.  dz is rounded to bf16 once (2^-8 of itself,
+and so of S of the products that take it; 2^-17 where dx is float32), SwiGLU's fast exponential is
+good to 2e-5.  What a sum of independent roundings comes to is checked in L2: a product p_i whose factor is rounded is off by e_i p_i, with
 e_i at most 2^-8 and 2^-8 / sqrt(3) in the root mean square, so sum e_i p_i has the root mean square
 2^-8 / sqrt(3) sqrt(sum p_i^2) (not a share of the sum itself, whose terms may cancel), and the
 result's own rounding adds 2^-8 / sqrt(3) of it; twice that is the bound.
@@ -266,9 +265,10 @@ def test_gradients_alone_and_repeated(sizes):
 
 
 @pytest.mark.gpu
-def test_graph_replays_follow_the_offsets():
-    c = Case([200, 0, 56, 100], 128, 128, True, seed=7)
-    other = Case([1, 300, 50, 5], 128, 128, True, seed=8)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_graph_replays_follow_the_offsets(dtype):
+    c = Case([200, 0, 56, 100], 128, 128, True, dtype=dtype, seed=7)
+    other = Case([1, 300, 50, 5], 128, 128, True, dtype=dtype, seed=8)
     c.forward(), c.backward()
     torch.cuda.synchronize()
     stream = torch.cuda.Stream()
