@@ -497,7 +497,7 @@ moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg, 
  * (MOE_ERR_INTERNAL).  Pointers need the alignment of their elements; x and w whose row stride is
  * a multiple of 16 bytes must start on a 16-byte boundary (MOE_ERR_MISALIGNED).  Float32
  * operands run as three bf16 parts per value, as moe_linear's; partial sums leave the tensor
- * cores every 128 values (float32 operands), 512 (float32 results) or 16384.
+ * cores every 64 values (float32 operands), 512 (float32 results) or 16384.
  * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work. */
 moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
                                 const int32_t* offsets, const void* w, void* y, void* z, void* ws,

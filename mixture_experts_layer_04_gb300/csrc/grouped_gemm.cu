@@ -17,7 +17,7 @@
 //    fills the rest of the block that the end cuts with zeros.  The plan kernel writes them; the
 //    blocks before the last use the call's own.
 //  - A float32 result leaves the tensor core every 512 values (float32 operands, six products per
-//    value: 128), a bf16 one every 16384, and is added up in registers: the tensor core truncates
+//    value: 64), a bf16 one every 16384, and is added up in registers: the tensor core truncates
 //    its additions.
 //
 // CTA pairs (256 x 256 tiles) where groups have many rows; single CTAs with the weights on the
@@ -39,8 +39,9 @@ constexpr int BK = 64;
 // K-blocks per accumulator: of a bf16 result, of a float one, of float operands.  An accumulator of
 // values of one sign falls short by 6.2e-9 of its size per value: 3.2e-6 over 512 values.  Draining
 // it every 256 values (4) cost the two-part input gradient 13400 clocks a tile, as much as half of
-// its MMAs.
-constexpr int kMaxChunk = 256, kFloatChunk = 8, kPartsChunk = 2;
+// its MMAs.  Float32 operands every 64 values: 1.0e-7 of the result in the root mean square, 5.9e-7
+// every 128, for 1 to 6% of the time.
+constexpr int kMaxChunk = 256, kFloatChunk = 8, kPartsChunk = 1;
 constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
 constexpr int kMostGroups = 1024;
 constexpr int kWideRows = 256, kWideStep = 32;  // rows of a tile of grouped_wide_kernel

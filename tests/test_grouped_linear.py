@@ -2,7 +2,7 @@
 
 Tolerances.  S is the sum of the products' absolute values.  A bf16 result is rounded once: 2^-8 of
 itself.  The tensor core adds 16 products at a time and truncates: at most 2^-22 of S a step, and a
-float32 addition per chunk of 128 values or more of at most 2^-24 of S: ACC(n) = (n / 16 + n / 128 +
+float32 addition per chunk of 64 values or more of at most 2^-24 of S: ACC(n) = (n / 16 + n / 128 +
 2) 2^-22.  Float32 operands are three bf16 parts (2^-24 of each value left, twice) and six products
 per value, added in as many steps: 6 ACC(n) + 2^-22.  dz is rounded to bf16 once (2^-8 of itself,
 and so of S of the products that take it; 2^-17 where dx is float32), SwiGLU's fast exponential is
