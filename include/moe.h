@@ -498,7 +498,8 @@ moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg, 
  * a multiple of 16 bytes must start on a 16-byte boundary (MOE_ERR_MISALIGNED).  Float32
  * operands run as three bf16 parts per value, as moe_linear's; partial sums leave the tensor
  * cores every 64 values (float32 operands), 512 (float32 results) or 16384.
- * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work. */
+ * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work.  Outputs must not
+ * overlap inputs or each other. */
 moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
                                 const int32_t* offsets, const void* w, void* y, void* z, void* ws,
                                 size_t ws_bytes, moe_stream_t stream);
@@ -514,7 +515,7 @@ moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
  * 16 bits instead, as two bf16 parts).  x may be NULL when dw is, w when dx is.  dy keeps to
  * the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds up to the
  * gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
- * gradient.  The same inputs give the same bits. */
+ * gradient.  The same inputs give the same bits.  Outputs must not overlap inputs or each other. */
 moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
                                          const void* x, const int32_t* offsets, const void* w,
                                          const void* z, void* dx, void* dw, void* ws,
@@ -550,8 +551,8 @@ moe_status_t moe_block_norm_workspace_size(const moe_block_norm_config_t* cfg, s
  *   x [rows,width] act; residual [rows,width] act or NULL (0); post_weight, channel_scale,
  *   norm_weight [width] float or NULL; gate [rows] float, NULL with MOE_GATE_NONE; sum [rows,width]
  *   act out or NULL; y [rows,width] act out or NULL (with norm_weight).
- * sum may be residual or x itself (same stride).  Pointers need the alignment of their elements.
- * One launch, no workspace. */
+ * sum may be residual or x itself (same stride); outputs must not overlap inputs otherwise.
+ * Pointers need the alignment of their elements.  One launch, no workspace. */
 moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
                             const void* residual, const float* post_weight, const float* gate,
                             const float* channel_scale, const float* norm_weight, void* sum,
@@ -569,7 +570,8 @@ moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
  *   [rows], dpost_weight, dchannel_scale, dnorm_weight [width] float out; each output may be NULL.
  *   ws: moe_block_norm_workspace_size() bytes, 16-byte aligned; NULL will do when no vector's
  *   gradient is asked for.
- * dx or dresidual may be dsum itself (same stride).  With rows == 0 the vectors' gradients are zeroed.
+ * dx or dresidual may be dsum itself (same stride); outputs must not overlap inputs otherwise.  With
+ * rows == 0 the vectors' gradients are zeroed.
  * The same inputs give the same bits. */
 moe_status_t moe_block_norm_backward(const moe_block_norm_config_t* cfg, const void* dy,
                                      const void* dsum, const void* x, const void* sum,

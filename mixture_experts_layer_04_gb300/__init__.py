@@ -196,9 +196,10 @@ class _Grad(ctypes.Structure):
 
 
 class GradList:
-    """The tensors of clip_grad_norm, contiguous bf16 or float32; outs: as many tensors of the same
-    sizes (the gradients themselves to clip in place), or None for the norm alone.  Holds the
-    tensors, whose storage it names."""
+    """The tensors of clip_grad_norm, contiguous bf16 or float32 on the GPU; outs: as many tensors of
+    the same sizes (the gradients themselves to clip in place), or None for the norm alone.  Holds
+    the tensors, whose storage it names.  Results that overlap one another, or another tensor's
+    gradient, are refused: they would be scaled in no fixed order."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -213,8 +214,30 @@ class GradList:
                     raise ValueError("gradients and results must be contiguous")
             if o is not None and o.numel() != g.numel():
                 raise ValueError("a result of another size than its gradient")
+            if o is not None and o.data_ptr() == g.data_ptr() and o.dtype != g.dtype:
+                raise ValueError("a result in its gradient's place but of another type")
             self.array[i] = _Grad(g.data_ptr(), None if o is None else o.data_ptr(), g.numel(),
                                   _dtype_of(g), _dtype_of(g if o is None else o))
+            for t in (g, o):
+                if t is not None and not t.is_cuda:
+                    raise ValueError("gradients and results must be on the GPU")
+        self._refuse_overlaps()
+
+    def _refuse_overlaps(self):
+        spans = []  # (first byte, end, written)
+        for g, o in zip(self.grads, self.outs or []):
+            in_place = o is not None and o.data_ptr() == g.data_ptr()
+            for t, written in ((None if in_place else g, False), (o, True)):
+                if t is not None and t.numel() > 0:
+                    at = t.data_ptr()
+                    spans.append((at, at + t.numel() * t.element_size(), written))
+        any_end = written_end = 0  # of the spans that start before
+        for at, end, written in sorted(spans):
+            if at < (any_end if written else written_end):
+                raise ValueError("a result overlaps another tensor of the list")
+            any_end = max(any_end, end)
+            if written:
+                written_end = max(written_end, end)
 
     def __len__(self):
         return len(self.grads)

@@ -215,6 +215,23 @@ def test_parts_left_out(post, gate, scale, residual, norm):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("width", [48, 64, 96, 184, 192, 368, 376, 384, 512, 1536])
+def test_many_rows_of_every_number_of_arrays(width):
+    """Rings of 46 to 48 KB among them, which need more shared memory than a launch has by default."""
+    for dtype in (BF16, F32):
+        for residual in (False, True):
+            c = Case(5000, width, dtype, residual=residual, seed=width)
+            c.check_forward(*c.forward())
+            c.check_backward(c.backward())
+            c.check_backward(c.backward(dsum=False), dsum=False)
+            c.check_backward(c.backward(dy=False), dy=False)
+            c.post = c.gate = None  # x is not read: one array, or two
+            c.cfg.gate, c.gate_kind = moe.GATE_NONE, "none"
+            c.check_backward(c.backward(outs="xr", ws=False))
+            c.check_backward(c.backward(outs="xr", ws=False, dy=False), dy=False)
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences():
     c = Case(3, 40, F32, seed=5, ab=1.25)
     g = torch.Generator(device="cuda").manual_seed(6)

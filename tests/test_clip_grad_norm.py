@@ -173,6 +173,24 @@ def test_bad_lists_in_the_binding():
             moe.GradList(grads, outs)
 
 
+@pytest.mark.gpu
+def test_results_that_overlap_are_refused():
+    flat = torch.zeros(100, device="cuda")
+    a, b = flat[:40], flat[40:80]
+    x, y = torch.zeros(40, device="cuda"), torch.zeros(40, device="cuda")
+    for grads, outs in (([x, y], [a, flat[39:79]]), ([x, x], [x, x]), ([x, a], [a, y]),
+                        ([a], [flat[1:41]]), ([x, flat], [b, None]), ([x], [x.bfloat16().float()[:39]])):
+        with pytest.raises(ValueError):
+            moe.GradList(grads, outs)
+    moe.GradList([x, x], [a, b])  # the same gradient twice is two summands
+    moe.GradList([a, b], [a, b])
+    moe.GradList([a, flat], None)
+    norm, ws = torch.zeros(1, device="cuda"), torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    x.fill_(2.0)
+    moe.clip_grad_norm(moe.GradList([x, x], [a, b]), 1.0, norm, ws)
+    assert abs(norm.item() - (80 * 4) ** 0.5) < 1e-5 and torch.equal(a, b)
+
+
 def test_bad_calls():
     lib, p = moe.load(), ctypes.c_void_p
     Grad = moe._Grad

@@ -190,6 +190,18 @@ def test_bf16(sizes, fin, fout, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("sizes", [[i % 3 for i in range(1024)], [0] * 1023 + [900],
+                                   [200] + [0] * 500 + [3] * 200, [65 + i for i in range(300)]],
+                         ids=["1024 groups", "the last", "few of 701", "300 groups"])
+def test_many_groups(sizes, dtype):
+    c = Case(sizes, 72, 64, True, dtype=dtype, tail=7, seed=12)
+    c.check_forward(*c.forward())
+    c.check_backward(*c.backward())
+    moe.sync_check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", [False, True])
 @pytest.mark.parametrize("sizes", [[4, 0, 30], [70, 1, 0, 200], [600, 300]], ids=str)
 def test_float32_results(sizes, act):
