@@ -30,7 +30,11 @@ constexpr int kPerLaunch = 512;  // tensors: 32 bytes each in the kernel's param
 constexpr int kFewTensors = 64;  // a list that short has a kernel with as short a parameter
 constexpr int kThreads = 512;
 constexpr int kLeastChunk = 4096, kMostChunk = 32768;  // elements
-constexpr int kSumBlocks = 2, kScaleBlocks = 4;  // per SM; the sum wants registers for its loads
+// Blocks per SM: the sum wants registers for its loads, and so does the scaling of a short list,
+// whose first loads wait for the factor (compiled for four blocks it spills: 640 M elements 647 us a
+// call instead of 608).
+constexpr int kSumBlocks = 2;
+constexpr int scale_blocks(int cap) { return cap <= kFewTensors ? 2 : 4; }
 constexpr int kMostBlocks = 1024;
 
 struct Entry {
@@ -39,11 +43,14 @@ struct Entry {
   int first_chunk;
   int types;  // bit 0: grad is bf16, bit 1: out is bf16
 };
-// CAP: tensors that a launch's list has room for.
+// CAP: tensors that a launch's list has room for.  A short list's chunks name their tensors, where
+// they are few, so that no block has to search for its own.
+constexpr int kNamedChunks = 1024;
 template <int CAP>
 struct ClipParams {
   Entry e[CAP];
   long long size[CAP];
+  unsigned char tensor_of[CAP <= kFewTensors ? kNamedChunks : 1];
   double* parts;
   float* norm;
   int tensors, chunks, chunk;
@@ -55,6 +62,7 @@ static_assert(sizeof(ClipParams<kPerLaunch>) <= 32764, "kernel parameters");
 
 template <int CAP>
 __device__ __forceinline__ int find(const ClipParams<CAP>& p, int chunk) {
+  if (CAP <= kFewTensors && p.chunks <= kNamedChunks) return p.tensor_of[chunk];
   int lo = 0, hi = p.tensors;
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
@@ -62,6 +70,23 @@ __device__ __forceinline__ int find(const ClipParams<CAP>& p, int chunk) {
     else hi = m;
   }
   return lo;
+}
+
+// A chunk of a tensor of a launch's list.
+struct Chunk {
+  const Entry* e;
+  long long at;
+  int n;
+};
+template <int CAP>
+__device__ __forceinline__ Chunk chunk_of(const ClipParams<CAP>& p, int c) {
+  const int t = find(p, c);
+  const long long at = static_cast<long long>(c - p.e[t].first_chunk) * p.chunk;
+  const long long left = p.size[t] - at;
+  return Chunk{&p.e[t], at, static_cast<int>(left < p.chunk ? left : p.chunk)};
+}
+__device__ __forceinline__ bool both_aligned(const void* a, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
@@ -176,14 +201,11 @@ __global__ void __launch_bounds__(kThreads, kSumBlocks) grad_squares_kernel(
   grid_dep_trigger();
   Squares sum;
   for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    const int t = find(p, c);
-    const long long at = static_cast<long long>(c - p.e[t].first_chunk) * p.chunk;
-    const long long left = p.size[t] - at;
-    const int n = static_cast<int>(left < p.chunk ? left : p.chunk);
-    if (p.e[t].types & 1)
-      chunk_squares(static_cast<const __nv_bfloat16*>(p.e[t].grad) + at, n, sum);
+    const Chunk k = chunk_of(p, c);
+    if (k.e->types & 1)
+      chunk_squares(static_cast<const __nv_bfloat16*>(k.e->grad) + k.at, k.n, sum);
     else
-      chunk_squares(static_cast<const float*>(p.e[t].grad) + at, n, sum);
+      chunk_squares(static_cast<const float*>(k.e->grad) + k.at, k.n, sum);
   }
   const double total = sum.total();
   if (threadIdx.x == 0) p.parts[p.parts_before + blockIdx.x] = total;
@@ -205,18 +227,23 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename T, typename O>
-__device__ __forceinline__ void chunk_scale(const T* g, O* out, int n, float f) {
+// first: the thread's first eight elements if `have`
+template <int U, typename T, typename O>
+__device__ __forceinline__ void chunk_scale(const T* g, O* out, int n, float f, const Raw8& first,
+                                            bool have) {
   int done = 0;
-  if (((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
+  if (both_aligned(g, out)) {
     const int vecs = n / 8;
     done = vecs * 8;
-    constexpr int U = 2;
     for (int i = threadIdx.x; i < vecs; i += U * kThreads) {
       Raw8 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + u * kThreads < vecs) r[u].load(g + (i + u * kThreads) * 8);
+        if (i + u * kThreads < vecs) {
+          if (u == 0 && have) r[u] = first;
+          else r[u].load(g + (i + u * kThreads) * 8);
+        }
+      have = false;
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (i + u * kThreads < vecs) {
@@ -246,8 +273,27 @@ __device__ __forceinline__ double quotient(double a, double b) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(
+__global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel(
     const __grid_constant__ ClipParams<CAP> p) {
+  // The gradients were complete before the launch that summed their squares: the first ones are on
+  // their way while it ends.
+  constexpr bool kAhead = CAP <= kFewTensors;
+  constexpr int U = 2;
+  int c = p.chunks - 1 - static_cast<int>(blockIdx.x);
+  Chunk k{};
+  Raw8 first;
+  bool have = false;
+  if (c >= 0) k = chunk_of(p, c);
+  if (kAhead && c >= 0) {
+    const bool bf16 = k.e->types & 1;
+    const char* g = static_cast<const char*>(k.e->grad) + k.at * (bf16 ? 2 : 4);
+    const char* out = static_cast<const char*>(k.e->out) + k.at * (k.e->types & 2 ? 2 : 4);
+    if (both_aligned(g, out) && static_cast<int>(threadIdx.x) < k.n / 8) {
+      if (bf16) first.load(reinterpret_cast<const __nv_bfloat16*>(g) + threadIdx.x * 8);
+      else first.load(reinterpret_cast<const float*>(g) + threadIdx.x * 8);
+      have = true;
+    }
+  }
   grid_dep_wait();
   grid_dep_trigger();
   // One warp adds the partial sums and one thread takes the root: the 64-bit units do two
@@ -269,29 +315,27 @@ __global__ void __launch_bounds__(kThreads, kScaleBlocks) grad_scale_kernel(
   }
   __syncthreads();
   const float f = factor;
-  for (int c = p.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
-    const int t = find(p, c);
-    const Entry& e = p.e[t];
-    if (f == 1.f && e.grad == e.out) continue;  // in place, nothing to change
-    const long long at = static_cast<long long>(c - e.first_chunk) * p.chunk;
-    const long long left = p.size[t] - at;
-    const int n = static_cast<int>(left < p.chunk ? left : p.chunk);
-    switch (e.types) {
-      case 0:
-        chunk_scale(static_cast<const float*>(e.grad) + at, static_cast<float*>(e.out) + at, n, f);
-        break;
-      case 1:
-        chunk_scale(static_cast<const __nv_bfloat16*>(e.grad) + at,
-                    static_cast<float*>(e.out) + at, n, f);
-        break;
-      case 2:
-        chunk_scale(static_cast<const float*>(e.grad) + at,
-                    static_cast<__nv_bfloat16*>(e.out) + at, n, f);
-        break;
-      default:
-        chunk_scale(static_cast<const __nv_bfloat16*>(e.grad) + at,
-                    static_cast<__nv_bfloat16*>(e.out) + at, n, f);
+  while (c >= 0) {
+    const Entry& e = *k.e;
+    const long long at = k.at;
+    if (f == 1.f && e.grad == e.out) {
+      // in place, nothing to change
+    } else if (e.types == 0) {
+      chunk_scale<U>(static_cast<const float*>(e.grad) + at, static_cast<float*>(e.out) + at, k.n, f,
+                  first, have);
+    } else if (e.types == 1) {
+      chunk_scale<U>(static_cast<const __nv_bfloat16*>(e.grad) + at, static_cast<float*>(e.out) + at,
+                  k.n, f, first, have);
+    } else if (e.types == 2) {
+      chunk_scale<U>(static_cast<const float*>(e.grad) + at, static_cast<__nv_bfloat16*>(e.out) + at,
+                  k.n, f, first, have);
+    } else {
+      chunk_scale<U>(static_cast<const __nv_bfloat16*>(e.grad) + at,
+                  static_cast<__nv_bfloat16*>(e.out) + at, k.n, f, first, have);
     }
+    c -= static_cast<int>(gridDim.x);
+    if (c >= 0) k = chunk_of(p, c);
+    have = false;
   }
 }
 
@@ -349,8 +393,12 @@ moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float ma
       e.out = g.out;
       e.first_chunk = static_cast<int>(chunks);
       e.types = (g.dtype == MOE_BF16 ? 1 : 0) | (g.out_dtype == MOE_BF16 ? 2 : 0);
+      const long long end_chunk = chunks + (g.size + p.chunk - 1) / p.chunk;
+      if (CAP <= kFewTensors)
+        for (long long c = chunks; c < end_chunk && c < kNamedChunks; ++c)
+          p.tensor_of[c] = static_cast<unsigned char>(p.tensors);
       p.size[p.tensors++] = g.size;
-      chunks += (g.size + p.chunk - 1) / p.chunk;
+      chunks = end_chunk;
       if (chunks >= (1ll << 30)) return false;
     }
     p.chunks = static_cast<int>(chunks);
@@ -379,7 +427,7 @@ moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float ma
     p.norm = out;
     p.parts_before = 0;
     p.parts_total = parts;
-    const int blocks = blocks_of(p.chunks, kScaleBlocks);
+    const int blocks = blocks_of(p.chunks, scale_blocks(CAP));
     if (launch_pdl(grad_scale_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
                    p) != cudaSuccess)
       return MOE_ERR_CUDA;
