@@ -16,7 +16,7 @@
 // 2^-55 and not 0) the eight are squared in 64 bits.
 //
 // Bound by memory: 150 bf16 tensors of 640 M elements 207 us (6.2 TB/s) and 394 us (6.5 TB/s), 608
-// us a call, 574 at a copy's rate with the second read.  23 tensors of 300 K elements 10.3 us: two
+// us a call, 574 at a copy's rate with the second read.  23 tensors of 300 K elements 7.9 us: two
 // launches.
 #include <cmath>
 

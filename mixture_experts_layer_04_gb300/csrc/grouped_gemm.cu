@@ -21,11 +21,11 @@
 //    its additions.
 //
 // Kernels, by the mean number of rows a group has (known on the host: rows and groups):
-//  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192 tokens
-//    of 8 experts of 128, 2048 -> 2 x 768 with SwiGLU: 292 us, 1,412 TFLOP/s, the tensor pipe 77%
-//    busy; rows that fill their tiles (8 groups of 1024, 14336 <-> 4096) run at 1,900;
-//  - grouped_kernel<1, 32 or 64, .., swapped>, to 32 and to 64: single CTAs, the weights on the side
-//    of 128, bound by the weights' read (512 rows over 119 of 128 groups, 768 -> 2048: 6.0 TB/s).
+//  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192
+//    tokens of 8 experts of 128, 2048 -> 2 x 768 with SwiGLU: 292 us, 1,412 TFLOP/s, the tensor pipe
+//    77% busy; rows that fill their tiles (8 groups of 1024, 14336 <-> 4096) run at 1,900;
+//  - grouped_kernel<1, 32 or 64, .., swapped>, to 32 and to 64: single CTAs, the weights on the
+//    side of 128, bound by the weights' read (512 rows over 119 of 128 groups, 768 -> 2048: 6.0 TB/s).
 //    They plan for themselves: a launch of its own took 1.8 us of one token's 15.4;
 //  - grouped_kernel<2, 256, ..>: CTA pairs for bf16 weight gradients, 256 x 256 tiles.  Bound by
 //    writing: 805 MB take 201 us by themselves here, 322 us with 412 GFLOP, 226 without the stores;
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_a);
     tma_prefetch_desc(&p.tm_b);
-    tma_prefetch_desc(&p.tm_c);
+    if (!SWAP && p.tma_c) tma_prefetch_desc(&p.tm_c);
   }
   if (warp == 1) {
     if constexpr (CTAS == 2) {
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_a);
     tma_prefetch_desc(&p.tm_b);
-    tma_prefetch_desc(&p.tm_c);
+    if (p.tma_c) tma_prefetch_desc(&p.tm_c);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), Cfg::kTmemCols);
@@ -1371,7 +1371,8 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
     if (!operand_map(tx, g.a, g.depth, rows, g.a_parts, g.lda, g.a_plane, ts.x_box))
       return cudaErrorInvalidValue;
     if (p->w_blocks ? !halves_map(tw, g)
-                    : !operand_map(tw, g.b, w_inner, w_rows, static_cast<long long>(g.b_parts) * g.groups, g.ldb,
+                    : !operand_map(tw, g.b, w_inner, w_rows,
+                                   static_cast<long long>(g.b_parts) * g.groups, g.ldb,
                                    g.ldb * w_rows, w_box))
       return cudaErrorInvalidValue;
     (ts.swap ? p->a_mn : p->b_mn) = mn;
@@ -1502,7 +1503,8 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& pla
   const bool f32 = g.a_parts == 3;
   p.chunk = f32 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk;
   if (f32) return launch_plain<1, 128, 3, 3, false>(&p, g, num_sms, s);
-  if (g.kind == GroupedKind::kWeightGrad) return launch_plain<2, 256, 1, 1, false>(&p, g, num_sms, s);
+  if (g.kind == GroupedKind::kWeightGrad)
+    return launch_plain<2, 256, 1, 1, false>(&p, g, num_sms, s);
   const bool two = g.a_parts == 2;
   switch (grouped_tile_rows(g.total_rows, g.groups, false)) {
     case 32:
