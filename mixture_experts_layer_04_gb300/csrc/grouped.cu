@@ -273,7 +273,8 @@ moe_status_t check_grouped_config(const moe_grouped_config_t* c) {
            {c->dx_stride, c->in_features}, {c->dw_stride, c->in_features}};
   for (const auto& v : q)
     if (v.stride != 0 && (v.stride < v.least || v.stride > most)) return MOE_ERR_INVALID_ARG;
-  // tiles of a product are numbered in 31 bits (the smallest tile: 32 rows, 64 features)
+  // tiles of a product are numbered in 31 bits (the smallest tile: 32 rows, 64 features, but for
+  // tiles that go round the SMs once)
   const long long rows = c->rows / 32 + c->groups;
   const long long widest = c->in_features > c->out_features ? c->in_features : c->out_features;
   const long long wg = (s.w_rows + 127ll) / 128 * ((c->in_features + 127ll) / 128) * c->groups;

@@ -79,13 +79,15 @@ struct GroupedParams {
   CUtensorMap tm_a, tm_b;  // as the sides of the tile: with swapped sides A is the weights
   CUtensorMap tm_c, tm_z;
   CUtensorMap tm_rows[3];  // wide kernel: B's map with boxes of 64, 32 and 16 rows (tm_b: 128)
-  int w_blocks;            // wide kernel, swiglu: tm_a takes both halves' blocks of 16 rows
+  int w_blocks;            // swapped sides, swiglu: tm_a takes both halves' blocks of 16 rows
   GroupPlan plan;
   GroupedKind kind;
   int groups, total_rows, num_kb, chunk;
   int beside;        // starts without waiting for the launch before it, and waits at its end
   int tiles_a;       // weight gradient: tiles along the rows of C_g
   int tiles_b;       // tiles along the features
+  int feat_step;     // features of C per tile
+  int quads;         // swapped sides: the tile's rows of weights, in 32
   int rows;          // weight gradient: rows of C_g
   int features, swiglu;
   int a_mn, b_mn;
@@ -218,7 +220,6 @@ __device__ __forceinline__ int4 fetch_tile(const GroupedParams& p, const Table& 
 template <typename Cfg>
 __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const int4& e) {
   Tile t;
-  const int step = p.swiglu ? Cfg::kTileFeatures / 2 : Cfg::kTileFeatures;
   if (p.kind != GroupedKind::kWeightGrad) {
     const int in = idx - e.z * p.tiles_b;
     const int tiles = e.w & 15, f = in / tiles;
@@ -226,7 +227,7 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const i
     t.rows = e.w >> 4;
     t.row0 = e.y + (in - f * tiles) * t.rows;
     t.row_end = 0;
-    t.feat0 = f * step;
+    t.feat0 = f * p.feat_step;
     t.k0 = 0;
     t.num_kb = p.num_kb;
     t.cut_kb = -1;
@@ -241,7 +242,7 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const i
     const int f = rest / h;
     t.row0 = (c * kRowChunk + rest - f * h) * Cfg::kTileRows;
     t.row_end = p.rows;
-    t.feat0 = f * step;
+    t.feat0 = f * p.feat_step;
     t.k0 = e.x;
     const int size = e.y - t.k0;
     t.num_kb = (size + BK - 1) / BK;
@@ -547,22 +548,26 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
           }
           const uint32_t fb = CTAS == 2 ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
           const uint32_t dst = smem_u32(smem) + stage * Cfg::kStageBytes;
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CTAS * Cfg::kStageBytes);
+          const int bytes = SWAP ? PA * p.quads * 4096 + PB * Cfg::kBBytes : CTAS * Cfg::kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(bytes));
           const int k = t.k0 + kb * BK;
 #pragma unroll
           for (int pl = 0; pl < PA; ++pl) {
             const uint32_t da = dst + pl * Cfg::kABytes;
             const int ta = a_third + pl * p.a_step;
             if constexpr (SWAP) {
-              if (p.swiglu) {  // 16 gate rows, then the same 16 up rows, for each 32 lanes
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
+              if (p.w_blocks) {  // 16 gate rows, then the same 16 up rows, for each 32 lanes
+                tma_load_5d(da, tm_a, fb, k, 0, 0, a_row >> 4, ta);
+              } else if (p.swiglu) {
+                for (int q = 0; q < p.quads; ++q) {
                   load_box<CTAS>(da + q * 4096u, tm_a, fb, k, a_row + 16 * q, ta);
                   load_box<CTAS>(da + q * 4096u + 2048u, tm_a, fb, k, p.features + a_row + 16 * q,
                                  ta);
                 }
-              } else {
+              } else if (p.quads > 2) {
                 load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
+              } else {
+                load_rows<CTAS, 64>(da, tm_a, fb, p.a_mn, a_row, k, ta);
               }
             } else {
               load_rows<CTAS, 128>(da, tm_a, fb, p.a_mn, a_row, k, ta);
@@ -726,6 +731,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
 
       if constexpr (SWAP) {
         // lanes are features, columns are rows of the groups
+        if (quad >= p.quads) continue;  // (lanes whose weights were not loaded)
         const int f = p.swiglu ? t.feat0 + quad * 16 + (lane & 15) : t.feat0 + quad * 32 + lane;
 #pragma unroll
         for (int q = 0; q < W; ++q) {
@@ -1290,9 +1296,9 @@ bool operand_map(CUtensorMap* m, const void* base, long long inner, long long ou
   return encode(m, false, base, dims, strides, BK, box_rows, 1);
 }
 
-// A swiglu layer's weights as [groups][blocks of 16][halves][16][inner], boxes of four blocks of both
+// A swiglu layer's weights as [groups][blocks of 16][halves][16][inner], boxes of some blocks of both
 // halves: 16 gate rows, the same 16 up rows, and so on.
-bool halves_map(CUtensorMap* m, const GroupedProduct& g) {
+bool halves_map(CUtensorMap* m, const GroupedProduct& g, int blocks) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t ld = static_cast<cuuint64_t>(g.ldb) * 2, half = ld * g.features;
@@ -1300,7 +1306,7 @@ bool halves_map(CUtensorMap* m, const GroupedProduct& g) {
                               static_cast<cuuint64_t>(g.features / 16),
                               static_cast<cuuint64_t>(g.groups)};
   const cuuint64_t strides[4] = {ld, half, 16 * ld, 2 * half};
-  const cuuint32_t box[5] = {BK, 16, 2, 4, 1}, estr[5] = {1, 1, 1, 1, 1};
+  const cuuint32_t box[5] = {BK, 16, 2, static_cast<cuuint32_t>(blocks), 1}, estr[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(g.b), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1355,6 +1361,20 @@ constexpr TileShape wide_shape() {
                    true};
 }
 
+// Rows of weights in a tile of swapped sides, in 32: fewer than 128 where the tiles then still go
+// round the SMs once, so that more of them stream (one token's 8 experts of 2 x 768: 96 tiles of 128
+// rows 14.1 us, 128 of 96 rows 13.8; with the weights in L2 11.7 and 11.0).  There are no more groups
+// with rows than rows.
+int tile_quads(const GroupedProduct& g, int num_sms) {
+  const long long active = std::min(g.groups, g.total_rows);
+  const bool mn = g.kind == GroupedKind::kInputGrad;  // boxes of 64
+  for (int q = 2; q < 4; ++q) {
+    if (mn && q == 3) continue;
+    if (active * ceil_div(g.features, (g.swiglu ? 16 : 32) * q) <= num_sms) return q;
+  }
+  return 4;
+}
+
 template <typename K>
 cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long>* done,
                    GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
@@ -1365,12 +1385,15 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
     const bool mn = g.kind == GroupedKind::kInputGrad;
     const long long w_rows = mn ? g.depth : g.swiglu ? 2ll * g.features : g.features;
     const long long w_inner = mn ? g.features : g.depth;
-    const int w_box = mn ? BK : g.swiglu ? ts.w_box_swiglu : ts.w_box;
+    const int w_box = mn         ? BK
+                      : g.swiglu ? ts.w_box_swiglu
+                      : p->quads ? 32 * p->quads
+                                 : ts.w_box;
     CUtensorMap* tx = ts.swap ? &p->tm_b : &p->tm_a;
     CUtensorMap* tw = ts.swap ? &p->tm_a : &p->tm_b;
     if (!operand_map(tx, g.a, g.depth, rows, g.a_parts, g.lda, g.a_plane, ts.x_box))
       return cudaErrorInvalidValue;
-    if (p->w_blocks ? !halves_map(tw, g)
+    if (p->w_blocks ? !halves_map(tw, g, p->quads ? p->quads : 4)
                     : !operand_map(tw, g.b, w_inner, w_rows,
                                    static_cast<long long>(g.b_parts) * g.groups, g.ldb,
                                    g.ldb * w_rows, w_box))
@@ -1385,7 +1408,9 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
     p->a_step = p->b_step = 1;
     p->tiles_a = ceil_div(g.rows, ts.rows);
   }
-  p->tiles_b = ceil_div(g.features, g.swiglu ? ts.features / 2 : ts.features);
+  p->feat_step = p->quads ? (g.swiglu ? 16 : 32) * p->quads
+                          : g.swiglu ? ts.features / 2 : ts.features;
+  p->tiles_b = ceil_div(g.features, p->feat_step);
   if (ts.staged) {
     const long long c_rows = weight_grad ? g.rows : rows;
     p->tma_c = output_map(&p->tm_c, g.c_f32, g.c, {g.features, c_rows, weight_grad ? g.groups : 1},
@@ -1429,6 +1454,8 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
 cudaError_t launch_plain(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
+  p->quads = SWAP ? tile_quads(g, num_sms) : 0;
+  p->w_blocks = SWAP && g.swiglu && g.features % 16 == 0;
   return launch(grouped_kernel<CTAS, BN, PA, PB, SWAP>,
                 plain_shape<GroupedCfg<CTAS, BN, PA, PB, SWAP>, CTAS, BN, SWAP>(), &done, p, g,
                 num_sms, s);
