@@ -625,7 +625,8 @@ moe_status_t moe_workspace_views(const moe_config_t* cfg, void* ws, float** logi
  * device: MOE_ERR_TIMEOUT if a bounded device-side wait gave up since the last check,
  * MOE_ERR_INTERNAL if a kernel of the debug build (compiled with -DMOE_DEBUG) found an
  * index out of range in its inputs (an expert id >= E, group offsets that decrease or
- * exceed the rows, an inverse-map or gather row out of range) and skipped that access,
+ * exceed the rows, an inverse-map or gather row out of range) and skipped that access, or if
+ * moe_grouped_linear or its backward, in any build, had to hold its offsets to the rows,
  * MOE_ERR_CUDA if the stream reports a CUDA error, MOE_OK otherwise. */
 moe_status_t moe_sync_check(moe_stream_t stream);
 
