@@ -21,9 +21,9 @@
 //    threads 265 us).  The backward does 40 operations on every element and two dependent sums per
 //    row: 8192 rows of 2048 46 us and 5 for the column sums, of 4096 81 us (5.0 TB/s); float32,
 //    with twice the bytes for the same work, 5.4 TB/s;
-//  - block_norm_kernel and block_norm_grad_kernel: few rows, rows that bulk copies cannot take, and
-//    rows of over 8192 columns, which are read again in each pass.  One row of 7168: 4.8 us, the
-//    launch.
+//  - block_norm_kernel and block_norm_grad_kernel: few rows, the forward of rows that are not
+//    multiples of 16 bytes apart and long, and rows of over 8192 columns, which are read again in
+//    each pass.  One row of 7168: 4.8 us, the launch.
 #include <atomic>
 #include <initializer_list>
 
@@ -232,64 +232,128 @@ __device__ __forceinline__ float root(float squares, float inv_width, float eps)
 
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxDepth = 8, kMostGroups = 16;
+// Shared memory that a row takes: itself, or the 16-byte pieces that hold it.
+__host__ __device__ constexpr int ring_place(int width, int value_bytes, bool aligned) {
+  return aligned ? width * value_bytes : (width * value_bytes + 30 + 15) / 16 * 16;
+}
 
 // Rows on their way to a group of threads: `depth` slots of shared memory, each with the row of up
 // to N arrays (null ones have no place), copied in bulk and counted on the slot's barrier.
-template <typename T, int N>
+//
+// Bulk copies take whole 16 bytes.  ALIGNED rows are that; of others the 16-byte pieces that hold
+// them are copied, with what they hold of the neighbouring rows.  The first and the last row have
+// no neighbour on one side, so a piece that is not all theirs is left out there and its few values
+// are read from the array (width >= 16: a piece reaches no further than the next row).
+template <typename T, int N, bool ALIGNED>
 struct Ring {
   const T* src[N];
   long long ld[N];
   uint32_t base, slot_bytes, bar0;
   uint8_t* smem;
-  int row_bytes, depth;
+  int width, rows, place, depth;  // place: bytes of a slot that a row takes
   volatile int* abort_flag;
   unsigned* err;
 
   __device__ __forceinline__ void issue(int row, int slot) const {
     const uint32_t bar = bar0 + 8u * slot;
-    mbar_arrive_expect_tx(bar, slot_bytes);
     uint32_t dst = base + slot * slot_bytes;
+    if constexpr (ALIGNED) {
+      mbar_arrive_expect_tx(bar, slot_bytes);
 #pragma unroll
-    for (int a = 0; a < N; ++a)
-      if (src[a] != nullptr) {
-        bulk_copy_g2s(dst, src[a] + row * ld[a], static_cast<uint32_t>(row_bytes), bar);
-        dst += row_bytes;
-      }
+      for (int a = 0; a < N; ++a)
+        if (src[a] != nullptr) {
+          bulk_copy_g2s(dst, src[a] + row * ld[a], static_cast<uint32_t>(place), bar);
+          dst += place;
+        }
+    } else {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int a = 0; a < N; ++a)
+        if (src[a] != nullptr) bytes += static_cast<uint32_t>(last(a, row) - first(a, row));
+      mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+      for (int a = 0; a < N; ++a)
+        if (src[a] != nullptr) {
+          const uintptr_t from = first(a, row);
+          bulk_copy_g2s(dst + static_cast<uint32_t>(from - (start(a, row) & ~kMask)),
+                        reinterpret_cast<const void*>(from),
+                        static_cast<uint32_t>(last(a, row) - from), bar);
+          dst += place;
+        }
+    }
   }
   __device__ __forceinline__ bool wait(int slot, uint32_t phase) const {
     return mbar_wait(bar0 + 8u * slot, phase, abort_flag, err);
   }
-  // column `at` on of the slot's rows (zeros for null arrays and past the end; FULL: there are none)
-  template <bool FULL>
-  __device__ __forceinline__ void read(int slot, int at, bool in, Eight<T> (&e)[N]) const {
-    const T* from = reinterpret_cast<const T*>(smem + slot * slot_bytes) + at;
-    if constexpr (FULL) {
+  // The thread's columns of the slot's rows (zeros for null arrays and past the end; FULL: there
+  // are none).
+  template <bool FULL, typename C>
+  __device__ __forceinline__ void read(int slot, int row, const C& col, int i,
+                                       Eight<T> (&e)[N]) const {
+    const uint8_t* from = smem + slot * slot_bytes;
+    if constexpr (ALIGNED) {
+      const int at = col.at(i, 0);
 #pragma unroll
       for (int a = 0; a < N; ++a) {
-        e[a].load(from);
-        from += row_bytes / static_cast<int>(sizeof(T));
+        if (FULL || (src[a] != nullptr && at < width))
+          e[a].load(reinterpret_cast<const T*>(from) + at);
+        else
+          e[a].zero();
+        if (FULL || src[a] != nullptr) from += place;
       }
-      return;
-    }
+    } else {
+      const bool edge = row == 0 || row == rows - 1;
 #pragma unroll
-    for (int a = 0; a < N; ++a) {
-      if (src[a] != nullptr && in) e[a].load(from);
-      else e[a].zero();
-      if (src[a] != nullptr) from += row_bytes / static_cast<int>(sizeof(T));
+      for (int a = 0; a < N; ++a) {
+        e[a].zero();
+        if (src[a] == nullptr) continue;
+        const T* values = reinterpret_cast<const T*>(from + (start(a, row) & kMask));
+        if (!edge) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (col.at(i, q) < width) e[a].set(q, values[col.at(i, q)]);
+        } else {
+          const T* array = src[a] + row * ld[a];
+          const uintptr_t lo = first(a, row), hi = last(a, row);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int c = col.at(i, q);
+            const uintptr_t at = reinterpret_cast<uintptr_t>(array + c);
+            if (c < width) e[a].set(q, at >= lo && at < hi ? values[c] : array[c]);
+          }
+        }
+        from += place;
+      }
     }
+  }
+
+ private:
+  static constexpr uintptr_t kMask = 15;
+  __device__ __forceinline__ uintptr_t start(int a, int row) const {
+    return reinterpret_cast<uintptr_t>(src[a] + row * ld[a]);
+  }
+  // what is copied of a row that is not aligned
+  __device__ __forceinline__ uintptr_t first(int a, int row) const {
+    return row == 0 ? (start(a, row) + kMask) & ~kMask : start(a, row) & ~kMask;
+  }
+  __device__ __forceinline__ uintptr_t last(int a, int row) const {
+    const uintptr_t end = start(a, row) + width * sizeof(T);
+    return row == rows - 1 ? end & ~kMask : (end + kMask) & ~kMask;
   }
 };
 
 // Sets a group's ring up and sends for its first rows.  Every thread of the block calls it.
-template <typename T, int N>
-__device__ __forceinline__ void start_ring(Ring<T, N>& r, uint8_t* rings, uint64_t* bars, int width,
-                                           int depth, int group, int groups, bool leader, int row,
-                                           int step, int rows) {
+template <typename T, int N, bool ALIGNED>
+__device__ __forceinline__ void start_ring(Ring<T, N, ALIGNED>& r, uint8_t* rings, uint64_t* bars,
+                                           int width, int depth, int group, int groups,
+                                           bool leader, int row, int step, int rows) {
   int arrays = 0;
 #pragma unroll
   for (int a = 0; a < N; ++a) arrays += r.src[a] != nullptr;
-  r.row_bytes = width * static_cast<int>(sizeof(T));
-  r.slot_bytes = static_cast<uint32_t>(arrays * r.row_bytes);
+  r.width = width;
+  r.rows = rows;
+  r.place = ring_place(width, static_cast<int>(sizeof(T)), ALIGNED);
+  r.slot_bytes = static_cast<uint32_t>(arrays * r.place);
   r.depth = depth;
   r.smem = rings + static_cast<size_t>(group) * depth * r.slot_bytes;
   r.base = smem_u32(r.smem);
@@ -616,7 +680,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   const float inv_width = 1.f / static_cast<float>(p.width);
   const int step = gridDim.x * groups;
   int row = blockIdx.x * groups + group;
-  Ring<T, 2> ring;
+  Ring<T, 2, true> ring;
   if (threadIdx.x == 0) gave_up = 0;
   ring.src[0] = static_cast<const T*>(p.x);
   ring.src[1] = static_cast<const T*>(p.residual);
@@ -655,8 +719,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
     Pair square = both(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int at = col.at(i, 0);
-      ring.template read<FULL>(slot, at, at < p.width, cur[i]);
+      ring.template read<FULL>(slot, r, col, i, cur[i]);
       if (p.post != nullptr) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -726,7 +789,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
 // The backward over many rows: the first sums of the next row are taken with the dot product of the
 // present one.  V: eights of columns per thread; with two, c and wn lie in shared memory.
 // FULL: every array is there and the threads' columns are the row's, as in the forward.
-template <typename T, int V, int NT, bool FULL>
+template <typename T, int V, int NT, bool FULL, bool ALIGNED>
 __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
     const __grid_constant__ NormParams p) {
   __shared__ __align__(16) float part[2][kPartFloats];
@@ -736,12 +799,12 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
   extern __shared__ __align__(128) uint8_t rings[];
   float* columns = reinterpret_cast<float*>(rings);
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
-  const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
+  const Columns<ALIGNED> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
   const int warp = col.t >> 5;
   const float inv_width = 1.f / static_cast<float>(p.width);
   const int step = gridDim.x * groups;
   int row = blockIdx.x * groups + group;
-  Ring<T, 4> ring;
+  Ring<T, 4, ALIGNED> ring;
   if (threadIdx.x == 0) gave_up = 0;
   ring.src[0] = static_cast<const T*>(p.x);
   ring.src[1] = static_cast<const T*>(p.sum_in);
@@ -797,7 +860,7 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = col.at(i, 0);
-      ring.template read<FULL>(slot, at, at < p.width, e[i]);
+      ring.template read<FULL>(slot, r, col, i, e[i]);
       if (!FULL && at >= p.width) continue;
       float w[8];
       wn[i].get(shared_w + at, w);
@@ -998,16 +1061,26 @@ Shape rows_shape(int width, int two_from, int block) {
 // threads leave, so rows that fill no more than 448 threads are compiled for that many (8192 bf16
 // rows of 7168: 206 us for 512 threads, 151 for 448).  Float32 rows would spill even so and have 8
 // columns a thread where 512 threads reach.
+//
+// Unaligned rows have 8, every `threads`-th, so that a warp's 2-byte accesses lie next to one
+// another, and no ring past 512 threads: 8000 bf16 rows of 2047 96 us, read directly 229; 700 rows
+// 22 and 34; 3000 of 333 19 and 27.  (The forward of such rows is bound by its accesses'
+// instructions either way and reads directly: 62 us through a ring, 64 without, 65536 rows of 257
+// 106 and 101.)
 constexpr int kGradBlock448 = 448;
-int grad_two_from(int dtype) { return dtype == MOE_F32 ? 8 * kRowsBlock + 1 : kTwoEights; }
-Shape grad_rows_shape(int width, int dtype) {
-  return rows_shape(width, grad_two_from(dtype), kRowsBlock);
+int grad_two_from(int dtype, bool vec) {
+  return dtype == MOE_F32 || !vec ? 8 * kRowsBlock + 1 : kTwoEights;
+}
+Shape grad_rows_shape(int width, int dtype, bool vec) {
+  Shape s = rows_shape(width, grad_two_from(dtype, vec), kRowsBlock);
+  if (!vec && (width < 16 || width > 8 * kRowsBlock)) s.keep = 0;  // (16: the ring's pieces)
+  return s;
 }
 
-// Rows in a group's ring, 0: read directly (few rows a group, or rows that bulk copies cannot take).
+// Rows in a group's ring, 0: read directly (few rows a group).
 constexpr int kRingBytes = 196608;
-int ring_depth(const Shape& s, bool vec, int rows, int blocks, int slot_bytes, int other) {
-  if (!s.keep || !vec || slot_bytes == 0) return 0;
+int ring_depth(const Shape& s, int rows, int blocks, int slot_bytes, int other) {
+  if (!s.keep || slot_bytes == 0) return 0;
   const int fits = (kRingBytes - other) / (slot_bytes * s.groups);
   const int depth = fits < kMaxDepth ? fits : kMaxDepth;
   return depth >= 2 && rows / (blocks * s.groups) >= 2 ? depth : 0;
@@ -1089,26 +1162,29 @@ cudaError_t launch_forward(const NormParams& p, int keep, bool vec, unsigned blo
 template <typename T>
 cudaError_t launch_backward(const NormParams& p, int keep, bool vec, unsigned blocks,
                             unsigned threads, size_t smem, cudaStream_t s) {
-  static std::atomic<unsigned long long> done[6];
+  static std::atomic<unsigned long long> done[7];
   if (p.depth > 0) {
+    if (!vec)
+      return launch_rows(block_norm_grad_rows_kernel<T, 1, 512, false, false>, p, blocks, threads,
+                         smem, &done[6], s);
     const bool there = p.x != nullptr && p.dy != nullptr && p.dsum != nullptr && p.dx != nullptr &&
                        p.dresidual != nullptr;
-    if (p.width < grad_two_from(sizeof(T) == 4 ? MOE_F32 : MOE_BF16))
+    if (p.width < grad_two_from(sizeof(T) == 4 ? MOE_F32 : MOE_BF16, true))
       return there && whole_rows(p, 8)
-                 ? launch_rows(block_norm_grad_rows_kernel<T, 1, 512, true>, p, blocks, threads,
-                               smem, &done[0], s)
-                 : launch_rows(block_norm_grad_rows_kernel<T, 1, 512, false>, p, blocks, threads,
-                               smem, &done[1], s);
+                 ? launch_rows(block_norm_grad_rows_kernel<T, 1, 512, true, true>, p, blocks,
+                               threads, smem, &done[0], s)
+                 : launch_rows(block_norm_grad_rows_kernel<T, 1, 512, false, true>, p, blocks,
+                               threads, smem, &done[1], s);
     const bool full = there && whole_rows(p, 16);
     if (threads <= kGradBlock448)
-      return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, true>, p, blocks,
-                                threads, smem, &done[2], s)
-                  : launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, false>, p, blocks,
-                                threads, smem, &done[3], s);
-    return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, 512, true>, p, blocks, threads,
-                              smem, &done[4], s)
-                : launch_rows(block_norm_grad_rows_kernel<T, 2, 512, false>, p, blocks, threads,
-                              smem, &done[5], s);
+      return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, true, true>, p,
+                                blocks, threads, smem, &done[2], s)
+                  : launch_rows(block_norm_grad_rows_kernel<T, 2, kGradBlock448, false, true>, p,
+                                blocks, threads, smem, &done[3], s);
+    return full ? launch_rows(block_norm_grad_rows_kernel<T, 2, 512, true, true>, p, blocks,
+                              threads, smem, &done[4], s)
+                : launch_rows(block_norm_grad_rows_kernel<T, 2, 512, false, true>, p, blocks,
+                              threads, smem, &done[5], s);
   }
   if (keep && threads <= 512)
     return launch_pdl(vec ? block_norm_grad_kernel<T, 1, true, 512>
@@ -1163,13 +1239,12 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
   // one group's rows follow one another through its ring, so a block per SM; without one, blocks
   // of a few groups fill the SMs
   const bool sums = post_weight != nullptr || y != nullptr;
-  const long long ab2 = static_cast<long long>(ab);
   const NormParams q = params_of(cfg, 0);
   const bool vec = all_vec(cfg->width, cfg->dtype,
                            {{x, q.ldx}, {residual, q.ldr}, {sum, q.lds}, {y, q.ldy}});
-  const int slot = static_cast<int>((residual != nullptr ? 2 : 1) * cfg->width * ab2);
+  const int slot = (residual != nullptr ? 2 : 1) * cfg->width * static_cast<int>(ab);
   Shape sh = rows_shape(cfg->width, kTwoEights, kRowsBlock);
-  const int depth = sums ? ring_depth(sh, vec, cfg->rows, sms, slot, 0) : 0;
+  const int depth = sums && vec ? ring_depth(sh, cfg->rows, sms, slot, 0) : 0;
   long long most = sms;
   if (depth == 0) {
     sh = shape_of(cfg->width, 256);
@@ -1264,11 +1339,12 @@ extern "C" moe_status_t moe_block_norm_backward(
                             {dx, p.lddx}, {dresidual, p.lddr}});
   int arrays = 0;
   for (const void* q : {p.x, p.sum_in, dy, dsum}) arrays += q != nullptr;
-  const int slot = arrays * cfg->width * static_cast<int>(ab);
-  const Shape rs = grad_rows_shape(cfg->width, cfg->dtype);
-  const int vector_bytes = cfg->width >= grad_two_from(cfg->dtype) ? 2 * cfg->width * 4 : 0;  // c and wn
+  const int slot = arrays * ring_place(cfg->width, static_cast<int>(ab), vec);
+  const Shape rs = grad_rows_shape(cfg->width, cfg->dtype, vec);
+  const int vector_bytes =  // c and wn
+      vec && cfg->width >= grad_two_from(cfg->dtype, vec) ? 2 * cfg->width * 4 : 0;
   int blocks = grad_blocks(cfg, sms < kMostSms ? sms : kMostSms);
-  p.depth = ring_depth(rs, vec, cfg->rows, blocks, slot, vector_bytes);
+  p.depth = ring_depth(rs, cfg->rows, blocks, slot, vector_bytes);
   if (p.depth > 0) {
     sh = rs;
     p.threads = sh.threads;

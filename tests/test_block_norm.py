@@ -231,6 +231,57 @@ def test_many_rows_of_every_number_of_arrays(width):
             c.check_backward(c.backward(outs="xr", ws=False, dy=False), dy=False)
 
 
+def embedded(t, width, start, pad):
+    """t's rows of `width` in a buffer of NaN, `start` values into it and `pad` apart."""
+    flat = torch.full((start + t.shape[0] * (width + pad) + 8,), float("nan"), dtype=t.dtype,
+                      device="cuda")
+    rows = flat[start:start + t.shape[0] * (width + pad)].view(t.shape[0], width + pad)
+    rows[:, :width] = t[:, :width]
+    return rows[:, :width]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width,pad", [(15, 0), (16, 1), (17, 0), (33, 2), (64, 3), (255, 0),
+                                       (257, 0), (511, 4), (512, 1), (513, 0), (1001, 5),
+                                       (2047, 0), (2048, 1), (4095, 0), (4097, 0), (5287, 0),
+                                       (8191, 0)])
+def test_many_unaligned_rows(width, pad, dtype):
+    """Their copies take pieces of the neighbouring rows along, which hold NaN here."""
+    rows = 5000 if width < 1000 else 700
+    for start in (0, 3):
+        for residual in (False, True):
+            c = Case(rows, width, dtype, residual=residual, pad=pad, seed=width)
+            for name in ("x", "res", "s", "ds", "dy"):
+                t = getattr(c, name)
+                if t is not None:
+                    setattr(c, name, embedded(t, width, start, pad))
+            c.check_forward(*c.forward())
+            c.check_backward(c.backward())
+            c.check_backward(c.backward(dsum=False), dsum=False)
+            c.check_backward(c.backward(dy=False), dy=False)
+            c.check_backward(c.backward(outs="xr", ws=False))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [1001, 2047])
+def test_many_unaligned_rows_in_place(width):
+    c = Case(2000, width, BF16, seed=8)
+    s0, y0 = c.forward()
+    for over in ("x", "res"):
+        ins = dict(x=c.x.clone(), res=c.res.clone())
+        y = c.matrix()
+        moe.block_norm(c.cfg, ins["x"], ins["res"], c.post, c.gate, c.scale, c.norm, ins[over], y)
+        assert torch.equal(ins[over], s0) and torch.equal(y, y0)
+    want = c.backward()
+    for over in (0, 1):
+        outs = [c.matrix(), c.matrix()]
+        outs[over] = ds = c.ds.clone()
+        moe.block_norm_backward(c.cfg, c.dy, ds, c.x, c.s, c.post, c.gate, c.scale, c.norm, *outs,
+                                None, None, None, None, None)
+        assert torch.equal(outs[0], want["dx"]) and torch.equal(outs[1], want["dres"])
+
+
 @pytest.mark.gpu
 def test_gradients_against_differences():
     c = Case(3, 40, F32, seed=5, ab=1.25)
