@@ -653,8 +653,12 @@ moe_status_t moe_debug_wait_timeout(unsigned limit_us, int* done, moe_stream_t s
  *  - the stages inside moe_layer_forward: "moe_layer_forward.route", ".permute",
  *    ".gate_up", ".shared", ".down", ".combine": checked before that stage's launches, so
  *    the earlier stages have been enqueued on the stream.  y is then untouched; the
- *    workspace (and y_f32 with MOE_FLAG_FUSED_COMBINE) may hold partial results.
- * Thread-safe; the fault is process-wide.  No GPU state is involved. */
+ *    workspace (and y_f32 with MOE_FLAG_FUSED_COMBINE) may hold partial results;
+ *  - "moe_block_norm.copy", "moe_block_norm_backward.copy": passed by the calls whose rows are
+ *    copied ahead through shared memory (many rows).  Here the call goes on and returns MOE_OK, but
+ *    one row of every block never counts as arrived: the bounded wait for it runs out after 2 ms,
+ *    the kernel ends with rows unwritten, and the next moe_sync_check reports MOE_ERR_TIMEOUT.
+ * Thread-safe; the fault is process-wide.  But for the last, no GPU state is involved. */
 moe_status_t moe_debug_set_fault(const char* point, int n);
 
 /* Number of kernels this library has launched in this process, on every device: each

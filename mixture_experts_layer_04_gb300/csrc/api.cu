@@ -469,6 +469,7 @@ const char* const kFaultPoints[] = {
     "moe_grouped_linear",      "moe_grouped_linear_backward", "moe_grouped_linear_workspace_size",
     "moe_block_norm",          "moe_block_norm_backward",   "moe_block_norm_workspace_size",
     "moe_clip_grad_norm",      "moe_clip_grad_norm_workspace_size",
+    "moe_block_norm.copy",     "moe_block_norm_backward.copy",
     "moe_layer_forward.route", "moe_layer_forward.permute", "moe_layer_forward.gate_up",
     "moe_layer_forward.shared", "moe_layer_forward.down",   "moe_layer_forward.combine"};
 

@@ -138,6 +138,8 @@ struct NormParams {
   int threads;  // per row
   int depth;    // rows on their way per group of threads (ring kernels)
   float eps, residual_scale, branch_scale;
+  int lost;  // fault injection: the second row of the blocks' first groups never counts as arrived
+  unsigned long long wait_ns;  // after which a ring gives up
   unsigned* err;
 };
 
@@ -251,6 +253,7 @@ struct Ring {
   uint32_t base, slot_bytes, bar0;
   uint8_t* smem;
   int width, rows, place, depth;  // place: bytes of a slot that a row takes
+  unsigned long long wait_ns;
   volatile int* abort_flag;
   unsigned* err;
 
@@ -283,7 +286,19 @@ struct Ring {
     }
   }
   __device__ __forceinline__ bool wait(int slot, uint32_t phase) const {
-    return mbar_wait(bar0 + 8u * slot, phase, abort_flag, err);
+    return mbar_wait(bar0 + 8u * slot, phase, abort_flag, err, wait_ns);
+  }
+  // The group has given up on `row`, whose slot is the next: what else was sent for must have landed
+  // before the ring's memory serves something else or goes back.  One more limit for all of it.
+  __device__ __forceinline__ void drain(int row, int step, int slot, uint32_t phase) const {
+    volatile int late = 0;
+    for (int k = 0; k < depth && row + k * step < rows; ++k) {
+      mbar_wait(bar0 + 8u * slot, phase, &late, err, wait_ns);
+      if (++slot == depth) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
   }
   // The thread's columns of the slot's rows (zeros for null arrays and past the end; FULL: there
   // are none).
@@ -345,7 +360,7 @@ struct Ring {
 // Sets a group's ring up and sends for its first rows.  Every thread of the block calls it.
 template <typename T, int N, bool ALIGNED>
 __device__ __forceinline__ void start_ring(Ring<T, N, ALIGNED>& r, uint8_t* rings, uint64_t* bars,
-                                           int width, int depth, int group, int groups,
+                                           int width, int depth, int lost, int group, int groups,
                                            bool leader, int row, int step, int rows) {
   int arrays = 0;
 #pragma unroll
@@ -359,7 +374,8 @@ __device__ __forceinline__ void start_ring(Ring<T, N, ALIGNED>& r, uint8_t* ring
   r.base = smem_u32(r.smem);
   r.bar0 = smem_u32(bars + group * kMaxDepth);
   if (leader)
-    for (int k = 0; k < depth; ++k) mbar_init(r.bar0 + 8u * k, 1);
+    for (int k = 0; k < depth; ++k)  // (a lost slot lacks an arrival)
+      mbar_init(r.bar0 + 8u * k, lost && group == 0 && k == 1 ? 2 : 1);
   fence_mbar_init();
   __syncthreads();
   grid_dep_wait();
@@ -673,6 +689,9 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   __shared__ __align__(16) float part[2][kPartFloats];
   __shared__ uint64_t bars[kMostGroups * kMaxDepth];
   __shared__ int gave_up;
+  // Each thread sees for itself whether its row arrived, but a row's threads go on, or leave,
+  // together: what is left here before the barrier of the row's sums, they all read behind it.
+  __shared__ volatile int missing[2][kMostGroups];
   extern __shared__ __align__(128) uint8_t rings[];
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
   const Columns<true> col{static_cast<int>(threadIdx.x) - group * p.threads, p.threads, p.width};
@@ -682,13 +701,17 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   int row = blockIdx.x * groups + group;
   Ring<T, 2, true> ring;
   if (threadIdx.x == 0) gave_up = 0;
+  if (threadIdx.x < 2 * kMostGroups)
+    missing[threadIdx.x / kMostGroups][threadIdx.x % kMostGroups] = 0;
   ring.src[0] = static_cast<const T*>(p.x);
   ring.src[1] = static_cast<const T*>(p.residual);
   ring.ld[0] = p.ldx;
   ring.ld[1] = p.ldr;
+  ring.wait_ns = p.wait_ns;
   ring.abort_flag = &gave_up;
   ring.err = p.err;
-  start_ring(ring, rings, bars, p.width, p.depth, group, groups, col.t == 0, row, step, p.rows);
+  start_ring(ring, rings, bars, p.width, p.depth, p.lost, group, groups, col.t == 0, row, step,
+             p.rows);
   Pair c[V][4], wn[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -731,14 +754,15 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
     sums[1] = add_up(square);
     return true;
   };
-  auto reduce = [&] {
+  auto reduce = [&](bool arrived) {
+    if (!arrived) missing[area][group] = 1;
     row_sum<2>(sums, part[area] + group * (p.threads >> 5) * 2, group, p.threads, warp);
+    if (p.threads == 32) __syncwarp();
+    arrived = missing[area][group] == 0;
     area ^= 1;
+    return arrived;
   };
-  if (ok) {
-    ok = next_row(row);
-    reduce();
-  }
+  if (ok) ok = reduce(next_row(row));
   for (; ok; row += step) {
     const float f = p.post != nullptr ? gate * root(sums[1], inv_width, p.eps) : gate;
     // the barrier has passed, so every thread has this row out of its slot
@@ -761,7 +785,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
       }
     sums[0] = add_up(square);
     const bool more = row + step < p.rows;
-    if (more) ok = next_row(row + step);
+    bool arrived = !more || next_row(row + step);
     if (FULL || p.sum != nullptr) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -770,7 +794,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
         col.template store<FULL>(static_cast<T*>(p.sum) + row * p.lds, i, v);
       }
     }
-    reduce();
+    arrived = reduce(arrived);
     if (FULL || p.y != nullptr) {
       const Pair rs = both(root(sums[0], inv_width, p.eps));
 #pragma unroll
@@ -782,8 +806,10 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
         col.template store<FULL>(static_cast<T*>(p.y) + row * p.ldy, i, v);
       }
     }
-    ok = ok && more;
+    ok = more && arrived;
   }
+  // (in the loop this cost 16384 rows of 7168 162 us instead of 142)
+  if (col.t == 0 && (missing[0][group] | missing[1][group]) != 0) ring.drain(row, step, slot, phase);
 }
 
 // The backward over many rows: the first sums of the next row are taken with the dot product of the
@@ -795,6 +821,7 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
   __shared__ __align__(16) float part[2][kPartFloats];
   __shared__ uint64_t bars[kMostGroups * kMaxDepth];
   __shared__ int gave_up;
+  __shared__ volatile int missing[2][kMostGroups];  // as in the forward
   // the rings, then (V > 1) c and wn; after the last row the groups' sums: [groups - 1][2][width]
   extern __shared__ __align__(128) uint8_t rings[];
   float* columns = reinterpret_cast<float*>(rings);
@@ -806,6 +833,8 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
   int row = blockIdx.x * groups + group;
   Ring<T, 4, ALIGNED> ring;
   if (threadIdx.x == 0) gave_up = 0;
+  if (threadIdx.x < 2 * kMostGroups)
+    missing[threadIdx.x / kMostGroups][threadIdx.x % kMostGroups] = 0;
   ring.src[0] = static_cast<const T*>(p.x);
   ring.src[1] = static_cast<const T*>(p.sum_in);
   ring.src[2] = static_cast<const T*>(p.dy);
@@ -813,9 +842,11 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
   ring.ld[0] = p.ldx;
   ring.ld[1] = ring.ld[3] = p.lds;
   ring.ld[2] = p.ldy;
+  ring.wait_ns = p.wait_ns;
   ring.abort_flag = &gave_up;
   ring.err = p.err;
-  start_ring(ring, rings, bars, p.width, p.depth, group, groups, col.t == 0, row, step, p.rows);
+  start_ring(ring, rings, bars, p.width, p.depth, p.lost, group, groups, col.t == 0, row, step,
+             p.rows);
   float* shared_c = reinterpret_cast<float*>(rings + static_cast<size_t>(groups) * p.depth *
                                                          ring.slot_bytes);
   const float* shared_w = shared_c + p.width;
@@ -877,14 +908,15 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
     sums[3] = add_up(ds);
     return true;
   };
-  auto reduce = [&] {
+  auto reduce = [&](bool arrived) {
+    if (!arrived) missing[area][group] = 1;
     row_sum<4>(sums, part[area] + group * (p.threads >> 5) * 4, group, p.threads, warp);
+    if (p.threads == 32) __syncwarp();
+    arrived = missing[area][group] == 0;
     area ^= 1;
+    return arrived;
   };
-  if (ok) {
-    ok = next_row(row, cur);
-    reduce();
-  }
+  if (ok) ok = reduce(next_row(row, cur));
   for (; ok; row += step) {
     const float rx = p.post != nullptr ? root(sums[1], inv_width, p.eps) : 1.f;
     const float rs = FULL || p.dy != nullptr ? root(sums[2], inv_width, p.eps) : 0.f;
@@ -929,8 +961,7 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
     }
     sums[0] = add_up(dot);
     const bool more = row + step < p.rows;
-    if (more) ok = next_row(row + step, cur);
-    reduce();
+    const bool arrived = reduce(!more || next_row(row + step, cur));
     if (p.dgate != nullptr && col.t == 0) p.dgate[row] = gate_slope * sums[0];
     if (FULL || p.dx != nullptr) {
       const Pair d2 = both(p.post != nullptr ? -rx * rx * (sums[0] * inv_width) : 0.f);
@@ -944,8 +975,9 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
         col.template store<FULL>(static_cast<T*>(p.dx) + row * p.lddx, i, out);
       }
     }
-    ok = ok && more;
+    ok = more && arrived;
   }
+  if (col.t == 0 && (missing[0][group] | missing[1][group]) != 0) ring.drain(row, step, slot, phase);
   if (p.parts == nullptr) return;
   __syncthreads();  // every group's last row has left its slot
   float n8[V][8], a8[V][8];
@@ -1106,7 +1138,15 @@ NormParams params_of(const moe_block_norm_config_t* c, int threads) {
   p.eps = c->eps;
   p.residual_scale = c->residual_scale;
   p.branch_scale = c->branch_scale;
+  p.wait_ns = kWaitLimitNs;
   return p;
+}
+
+// Fault injection: a row that never counts as arrived, so a wait runs out, in 2 ms.
+void maybe_lose_a_row(const char* point, NormParams* p) {
+  if (p->depth == 0 || fault_point(point) == MOE_OK) return;
+  p->lost = 1;
+  p->wait_ns = 2000000;
 }
 
 // 16-byte accesses to every array, null ones aside.
@@ -1254,6 +1294,7 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
   const long long need = (static_cast<long long>(cfg->rows) + sh.groups - 1) / sh.groups;
   NormParams p = params_of(cfg, sh.threads);
   p.depth = depth;
+  maybe_lose_a_row("moe_block_norm.copy", &p);
   p.err = device_error_word();
   p.x = x;
   p.residual = residual;
@@ -1352,6 +1393,7 @@ extern "C" moe_status_t moe_block_norm_backward(
     if (blocks > most) blocks = most;
   }
   const unsigned threads = static_cast<unsigned>(sh.threads * sh.groups);
+  maybe_lose_a_row("moe_block_norm_backward.copy", &p);
   p.err = device_error_word();
   // the groups' column sums take the rings' place in the end
   const size_t column_sums =
