@@ -275,8 +275,7 @@ __device__ __forceinline__ double quotient(double a, double b) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel(
     const __grid_constant__ ClipParams<CAP> p) {
-  // The gradients were complete before the launch that summed their squares: the first ones are on
-  // their way while it ends.
+  // A short list's first gradients are on their way while the factor is worked out.
   constexpr bool kAhead = CAP <= kFewTensors;
   constexpr int U = 2;
   int c = p.chunks - 1 - static_cast<int>(blockIdx.x);
@@ -284,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel
   Raw8 first;
   bool have = false;
   if (c >= 0) k = chunk_of(p, c);
+  grid_dep_wait();
+  grid_dep_trigger();
   if (kAhead && c >= 0) {
     const bool bf16 = k.e->types & 1;
     const char* g = static_cast<const char*>(k.e->grad) + k.at * (bf16 ? 2 : 4);
@@ -294,8 +295,6 @@ __global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel
       have = true;
     }
   }
-  grid_dep_wait();
-  grid_dep_trigger();
   // One warp adds the partial sums and one thread takes the root: the 64-bit units do two
   // operations a clock (in all 512 threads this took 6 us).
   __shared__ float factor;
