@@ -9,6 +9,7 @@
 //    (101 at a copy's rate).
 #include "common.cuh"
 #include "grouped.h"
+#include "grouped_plan.cuh"
 #include "kernels.h"
 #include "linear_act.cuh"
 
@@ -111,8 +112,9 @@ struct DzTask {
 struct PrepareParams {
   const int32_t* offsets;
   int rows, groups;
+  PlanTask plan;
   DzTask dz;
-  PackTask x, w;
+  PackTask dy, x, w;
 };
 
 // Calls f(row, eight of columns) for the items that are this thread's; 32-bit divisions where they
@@ -197,12 +199,19 @@ __device__ __forceinline__ void dz_task(const DzTask& t, int used, int block) {
   });
 }
 
-// Launched behind the plan kernel, on which it does not depend: the plan lets it start once what
-// came before the call is complete, and it waits for the plan at its end, for the products' sake.
+// The plan's blocks first: they are the longest where little is packed.  (One launch for both: a
+// packing that followed the plan's launch took 2 to 5 us more.)
 template <typename T, int PL>
 __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams p) {
   __shared__ int s_used;
+  grid_dep_wait();
   grid_dep_trigger();
+  int b = static_cast<int>(blockIdx.x);
+  if (b < p.plan.blocks) {
+    plan_block(p.plan, b);
+    return;
+  }
+  b -= p.plan.blocks;
   if (threadIdx.x == 0) s_used = 0;
   __syncthreads();
   // the end of the last group: the largest offset, held to the rows
@@ -212,19 +221,26 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
   if ((threadIdx.x & 31) == 0) atomicMax(&s_used, used);
   __syncthreads();
   used = min(s_used, p.rows);
-  int b = static_cast<int>(blockIdx.x);
   if (b < p.dz.blocks) {
     dz_task<T, PL>(p.dz, used, b);
-  } else {
-    b -= p.dz.blocks;
-    if (b < p.x.blocks) pack_task<T, PL>(p.x, p, used, b);
-    else pack_task<T, PL>(p.w, p, used, b - p.x.blocks);
+    return;
   }
-  grid_dep_wait();
+  b -= p.dz.blocks;
+  const PackTask* t = &p.dy;
+  if (b >= p.dy.blocks) {
+    b -= p.dy.blocks;
+    t = &p.x;
+    if (b >= p.x.blocks) {
+      b -= p.x.blocks;
+      t = &p.w;
+    }
+  }
+  pack_task<T, PL>(*t, p, used, b);
 }
 
 cudaError_t launch_prepare(const PrepareParams& p, bool f32, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.dz.blocks + p.x.blocks + p.w.blocks));
+  const dim3 grid(static_cast<unsigned>(p.plan.blocks + p.dz.blocks + p.dy.blocks + p.x.blocks +
+                                        p.w.blocks));
   return f32 ? launch_pdl(prepare_kernel<float, 3>, grid, dim3(256), 0, s, p)
              : launch_pdl(prepare_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s, p);
 }
@@ -427,14 +443,13 @@ extern "C" moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, cons
   const Operand ow = operand(w, sh.w, static_cast<long long>(cfg->groups) * sh.w_rows,
                              cfg->in_features, sh.w_rows, cfg->dtype, l.pack_w, at.at<void>(l.w),
                              sms, &pp.w);
-  const bool prepare = pp.x.blocks + pp.w.blocks > 0;
-  if (!prepare && grouped_plans_itself(l.tile_rows, sh.f32)) {
+  if (pp.x.blocks + pp.w.blocks == 0 && grouped_plans_itself(l.tile_rows, sh.f32)) {
     plan.offsets = offsets;
-  } else if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan, nullptr, err,
-                               s) != cudaSuccess) {
+  } else if (!group_plan_task(offsets, cfg->rows, cfg->groups, l.tile_rows, plan, nullptr, err,
+                              &pp.plan) ||
+             launch_prepare(pp, sh.f32, s) != cudaSuccess) {
     return MOE_ERR_CUDA;
   }
-  if (prepare && launch_prepare(pp, sh.f32, s) != cudaSuccess) return MOE_ERR_CUDA;
   GroupedProduct g{};
   g.kind = GroupedKind::kForward;
   g.groups = cfg->groups;
@@ -508,10 +523,9 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   if (dx != nullptr)
     ow = operand(w, sh.w, static_cast<long long>(cfg->groups) * sh.w_rows, cfg->in_features,
                  sh.w_rows, cfg->dtype, l.pack_w, at.at<void>(l.w), sms, &pp.w);
-  PackTask pack_dy{};
   if (l.make_dz && !sh.swiglu) {
     odz = operand(dy, sh.y, cfg->rows, cfg->out_features, 0, cfg->dtype, true, at.at<void>(l.dz),
-                  sms, &pack_dy);
+                  sms, &pp.dy);
   } else if (l.make_dz) {
     DzTask& t = pp.dz;
     t.dy = dy;
@@ -562,21 +576,14 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   // a float32 weight gradient fills the SMs that the input gradient leaves idle (both wait for the
   // packing alone); the others take CTA pairs, which run in stream order
   gw.beside = sh.f32 && dx != nullptr;
-  const bool prepare = pack_dy.blocks + pp.dz.blocks + pp.x.blocks + pp.w.blocks > 0;
-  if (dw == nullptr && !prepare && grouped_plans_itself(l.tile_rows, sh.f32)) {
+  const bool pack = pp.dz.blocks + pp.dy.blocks + pp.x.blocks + pp.w.blocks > 0;
+  if (dw == nullptr && !pack && grouped_plans_itself(l.tile_rows, sh.f32)) {
     plan.offsets = offsets;
-  } else if (launch_group_plan(offsets, cfg->rows, cfg->groups, l.tile_rows, plan,
-                               dw != nullptr ? &gw : nullptr, err, s) != cudaSuccess) {
+  } else if (!group_plan_task(offsets, cfg->rows, cfg->groups, l.tile_rows, plan,
+                              dw != nullptr ? &gw : nullptr, err, &pp.plan) ||
+             launch_prepare(pp, sh.f32, s) != cudaSuccess) {
     return MOE_ERR_CUDA;
   }
-  if (pack_dy.blocks > 0) {
-    PrepareParams first = pp;
-    first.w = PackTask{};
-    first.x = pack_dy;
-    if (launch_prepare(first, sh.f32, s) != cudaSuccess) return MOE_ERR_CUDA;
-  }
-  if (pp.dz.blocks + pp.x.blocks + pp.w.blocks > 0 && launch_prepare(pp, sh.f32, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
   if (dx != nullptr && launch_grouped_product(gx, plan, err, sms, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (dw != nullptr && launch_grouped_product(gw, plan, err, sms, s) != cudaSuccess)

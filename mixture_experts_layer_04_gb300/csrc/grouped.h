@@ -11,7 +11,7 @@ enum class GroupedKind : int {
   kWeightGrad = 2,    // C_g [rows][features] = A_g^T . B_g           (A_g, B_g: the group's rows)
 };
 
-// What the kernels need to know about the groups, in device memory: written by the plan kernel.
+// What the kernels need to know about the groups, in device memory: made by grouped_plan.cuh.
 struct GroupPlan {
   int* bounds;    // [groups + 1], the offsets clamped to ascend within 0..rows
   int4* tiles;    // per tile of rows: {group, first row of its chunk, first tile of its chunk,
@@ -52,10 +52,6 @@ int grouped_tile_rows(int total_rows, int groups, bool f32);
 bool grouped_plans_itself(int tile_rows, bool f32);
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows);
 
-// Reads the offsets; with `weight_grad` (may be null) also writes its operands' maps.
-cudaError_t launch_group_plan(const int32_t* offsets, int rows, int groups, int tile_rows,
-                              const GroupPlan& plan, const GroupedProduct* weight_grad, unsigned* err,
-                              cudaStream_t s);
 cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& plan, unsigned* err,
                                 int num_sms, cudaStream_t s);
 

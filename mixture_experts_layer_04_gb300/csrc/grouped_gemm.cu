@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "grouped.h"
+#include "grouped_plan.cuh"
 #include "linear_act.cuh"
 #include "tc_operand.cuh"
 
@@ -49,9 +50,6 @@ constexpr int BK = 64;
 // its MMAs.  Float32 operands every 64 values: 1.0e-7 of the result in the root mean square, 5.9e-7
 // every 128, for 1 to 6% of the time.
 constexpr int kMaxChunk = 256, kFloatChunk = 8, kPartsChunk = 1;
-constexpr int kRowChunk = 8;    // tiles of rows that share the weights' tiles in L2
-constexpr int kMostGroups = 1024;
-constexpr int kWideRows = 256, kWideStep = 32;  // rows of a tile of grouped_wide_kernel
 
 // PA, PB: bf16 parts per value on the A and on the B side.
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
@@ -106,102 +104,9 @@ struct Tile {
   int cut_kb;      // the block that the group's end cuts (weight gradient), or -1
 };
 
-// The plan in shared memory of a kernel that plans for itself (bound null: the plan kernel's).
-struct Table {
-  int* bound;  // [groups + 1]
-  int* first;  // [groups + 1]: first tile of rows of each group, then their number
-};
-
 __device__ __forceinline__ int total_tiles(const GroupedParams& p, const Table& table) {
   if (p.kind == GroupedKind::kWeightGrad) return p.groups * p.tiles_a * p.tiles_b;
   return (table.bound != nullptr ? table.first[p.groups] : *p.plan.count) * p.tiles_b;
-}
-
-// The last group whose first tile is not past tile i (so one that has tiles).
-__device__ __forceinline__ int group_of_tile(const int* first, int groups, int i) {
-  int lo = 0, hi = groups;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (first[m] <= i) lo = m;
-    else hi = m;
-  }
-  return lo;
-}
-
-// Tile i of rows as the table of tiles has it.
-__device__ __forceinline__ int4 table_entry(const Table& t, int groups, int i, int tile_rows) {
-  const int g = group_of_tile(t.first, groups, i);
-  const int first = t.first[g], tiles = t.first[g + 1] - first;
-  const int chunk = first + (i - first) / kRowChunk * kRowChunk;
-  // rows of the group's tiles: even shares, where a tile need not be full
-  const int size = t.bound[g + 1] - t.bound[g];
-  const int rows = tile_rows == kWideRows
-                       ? ((size + tiles - 1) / tiles + kWideStep - 1) / kWideStep * kWideStep
-                       : tile_rows;
-  return make_int4(g, t.bound[g] + (chunk - first) * rows, chunk,
-                   min(kRowChunk, first + tiles - chunk) | rows << 4);
-}
-
-// Reads the offsets (at most 1025) and makes them ascend within 0..rows: a running maximum, so that
-// bad ones cannot lead a kernel out of its buffers; `report`: one block tells of them through the
-// error word.  Then the groups' first tiles.  Every thread of the block calls it; PER groups a
-// thread; scratch: 32 ints.
-template <int PER>
-__device__ __forceinline__ void make_table(const int32_t* offsets, int rows, int groups,
-                                           int tile_rows, const Table& t, int* scratch, bool report,
-                                           unsigned* err) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int start = min(max(offsets[0], 0), rows);
-  int given[PER], bound[PER];
-  int most = start;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int g = tid * PER + k;
-    given[k] = g < groups ? offsets[g + 1] : start;
-    most = max(most, min(max(given[k], 0), rows));
-    bound[k] = most;
-  }
-  int before = most;  // running maximum over the threads up to this one
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before = max(before, n);
-  }
-  if (lane == 31) scratch[warp] = before;
-  before = __shfl_up_sync(0xffffffffu, before, 1);
-  if (lane == 0) before = start;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) before = max(before, scratch[w]);
-  bool bad = tid == 0 && offsets[0] != start;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int g = tid * PER + k;
-    bound[k] = max(bound[k], before);
-    if (g < groups) {
-      t.bound[g + 1] = bound[k];
-      bad |= given[k] != bound[k];
-    }
-  }
-  if (tid == 0) t.bound[0] = start;
-  if (report && bad) report_error(err, MOE_DEVERR_BOUNDS);
-  __syncthreads();
-  int tiles[PER], sum = 0;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int g = tid * PER + k;
-    tiles[k] = g < groups ? (t.bound[g + 1] - t.bound[g] + tile_rows - 1) / tile_rows : 0;
-    sum += tiles[k];
-  }
-  int total;
-  int at = block_exclusive_scan(sum, scratch, &total);
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int g = tid * PER + k;
-    if (g < groups) t.first[g] = at;
-    at += tiles[k];
-  }
-  if (tid == 0) t.first[groups] = total;
-  __syncthreads();
 }
 
 // What tile idx's place is read from, to be loaded while the tile before it is worked on: the
@@ -1210,64 +1115,6 @@ __global__ void __launch_bounds__(WideCfg<PB>::kThreads, 1)
   cluster_sync_all();  // the pair gives its TMEM back before either CTA leaves
 }
 
-// ---------------------------------------------------------------------- plan ----
-
-struct PlanParams {
-  const int32_t* offsets;
-  GroupPlan plan;
-  int rows, groups, tile_rows;
-  unsigned* err;
-  CUtensorMap tm_a, tm_b;  // whole operands of the weight gradient
-};
-
-constexpr int kPlanThreads = kMostGroups;
-
-// Every block makes the table for itself; block 0 writes the bounds and the table of the tiles of
-// rows, and all blocks share the groups' tensor maps.
-__global__ void __launch_bounds__(kPlanThreads) group_plan_kernel(
-    const __grid_constant__ PlanParams p) {
-  __shared__ int s_bound[kMostGroups + 1], s_first[kMostGroups + 1];
-  __shared__ int scratch[32];
-  __shared__ alignas(128) uint32_t s_map[kPlanThreads / 32][32];
-  grid_dep_wait();
-  grid_dep_trigger();
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const Table table{s_bound, s_first};
-  make_table<1>(p.offsets, p.rows, p.groups, p.tile_rows, table, scratch, blockIdx.x == 0, p.err);
-  if (blockIdx.x == 0) {
-    const int total = s_first[p.groups];
-    if (t == 0) {
-      *p.plan.count = total;
-      p.plan.bounds[0] = s_bound[0];
-    }
-    if (t < p.groups) p.plan.bounds[t + 1] = s_bound[t + 1];
-    for (int i = t; i < total; i += kPlanThreads)
-      p.plan.tiles[i] = table_entry(table, p.groups, i, p.tile_rows);
-  }
-  if (p.plan.maps == nullptr) return;
-  const int warps = gridDim.x * (kPlanThreads / 32);
-  for (int i = blockIdx.x * (kPlanThreads / 32) + warp; i < 2 * p.groups; i += warps) {
-    const CUtensorMap* from = i & 1 ? &p.tm_b : &p.tm_a;
-    s_map[warp][lane] = reinterpret_cast<const uint32_t*>(from)[lane];
-    __syncwarp();
-    const uint32_t sm = smem_u32(s_map[warp]);
-    if (lane == 0) {
-      // (a map with no rows is never used)
-      asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(sm),
-                   "r"(max(s_bound[(i >> 1) + 1], 1))
-                   : "memory");
-    }
-    __syncwarp();
-    asm volatile(
-        "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
-        "[%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(
-            static_cast<CUtensorMap*>(p.plan.maps) + i)),
-        "r"(sm)
-        : "memory");
-    __syncwarp();
-  }
-}
-
 // ---------------------------------------------------------------------- host ----
 
 inline int ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
@@ -1486,26 +1333,24 @@ size_t grouped_max_tiles(int total_rows, int groups, int tile_rows) {
          static_cast<size_t>(std::min(groups, total_rows));
 }
 
-cudaError_t launch_group_plan(const int32_t* offsets, int rows, int groups, int tile_rows,
-                              const GroupPlan& plan, const GroupedProduct* wg, unsigned* err,
-                              cudaStream_t s) {
-  PlanParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.offsets = offsets;
-  p.plan = plan;
-  p.rows = rows;
-  p.groups = groups;
-  p.tile_rows = tile_rows;
-  p.err = err;
-  unsigned blocks = 1;
-  if (wg != nullptr) {
-    if (!rows_map(&p.tm_a, *wg, true) || !rows_map(&p.tm_b, *wg, false))
-      return cudaErrorInvalidValue;
-    blocks = static_cast<unsigned>(ceil_div(2ll * groups, kPlanThreads / 32));
-  } else {
-    p.plan.maps = nullptr;
+bool group_plan_task(const int32_t* offsets, int rows, int groups, int tile_rows,
+                     const GroupPlan& plan, const GroupedProduct* wg, unsigned* err, PlanTask* t) {
+  std::memset(t, 0, sizeof(*t));
+  t->offsets = offsets;
+  t->plan = plan;
+  t->rows = rows;
+  t->groups = groups;
+  t->tile_rows = tile_rows;
+  t->err = err;
+  // 256 tiles of rows a block, up to 16 of them; a map a warp
+  const size_t tiles = grouped_max_tiles(rows, groups, tile_rows) / kPlanThreads + 1;
+  t->blocks = static_cast<int>(std::min<size_t>(tiles, 16));
+  if (wg == nullptr) {
+    t->plan.maps = nullptr;
+    return true;
   }
-  return launch_pdl(group_plan_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, p);
+  t->blocks = std::max(t->blocks, ceil_div(2ll * groups, kPlanThreads / 32));
+  return rows_map(&t->tm_a, *wg, true) && rows_map(&t->tm_b, *wg, false);
 }
 
 cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& plan, unsigned* err,

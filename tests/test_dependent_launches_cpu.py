@@ -16,7 +16,7 @@ from tests.conftest import ROOT
 
 CSRC = os.path.join(ROOT, "mixture_experts_layer_04_gb300", "csrc")
 WAIT, TRIGGER = "grid_dep_wait();", "grid_dep_trigger();"
-LEFT = ("grouped.cu", "grouped_gemm.cu")
+LEFT = ("grouped_gemm.cu",)
 READS = re.compile(r"\.load\(|__ldg\(|\bload\w*\(|p\.offsets\[|\bcol\.vector\(")
 
 
