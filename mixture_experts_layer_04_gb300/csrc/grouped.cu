@@ -226,16 +226,13 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
     return;
   }
   b -= p.dz.blocks;
-  const PackTask* t = &p.dy;
-  if (b >= p.dy.blocks) {
-    b -= p.dy.blocks;
-    t = &p.x;
-    if (b >= p.x.blocks) {
-      b -= p.x.blocks;
-      t = &p.w;
-    }
+  if (b < p.dy.blocks) {
+    pack_task<T, PL>(p.dy, p, used, b);
+    return;
   }
-  pack_task<T, PL>(*t, p, used, b);
+  b -= p.dy.blocks;
+  if (b < p.x.blocks) pack_task<T, PL>(p.x, p, used, b);
+  else pack_task<T, PL>(p.w, p, used, b - p.x.blocks);
 }
 
 cudaError_t launch_prepare(const PrepareParams& p, bool f32, cudaStream_t s) {
@@ -470,7 +467,7 @@ extern "C" moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, cons
   g.z = z;
   g.z_f32 = sh.f32;
   g.ldz = sh.z;
-  return status_of(launch_grouped_product(g, plan, err, sms, s));
+  return status_of(launch_grouped_products(&g, 1, plan, err, sms, s));
 }
 
 extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
@@ -573,9 +570,6 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   gw.ldc = sh.dw;
   gw.c_group = sh.dw * sh.w_rows;
 
-  // a float32 weight gradient fills the SMs that the input gradient leaves idle (both wait for the
-  // packing alone); the others take CTA pairs, which run in stream order
-  gw.beside = sh.f32 && dx != nullptr;
   const bool pack = pp.dz.blocks + pp.dy.blocks + pp.x.blocks + pp.w.blocks > 0;
   if (dw == nullptr && !pack && grouped_plans_itself(l.tile_rows, sh.f32)) {
     plan.offsets = offsets;
@@ -584,9 +578,9 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
              launch_prepare(pp, sh.f32, s) != cudaSuccess) {
     return MOE_ERR_CUDA;
   }
-  if (dx != nullptr && launch_grouped_product(gx, plan, err, sms, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  if (dw != nullptr && launch_grouped_product(gw, plan, err, sms, s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return MOE_OK;
+  GroupedProduct both[2];
+  int n = 0;
+  if (dx != nullptr) both[n++] = gx;
+  if (dw != nullptr) both[n++] = gw;
+  return status_of(launch_grouped_products(both, n, plan, err, sms, s));
 }

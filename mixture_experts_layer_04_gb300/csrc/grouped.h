@@ -40,7 +40,6 @@ struct GroupedProduct {
   void* c;
   int c_f32;
   long long ldc, c_group;  // c_group: elements between the groups of a weight gradient
-  int beside;              // needs nothing of the launch before it but what that one needed itself
   void* z;                 // forward with swiglu: [total rows][2 features] or null
   int z_f32;
   long long ldz;
@@ -52,7 +51,8 @@ int grouped_tile_rows(int total_rows, int groups, bool f32);
 bool grouped_plans_itself(int tile_rows, bool f32);
 size_t grouped_max_tiles(int total_rows, int groups, int tile_rows);
 
-cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& plan, unsigned* err,
-                                int num_sms, cudaStream_t s);
+// n products (1 or 2) one after the other; those of float32 operands in one launch.
+cudaError_t launch_grouped_products(const GroupedProduct* g, int n, const GroupPlan& plan,
+                                    unsigned* err, int num_sms, cudaStream_t s);
 
 }  // namespace moe

