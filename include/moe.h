@@ -599,8 +599,8 @@ moe_status_t moe_clip_grad_norm_workspace_size(int n, size_t* bytes);
  * out  = grad * grad_scale * min(1, max_norm / (norm + eps)) where out is not NULL.
  * Squares are summed in 64 bits, those outside float's range included; the factor is rounded to
  * float once, each output once.  A norm that is NaN makes every output NaN; an infinite one makes
- * the factor 0.  max_norm may be infinite (the scale alone).  In place, where the factor is 1,
- * nothing is written.
+ * the factor 0 (an infinite element then becomes NaN).  max_norm may be infinite: the factor is
+ * grad_scale, unless the norm is NaN.  In place, where the factor is 1, nothing is written.
  *   grads: n entries in HOST memory, read during the call only (0 <= n <= 2^20); norm [1] float
  *   out (device) or NULL; ws: moe_clip_grad_norm_workspace_size() bytes, 16-byte aligned.
  * grad_scale > 0 and finite (1 over a loss scale), max_norm > 0, eps >= 0.  Pointers need the

@@ -306,8 +306,12 @@ __global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel
     if (threadIdx.x == 0) {
       const double norm = root_of(total) * static_cast<double>(p.scale);
       if (p.norm != nullptr && blockIdx.x == 0) *p.norm = static_cast<float>(norm);
-      const double room = quotient(static_cast<double>(p.max_norm), norm + static_cast<double>(p.eps));
-      // (a norm that is NaN makes the factor NaN; an infinite one makes it 0)
+      // a norm that is NaN makes the factor NaN; an infinite one makes it 0, but where max_norm is
+      // infinite, too: then there is nothing to clip to, and the quotient would be NaN
+      const double room =
+          p.max_norm < INFINITY
+              ? quotient(static_cast<double>(p.max_norm), norm + static_cast<double>(p.eps))
+              : norm == norm ? 1.0 : norm;
       factor = static_cast<float>(static_cast<double>(p.scale) *
                                   (room < 1.0 || room != room ? room : 1.0));
     }
