@@ -214,7 +214,9 @@ class GradList:
                     raise ValueError("gradients and results must be contiguous")
             if o is not None and o.numel() != g.numel():
                 raise ValueError("a result of another size than its gradient")
-            if o is not None and o.data_ptr() == g.data_ptr() and o.dtype != g.dtype:
+            # (tensors without elements have no place: their addresses are all 0)
+            if (o is not None and g.numel() > 0 and o.data_ptr() == g.data_ptr()
+                    and o.dtype != g.dtype):
                 raise ValueError("a result in its gradient's place but of another type")
             self.array[i] = _Grad(g.data_ptr(), None if o is None else o.data_ptr(), g.numel(),
                                   _dtype_of(g), _dtype_of(g if o is None else o))
