@@ -223,6 +223,8 @@ class GradList:
             for t in (g, o):
                 if t is not None and not t.is_cuda:
                     raise ValueError("gradients and results must be on the GPU")
+                if t is not None and t.device != self.grads[0].device:
+                    raise ValueError("gradients and results must be on one GPU")
         self._refuse_overlaps()
 
     def _refuse_overlaps(self):

@@ -37,3 +37,12 @@ def test_empty_gradients_with_results_of_another_type():
     assert (lst.array[1].dtype, lst.array[1].out_dtype) == (moe.BF16, moe.F32)
     with pytest.raises(ValueError):  # in place, with elements
         moe.GradList([OnGpu(A, 8, torch.bfloat16)], [OnGpu(A, 8)])
+
+
+def test_tensors_of_two_gpus_are_refused():
+    """One launch reads all of them: on another GPU that is a fault, or slow."""
+    a, b = OnGpu(A, 8), OnGpu(A + 64, 8, device=1)
+    for grads, outs in (([a, b], None), ([a], [b]), ([b], [a]), ([a, OnGpu(A + 128, 4)], [a, b])):
+        with pytest.raises(ValueError):
+            moe.GradList(grads, outs)
+    moe.GradList([b, OnGpu(A + 128, 4, device=1)], None)
