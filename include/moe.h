@@ -551,7 +551,8 @@ moe_status_t moe_block_norm_workspace_size(const moe_block_norm_config_t* cfg, s
  *   x [rows,width] act; residual [rows,width] act or NULL (0); post_weight, channel_scale,
  *   norm_weight [width] float or NULL; gate [rows] float, NULL with MOE_GATE_NONE; sum [rows,width]
  *   act out or NULL; y [rows,width] act out or NULL (with norm_weight).
- * sum may be residual or x itself (same stride); outputs must not overlap inputs otherwise.
+ * sum may be residual or x itself, with the same stride (MOE_ERR_INVALID_ARG: another one); outputs
+ * must not overlap inputs otherwise.
  * Pointers need the alignment of their elements.  One launch, no workspace. */
 moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
                             const void* residual, const float* post_weight, const float* gate,
@@ -570,8 +571,8 @@ moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const void* x,
  *   [rows], dpost_weight, dchannel_scale, dnorm_weight [width] float out; each output may be NULL.
  *   ws: moe_block_norm_workspace_size() bytes, 16-byte aligned; NULL will do when no vector's
  *   gradient is asked for.
- * dx or dresidual may be dsum itself (same stride); outputs must not overlap inputs otherwise.  With
- * rows == 0 the vectors' gradients are zeroed.
+ * dx or dresidual may be dsum itself, with the same stride (MOE_ERR_INVALID_ARG: another one); outputs
+ * must not overlap inputs otherwise.  With rows == 0 the vectors' gradients are zeroed.
  * The same inputs give the same bits. */
 moe_status_t moe_block_norm_backward(const moe_block_norm_config_t* cfg, const void* dy,
                                      const void* dsum, const void* x, const void* sum,

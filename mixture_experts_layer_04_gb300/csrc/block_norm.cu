@@ -1273,13 +1273,17 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_config_t* cfg, const
     if (unaligned(q, ab)) return MOE_ERR_MISALIGNED;
   for (const float* q : {post_weight, gate, channel_scale, norm_weight})
     if (unaligned(q, 4)) return MOE_ERR_MISALIGNED;
+  const NormParams q = params_of(cfg, 0);
+  // in place, but rows elsewhere: one row's result would overwrite another's input
+  if ((sum != nullptr && sum == x && q.lds != q.ldx) ||
+      (sum != nullptr && sum == residual && q.lds != q.ldr))
+    return MOE_ERR_INVALID_ARG;
   st = check_current_device();
   if (st != MOE_OK) return st;
   const int sms = device_num_sms();
   // one group's rows follow one another through its ring, so a block per SM; without one, blocks
   // of a few groups fill the SMs
   const bool sums = post_weight != nullptr || y != nullptr;
-  const NormParams q = params_of(cfg, 0);
   const bool vec = all_vec(cfg->width, cfg->dtype,
                            {{x, q.ldx}, {residual, q.ldr}, {sum, q.lds}, {y, q.ldy}});
   const int slot = (residual != nullptr ? 2 : 1) * cfg->width * static_cast<int>(ab);
@@ -1354,14 +1358,17 @@ extern "C" moe_status_t moe_block_norm_backward(
       (dnorm_weight != nullptr && dy == nullptr) ||
       (x == nullptr && (own || (dx != nullptr && post_weight != nullptr))))
     return MOE_ERR_INVALID_ARG;
+  Shape sh = shape_of(cfg->width, kGradBlock);
+  NormParams p = params_of(cfg, sh.threads);
+  // in place, but rows elsewhere, as in the forward
+  if (dsum != nullptr && ((dx == dsum && p.lddx != p.lds) || (dresidual == dsum && p.lddr != p.lds)))
+    return MOE_ERR_INVALID_ARG;
   const int sms = device_num_sms();
   const size_t need = static_cast<size_t>(grad_blocks(cfg, kMostSms)) * 2 * cfg->width * 4 + 16;
   if (vectors && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   if (vectors && unaligned(ws, 16)) return MOE_ERR_MISALIGNED;
   st = check_current_device();
   if (st != MOE_OK) return st;
-  Shape sh = shape_of(cfg->width, kGradBlock);
-  NormParams p = params_of(cfg, sh.threads);
   // (read only where something needs it)
   p.x = own || (dx != nullptr && post_weight != nullptr) ? x : nullptr;
   p.sum_in = dy != nullptr ? sum : nullptr;
