@@ -6,9 +6,10 @@
 //   input gradient   C_r  = sum_n A[r,n] B_g[n,f]      the same rows; reduction over outputs
 //   weight gradient  C_g  = sum_r A[r,n] B[r,f]        reduction over the group's rows
 //
-// One persistent kernel for all three: TMA loads either operand layout in 128-byte swizzled boxes
-// (k-contiguous, or row-contiguous for the weights of the input gradient and both operands of the
-// weight gradient) and the descriptors name the layout, so nothing is transposed in memory.
+// Two persistent kernels (grouped_kernel in several forms): TMA loads either operand layout in
+// 128-byte swizzled boxes (k-contiguous, or row-contiguous for the weights of the input gradient and
+// both operands of the weight gradient) and the descriptors name the layout, so nothing is transposed
+// in memory.
 //  - Tiles of rows start at a group's first row and run over its end; the rows past it belong to
 //    the next group (a row of the result depends on its own row of A alone) and are not stored.
 //  - The reduction of the weight gradient must end with the group: what follows may be another
@@ -360,6 +361,12 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
     grouped_kernel(const __grid_constant__ GroupedJobs<kMostJobs<PA>> jobs) {
   using Cfg = GroupedCfg<CTAS, BN, PA, PB, SWAP>;
   constexpr int S = Cfg::kStages;
+  // what a kernel of this form is launched for
+  static_assert(SWAP ? CTAS == 1 && PA == 1 : (CTAS == 2 && PB == 1) || (PA == 3 && PB == 3), "form");
+  auto is_weight_grad = [](const GroupedParams& p) {  // CTA pairs: always; swapped sides: never
+    return CTAS == 2 || (!SWAP && p.kind == GroupedKind::kWeightGrad);
+  };
+  auto with_swiglu = [](const GroupedParams& p) { return CTAS == 1 && p.swiglu != 0; };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -463,22 +470,13 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         if (idx + step < total) entry = fetch(idx + step);
         const CUtensorMap* tm_a = &p.tm_a;
         const CUtensorMap* tm_b = &p.tm_b;
-        int a_row, b_row, a_third, b_third;
-        if (p.kind == GroupedKind::kWeightGrad) {
-          a_row = t.row0 + static_cast<int>(rank) * 128;
-          b_row = t.feat0 + static_cast<int>(rank) * Cfg::kBRows;
-          a_third = b_third = 0;
-        } else if constexpr (SWAP) {
+        int a_row = t.row0 + static_cast<int>(rank) * 128, a_third = 0;
+        int b_row = t.feat0 + static_cast<int>(rank) * Cfg::kBRows, b_third = 0;
+        if constexpr (SWAP) {
           a_row = t.feat0;
           b_row = t.row0;
           a_third = t.group;
-          b_third = 0;
-        } else {
-          a_row = t.row0 + static_cast<int>(rank) * 128;
-          // with swiglu the odd CTA has the up half's rows
-          b_row = p.swiglu ? t.feat0 + static_cast<int>(rank) * p.features
-                           : t.feat0 + static_cast<int>(rank) * Cfg::kBRows;
-          a_third = 0;
+        } else if (!is_weight_grad(p)) {
           b_third = t.group;
         }
         for (int kb = 0; kb < t.num_kb; ++kb) {
@@ -525,7 +523,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
             const int tb = b_third + pl * p.b_step;
             if constexpr (SWAP) {
               load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
-            } else if (CTAS == 1 && p.swiglu) {  // gate and up halves of the tile
+            } else if (with_swiglu(p)) {  // gate and up halves of the tile
               load_box<CTAS>(db, tm_b, fb, k, b_row, tb);
               load_box<CTAS>(db + Cfg::kBBytes / 2, tm_b, fb, k, p.features + b_row, tb);
             } else {
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
                              static_cast<uint32_t>((local & 1) * BN);
         // with swiglu (sides not swapped) the first half of a warp's columns are the gate's
         auto column = [&](int i) {
-          return !SWAP && p.swiglu ? (i / ((NP + 1) / 2)) * W + part * (W / 2) +
+          return !SWAP && with_swiglu(p) ? (i / ((NP + 1) / 2)) * W + part * (W / 2) +
                                          (i % ((NP + 1) / 2)) * P
                                    : part * W + i * P;
         };
@@ -706,7 +704,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         uint8_t* stg = stg_all + (warp - 2) * 4096;
         const int row0 = t.row0 + static_cast<int>(rank) * 128 + quad * 32;
         if (row0 >= t.row_end) continue;
-        const bool weight_grad = p.kind == GroupedKind::kWeightGrad;
+        const bool weight_grad = is_weight_grad(p);
         // rows past a weight's last are clipped by TMA, those past a group's end would not be
         const bool whole = weight_grad || row0 + 32 <= t.row_end;
         Out oc{&p.tm_c, static_cast<char*>(p.c), p.ldc, p.features, 0, 0, p.tma_c, p.vec_c};
@@ -738,22 +736,22 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
         constexpr integral_constant<int, 0> zero{};
         constexpr integral_constant<int, NP / 2> mid{};
         constexpr integral_constant<int, NP> all{};
-        if (!p.swiglu) {
+        if (!with_swiglu(p)) {
           emit(oc, t.feat0 + part * W, zero, all);
-        } else {
+        } else if constexpr (CTAS == 1) {
           const int col = t.feat0 + part * (W / 2);
           if (p.z != nullptr) {
             Out oz{&p.tm_z, static_cast<char*>(p.z), p.ldz, p.features, 0, 1, p.tma_z, p.vec_z};
             emit(oz, col, zero, mid);
             oz.third = 1;
-            oz.base += static_cast<long long>(p.features) * (PA == 3 ? 4 : 2);
+            oz.base += static_cast<long long>(p.features) * 4;
             emit(oz, col, mid, mid);
           }
 #pragma unroll
           for (int i = 0; i < NP / 2; ++i)
 #pragma unroll
             for (int q = 0; q < P; ++q)
-              sum[i][q] = act_value<PA != 3>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
+              sum[i][q] = act_value<false>(MOE_ACT_SILU, sum[i][q]) * sum[i + NP / 2][q];
           emit(oc, col, zero, mid);
         }
       }
@@ -1242,7 +1240,7 @@ template <typename Cfg, int CTAS, int BN, bool SWAP>
 constexpr TileShape plain_shape() {
   return TileShape{Cfg::kTileRows, Cfg::kTileFeatures, SWAP, SWAP ? BN : 128,
                    SWAP ? 128 : Cfg::kBRows,
-                   SWAP ? 16 : CTAS == 1 ? Cfg::kBRows / 2 : Cfg::kBRows,
+                   SWAP ? 16 : Cfg::kBRows / 2,
                    CTAS, Cfg::kThreads, Cfg::kSmem, !SWAP};
 }
 template <int PB>
