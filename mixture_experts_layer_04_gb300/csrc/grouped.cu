@@ -162,14 +162,13 @@ __device__ __forceinline__ void store_dz(__nv_bfloat16* dst, const DzTask& t, in
   else store_parts<2>(dst, t.plane, n, t.vec_dz != 0, v);
 }
 
-// silu(z) = z p and its slope p (1 + z q), with p the logistic function of z and q = 1 - p, for bf16
-// z: one exponential and one reciprocal for both.  The slope is good to 2^-22 of 1; the bf16 numbers
-// nearest to its zero (-1.2785) have slopes over 2^-11, so to 2^-11 of itself.
+// silu(z) = z p and its slope, with p the logistic function of z, for bf16 z: one exponential and one
+// reciprocal for both.
 __device__ __forceinline__ void silu_both(float z, float* value, float* slope) {
   const float t = __expf(-fabsf(z)), r = rcp_ftz(1.0f + t), tr = t * r;
   const float p = z > 0.f ? r : tr, q = z > 0.f ? tr : r;
   *value = z * p;
-  *slope = p * fmaf(z, q, 1.0f);
+  *slope = silu_slope<true>(z, p, q);
 }
 
 template <typename T, int PL>

@@ -84,6 +84,23 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
   }
 }
 
+// The slope of silu at z, whose logistic function is p = 1 - q.  p (1 + z q); for z < 0 the bracket is
+// q (1 + z + e^z), which vanishes at z0 and is there d + e^z0 (e^d - 1) with d = z - z0, whose terms
+// have one sign: nothing cancels.
+template <bool kFast>
+__device__ __forceinline__ float silu_slope(float z, float p, float q) {
+  const float d = (z + 1.2784645557403564f) - 1.2979282759673083e-08f;
+  float bracket = fmaf(z, q, 1.0f);
+  if (kFast) {  // a column's sum is float32, so near z0 the slope keeps its accuracy too
+    const float series =  // e^d - 1 to 2e-6 of itself for |d| < 1/4
+        d * fmaf(d, fmaf(d, fmaf(d, fmaf(d, 1.0f / 120.f, 1.0f / 24.f), 1.0f / 6.f), 0.5f), 1.0f);
+    bracket = fabsf(d) < 0.25f ? q * fmaf(0.27846454f, series, d) : bracket;
+  } else if (z < 0.f) {
+    bracket = q * fmaf(0.2784645427610737f, expm1f(d), d);
+  }
+  return p * bracket;
+}
+
 // d act / d z (ReLU: 0 at 0).
 template <bool kFast>
 __device__ __forceinline__ float act_slope(int act, float z) {
@@ -108,22 +125,9 @@ __device__ __forceinline__ float act_slope(int act, float z) {
       return q > 0.f ? fmaf(z * q, c * fmaf(0.134145f, z2, 1.0f), p) : p;
     }
     case MOE_ACT_SILU: {
-      // p (1 + z q) with q = 1 - p; for z < 0 the bracket is q (1 + z + e^z), which vanishes at
-      // z0 and is there d + e^z0 (e^d - 1) with d = z - z0, whose terms have one sign: nothing
-      // cancels
-      const float d = (z + 1.2784645557403564f) - 1.2979282759673083e-08f;
       const float t = kFast ? __expf(-fabsf(z)) : expf(-fabsf(z));
       const float r = kFast ? rcp_ftz(1.0f + t) : 1.0f / (1.0f + t);
-      const float p = z > 0.f ? r : t * r, q = z > 0.f ? t * r : r;
-      float bracket = fmaf(z, q, 1.0f);
-      if (kFast) {  // a column's sum is float32, so near z0 the slope keeps its accuracy too
-        const float series =  // e^d - 1 to 2e-6 of itself for |d| < 1/4
-            d * fmaf(d, fmaf(d, fmaf(d, fmaf(d, 1.0f / 120.f, 1.0f / 24.f), 1.0f / 6.f), 0.5f), 1.0f);
-        bracket = fabsf(d) < 0.25f ? q * fmaf(0.27846454f, series, d) : bracket;
-      } else if (z < 0.f) {
-        bracket = q * fmaf(0.2784645427610737f, expm1f(d), d);
-      }
-      return p * bracket;
+      return silu_slope<kFast>(z, z > 0.f ? r : t * r, z > 0.f ? t * r : r);
     }
     default:
       return 1.f;
