@@ -496,8 +496,9 @@ moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg, 
  * held to the largest before them and to rows, and reported by moe_sync_check
  * (MOE_ERR_INTERNAL).  Pointers need the alignment of their elements; x and w whose row stride is
  * a multiple of 16 bytes must start on a 16-byte boundary (MOE_ERR_MISALIGNED).  Float32
- * operands run as three bf16 parts per value, as moe_linear's; partial sums leave the tensor
- * cores every 64 values (float32 operands), 512 (float32 results) or 16384.
+ * operands run as three bf16 parts per value, as moe_linear's (where an input is infinite or NaN the
+ * outputs that it reaches are not finite); partial sums leave the tensor cores every 64 values
+ * (float32 operands), 256 (float32 results; with over 64 rows a group in the mean, 512) or 16384.
  * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work.  Outputs must not
  * overlap inputs or each other. */
 moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,

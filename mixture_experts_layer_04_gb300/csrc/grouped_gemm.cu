@@ -17,9 +17,9 @@
 //    of tensor maps, copies of the call's maps whose number of rows is the group's end: TMA then
 //    fills the rest of the block that the end cuts with zeros.  The plan kernel writes them; the
 //    blocks before the last use the call's own.
-//  - A float32 result leaves the tensor core every 512 values (float32 operands, six products per
-//    value: 64), a bf16 one every 16384, and is added up in registers: the tensor core truncates
-//    its additions.
+//  - A float32 result leaves the tensor core every 256 values (many rows a group: 512; float32
+//    operands, six products per value: 64), a bf16 one every 16384, and is added up in registers:
+//    the tensor core truncates its additions.
 //
 // Kernels, by the mean number of rows a group has (known on the host: rows and groups):
 //  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192
@@ -45,12 +45,14 @@ namespace moe {
 namespace {
 
 constexpr int BK = 64;
-// K-blocks per accumulator: of a bf16 result, of a float one, of float operands.  An accumulator of
-// values of one sign falls short by 6.2e-9 of its size per value: 3.2e-6 over 512 values.  Draining
-// it every 256 values (4) cost the two-part input gradient 13400 clocks a tile, as much as half of
-// its MMAs.  Float32 operands every 64 values: 1.0e-7 of the result in the root mean square, 5.9e-7
-// every 128, for 1 to 6% of the time.
-constexpr int kMaxChunk = 256, kFloatChunk = 8, kPartsChunk = 1;
+// K-blocks per accumulator: of a bf16 result, of a float one of few rows a group, of one of many, of
+// float operands.  An accumulator of values of one sign falls short by up to 6.2e-9 of its size per
+// value: 1.6e-6 over 256 values, 3.2e-6 over 512.  Few rows wait for the weights' read, so every 256
+// values cost them nothing (63.1 us and 63.3, 512 rows of 119 groups, 768 -> 2048); in the wide kernel
+// they would cost a forward of 65536 rows of these 253 -> 323 us, the two-part input gradient 505 ->
+// 560 (13400 clocks a tile, as much as half of its MMAs).  Float32 operands every 64 values: 1.0e-7 of
+// the result in the root mean square, 5.9e-7 every 128, for 1 to 6% of the time.
+constexpr int kMaxChunk = 256, kFloatChunk = 4, kWideFloatChunk = 8, kPartsChunk = 1;
 
 // PA, PB: bf16 parts per value on the A and on the B side.
 template <int CTAS, int BN, int PA, int PB, bool SWAP>
@@ -1405,6 +1407,7 @@ cudaError_t launch_wide(const GroupedProduct& g, const Launch& l) {
                      64 >> b))
       return cudaErrorInvalidValue;
   p.w_blocks = g.swiglu && g.features % 16 == 0;
+  if (g.c_f32) p.chunk = kWideFloatChunk;
   long long tiles = 0;
   const cudaError_t e = lay_out(wide_shape<PB>(), &p, g, &tiles);
   if (e != cudaSuccess) return e;

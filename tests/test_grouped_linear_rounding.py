@@ -35,3 +35,29 @@ def test_the_slope_keeps_its_accuracy_near_its_zero():
     want = c.dy.double() * c.z[:, n:].double() * (s * (1 + g * (1 - s)))
     assert_close(dx, want, want.abs() * (PARTS + FAST) + 1e-37)
     moe.sync_check()
+
+
+@pytest.mark.parametrize("sizes", [[9, 0, 20], [70, 50]], ids=str)
+@pytest.mark.parametrize("fin,fout", [(14336, 64), (4096, 200)])
+def test_float32_sums_leave_the_tensor_core_every_256_values(sizes, fin, fout):
+    """Values of one sign, whose truncated additions add up in the mean error of the results (their own
+    roundings, 2^-25 each, average out).  The linear layers leave 1.4e-8 with 256 values and 7.3e-7
+    with 1024; the limit lies between, as in test_linear_accumulation.  (Over 64 rows a group they leave
+    it every 512.)"""
+    c = Case(sizes, fin, fout, False, out=F32, seed=32)
+    c.x.copy_(torch.rand(c.x.shape, device="cuda") + 0.5)
+    c.w.copy_(torch.rand(c.w.shape, device="cuda") + 0.5)
+    y, _ = c.forward()
+    for e, at, w in c.groups():
+        want = c.x[at].double() @ w.t()
+        rel = (y[at].double() - want) / want
+        assert abs(rel.mean().item()) < 1.5e-7
+    d = Case(sizes, fout, fin, False, dx=F32, seed=33)  # the reduction of dx: over outputs
+    d.dy.copy_(torch.rand(d.dy.shape, device="cuda") + 0.5)
+    d.w.copy_(torch.rand(d.w.shape, device="cuda") + 0.5)
+    dx, _ = d.backward(want_dw=False)
+    for e, at, w in d.groups():
+        want = d.dy[at].double() @ w
+        rel = (dx[at].double() - want) / want
+        assert abs(rel.mean().item()) < 1.5e-7
+    moe.sync_check()
