@@ -472,7 +472,7 @@ typedef struct {
   int32_t out_features;    /* 1..2^18; columns of y */
   int32_t dtype;           /* moe_dtype_t of x, w, z, dy and dw ("act") */
   int32_t out_dtype;       /* moe_dtype_t of y: dtype, or MOE_F32 */
-  int32_t dx_dtype;        /* moe_dtype_t of dx: dtype, or MOE_F32 */
+  int32_t dx_dtype;        /* moe_dtype_t of dx: dtype, or MOE_F32 (dw's accuracy goes by it) */
   int32_t activation;      /* MOE_ACT_NONE or MOE_ACT_SWIGLU */
   /* elements between rows, 0 = contiguous; the groups' weights follow one another */
   int64_t x_stride, w_stride, y_stride, z_stride, dx_stride, dw_stride;
@@ -512,10 +512,11 @@ moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
  *   returned it (NULL without an activation); dx [rows,in] dx_dtype out or NULL, rows that belong
  *   to no group left as they were; dw [groups, out or 2 out, in] act out or NULL, every element
  *   written; ws as above (NULL with rows == 0, which zeroes dw).
- * dz is rounded to act before the products (for a float32 dx of a bf16 SWIGLU layer it is held in
- * 16 bits instead, as two bf16 parts).  x may be NULL when dw is, w when dx is.  dy keeps to
- * the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds up to the
- * gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
+ * dz is rounded to act before the products; but with dx_dtype MOE_F32 a bf16 SWIGLU layer holds it
+ * in 16 bits, as two bf16 parts, for dx and dw alike (and where dx is NULL): dw is then off by
+ * little more than its own rounding, in up to twice the time.  x may be NULL when dw is, w when dx
+ * is.  dy keeps to the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds
+ * up to the gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
  * gradient.  The same inputs give the same bits.  Outputs must not overlap inputs or each other. */
 moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
                                          const void* x, const int32_t* offsets, const void* w,

@@ -22,9 +22,9 @@ struct GroupPlan {
 };
 
 // One grouped product.  Operands are bf16, in parts whose sum is the value (1; 3 each for float32
-// values; 2 of A for a gradient that a float32 result wants exact to 16 bits), with rows at 16-byte
-// boundaries.  A: activations [total rows][a_inner]; B: weights
-// [groups][w_rows][w_inner], or for the weight gradient activations [total rows][b_inner].
+// values; 2 of A for the gradients of bf16 SwiGLU layers that want 16 bits of dz), with rows at
+// 16-byte boundaries.  A: activations [total rows][a_inner]; B: weights [groups][w_rows][w_inner],
+// or for the weight gradient activations [total rows][b_inner].
 struct GroupedProduct {
   GroupedKind kind;
   int groups, total_rows;

@@ -1366,7 +1366,7 @@ GroupedParams params_of(const GroupedProduct& g, const GroupPlan& plan, unsigned
   p.ldz = g.ldz;
   p.c_f32 = g.c_f32;
   p.err = err;
-  p.chunk = g.a_parts == 3 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk;
+  p.chunk = g.a_parts == 3 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk / g.a_parts;
   return p;
 }
 
@@ -1455,11 +1455,12 @@ cudaError_t launch_grouped_products(const GroupedProduct* g, int n, const GroupP
   if (n > 0 && g[0].a_parts == 3) return launch_plain<1, 128, 3, 3, false>(g, n, l);
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < n && e == cudaSuccess; ++i) {
+    const bool two = g[i].a_parts == 2;
     if (g[i].kind == GroupedKind::kWeightGrad) {
-      e = launch_plain<2, 256, 1, 1, false>(&g[i], 1, l);
+      e = two ? launch_plain<2, 256, 2, 1, false>(&g[i], 1, l)
+              : launch_plain<2, 256, 1, 1, false>(&g[i], 1, l);
       continue;
     }
-    const bool two = g[i].a_parts == 2;
     switch (grouped_tile_rows(g[i].total_rows, g[i].groups, false)) {
       case 32:
         e = two ? launch_plain<1, 32, 1, 2, true>(&g[i], 1, l)
