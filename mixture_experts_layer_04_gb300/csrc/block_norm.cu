@@ -177,7 +177,7 @@ struct Columns {
   __device__ __forceinline__ void vector(const float* p, int i, float none, float (&v)[8]) const {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      v[q] = p == nullptr ? none : at(i, q) < width ? __ldg(p + at(i, q)) : 0.f;
+      v[q] = p == nullptr ? none : at(i, q) < width ? __ldca(p + at(i, q)) : 0.f;
   }
 };
 

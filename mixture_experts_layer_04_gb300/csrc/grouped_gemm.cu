@@ -125,9 +125,9 @@ template <typename Cfg>
 __device__ __forceinline__ int4 fetch_tile(const GroupedParams& p, const Table& table, int idx) {
   if (table.bound != nullptr)
     return table_entry(table, p.groups, idx / p.tiles_b, Cfg::kTileRows);
-  if (p.kind != GroupedKind::kWeightGrad) return __ldg(p.plan.tiles + idx / p.tiles_b);
+  if (p.kind != GroupedKind::kWeightGrad) return p.plan.tiles[idx / p.tiles_b];
   const int g = idx / (p.tiles_a * p.tiles_b);
-  return make_int4(__ldg(p.plan.bounds + g), __ldg(p.plan.bounds + g + 1), g, 0);
+  return make_int4(p.plan.bounds[g], p.plan.bounds[g + 1], g, 0);
 }
 
 // Tiles of up to kRowChunk tiles of rows of a group share every tile of features in turn.
@@ -169,7 +169,7 @@ __device__ __forceinline__ Tile tile_at(const GroupedParams& p, int idx, const i
 __device__ __forceinline__ int row_end_of(const GroupedParams& p, const Table& table,
                                           const Tile& t) {
   if (table.bound != nullptr) return table.bound[t.group + 1];
-  return p.kind == GroupedKind::kWeightGrad ? p.rows : __ldg(p.plan.bounds + t.group + 1);
+  return p.kind == GroupedKind::kWeightGrad ? p.rows : p.plan.bounds[t.group + 1];
 }
 
 // ------------------------------------------------------------------- loading ----

@@ -49,3 +49,12 @@ def test_the_wait_comes_first(body):
     assert triggers[0] > waits[0]
     opening = next(i for i, q in enumerate(code) if "__global__" in q or "__device__" in q)
     assert not [q for q in code[opening:waits[0]] if READS.search(q)]
+
+
+@pytest.mark.parametrize("name", ["grouped_gemm.cu", "grouped.cu", "grouped_plan.cuh", "block_norm.cu",
+                                  "grad_norm.cu"])
+def test_no_read_only_loads_of_what_the_kernel_before_wrote(name):
+    """ld.global.nc is for memory that nothing writes while the kernel runs, and these kernels run while
+    the one before them still writes the plan (or a vector of a norm)."""
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        assert "__ldg" not in f.read()
