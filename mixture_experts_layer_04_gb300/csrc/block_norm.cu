@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   __shared__ uint64_t bars[kMostGroups * kMaxDepth];
   __shared__ int gave_up;
   // Each thread sees for itself whether its row arrived, but a row's threads go on, or leave,
-  // together: what is left here before the barrier of the row's sums, they all read behind it.
+  // together: what is left here before the barrier of the row's sums, they all read behind it (one
+  // warp votes: 65536 rows of 256 31.7 us through this).
   __shared__ volatile int missing[2][kMostGroups];
   extern __shared__ __align__(128) uint8_t rings[];
   const int group = threadIdx.x / p.threads, groups = blockDim.x / p.threads;
@@ -757,8 +758,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
   auto reduce = [&](bool arrived) {
     if (!arrived) missing[area][group] = 1;
     row_sum<2>(sums, part[area] + group * (p.threads >> 5) * 2, group, p.threads, warp);
-    if (p.threads == 32) __syncwarp();
-    arrived = missing[area][group] == 0;
+    arrived = p.threads == 32 ? __all_sync(0xffffffffu, arrived) : missing[area][group] == 0;
     area ^= 1;
     return arrived;
   };
@@ -809,6 +809,7 @@ __global__ void __launch_bounds__(512) block_norm_rows_kernel(const __grid_const
     ok = more && arrived;
   }
   // (in the loop this cost 16384 rows of 7168 162 us instead of 142)
+  __syncwarp();
   if (col.t == 0 && (missing[0][group] | missing[1][group]) != 0) ring.drain(row, step, slot, phase);
 }
 
@@ -911,8 +912,7 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
   auto reduce = [&](bool arrived) {
     if (!arrived) missing[area][group] = 1;
     row_sum<4>(sums, part[area] + group * (p.threads >> 5) * 4, group, p.threads, warp);
-    if (p.threads == 32) __syncwarp();
-    arrived = missing[area][group] == 0;
+    arrived = p.threads == 32 ? __all_sync(0xffffffffu, arrived) : missing[area][group] == 0;
     area ^= 1;
     return arrived;
   };
@@ -977,6 +977,7 @@ __global__ void __launch_bounds__(NT) block_norm_grad_rows_kernel(
     }
     ok = more && arrived;
   }
+  __syncwarp();
   if (col.t == 0 && (missing[0][group] | missing[1][group]) != 0) ring.drain(row, step, slot, phase);
   if (p.parts == nullptr) return;
   __syncthreads();  // every group's last row has left its slot
