@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "operand_io.cuh"
 #include "tc_operand.cuh"
 #include "topk.cuh"
 
@@ -1118,9 +1119,6 @@ int ring_depth(const Shape& s, int rows, int blocks, int slot_bytes, int other) 
   const int depth = fits < kMaxDepth ? fits : kMaxDepth;
   return depth >= 2 && rows / (blocks * s.groups) >= 2 ? depth : 0;
 }
-
-inline bool unaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-inline moe_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 long long pick(long long s, int width) { return s != 0 ? s : width; }
 

@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "operand_io.cuh"
 
 namespace moe {
 namespace {
@@ -89,14 +90,6 @@ __device__ __forceinline__ bool both_aligned(const void* a, const void* b) {
   return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15u) == 0;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 struct Raw8 {
   uint4 a, b;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
@@ -113,9 +106,6 @@ struct Raw8 {
     v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
   }
 };
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-
 // A thread's sum: hi + lo is exact but for lo's own roundings (2^-48 of the sum), `rest` takes what
 // leaves float's range.
 struct Squares {
