@@ -498,7 +498,8 @@ moe_status_t moe_grouped_linear_workspace_size(const moe_grouped_config_t* cfg, 
  * a multiple of 16 bytes must start on a 16-byte boundary (MOE_ERR_MISALIGNED).  Float32
  * operands run as three bf16 parts per value, as moe_linear's (where an input is infinite or NaN the
  * outputs that it reaches are not finite); partial sums leave the tensor cores every 64 values
- * (float32 operands), 256 (float32 results; with over 64 rows a group in the mean, 512) or 16384.
+ * (float32 operands), 256 (float32 results; with over 64 rows a group in the mean, and no dz in
+ * parts, 512) or 16384 (dz in parts: 8192).
  * MOE_ERR_UNSUPPORTED: another activation, or more than 2^30 tiles of work.  Outputs must not
  * overlap inputs or each other. */
 moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
@@ -512,12 +513,13 @@ moe_status_t moe_grouped_linear(const moe_grouped_config_t* cfg, const void* x,
  *   returned it (NULL without an activation); dx [rows,in] dx_dtype out or NULL, rows that belong
  *   to no group left as they were; dw [groups, out or 2 out, in] act out or NULL, every element
  *   written; ws as above (NULL with rows == 0, which zeroes dw).
- * dz is rounded to act before the products; but with dx_dtype MOE_F32 a bf16 SWIGLU layer holds it
- * in 16 bits, as two bf16 parts, for dx and dw alike (and where dx is NULL): dw is then off by
- * little more than its own rounding, in up to twice the time.  x may be NULL when dw is, w when dx
- * is.  dy keeps to the rule on 16 bytes that x and w have.  dx in float32 is what moe_combine adds
- * up to the gradient of the tokens: with every weight 1 its sum over a token's rows is moe_permute's
- * gradient.  The same inputs give the same bits.  Outputs must not overlap inputs or each other. */
+ * dz is rounded to act before the products; but with dx_dtype MOE_F32 a bf16 SWIGLU layer keeps dz's
+ * 24 bits for dx (three bf16 parts) and 16 for dw (two of them; also where dx is NULL): both are
+ * then off by little more than their own rounding, in about twice the time.  x may be NULL when dw
+ * is, w when dx is.  dy keeps to the rule on 16 bytes that x and w have.  dx in float32 is what
+ * moe_combine adds up to the gradient of the tokens: with every weight 1 its sum over a token's rows
+ * is moe_permute's gradient.  The same inputs give the same bits.  Outputs must not overlap inputs
+ * or each other. */
 moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* cfg, const void* dy,
                                          const void* x, const int32_t* offsets, const void* w,
                                          const void* z, void* dx, void* dw, void* ws,

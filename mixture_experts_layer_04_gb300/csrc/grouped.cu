@@ -4,7 +4,7 @@
 //  - prepare_kernel: the plan of the groups (grouped_plan.cuh); operands the tensor cores cannot read
 //    in place (float32 values become three bf16 parts, rows whose stride is not a multiple of 16
 //    bytes are copied to one that is); and the gradient of SwiGLU, dz = (dy u silu'(g), dy silu(g)),
-//    in three bf16 parts for float32 layers, one or two for bf16 ones.  Rows that belong to no
+//    in one bf16 part or three.  Rows that belong to no
 //    group and weights of empty groups are passed over.  Bound by reading dy and z and writing dz:
 //    63011 rows of 768 with two parts, 678 MB: 110 us (101 at a copy's rate).
 #include "common.cuh"
@@ -129,7 +129,7 @@ template <int PL>
 __device__ __forceinline__ void store_dz(__nv_bfloat16* dst, const DzTask& t, int n,
                                          float (&v)[8]) {
   if (PL == 3 || t.parts == 1) store_parts<PL>(dst, t.plane, n, t.vec_dz != 0, v);
-  else store_parts<2>(dst, t.plane, n, t.vec_dz != 0, v);
+  else store_parts<3>(dst, t.plane, n, t.vec_dz != 0, v);
 }
 
 // silu(z) = z p and its slope, with p the logistic function of z, for bf16 z: one exponential and one
@@ -277,10 +277,11 @@ Layout layout_of(const moe_grouped_config_t* c) {
   const Shape s = shape_of(c);
   Layout l;
   l.parts = s.f32 ? 3 : 1;
-  // The caller's choice, by dx_dtype: dz rounded to bf16, as a program that keeps it in bf16 has it
-  // (dw 2.3e-3 off in relative L2, of which 1.7e-3 are dw's own rounding), or in two parts, which
-  // keep 16 bits (1.7e-3): 63011 rows of 128 groups, 2048 -> 768, 733 us and 1,220.
-  l.dz_parts = s.f32 ? 3 : s.swiglu && c->dx_dtype == MOE_F32 ? 2 : 1;
+  // The caller's choice, by dx_dtype.  MOE_BF16: dz rounded to bf16, as a program that keeps it in bf16
+  // has it (dw 2.3e-3 off in relative L2, of which 1.7e-3 are dw's own rounding).  MOE_F32: its 24
+  // bits for dx, in three parts, and two of these for dw (1.7e-3).  63011 rows of 128 groups, 2048 ->
+  // 768: 745 us and 1,500; two parts for both left a float32 dx 2.7e-6 off instead of 8e-7 (1,210 us).
+  l.dz_parts = s.f32 || (s.swiglu && c->dx_dtype == MOE_F32) ? 3 : 1;
   l.tile_rows = grouped_tile_rows(c->rows, c->groups, s.f32);
   l.pack_x = s.f32 || odd_stride(s.x, c->dtype);
   l.pack_w = s.f32 || odd_stride(s.w, c->dtype);
@@ -517,6 +518,7 @@ extern "C" moe_status_t moe_grouped_linear_backward(const moe_grouped_config_t* 
   gx.c_f32 = cfg->dx_dtype == MOE_F32;
   gx.ldc = sh.dx;
   gw.kind = GroupedKind::kWeightGrad;
+  if (!sh.f32 && gw.a_parts == 3) gw.a_parts = 2;  // (16 bits of dz, for a bf16 result)
   gw.rows = sh.w_rows;
   gw.b = ox.p;
   gw.ldb = ox.ld;

@@ -17,9 +17,9 @@
 //    of tensor maps, copies of the call's maps whose number of rows is the group's end: TMA then
 //    fills the rest of the block that the end cuts with zeros.  The plan kernel writes them; the
 //    blocks before the last use the call's own.
-//  - A float32 result leaves the tensor core every 256 values (many rows a group: 512; float32
-//    operands, six products per value: 64), a bf16 one every 16384, and is added up in registers:
-//    the tensor core truncates its additions.
+//  - A float32 result leaves the tensor core every 256 values (many rows a group, one part: 512;
+//    float32 operands, six products per value: 64), a bf16 one every 16384 (two parts: 8192), and
+//    is added up in registers: the tensor core truncates its additions.
 //
 // Kernels, by the mean number of rows a group has (known on the host: rows and groups):
 //  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192
@@ -45,13 +45,15 @@ namespace moe {
 namespace {
 
 constexpr int BK = 64;
-// K-blocks per accumulator: of a bf16 result, of a float one of few rows a group, of one of many, of
+// K-blocks per accumulator: of a bf16 result, of a float one, of a float one of many rows a group, of
 // float operands.  An accumulator of values of one sign falls short by up to 6.2e-9 of its size per
 // value: 1.6e-6 over 256 values, 3.2e-6 over 512.  Few rows wait for the weights' read, so every 256
 // values cost them nothing (63.1 us and 63.3, 512 rows of 119 groups, 768 -> 2048); in the wide kernel
-// they would cost a forward of 65536 rows of these 253 -> 323 us, the two-part input gradient 505 ->
-// 560 (13400 clocks a tile, as much as half of its MMAs).  Float32 operands every 64 values: 1.0e-7 of
-// the result in the root mean square, 5.9e-7 every 128, for 1 to 6% of the time.
+// they would cost a forward of 65536 rows of these 253 -> 323 us.  With dz in three parts, whose
+// products are added up in the same accumulator, the error would be 1.7e-6 in relative L2 after 512
+// values, after 256 8.1e-7 (1,485 and 1,527 us for the gradients of 8192 tokens' gate/up).  Float32
+// operands every 64 values: 1.0e-7 of the result in the root mean square, 5.9e-7 every 128, for 1 to
+// 6% of the time.
 constexpr int kMaxChunk = 256, kFloatChunk = 4, kWideFloatChunk = 8, kPartsChunk = 1;
 
 // PA, PB: bf16 parts per value on the A and on the B side.
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
             constexpr bool kThree = PA == 3 && PB == 3;
             constexpr int kTerms = kThree ? 6 : PA * PB;
             constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
-            static_assert(kThree || PA * PB <= 2, "parts");
+            static_assert(kThree || PA == 1 || PB == 1, "parts");
 #pragma unroll
             for (int q = 0; q < kTerms; ++q) {
               const int qa = kThree ? pa[q] : PA - 1 - (PA > 1 ? q : 0);
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(GroupedCfg<CTAS, BN, PA, PB, SWAP>::kThreads, 
 // The forward and the input gradient of groups with many rows.  A CTA pair's tile is 256 features
 // (the weights are the MMA's A side) times a group's share of up to 256 rows in steps of 32: the
 // MMA's N follows the group, so a group of 524 rows costs three tiles of 192 instead of three of
-// 256.  Per stage 16 KB of weights and up to 16 KB (two parts: 32 KB) of rows in each CTA.
+// 256.  Per stage 16 KB of weights and up to 16 KB (three parts: 48 KB) of rows in each CTA.
 //
 // The accumulator has features in its lanes and rows in its columns.  The epilogue reads it in 16 x
 // 8 fragments and stores them transposed (stmatrix), 32 rows at a time, into 128-byte rows that TMA
@@ -1366,7 +1368,7 @@ GroupedParams params_of(const GroupedProduct& g, const GroupPlan& plan, unsigned
   p.ldz = g.ldz;
   p.c_f32 = g.c_f32;
   p.err = err;
-  p.chunk = g.a_parts == 3 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk / g.a_parts;
+  p.chunk = g.b_parts == 3 ? kPartsChunk : g.c_f32 ? kFloatChunk : kMaxChunk / g.a_parts;
   return p;
 }
 
@@ -1407,7 +1409,7 @@ cudaError_t launch_wide(const GroupedProduct& g, const Launch& l) {
                      64 >> b))
       return cudaErrorInvalidValue;
   p.w_blocks = g.swiglu && g.features % 16 == 0;
-  if (g.c_f32) p.chunk = kWideFloatChunk;
+  if (g.c_f32 && PB == 1) p.chunk = kWideFloatChunk;
   long long tiles = 0;
   const cudaError_t e = lay_out(wide_shape<PB>(), &p, g, &tiles);
   if (e != cudaSuccess) return e;
@@ -1452,26 +1454,26 @@ bool group_plan_task(const int32_t* offsets, int rows, int groups, int tile_rows
 cudaError_t launch_grouped_products(const GroupedProduct* g, int n, const GroupPlan& plan,
                                     unsigned* err, int num_sms, cudaStream_t s) {
   const Launch l{plan, err, num_sms, s};
-  if (n > 0 && g[0].a_parts == 3) return launch_plain<1, 128, 3, 3, false>(g, n, l);
+  if (n > 0 && g[0].b_parts == 3) return launch_plain<1, 128, 3, 3, false>(g, n, l);
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < n && e == cudaSuccess; ++i) {
-    const bool two = g[i].a_parts == 2;
+    const bool parts = g[i].a_parts > 1;  // two for a weight gradient, three for an input gradient
     if (g[i].kind == GroupedKind::kWeightGrad) {
-      e = two ? launch_plain<2, 256, 2, 1, false>(&g[i], 1, l)
-              : launch_plain<2, 256, 1, 1, false>(&g[i], 1, l);
+      e = parts ? launch_plain<2, 256, 2, 1, false>(&g[i], 1, l)
+                : launch_plain<2, 256, 1, 1, false>(&g[i], 1, l);
       continue;
     }
     switch (grouped_tile_rows(g[i].total_rows, g[i].groups, false)) {
       case 32:
-        e = two ? launch_plain<1, 32, 1, 2, true>(&g[i], 1, l)
-                : launch_plain<1, 32, 1, 1, true>(&g[i], 1, l);
+        e = parts ? launch_plain<1, 32, 1, 3, true>(&g[i], 1, l)
+                  : launch_plain<1, 32, 1, 1, true>(&g[i], 1, l);
         break;
       case 64:
-        e = two ? launch_plain<1, 64, 1, 2, true>(&g[i], 1, l)
-                : launch_plain<1, 64, 1, 1, true>(&g[i], 1, l);
+        e = parts ? launch_plain<1, 64, 1, 3, true>(&g[i], 1, l)
+                  : launch_plain<1, 64, 1, 1, true>(&g[i], 1, l);
         break;
       default:
-        e = two ? launch_wide<2>(g[i], l) : launch_wide<1>(g[i], l);
+        e = parts ? launch_wide<3>(g[i], l) : launch_wide<1>(g[i], l);
     }
   }
   return e;

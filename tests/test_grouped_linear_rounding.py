@@ -88,3 +88,21 @@ def test_dw_is_off_by_little_more_than_its_own_rounding(sizes, fin, fout, want_d
     if want_dx:
         c.check_backward(dx, dw)
     moe.sync_check()
+
+
+@pytest.mark.parametrize("sizes", [[16] * 6, [60, 0, 40], [300, 90], [3000]], ids=str)
+@pytest.mark.parametrize("fin,fout", [(320, 768), (333, 201)])
+def test_a_float32_dx_keeps_the_bits_of_dz(sizes, fin, fout):
+    """In relative L2: the float32 results' own rounding (2^-24), three parts' (2^-24) and the fast
+    exponential (some 2^-22 of a term, in sums of hundreds of them of either sign) stay below 3e-7,
+    the truncating accumulators, drained every 256 values, below 9e-7: 2.3e-7 for one product of 2048
+    values, and three share one here.  The limit is 1e-6; two parts would leave 2.2e-6 alone."""
+    c = Case(sizes, fin, fout, True, dx=F32, pad=0 if fin == 320 else 3, tail=3, seed=35)
+    dx, _ = c.backward()
+    err = size = 0.0
+    for e, at, w in c.groups():
+        want = c.dz(at) @ w
+        err += ((dx[at, :fin].double() - want) ** 2).sum().item()
+        size += (want ** 2).sum().item()
+    assert (err / size) ** 0.5 < 1e-6
+    moe.sync_check()
