@@ -15,8 +15,8 @@
 // can do).  Where a square would leave float's range (above 2^96, or the largest element below
 // 2^-55 and not 0) the eight are squared in 64 bits.
 //
-// Bound by memory: 150 bf16 tensors of 640 M elements 207 us (6.2 TB/s) and 394 us (6.5 TB/s), 608
-// us a call, 574 at a copy's rate with the second read.  23 tensors of 300 K elements 7.9 us: two
+// Bound by memory: 150 bf16 tensors of 640 M elements 206 us (6.2 TB/s) and 393 us (6.5 TB/s), 603
+// us a call, 574 at a copy's rate with the second read.  23 tensors of 300 K elements 8.1 us: two
 // launches.
 #include <cmath>
 
@@ -31,11 +31,11 @@ constexpr int kPerLaunch = 512;  // tensors: 32 bytes each in the kernel's param
 constexpr int kFewTensors = 64;  // a list that short has a kernel with as short a parameter
 constexpr int kThreads = 512;
 constexpr int kLeastChunk = 4096, kMostChunk = 32768;  // elements
-// Blocks per SM: the sum wants registers for its loads, and so does the scaling of a short list,
-// whose first loads wait for the factor (compiled for four blocks it spills: 640 M elements 647 us a
-// call instead of 608).
-constexpr int kSumBlocks = 2;
-constexpr int scale_blocks(int cap) { return cap <= kFewTensors ? 2 : 4; }
+// Blocks per SM: both kernels want registers for their loads (the scaling compiled for four blocks of
+// 32 registers spills 268 bytes: 640 M elements 608 us a call instead of 603, 23 tensors of 300 K
+// 9.7 instead of 8.1).  The short list's holds its first loads while it works the factor out, and
+// spills 132 bytes even so.
+constexpr int kBlocksPerSm = 2;
 constexpr int kMostBlocks = 1024;
 
 struct Entry {
@@ -185,7 +185,7 @@ __device__ __forceinline__ void chunk_squares(const T* g, int n, Squares& sum) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kSumBlocks) grad_squares_kernel(
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) grad_squares_kernel(
     const __grid_constant__ ClipParams<CAP> p) {
   grid_dep_wait();
   grid_dep_trigger();
@@ -263,7 +263,7 @@ __device__ __forceinline__ double quotient(double a, double b) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, scale_blocks(CAP)) grad_scale_kernel(
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) grad_scale_kernel(
     const __grid_constant__ ClipParams<CAP> p) {
   // A short list's first gradients are on their way while the factor is worked out.
   constexpr bool kAhead = CAP <= kFewTensors;
@@ -357,8 +357,8 @@ template <int CAP>
 moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float max_norm, float eps,
                       float* norm, void* ws, cudaStream_t s) {
   const int sms = device_num_sms();
-  auto blocks_of = [&](int chunks, int per_sm) {
-    const int most = sms * per_sm < kMostBlocks ? sms * per_sm : kMostBlocks;
+  auto blocks_of = [&](int chunks) {
+    const int most = sms * kBlocksPerSm < kMostBlocks ? sms * kBlocksPerSm : kMostBlocks;
     return chunks < most ? (chunks > 0 ? chunks : 1) : most;
   };
   const long long launches = n == 0 ? 1 : (n + CAP - 1) / CAP;
@@ -406,7 +406,7 @@ moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float ma
     p.parts_before = parts;
     p.parts_total = 0;
     if (p.chunks == 0) continue;
-    const int blocks = blocks_of(p.chunks, kSumBlocks);
+    const int blocks = blocks_of(p.chunks);
     if (launch_pdl(grad_squares_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
                    s, p) != cudaSuccess)
       return MOE_ERR_CUDA;
@@ -420,7 +420,7 @@ moe_status_t run_clip(const moe_grad_t* grads, int n, float grad_scale, float ma
     p.norm = out;
     p.parts_before = 0;
     p.parts_total = parts;
-    const int blocks = blocks_of(p.chunks, scale_blocks(CAP));
+    const int blocks = blocks_of(p.chunks);
     if (launch_pdl(grad_scale_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
                    p) != cudaSuccess)
       return MOE_ERR_CUDA;
