@@ -463,7 +463,12 @@ moe_status_t moe_linear_backward(const moe_linear_config_t* cfg, const void* dy,
 /* ------------------------------------------------------------------------------------
  * Matrix products grouped by expert, with their gradients: what trains the experts (and runs
  * ones of any size).  Rows and offsets are those of moe_permute; the order of the stages is
- * that of the layer. */
+ * that of the layer.
+ * For inference at sizes that are multiples of 64, moe_expert_gate_up and moe_expert_down compute
+ * the same products (h is y, out_perm a float32 y) and are the faster ones from a few tokens on:
+ * they start from weights in HBM sooner, and their float32 rows leave faster.  These here take any
+ * size and stride, keep z, and are as fast at one token, and faster for the gate/up product of
+ * thousands of tokens. */
 
 typedef struct {
   int32_t rows;            /* rows that x, y, z, dy and dx have room for, 0..2^30 */
@@ -551,7 +556,8 @@ moe_status_t moe_block_norm_workspace_size(const moe_block_norm_config_t* cfg, s
  *   p   = x[t] R(x[t]) post_weight        (post_weight NULL: p = x[t]);
  *   s   = residual_scale * residual[t] + branch_scale * gate[t] * channel_scale * p;
  *   sum[t] = s;   y[t] = s R(s) norm_weight,
- * in fp32, y from the unrounded s, each output rounded once.
+ * in fp32, y from the unrounded s, each output rounded once.  A row whose squares add up to more than
+ * float's largest has R = 0.
  *   x [rows,width] act; residual [rows,width] act or NULL (0); post_weight, channel_scale,
  *   norm_weight [width] float or NULL; gate [rows] float, NULL with MOE_GATE_NONE; sum [rows,width]
  *   act out or NULL; y [rows,width] act out or NULL (with norm_weight).
@@ -602,8 +608,10 @@ moe_status_t moe_clip_grad_norm_workspace_size(int n, size_t* bytes);
 
 /* norm = grad_scale * the 2-norm over all elements of all n tensors;
  * out  = grad * grad_scale * min(1, max_norm / (norm + eps)) where out is not NULL.
- * Squares are summed in 64 bits, those outside float's range included; the factor is rounded to
- * float once, each output once.  A norm that is NaN makes every output NaN; an infinite one makes
+ * Eight squares at a time are added in float32, those sums in two floats each (48 bits), and in 64
+ * bits across threads; eights with squares outside float's range are squared and added in 64 bits.
+ * norm is within 5 * 2^-24 of itself.  The factor is worked out in 64 bits and rounded to float
+ * once (below 2^-126 it keeps fewer bits), each output once.  A norm that is NaN makes every output NaN; an infinite one makes
  * the factor 0 (an infinite element then becomes NaN).  max_norm may be infinite: the factor is
  * grad_scale, unless the norm is NaN.  In place, where the factor is 1, nothing is written.
  *   grads: n entries in HOST memory, read during the call only (0 <= n <= 2^20); norm [1] float

@@ -196,10 +196,14 @@ class _Grad(ctypes.Structure):
 
 
 class GradList:
-    """The tensors of clip_grad_norm, contiguous bf16 or float32 on the GPU; outs: as many tensors of
+    """The tensors of clip_grad_norm, contiguous bf16 or float32 on one GPU; outs: as many tensors of
     the same sizes (the gradients themselves to clip in place), or None for the norm alone.  Holds
     the tensors, whose storage it names.  Results that overlap one another, or another tensor's
-    gradient, are refused: they would be scaled in no fixed order."""
+    gradient, are refused: they would be scaled in no fixed order.
+
+    Making a list asks every tensor a dozen questions: some 8 us each on the host, 1.2 ms for 150,
+    where clipping them takes 0.6 ms of the GPU.  So make it once, over gradients that stay where
+    they are (kept and zeroed, not set to None, between the steps), and pass it every step."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)

@@ -1,12 +1,12 @@
 // moe_grouped_linear and moe_grouped_linear_backward: argument checks, the workspace and the
 // passes around the grouped tensor-core product (grouped_gemm.cu).
 //
-//  - prepare_kernel: the plan of the groups (grouped_plan.cuh); operands the tensor cores cannot read
-//    in place (float32 values become three bf16 parts, rows whose stride is not a multiple of 16
-//    bytes are copied to one that is); and the gradient of SwiGLU, dz = (dy u silu'(g), dy silu(g)),
-//    in one bf16 part or three.  Rows that belong to no
-//    group and weights of empty groups are passed over.  Bound by reading dy and z and writing dz:
-//    63011 rows of 768 with two parts, 678 MB: 110 us (101 at a copy's rate).
+//  - prepare_kernel: the plan of the groups (grouped_plan.cuh); operands the tensor cores cannot
+//    read in place (float32 values become three bf16 parts, rows whose stride is not a multiple of
+//    16 bytes are copied to one that is); and the gradient of SwiGLU, dz = (dy u silu'(g),
+//    dy silu(g)), in one bf16 part or three.  Rows that belong to no group and weights of empty
+//    groups are passed over.  Bound by reading dy and z and writing dz: 63011 rows of 768 with three
+//    parts, 871 MB: 152 us (130 at a copy's rate).
 #include "common.cuh"
 #include "grouped.h"
 #include "grouped_plan.cuh"

@@ -23,8 +23,8 @@ struct GroupPlan {
 
 // One grouped product.  Operands are bf16, in parts whose sum is the value (1; 3 each for float32
 // values; for a bf16 SwiGLU layer's gradients with a float32 dx 3 of A for dx and 2 for dw), with
-// rows at 16-byte boundaries.  A: activations [total rows][a_inner]; B: weights [groups][w_rows][w_inner],
-// or for the weight gradient activations [total rows][b_inner].
+// rows at 16-byte boundaries.  A: activations [total rows][a_inner]; B: weights
+// [groups][w_rows][w_inner], or for the weight gradient activations [total rows][b_inner].
 struct GroupedProduct {
   GroupedKind kind;
   int groups, total_rows;

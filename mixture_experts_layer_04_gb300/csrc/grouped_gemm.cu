@@ -23,14 +23,19 @@
 //
 // Kernels, by the mean number of rows a group has (known on the host: rows and groups):
 //  - grouped_wide_kernel, over 64: CTA pairs, 256 features x up to 256 rows (see there).  8192
-//    tokens of 8 experts of 128, 2048 -> 2 x 768 with SwiGLU: 292 us, 1,412 TFLOP/s, the tensor pipe
-//    77% busy; rows that fill their tiles (8 groups of 1024, 14336 <-> 4096) run at 1,900;
+//    tokens of 8 experts of 128, 2048 -> 2 x 768 with SwiGLU: 288 us, 1,430 TFLOP/s, the tensor pipe
+//    77% busy; rows that fill their tiles (8 groups of 1024, 14336 <-> 4096) run at 1,800 to 1,900;
 //  - grouped_kernel<1, 32 or 64, .., swapped>, to 32 and to 64: single CTAs, the weights on the
 //    side of 128, bound by the weights' read (512 rows over 119 of 128 groups, 768 -> 2048: 6.0 TB/s).
-//    They plan for themselves: a launch of its own took 1.8 us of one token's 15.4;
-//  - grouped_kernel<2, 256, ..>: CTA pairs for bf16 weight gradients, 256 x 256 tiles.  Bound by
-//    writing: 805 MB take 201 us by themselves here, 322 us with 412 GFLOP, 226 without the stores;
+//    They plan for themselves: a launch of its own took 1.8 us of one token's 15.4.  (rows / groups is
+//    what the buffers hold: 8 rows of 128 groups take 10.6 us in buffers of 8 to 4096 rows, 16.5 in
+//    those of 9000 and more, with the weights in L2);
+//  - grouped_kernel<2, 256, 1 or 2, ..>: CTA pairs for bf16 weight gradients, 256 x 256 tiles.  Bound
+//    by writing: 805 MB take 201 us by themselves here, 356 us with 412 GFLOP, 226 without the stores;
+//    two parts (825 GFLOP) 517;
 //  - grouped_kernel<1, 128, 3, 3>: float32 operands in three parts, all three products.
+// The kernels on CTA pairs hold a tile's sums in 128 registers of an epilogue thread's 168 and spill
+// around them (108 bytes in the wide one, 140 in the weight gradients').
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
