@@ -107,7 +107,8 @@ struct GroupedParams {
 };
 
 // The products of a launch: one, or both gradients of a float32 layer, whose tiles follow one another
-// (small layers: 33 tiles of dx and 42 of dw, 517 rows of 333 -> 201, leave half of the SMs idle).
+// (517 rows of 7 groups, 333 -> 201: 33 tiles of dx and 84 of dw; one after the other 43 us a call
+// instead of 27.5).
 template <int N>
 struct GroupedJobs {
   GroupedParams p[N];
